@@ -302,6 +302,117 @@ int dense_ffn_forward_q2(const void *x, int32_t m, int32_t hidden,
                          const q2_weight *wu, const q2_weight *wd, void *out,
                          void *stream);
 
+/* ---- 8-bit paged KV cache ----------------------------------------------------
+ * The attention half of a decoder layer at serving time, next to the FFN:
+ * a cache of K and V in E4M3 with one scale for each page of tokens and KV
+ * head, the attention that reads it, and eviction by the attention that its
+ * tokens received.  (Not on the pages; the formulas below define it.)
+ *
+ * A cache is a pool of pages of `page` tokens:
+ *   k_codes, v_codes  : device, uint8 [pages][heads][page * dim], E4M3FN;
+ *   k_scales, v_scales: device, uint8 [pages][heads], E8M0 (1..254):
+ *                       value = e4m3(code) * 2^(scale - 127);
+ *   weights           : device, fp32 [pages][page], the attention weight each
+ *                       token has received so far; null if not kept.
+ * A page's codes of one head are page/16 units of 16 tokens, 16 * dim bytes
+ * each.  K unit: [dim/16][16 tokens][16 channels].  V unit:
+ * [dim/64][g 4][b 16][c 4][i 4] with token 4 g + i and channel
+ * 64 a + 16 c + b (a the first index).
+ * dim is 64, 128 or 256; page is 16, 32, 64 or 128; codes are 16-byte, weights
+ * 4-byte aligned.  The pool may be larger than 4 GiB. */
+typedef struct kv8_cache {
+  uint8_t *k_codes;
+  uint8_t *v_codes;
+  uint8_t *k_scales;
+  uint8_t *v_scales;
+  float *weights;
+  int32_t pages;
+  int32_t heads;
+  int32_t dim;
+  int32_t page;
+} kv8_cache;
+
+/* The sequences of a call.
+ *   table : device, int32 [seqs][cols]; entry c of a sequence names the page
+ *           of its tokens page * c ...  An entry outside the pool names no
+ *           page: its tokens are neither written nor seen.
+ *   lens  : device, int32 [seqs], the sequence's tokens, those of this call's
+ *           rows with them (a length is held to 0 .. cols * page).
+ *   starts: device, int32 [seqs + 1], sequence b's rows are starts[b] ..
+ *           starts[b+1] - 1 of the row arrays; null: rows / seqs each.
+ *   rows  : rows of the row arrays in all;
+ *   max_rows, max_len: bounds on one sequence's rows and tokens.  They size
+ *           the launch: rows and tokens beyond them are left out.
+ * Row i of a sequence with n tokens and r rows is its token n - r + i. */
+typedef struct kv8_batch {
+  const int32_t *table;
+  const int32_t *lens;
+  const int32_t *starts;
+  int32_t seqs;
+  int32_t cols;
+  int32_t rows;
+  int32_t max_rows;
+  int32_t max_len;
+} kv8_batch;
+
+/* bf16 [rows][heads][dim], the last dimension contiguous; strides in
+ * elements, multiples of 8; 16-byte aligned.  (A part of a projection's
+ * output is such an array.) */
+typedef struct kv8_rows {
+  const void *ptr;
+  int64_t row_stride;
+  int64_t head_stride;
+} kv8_rows;
+
+/* Writes the rows' K and V into the cache.  A page's scale of one head is
+ * 2^E, E the smallest in -117 .. 119 with |x| <= 448 * 2^E for its finite
+ * values; the page's older tokens keep E from falling, and where it rises
+ * their codes move to it (exact but for codes that become subnormal).  Codes
+ * are nearest, ties to even; infinities saturate, NaN is kept and counts for
+ * no scale.  The first token of a page starts it afresh.  The rows' weights,
+ * where the cache keeps them, become 0.  No two sequences may write to one
+ * page in one call. */
+int kv8_append(const kv8_rows *k, const kv8_rows *v, const kv8_cache *cache,
+               const kv8_batch *batch, void *stream);
+
+/* Bytes of workspace that kv8_attention takes for these sizes (an upper
+ * bound for smaller max_len and max_rows); negative status on an error. */
+int64_t kv8_attention_workspace(int32_t q_heads, const kv8_cache *cache, const kv8_batch *batch);
+
+/* Attention of the rows over the cache.  Row i of query head u sees the
+ * tokens j <= p of its sequence, p = n - r + i its own position, with
+ * window > 0 only j > p - window; u reads KV head u / (q_heads / heads):
+ *   s_j = scale * q . k_j,  lse = log sum e^s_j,  out = sum e^(s_j - lse) v_j.
+ * A row that sees nothing gives out = 0 and lse = -inf.  Tokens that a row
+ * does not see have no influence on it, whatever their codes.
+ *   out: bf16 [rows][q_heads][dim]; lse: fp32 [rows][q_heads] or null.
+ * accumulate != 0 (needs lse and the cache's weights) also adds to each
+ * token's weight the sum of e^(s_j - lse) over the rows and query heads that
+ * see it, in an order that does not change from call to call.
+ * fp32 throughout, except that e^(s_j - m) is rounded to bf16 before its
+ * product with V (as the other operand of that product is at most bf16).
+ * workspace: device memory of kv8_attention_workspace bytes, 256-byte
+ * aligned, all zero before its first use and left as it needs to be for the
+ * next; one per stream that calls may overlap on.  Null: the library's
+ * scratch arena (see above). */
+int kv8_attention(const kv8_rows *q, int32_t q_heads, float scale, int32_t window,
+                  const kv8_cache *cache, const kv8_batch *batch, void *out, float *lse,
+                  int32_t accumulate, void *workspace, int64_t workspace_bytes, void *stream);
+
+/* Keeps at most `keep` tokens of each sequence: the first `sink`, the last
+ * `recent` (sink + recent <= keep) and of the others those with the largest
+ * weights, of equal ones the earlier.  (A weight that is NaN counts as the
+ * largest.)  They are written, in order, to the pages of new_table (device,
+ * int32 [seqs][new_cols], new_cols >= ceil(keep / page)), with scales found
+ * from the kept tokens as in kv8_append, and with their weights.  A sequence
+ * of at most `keep` tokens is copied whole.  new_lens: device, int32 [seqs];
+ * kept: device, int32 [seqs][keep], the kept positions, then -1.  No page of
+ * new_table may be one that the batch's table names.  batch's rows are not
+ * used. */
+int kv8_evict(const kv8_cache *cache, const kv8_batch *batch, const int32_t *new_table,
+              int32_t new_cols, int32_t keep, int32_t recent, int32_t sink, int32_t *new_lens,
+              int32_t *kept, void *stream);
+
 /* The calling thread's last error message ("" if none).  The pages' ops
  * return an error value whose message names the failed check (page
  * layers/dense_ffn_fixed.rs, the `ensure!`/`bail!` checks of

@@ -1,5 +1,5 @@
 """Python binding of ``libnvfp4ffn.so``, the MI355X (gfx950) dense SwiGLU FFN
-with NVFP4 weights.
+with NVFP4 weights, and the 8-bit paged KV cache and its attention next to it.
 
 Argument marshalling only: every step of the FFN runs in the library's HIP
 kernels; PyTorch supplies device memory and the current stream.  The names
@@ -12,7 +12,9 @@ the GPU; a weight is any object with ``codes`` (uint8 ``[n, k/2]``),
 ``scales`` (uint8 ``[n, k/16]``, E4M3 bits) and ``tensor_scale`` (or
 ``ts``) -- see :class:`NVFP4Weight`; a W8A8 weight has ``codes`` (uint8
 ``[n, k]``, E4M3 bits) and ``scales`` (float32 ``[ceil(n/128),
-ceil(k/128)]``) -- see :class:`FP8Weight`.
+ceil(k/128)]``) -- see :class:`FP8Weight`.  The ``kv8_*`` calls take a
+:class:`KV8Cache`, a page table and lengths (int32, on the GPU) and bf16
+``[rows, heads, dim]`` arrays that may be parts of a larger one.
 """
 
 from __future__ import annotations
@@ -39,6 +41,7 @@ __all__ = [
     "nvfp4_gate_up_views", "dense_ffn_forward_fused", "LoraPair", "nvfp4_lora_delta",
     "dense_ffn_forward_lora", "FP8Weight", "fp8_quantize_rows", "fp8_gemm_w8a8",
     "dense_ffn_forward_w8a8", "Q2Weight", "q2_gemm_w2a16", "dense_ffn_forward_q2",
+    "KV8Cache", "kv8_cache", "kv8_append", "kv8_attention", "kv8_workspace", "kv8_evict",
     "nvfp4_last_error", "nvfp4_release", "nvfp4_abi_version", "load_library",
     "nvfp4_probe_mfma_bf16",
     "nvfp4_probe_read",
@@ -129,6 +132,53 @@ class _CQ2Weight(ctypes.Structure):
     ]
 
 
+@dataclass
+class KV8Cache:
+    """A pool of pages of an 8-bit KV cache on the GPU.  A page's codes of one
+    head are in the kernels' operand order (include/nvfp4ffn.h), not in
+    [page, dim] order; the shape gives their sizes."""
+    k_codes: torch.Tensor   # uint8 [pages, heads, page, dim], E4M3FN bit patterns
+    v_codes: torch.Tensor   # as k_codes
+    k_scales: torch.Tensor  # uint8 [pages, heads], E8M0: value = e4m3(code) * 2^(scale - 127)
+    v_scales: torch.Tensor  # as k_scales
+    weights: torch.Tensor | None = None  # float32 [pages, page], attention weight received
+
+
+class _CKv8Cache(ctypes.Structure):
+    _fields_ = [
+        ("k_codes", ctypes.c_void_p),
+        ("v_codes", ctypes.c_void_p),
+        ("k_scales", ctypes.c_void_p),
+        ("v_scales", ctypes.c_void_p),
+        ("weights", ctypes.c_void_p),
+        ("pages", ctypes.c_int32),
+        ("heads", ctypes.c_int32),
+        ("dim", ctypes.c_int32),
+        ("page", ctypes.c_int32),
+    ]
+
+
+class _CKv8Batch(ctypes.Structure):
+    _fields_ = [
+        ("table", ctypes.c_void_p),
+        ("lens", ctypes.c_void_p),
+        ("starts", ctypes.c_void_p),
+        ("seqs", ctypes.c_int32),
+        ("cols", ctypes.c_int32),
+        ("rows", ctypes.c_int32),
+        ("max_rows", ctypes.c_int32),
+        ("max_len", ctypes.c_int32),
+    ]
+
+
+class _CKv8Rows(ctypes.Structure):
+    _fields_ = [
+        ("ptr", ctypes.c_void_p),
+        ("row_stride", ctypes.c_int64),
+        ("head_stride", ctypes.c_int64),
+    ]
+
+
 _lib = None
 
 
@@ -143,6 +193,7 @@ def load_library(path: str = LIB_PATH):
     L = ctypes.CDLL(path)
     vp, i32, i64 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64
     wp = ctypes.POINTER(_CWeight)
+    kc, kb, kr = (ctypes.POINTER(t) for t in (_CKv8Cache, _CKv8Batch, _CKv8Rows))
     sig = {
         "nvfp4_gemm_w4a16": [vp, i32, wp, vp, vp],
         "nvfp4_gemm_w4a4": [vp, i32, wp, vp, vp],
@@ -163,6 +214,9 @@ def load_library(path: str = LIB_PATH):
         "fp8_gemm_w8a8": [vp, i32, ctypes.POINTER(_CFp8Weight), vp, vp],
         "dense_ffn_forward_w8a8": [vp, i32, i32, i32, ctypes.POINTER(_CFp8Weight),
                                    ctypes.POINTER(_CFp8Weight), ctypes.POINTER(_CFp8Weight), vp, vp],
+        "kv8_append": [kr, kr, kc, kb, vp],
+        "kv8_attention": [kr, i32, ctypes.c_float, i32, kc, kb, vp, vp, i32, vp, i64, vp],
+        "kv8_evict": [kc, kb, vp, i32, i32, i32, i32, vp, vp, vp],
     }
     for name, args in sig.items():
         f = getattr(L, name)
@@ -174,6 +228,8 @@ def load_library(path: str = LIB_PATH):
     L.nvfp4_probe_read.restype = ctypes.c_int
     L.nvfp4_probe_encode.argtypes = [vp, i64, ctypes.c_float, vp, vp, vp, vp]
     L.nvfp4_probe_encode.restype = ctypes.c_int
+    L.kv8_attention_workspace.argtypes = [i32, kc, kb]
+    L.kv8_attention_workspace.restype = i64
     L.nvfp4_last_error.argtypes = []
     L.nvfp4_last_error.restype = ctypes.c_char_p
     L.nvfp4_release.argtypes = []
@@ -583,3 +639,157 @@ def dense_ffn_forward_q2(x: torch.Tensor, wg, wu, wd, out: torch.Tensor | None =
     _check(L.dense_ffn_forward_q2(_ptr(x), m, hidden, inter, ctypes.byref(cg), ctypes.byref(cu),
                                   ctypes.byref(cd), _ptr(out), _stream(stream)))
     return out
+
+
+# ---- 8-bit paged KV cache -----------------------------------------------------------
+
+def kv8_cache(pages: int, heads: int, dim: int, page: int = 64, weights: bool = False,
+              device="cuda") -> KV8Cache:
+    """An empty pool: `pages` pages of `page` tokens (16, 32, 64 or 128) of
+    `heads` KV heads of size `dim` (64, 128 or 256); with weights, the
+    attention weight each token receives is kept too (kv8_evict needs it)."""
+    codes = [torch.zeros((pages, heads, page, dim), dtype=torch.uint8, device=device) for _ in "kv"]
+    scales = [torch.full((pages, heads), 127, dtype=torch.uint8, device=device) for _ in "kv"]
+    w = torch.zeros((pages, page), dtype=torch.float32, device=device) if weights else None
+    return KV8Cache(*codes, *scales, w)
+
+
+def _ckv8(c: KV8Cache) -> _CKv8Cache:
+    k, v, ks, vs, w = c.k_codes, c.v_codes, c.k_scales, c.v_scales, c.weights
+    if k.dtype != torch.uint8 or k.dim() != 4 or not k.is_contiguous():
+        raise ValueError("k_codes: expected a contiguous uint8 [pages, heads, page, dim] tensor")
+    if v.dtype != torch.uint8 or v.shape != k.shape or not v.is_contiguous():
+        raise ValueError("v_codes: expected a contiguous uint8 tensor of k_codes' shape")
+    pages, heads, page, dim = k.shape
+    for t, nm in ((ks, "k_scales"), (vs, "v_scales")):
+        if t.dtype != torch.uint8 or tuple(t.shape) != (pages, heads) or not t.is_contiguous():
+            raise ValueError(f"{nm}: expected a contiguous uint8 [{pages}, {heads}] tensor")
+    if w is not None and (w.dtype != torch.float32 or tuple(w.shape) != (pages, page) or not w.is_contiguous()):
+        raise ValueError(f"weights: expected a contiguous float32 [{pages}, {page}] tensor")
+    return _CKv8Cache(k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr(),
+                      None if w is None else w.data_ptr(), pages, heads, dim, page)
+
+
+def _ckv8_rows(x: torch.Tensor, name: str, dim: int, heads: int | None = None) -> _CKv8Rows:
+    """A bf16 [rows, heads, dim] array with strides of whole 16-byte pieces."""
+    if not isinstance(x, torch.Tensor) or x.dtype != torch.bfloat16 or x.dim() != 3:
+        raise ValueError(f"{name}: expected a 3-D bfloat16 tensor [rows, heads, dim]")
+    if x.shape[2] != dim or (heads is not None and x.shape[1] != heads):
+        raise ValueError(f"{name}: has shape {tuple(x.shape)}, the cache has {heads or 'n'} heads of size {dim}")
+    rs, hs, ds = x.stride()
+    if ds != 1 or rs % 8 or hs % 8:
+        raise ValueError(f"{name}: strides {x.stride()}: expected the last 1, the others multiples of 8")
+    return _CKv8Rows(x.data_ptr(), rs, hs)
+
+
+def _ckv8_batch(table, lens, starts, rows, max_rows, max_len, page) -> _CKv8Batch:
+    if table.dtype != torch.int32 or table.dim() != 2 or not table.is_contiguous():
+        raise ValueError("table: expected a contiguous int32 [seqs, cols] tensor")
+    seqs, cols = table.shape
+    if lens.dtype != torch.int32 or tuple(lens.shape) != (seqs,) or not lens.is_contiguous():
+        raise ValueError(f"lens: expected a contiguous int32 [{seqs}] tensor")
+    if starts is not None and (starts.dtype != torch.int32 or tuple(starts.shape) != (seqs + 1,)
+                               or not starts.is_contiguous()):
+        raise ValueError(f"starts: expected a contiguous int32 [{seqs + 1}] tensor")
+    if max_rows is None or starts is None:
+        max_rows = rows if starts is not None else rows // max(seqs, 1)
+    if max_len is None:
+        max_len = cols * page
+    return _CKv8Batch(table.data_ptr(), lens.data_ptr(), None if starts is None else starts.data_ptr(),
+                      seqs, cols, rows, int(max_rows), int(max_len))
+
+
+def kv8_append(k: torch.Tensor, v: torch.Tensor, cache: KV8Cache, table: torch.Tensor,
+               lens: torch.Tensor, starts: torch.Tensor | None = None, *, max_rows: int | None = None,
+               stream=None) -> None:
+    """Write the rows of k and v (bf16 [rows, heads, dim]) into the cache.
+
+    lens [seqs] counts each sequence's tokens with these; row i of a sequence
+    with r rows is its token lens - r + i, on page table[seq, token // page].
+    starts [seqs + 1] gives each sequence's rows; without it every sequence
+    has rows / seqs.  max_rows bounds one sequence's rows (default: rows)."""
+    L = load_library()
+    cc = _ckv8(cache)
+    ck, cv = _ckv8_rows(k, "k", cc.dim, cc.heads), _ckv8_rows(v, "v", cc.dim, cc.heads)
+    if v.shape[0] != k.shape[0]:
+        raise ValueError(f"v: {v.shape[0]} rows, k has {k.shape[0]}")
+    cb = _ckv8_batch(table, lens, starts, k.shape[0], max_rows, None, cc.page)
+    _gpu(k, v, cache.k_codes, cache.v_codes, cache.k_scales, cache.v_scales, cache.weights, table, lens, starts)
+    _check(L.kv8_append(ctypes.byref(ck), ctypes.byref(cv), ctypes.byref(cc), ctypes.byref(cb), _stream(stream)))
+
+
+def kv8_workspace(q_heads: int, cache: KV8Cache, table: torch.Tensor, lens: torch.Tensor, rows: int,
+                  starts: torch.Tensor | None = None, *, max_rows: int | None = None,
+                  max_len: int | None = None) -> torch.Tensor:
+    """A workspace for kv8_attention calls of these sizes or smaller ones, for
+    one stream (without one, calls share the library's scratch arena)."""
+    L = load_library()
+    cc = _ckv8(cache)
+    n = L.kv8_attention_workspace(int(q_heads), ctypes.byref(cc), ctypes.byref(
+        _ckv8_batch(table, lens, starts, int(rows), max_rows, max_len, cc.page)))
+    if n < 0:
+        _check(int(n))
+    return torch.zeros((max(n, 256),), dtype=torch.uint8, device=cache.k_codes.device)
+
+
+def kv8_attention(q: torch.Tensor, cache: KV8Cache, table: torch.Tensor, lens: torch.Tensor,
+                  starts: torch.Tensor | None = None, *, scale: float | None = None, window: int = 0,
+                  max_rows: int | None = None, max_len: int | None = None, out: torch.Tensor | None = None,
+                  lse=None, accumulate: bool = False, workspace: torch.Tensor | None = None, stream=None):
+    """Causal attention of the rows of q (bf16 [rows, q_heads, dim]) over the
+    cache; rows, lens, starts and table as in kv8_append, whose rows the cache
+    already holds.  scale defaults to dim ** -0.5; window > 0 limits a row to
+    the last `window` tokens up to its own.  max_rows and max_len bound one
+    sequence's rows and tokens (they size the launch; default: from rows and
+    the table's width).
+
+    Returns out (bf16 [rows, q_heads, dim]); with lse (True, or a float32
+    [rows, q_heads] tensor to write to) returns (out, lse).  accumulate adds
+    the attention weight each token receives to cache.weights."""
+    L = load_library()
+    cc = _ckv8(cache)
+    cq = _ckv8_rows(q, "q", cc.dim)
+    rows, q_heads, dim = q.shape
+    cb = _ckv8_batch(table, lens, starts, rows, max_rows, max_len, cc.page)
+    if out is None:
+        out = torch.empty((rows, q_heads, dim), dtype=torch.bfloat16, device=q.device)
+    elif out.dtype != torch.bfloat16 or tuple(out.shape) != (rows, q_heads, dim) or not out.is_contiguous():
+        raise ValueError(f"out: expected a contiguous bfloat16 [{rows}, {q_heads}, {dim}] tensor")
+    give = lse is not None and lse is not False
+    if lse is True or (accumulate and not give):
+        lse = torch.empty((rows, q_heads), dtype=torch.float32, device=q.device)
+    elif not give:
+        lse = None
+    elif lse.dtype != torch.float32 or tuple(lse.shape) != (rows, q_heads) or not lse.is_contiguous():
+        raise ValueError(f"lse: expected a contiguous float32 [{rows}, {q_heads}] tensor")
+    if workspace is not None and (workspace.dtype != torch.uint8 or not workspace.is_contiguous()):
+        raise ValueError("workspace: expected a contiguous uint8 tensor (kv8_workspace)")
+    _gpu(q, out, lse, workspace, cache.k_codes, cache.v_codes, cache.k_scales, cache.v_scales, cache.weights,
+         table, lens, starts)
+    _check(L.kv8_attention(ctypes.byref(cq), q_heads, dim ** -0.5 if scale is None else float(scale), int(window),
+                           ctypes.byref(cc), ctypes.byref(cb), _ptr(out), _ptr(lse), 1 if accumulate else 0,
+                           _ptr(workspace), 0 if workspace is None else workspace.numel(), _stream(stream)))
+    return (out, lse) if give else out
+
+
+def kv8_evict(cache: KV8Cache, table: torch.Tensor, lens: torch.Tensor, new_table: torch.Tensor, keep: int, *,
+              recent: int = 0, sink: int = 0, max_len: int | None = None, stream=None):
+    """Cut each sequence to at most `keep` tokens -- its first `sink`, its last
+    `recent` and of the others those with the largest cache.weights -- and
+    write them, in order, to the pages of new_table (int32 [seqs, new_cols],
+    none of them a page of table).  Returns (new lens [seqs], kept positions
+    [seqs, keep] padded with -1), int32."""
+    L = load_library()
+    cc = _ckv8(cache)
+    cb = _ckv8_batch(table, lens, None, 0, None, max_len, cc.page)
+    if new_table.dtype != torch.int32 or new_table.dim() != 2 or new_table.shape[0] != cb.seqs \
+            or not new_table.is_contiguous():
+        raise ValueError(f"new_table: expected a contiguous int32 [{cb.seqs}, new_cols] tensor")
+    if int(keep) <= 0:
+        raise ValueError(f"keep: {keep}, expected at least 1")
+    _gpu(table, lens, new_table, cache.k_codes, cache.v_codes, cache.k_scales, cache.v_scales, cache.weights)
+    new_lens = torch.empty((cb.seqs,), dtype=torch.int32, device=table.device)
+    kept = torch.empty((cb.seqs, int(keep)), dtype=torch.int32, device=table.device)
+    _check(L.kv8_evict(ctypes.byref(cc), ctypes.byref(cb), _ptr(new_table), new_table.shape[1], int(keep),
+                       int(recent), int(sink), _ptr(new_lens), _ptr(kept), _stream(stream)))
+    return new_lens, kept

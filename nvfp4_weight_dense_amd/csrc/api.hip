@@ -494,6 +494,63 @@ int run_q2(const void *x, int m, int k, int n, int gshift, int nmat, const Q2Mat
                     "packed-Q2 projection launch");
 }
 
+// ---- 8-bit paged KV cache ---------------------------------------------------------
+
+int check_kv8_cache(const kv8_cache *c) {
+  if (!c) return fail(NVFP4_EINVAL, "kv8 cache: null descriptor");
+  if (!c->k_codes || !c->v_codes || !c->k_scales || !c->v_scales)
+    return fail(NVFP4_EINVAL, "kv8 cache: null codes or scales pointer");
+  if (misaligned(c->k_codes) || misaligned(c->v_codes) || ((uintptr_t)c->weights & 3u))
+    return fail(NVFP4_EINVAL, "kv8 cache: codes must be 16-byte and weights 4-byte aligned");
+  if (c->pages <= 0 || c->heads <= 0 || c->heads > 4096)
+    return fail(NVFP4_ESHAPE, "kv8 cache: pages=%d must be positive, heads=%d in 1..4096", c->pages, c->heads);
+  if (c->dim != 64 && c->dim != 128 && c->dim != 256)
+    return fail(NVFP4_ESHAPE, "kv8 cache: dim=%d is not 64, 128 or 256", c->dim);
+  if (c->page != 16 && c->page != 32 && c->page != 64 && c->page != 128)
+    return fail(NVFP4_ESHAPE, "kv8 cache: page=%d is not 16, 32, 64 or 128", c->page);
+  return NVFP4_OK;
+}
+
+// with_rows: the call reads row arrays (append, attention)
+int check_kv8_batch(const kv8_batch *b, const kv8_cache *c, bool with_rows) {
+  if (!b) return fail(NVFP4_EINVAL, "kv8 batch: null descriptor");
+  if (b->seqs < 0 || b->rows < 0 || b->max_rows < 0 || b->max_len < 0)
+    return fail(NVFP4_EINVAL, "kv8 batch: seqs=%d, rows=%d, max_rows=%d and max_len=%d must not be negative",
+                b->seqs, b->rows, b->max_rows, b->max_len);
+  if (b->seqs > 65535) return fail(NVFP4_ESHAPE, "kv8 batch: seqs=%d exceeds 65535", b->seqs);
+  if (b->seqs > 0 && (!b->table || !b->lens)) return fail(NVFP4_EINVAL, "kv8 batch: null table or lens pointer");
+  if (((uintptr_t)b->table | (uintptr_t)b->lens | (uintptr_t)b->starts) & 3u)
+    return fail(NVFP4_EINVAL, "kv8 batch: table, lens and starts must be 4-byte aligned");
+  // (positions and the table's tokens stay far below 2^31)
+  if (b->cols <= 0 || (int64_t)b->cols * c->page > (1 << 28))
+    return fail(NVFP4_ESHAPE, "kv8 batch: cols=%d pages of %d tokens: expected 1 to 2^28 tokens", b->cols, c->page);
+  if (with_rows && b->rows > (1 << 24)) return fail(NVFP4_ESHAPE, "kv8 batch: rows=%d exceeds 2^24", b->rows);
+  if (with_rows && !b->starts && b->seqs > 0 && b->rows % b->seqs != 0)
+    return fail(NVFP4_ESHAPE, "kv8 batch: %d rows over %d sequences without starts", b->rows, b->seqs);
+  return NVFP4_OK;
+}
+
+int check_kv8_rows(const kv8_rows *x, const char *name) {
+  if (!x || !x->ptr) return fail(NVFP4_EINVAL, "%s: null pointer", name);
+  if (misaligned(x->ptr)) return fail(NVFP4_EINVAL, "%s: must be 16-byte aligned", name);
+  if (x->row_stride < 0 || x->head_stride < 0 || x->row_stride % 8 != 0 || x->head_stride % 8 != 0)
+    return fail(NVFP4_ESHAPE, "%s: strides %lld and %lld must be multiples of 8, not negative", name,
+                (long long)x->row_stride, (long long)x->head_stride);
+  return NVFP4_OK;
+}
+
+Kv8Pool kv8_pool(const kv8_cache *c) {
+  int shift = 4;
+  while ((1 << shift) < c->page) ++shift;
+  return Kv8Pool{c->k_codes, c->v_codes, c->k_scales, c->v_scales, c->weights, c->pages, c->heads, shift};
+}
+
+Kv8Rows kv8_rows_ref(const kv8_rows *x) { return Kv8Rows{x->ptr, x->row_stride, x->head_stride}; }
+
+Kv8Batch kv8_batch_ref(const kv8_batch *b) {
+  return Kv8Batch{b->table, b->lens, b->starts, b->seqs, b->cols, b->rows, std::min(b->max_rows, b->rows)};
+}
+
 struct NoAllocDev {
   bool ready = false;
   void *ptr = nullptr;
@@ -1063,6 +1120,83 @@ int dense_ffn_forward_q2(const void *x, int32_t m, int32_t hidden, int32_t inter
   Q2MatRef w2[2] = {mg, mu};
   if ((rc = run_q2(x, m, hidden, inter, gsg, 2, w2, act, scr, s))) return rc;
   return run_q2(act, m, inter, hidden, gsd, 1, &md, out, scr, s);
+}
+
+// ---- 8-bit paged KV cache ---------------------------------------------------------
+
+int kv8_append(const kv8_rows *k, const kv8_rows *v, const kv8_cache *cache, const kv8_batch *batch,
+               void *stream) {
+  g_err.clear();
+  int rc;
+  if ((rc = check_kv8_cache(cache)) || (rc = check_kv8_batch(batch, cache, true))) return rc;
+  if (batch->seqs == 0 || batch->rows == 0 || batch->max_rows == 0) return NVFP4_OK;
+  if ((rc = check_kv8_rows(k, "k")) || (rc = check_kv8_rows(v, "v"))) return rc;
+  hipStream_t s = (hipStream_t)stream;
+  ProfileScope ps("kv8_append", batch->rows, s);
+  return hip_status(launch_kv8_append(kv8_rows_ref(k), kv8_rows_ref(v), kv8_pool(cache), kv8_batch_ref(batch),
+                                      cache->dim, s),
+                    "kv8_append launch");
+}
+
+int64_t kv8_attention_workspace(int32_t q_heads, const kv8_cache *cache, const kv8_batch *batch) {
+  g_err.clear();
+  int rc;
+  if ((rc = check_kv8_cache(cache)) || (rc = check_kv8_batch(batch, cache, true))) return rc;
+  if (q_heads <= 0 || q_heads % cache->heads != 0 || q_heads > 65535)
+    return fail(NVFP4_ESHAPE, "kv8_attention: q_heads=%d is not a multiple of heads=%d up to 65535", q_heads,
+                cache->heads);
+  return 0;
+}
+
+int kv8_attention(const kv8_rows *q, int32_t q_heads, float scale, int32_t window, const kv8_cache *cache,
+                  const kv8_batch *batch, void *out, float *lse, int32_t accumulate, void *workspace,
+                  int64_t workspace_bytes, void *stream) {
+  const int64_t need = kv8_attention_workspace(q_heads, cache, batch);  // checks them too
+  if (need < 0) return (int)need;
+  int rc;
+  if (!(fabsf(scale) < INFINITY)) return fail(NVFP4_EINVAL, "kv8_attention: scale is not finite");
+  if (window < 0) return fail(NVFP4_EINVAL, "kv8_attention: window=%d is negative", window);
+  if (batch->seqs == 0 || batch->rows == 0 || batch->max_rows == 0) return NVFP4_OK;
+  if ((rc = check_kv8_rows(q, "q"))) return rc;
+  if (!out) return fail(NVFP4_EINVAL, "kv8_attention: null out pointer");
+  if (misaligned(out) || ((uintptr_t)lse & 3u))
+    return fail(NVFP4_EINVAL, "kv8_attention: out must be 16-byte and lse 4-byte aligned");
+  if (accumulate && (!lse || !cache->weights))
+    return fail(NVFP4_EINVAL, "kv8_attention: accumulate needs lse and the cache's weights");
+  if (workspace && (workspace_bytes < need || ((uintptr_t)workspace & 255u)))
+    return fail(NVFP4_EINVAL, "kv8_attention: the workspace must be 256-byte aligned and of %lld bytes",
+                (long long)need);
+  hipStream_t s = (hipStream_t)stream;
+  const Kv8Attn a{kv8_rows_ref(q), q_heads, std::min(batch->max_len, batch->cols * cache->page), window, scale,
+                  out, lse};
+  ProfileScope ps("kv8_attention", batch->rows, s);
+  if ((rc = hip_status(launch_kv8_attention(a, kv8_pool(cache), kv8_batch_ref(batch), cache->dim, s),
+                       "kv8_attention launch")) || !accumulate)
+    return rc;
+  return hip_status(launch_kv8_weights(a, kv8_pool(cache), kv8_batch_ref(batch), cache->dim, s),
+                    "kv8_attention weights launch");
+}
+
+int kv8_evict(const kv8_cache *cache, const kv8_batch *batch, const int32_t *new_table, int32_t new_cols,
+              int32_t keep, int32_t recent, int32_t sink, int32_t *new_lens, int32_t *kept, void *stream) {
+  g_err.clear();
+  int rc;
+  if ((rc = check_kv8_cache(cache)) || (rc = check_kv8_batch(batch, cache, false))) return rc;
+  if (!cache->weights) return fail(NVFP4_EINVAL, "kv8_evict: the cache keeps no weights");
+  if (keep <= 0 || recent < 0 || sink < 0 || (int64_t)recent + sink > keep)
+    return fail(NVFP4_EINVAL, "kv8_evict: keep=%d must be positive and hold recent=%d and sink=%d", keep, recent,
+                sink);
+  if ((int64_t)new_cols * cache->page < keep || keep > (1 << 28))
+    return fail(NVFP4_ESHAPE, "kv8_evict: %d pages of %d tokens do not hold keep=%d", new_cols, cache->page, keep);
+  if (batch->seqs == 0) return NVFP4_OK;
+  if (!new_table || !new_lens || !kept) return fail(NVFP4_EINVAL, "kv8_evict: null pointer");
+  if (((uintptr_t)new_table | (uintptr_t)new_lens | (uintptr_t)kept) & 3u)
+    return fail(NVFP4_EINVAL, "kv8_evict: arrays must be 4-byte aligned");
+  hipStream_t s = (hipStream_t)stream;
+  ProfileScope ps("kv8_evict", batch->seqs, s);
+  return hip_status(launch_kv8_evict(kv8_pool(cache), kv8_batch_ref(batch), cache->dim, new_table, new_cols, keep,
+                                     recent, sink, new_lens, kept, s),
+                    "kv8_evict launch");
 }
 
 }  // extern "C"

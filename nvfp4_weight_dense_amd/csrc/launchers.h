@@ -268,4 +268,49 @@ hipError_t launch_read_probe(const void *src, size_t bytes, uint32_t never, floa
 hipError_t launch_encode_probe(const float *x, int64_t n, float d, float *q, uint8_t *e2m1, uint8_t *e4m3,
                                hipStream_t stream);
 
+// ---- 8-bit paged KV cache (head size dim 64, 128 or 256; layout: kv8_common.h) ----
+
+struct Kv8Pool {
+  uint8_t *k, *v;    // codes  [pages][heads][page * D]
+  uint8_t *ks, *vs;  // scales [pages][heads]
+  float *w;          // accumulated attention weight [pages][page], or null
+  int pages, heads, shift;
+};
+
+struct Kv8Batch {
+  const int *table;   // [seqs][cols] page of each block of tokens
+  const int *lens;    // [seqs] tokens, the call's own with them
+  const int *starts;  // [seqs + 1] first row of each sequence, or null: rows / seqs each
+  int seqs, cols, rows, max_rows;
+};
+
+struct Kv8Rows {  // bf16 [rows][heads][dim], the last dimension contiguous
+  const void *ptr;
+  int64_t row_stride, head_stride;  // elements
+};
+
+hipError_t launch_kv8_append(const Kv8Rows &k, const Kv8Rows &v, const Kv8Pool &c, const Kv8Batch &s,
+                             int dim, hipStream_t stream);
+hipError_t launch_kv8_evict(const Kv8Pool &c, const Kv8Batch &s, int dim, const int *new_table,
+                            int new_cols, int keep, int recent, int sink, int *new_lens, int *kept,
+                            hipStream_t stream);
+
+// Attention of rows over the cache: out bf16 [rows][q_heads][dim], lse fp32
+// [rows][q_heads].  `max_len` bounds the lengths (the grid's size only: a
+// longer sequence is a caller's error that leaves its further tokens unseen).
+struct Kv8Attn {
+  Kv8Rows q;
+  int q_heads, max_len;
+  int window;   // 0: none
+  float scale;
+  void *out;
+  float *lse;   // or null
+};
+hipError_t launch_kv8_attention(const Kv8Attn &a, const Kv8Pool &c, const Kv8Batch &s, int dim,
+                                hipStream_t stream);
+// Adds each visible token's attention weight, summed over rows and query
+// heads, to c.w, from the lse that the attention wrote.
+hipError_t launch_kv8_weights(const Kv8Attn &a, const Kv8Pool &c, const Kv8Batch &s, int dim,
+                              hipStream_t stream);
+
 }  // namespace nvfp4
