@@ -1145,7 +1145,11 @@ int64_t kv8_attention_workspace(int32_t q_heads, const kv8_cache *cache, const k
   if (q_heads <= 0 || q_heads % cache->heads != 0 || q_heads > 65535)
     return fail(NVFP4_ESHAPE, "kv8_attention: q_heads=%d is not a multiple of heads=%d up to 65535", q_heads,
                 cache->heads);
-  return 0;
+  Kv8Attn a{};
+  a.q_heads = q_heads;
+  a.max_len = std::min(batch->max_len, batch->cols * cache->page);
+  return (int64_t)(align256(kKv8MaxItems * 4) +
+                   align256(4 * kv8_part_bound(a, kv8_pool(cache), kv8_batch_ref(batch), cache->dim)));
 }
 
 int kv8_attention(const kv8_rows *q, int32_t q_heads, float scale, int32_t window, const kv8_cache *cache,
@@ -1169,12 +1173,23 @@ int kv8_attention(const kv8_rows *q, int32_t q_heads, float scale, int32_t windo
   hipStream_t s = (hipStream_t)stream;
   const Kv8Attn a{kv8_rows_ref(q), q_heads, std::min(batch->max_len, batch->cols * cache->page), window, scale,
                   out, lse};
+  const Kv8Pool pool = kv8_pool(cache);
+  const Kv8Batch seqs = kv8_batch_ref(batch);
+  const Kv8Plan pl = kv8_plan(a, pool, seqs, cache->dim);
+  unsigned *counters = (unsigned *)workspace;
+  float *part = (float *)((char *)workspace + align256(pl.counter_bytes));
+  if (!workspace) {
+    void *base = nullptr;
+    if ((rc = counters_get(pl.counter_bytes / 4, &counters)) ||
+        (pl.part_floats && (rc = arena_get(pl.part_floats * 4, &base))))
+      return rc;
+    part = (float *)base;
+  }
   ProfileScope ps("kv8_attention", batch->rows, s);
-  if ((rc = hip_status(launch_kv8_attention(a, kv8_pool(cache), kv8_batch_ref(batch), cache->dim, s),
+  if ((rc = hip_status(launch_kv8_attention(a, pool, seqs, cache->dim, pl, counters, part, s),
                        "kv8_attention launch")) || !accumulate)
     return rc;
-  return hip_status(launch_kv8_weights(a, kv8_pool(cache), kv8_batch_ref(batch), cache->dim, s),
-                    "kv8_attention weights launch");
+  return hip_status(launch_kv8_weights(a, pool, seqs, cache->dim, pl, part, s), "kv8_attention weights launch");
 }
 
 int kv8_evict(const kv8_cache *cache, const kv8_batch *batch, const int32_t *new_table, int32_t new_cols,

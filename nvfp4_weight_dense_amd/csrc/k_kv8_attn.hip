@@ -6,6 +6,8 @@
 // e^(s_ij - m), lse_i = m + log sum_j e^(s_ij - m); a row that sees nothing
 // gives zeros and -inf.  Sums and the softmax's statistics are fp32, powers
 // are of two (log2 e is folded into the scale).
+#include <algorithm>
+
 #include "kv8_common.h"
 #include "launchers.h"
 
@@ -99,40 +101,515 @@ __global__ __launch_bounds__(64) void k_kv8_attn_row(AttnParams p) {
   if (lane == 0 && p.a.lse) p.a.lse[at] = l > 0.f || l != l ? (m + log2f(l)) * kLn2 : -__builtin_inff();
 }
 
-// One wave: 64 tokens of one sequence, a lane each; every row and query head
-// in order, so a token's sum has one order.
+// ---- few rows: one pass over the cache, split along the tokens ---------------------
+//
+// What bounds it: the bytes of the codes.  A step is 32 tokens of one KV
+// head, 64 * D bytes of codes that a wave loads as contiguous 1 KB pieces
+// straight into matrix operands.  S^T = K Q^T (rows: tokens, columns: the
+// group's query heads of up to 16 * CT (row, head) pairs) leaves lane
+// (g, n) with tokens 4 g .. 4 g + 3 of each 16-token unit for column n, which
+// is the operand layout that O^T = V^T P^T wants, so P goes from the
+// accumulators to the next product without LDS or shuffles.  The running
+// maximum is raised only when a score passes it by 2^8 (the sums are fp32
+// and P is a floating type, so a factor up to 256 costs nothing), which
+// takes the cross-lane maximum out of almost every step.
+//
+// A workgroup's four waves take its steps in turn; their results are joined
+// in LDS, those of a sequence's workgroups by the last of them to arrive, in
+// the order of the tokens.
+
+constexpr int kDecodeWaves = 4;
+constexpr float kLowest = -3.4028234663852886e38f;  // below every finite score
+
+struct DecodeParams {
+  Kv8Attn a;
+  Kv8Pool c;
+  Kv8Batch s;
+  int group, blocks;  // query heads per KV head; column blocks
+  int spw, splits;    // steps per wave; workgroups per item at most
+  float *part;        // [item][split][cols][D + 2]
+  unsigned *counters;
+};
+
+__device__ __forceinline__ bf16x8 fp8x8_to_bf16(uint32_t lo, uint32_t hi, float scale) {
+  const bf16x2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, scale, false);
+  const bf16x2 b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, scale, true);
+  const bf16x2 c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, scale, false);
+  const bf16x2 d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, scale, true);
+  return bf16x8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
+}
+// 0x80 in each byte that is a NaN code
+__device__ __forceinline__ uint32_t nan_bytes(uint32_t w) {
+  return ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
+}
+
 template <int D>
-__global__ __launch_bounds__(64) void k_kv8_weights_token(AttnParams p) {
-  __shared__ float q[D];
-  const int b = (int)blockIdx.y, lane = (int)threadIdx.x, j = (int)blockIdx.x * 64 + lane;
-  const Kv8Span sp = kv8_span(p.s, p.c.shift, b);
-  if ((int)blockIdx.x * 64 >= sp.len) return;
-  const int page = 1 << p.c.shift, group = p.a.q_heads / p.c.heads;
-  const int id = j < min(sp.len, p.a.max_len) ? kv8_page(p.s, p.c, b, j >> p.c.shift) : -1;
-  float sum = 0.f;
-  for (int i = 0; i < sp.rows; ++i) {
+struct Step {       // the codes of 32 tokens, as one lane holds them
+  uint4 k[2][D / 64];  // [unit][t]: token lane % 16, channels 64 t + 16 g ..
+  uint4 v[2][D / 64];  // [unit][a]: tokens 4 g .., channels 64 a + 16 c + lane % 16
+};
+
+template <int D, int CT>
+__global__ __launch_bounds__(64 * kDecodeWaves) void k_kv8_decode(DecodeParams p) {
+  constexpr int kCols = 16 * CT, kPad = D + 4;
+  __shared__ __align__(16) float osum[kDecodeWaves][16][kPad];
+  __shared__ float stat[2][kDecodeWaves][kCols];
+  __shared__ bool last_flag;
+  const int split = (int)blockIdx.x, h = (int)blockIdx.y / p.blocks, cb = (int)blockIdx.y % p.blocks;
+  const int b = (int)blockIdx.z, tid = (int)threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int n = lane & 15, g = lane >> 4, shift = p.c.shift;
+  const Kv8Span sp = kv8_span(p.s, shift, b);
+  const int c0 = cb * kCols, cols = min(min(sp.rows, p.s.max_rows) * p.group - c0, kCols);
+  if (cols <= 0) return;
+
+  // the tokens that the block's first and last rows see: [lo, hi] of each
+  const int first = sp.len - sp.rows + c0 / p.group, final = sp.len - sp.rows + (c0 + cols - 1) / p.group;
+  const int end = min(sp.len, p.a.max_len);
+  auto low = [&](int pos) { return p.a.window ? max(pos - p.a.window + 1, 0) : 0; };
+  const int step0 = low(first) >> 5, step1 = (min(final + 1, end) + 31) >> 5;
+  const int per = p.spw * kDecodeWaves;
+  const int nsplit = max((step1 - step0 + per - 1) / per, 1);
+  if (split >= nsplit) return;
+  const int full_lo = low(final), full_hi = min(first, end - 1);  // every row sees these
+
+  const int base = step0 + split * per + wave;  // this wave's steps: base + 4 s
+  const int count = min(max((step1 - base + kDecodeWaves - 1) / kDecodeWaves, 0), p.spw);
+
+  // columns of this lane
+  bf16x8 q[CT][D / 32];
+  int lo[CT], hi[CT];
+#pragma unroll
+  for (int ct = 0; ct < CT; ++ct) {
+    const int c = ct * 16 + n, i = (c0 + c) / p.group;
+    const bool in = c < cols;
+    const __bf16 *qr = (const __bf16 *)p.a.q.ptr + (int64_t)(sp.r0 + (in ? i : 0)) * p.a.q.row_stride +
+                       (int64_t)(h * p.group + (in ? (c0 + c) % p.group : 0)) * p.a.q.head_stride;
+#pragma unroll
+    for (int t = 0; t < D / 64; ++t)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const uint4 w = *(const uint4 *)(qr + 64 * t + 16 * g + 8 * e);
+        q[ct][2 * t + e] = as_bf16x8(in ? w : uint4{0, 0, 0, 0});
+      }
     const int pos = sp.len - sp.rows + i;
-    if (pos < (int)blockIdx.x * 64) continue;
-    for (int hq = 0; hq < p.a.q_heads; ++hq) {
-      const __bf16 *qr = (const __bf16 *)p.a.q.ptr + (int64_t)(sp.r0 + i) * p.a.q.row_stride +
-                         (int64_t)hq * p.a.q.head_stride;
-      __syncthreads();
-      for (int d = lane; d < D; d += 64) q[d] = (float)qr[d];
-      __syncthreads();
-      if (id < 0 || j > pos || (p.a.window && j <= pos - p.a.window)) continue;
-      const size_t ph = (size_t)id * p.c.heads + hq / group;
-      const float s = dot_token<D>(q, p.c.k + (ph << p.c.shift) * D, j & (page - 1)) *
-                      (p.a.scale * kLog2e * kv8_scale(p.c.ks[ph]));
-      sum += __builtin_amdgcn_exp2f(s - p.a.lse[(size_t)(sp.r0 + i) * p.a.q_heads + hq] * kLog2e);
+    lo[ct] = low(pos);
+    hi[ct] = min(pos, end - 1);
+  }
+
+  // lane 2 s + u: unit u of step s
+  int at = -1;
+  float ksc = 1.f, vsc = 1.f;
+  {
+    const int t0 = (base + kDecodeWaves * (lane >> 1)) * 32 + (lane & 1) * 16;
+    if ((lane >> 1) < count && t0 < end) {
+      const int id = kv8_page(p.s, p.c, b, t0 >> shift);
+      if (id >= 0) {
+        const size_t ph = (size_t)id * p.c.heads + h;
+        at = (int)((ph << (shift - 4)) + ((t0 >> 4) & ((1 << (shift - 4)) - 1)));
+        ksc = p.a.scale * kLog2e * kv8_scale(p.c.ks[ph]);
+        vsc = kv8_scale(p.c.vs[ph]);
+      }
     }
   }
-  if (id >= 0) p.c.w[((size_t)id << p.c.shift) + (j & (page - 1))] += sum;
+  auto load = [&](Step<D> &x, int s) {
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const uint32_t unit = (uint32_t)__builtin_amdgcn_readlane(at, 2 * s + u);
+      // (a unit that no page holds reads the pool's first; its scores are masked)
+      const size_t off = (size_t)(unit == 0xFFFFFFFFu ? 0u : unit) * (16 * D);
+      const uint4 *k = (const uint4 *)(p.c.k + off) + lane, *v = (const uint4 *)(p.c.v + off) + lane;
+#pragma unroll
+      for (int t = 0; t < D / 64; ++t) x.k[u][t] = k[64 * t];
+#pragma unroll
+      for (int t = 0; t < D / 64; ++t) x.v[u][t] = v[64 * t];
+    }
+  };
+
+  f32x4 o[CT][D / 16] = {};
+  float m[CT], l[CT] = {};
+#pragma unroll
+  for (int ct = 0; ct < CT; ++ct) m[ct] = kLowest;
+
+  auto compute = [&](const Step<D> &x, int s) {
+    const int t0 = (base + kDecodeWaves * s) * 32;
+    f32x4 sc[CT][2] = {};
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+      for (int t = 0; t < D / 64; ++t) {
+        const bf16x8 k0 = fp8x8_to_bf16(x.k[u][t].x, x.k[u][t].y, 1.0f);
+        const bf16x8 k1 = fp8x8_to_bf16(x.k[u][t].z, x.k[u][t].w, 1.0f);
+#pragma unroll
+        for (int ct = 0; ct < CT; ++ct) {
+          sc[ct][u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k0, q[ct][2 * t], sc[ct][u], 0, 0, 0);
+          sc[ct][u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k1, q[ct][2 * t + 1], sc[ct][u], 0, 0, 0);
+        }
+      }
+    int valid[2];
+    float vscale[2];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const float f = __builtin_bit_cast(
+          float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, ksc), 2 * s + u));
+      vscale[u] = __builtin_bit_cast(
+          float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, vsc), 2 * s + u));
+      valid[u] = __builtin_amdgcn_readlane(at, 2 * s + u) != -1;
+#pragma unroll
+      for (int ct = 0; ct < CT; ++ct) sc[ct][u] *= f;
+    }
+    const bool whole = t0 >= full_lo && t0 + 31 <= full_hi && valid[0] && valid[1];
+    uint32_t seen[CT];
+#pragma unroll
+    for (int ct = 0; ct < CT; ++ct) seen[ct] = 0xFFu;
+    if (!whole) {
+#pragma unroll
+      for (int ct = 0; ct < CT; ++ct) {
+        seen[ct] = 0;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const int j = t0 + 16 * (e >> 2) + 4 * g + (e & 3);
+          const bool yes = valid[e >> 2] && j >= lo[ct] && j <= hi[ct];
+          seen[ct] |= (yes ? 1u : 0u) << e;
+          sc[ct][e >> 2][e & 3] = yes ? sc[ct][e >> 2][e & 3] : -__builtin_inff();
+        }
+      }
+    }
+    bf16x8 pr[CT];
+#pragma unroll
+    for (int ct = 0; ct < CT; ++ct) {
+      float top = fmaxf(fmaxf(sc[ct][0][0], sc[ct][0][1]), fmaxf(sc[ct][0][2], sc[ct][0][3]));
+      top = fmaxf(top, fmaxf(fmaxf(sc[ct][1][0], sc[ct][1][1]), fmaxf(sc[ct][1][2], sc[ct][1][3])));
+      if (__any(top > m[ct] + 8.0f)) {
+        top = fmaxf(top, __shfl_xor(top, 16));
+        top = fmaxf(top, __shfl_xor(top, 32));
+        const float mn = fmaxf(m[ct], top), down = __builtin_amdgcn_exp2f(m[ct] - mn);
+        m[ct] = mn;
+        l[ct] *= down;
+#pragma unroll
+        for (int d = 0; d < D / 16; ++d) o[ct][d] *= down;
+      }
+      float e[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) e[i] = __builtin_amdgcn_exp2f(sc[ct][i >> 2][i & 3] - m[ct]);
+      l[ct] += ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
+      // (bf16, the type of the product's other operand; l sums the fp32 values)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) pr[ct][i] = (__bf16)e[i];
+    }
+    bool odd = false;
+    if (!whole) {  // a NaN code of a token that some row does not see must not reach that row
+      uint32_t any = 0;
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int a = 0; a < D / 64; ++a)
+          any |= nan_bytes(x.v[u][a].x) | nan_bytes(x.v[u][a].y) | nan_bytes(x.v[u][a].z) | nan_bytes(x.v[u][a].w);
+      odd = __any(any != 0);
+    }
+#pragma unroll
+    for (int a = 0; a < D / 64; ++a) {
+      const uint32_t v0[4] = {x.v[0][a].x, x.v[0][a].y, x.v[0][a].z, x.v[0][a].w};
+      const uint32_t v1[4] = {x.v[1][a].x, x.v[1][a].y, x.v[1][a].z, x.v[1][a].w};
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        uint32_t w0 = v0[c], w1 = v1[c];
+        if (odd) {
+          // ones where a code is NaN, against ones where a row sees the token
+          const uint32_t b0 = nan_bytes(w0) >> 7, b1 = nan_bytes(w1) >> 7;
+          w0 &= ~(b0 * 0xFFu);
+          w1 &= ~(b1 * 0xFFu);
+          bf16x8 here;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            here[i] = (__bf16)(float)((b0 >> (8 * i)) & 1u);
+            here[4 + i] = (__bf16)(float)((b1 >> (8 * i)) & 1u);
+          }
+#pragma unroll
+          for (int ct = 0; ct < CT; ++ct) {
+            bf16x8 sees;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) sees[i] = (__bf16)(float)((seen[ct] >> i) & 1u);
+            f32x4 hit = {};
+            hit = __builtin_amdgcn_mfma_f32_16x16x32_bf16(here, sees, hit, 0, 0, 0);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (hit[i] > 0.f) o[ct][4 * a + c][i] = __builtin_nanf("");
+          }
+        }
+        const bf16x2 x0 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w0, vscale[0], false);
+        const bf16x2 x1 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w0, vscale[0], true);
+        const bf16x2 y0 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w1, vscale[1], false);
+        const bf16x2 y1 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w1, vscale[1], true);
+        const bf16x8 vt = {x0[0], x0[1], x1[0], x1[1], y0[0], y0[1], y1[0], y1[1]};
+#pragma unroll
+        for (int ct = 0; ct < CT; ++ct)
+          o[ct][4 * a + c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vt, pr[ct], o[ct][4 * a + c], 0, 0, 0);
+      }
+    }
+  };
+
+  // two steps' codes in turn: one loads while the other is used
+  Step<D> xa, xb;
+  if (count > 0) load(xa, 0);
+  for (int s = 0; s < count; s += 2) {
+    if (s + 1 < count) load(xb, s + 1);
+    compute(xa, s);
+    if (s + 1 < count) {
+      if (s + 2 < count) load(xa, s + 2);
+      compute(xb, s + 1);
+    }
+  }
+
+  // ---- join the waves
+#pragma unroll
+  for (int ct = 0; ct < CT; ++ct) {
+    l[ct] += __shfl_xor(l[ct], 16);
+    l[ct] += __shfl_xor(l[ct], 32);
+    if (g == 0) {
+      stat[0][wave][ct * 16 + n] = m[ct];
+      stat[1][wave][ct * 16 + n] = l[ct];
+    }
+  }
+  __syncthreads();
+  const int item = ((int)blockIdx.z * p.c.heads + h) * p.blocks + cb;
+  constexpr int width = D + 2;
+  const __amdgpu_buffer_rsrc_t pr =  // (not touched when there is one split)
+      rsrc_uniform(p.part + (size_t)item * p.splits * kCols * width, (size_t)nsplit * kCols * width * 4);
+  const int64_t row0 = (int64_t)sp.r0 * p.a.q_heads + (int64_t)h * p.group;
+  auto put = [&](int c, int d, f32x4 x, float ll) {  // four channels of column c, done
+    const float inv = ll > 0.f || ll != ll ? 1.0f / ll : 0.f;
+    const int64_t r = row0 + (int64_t)((c0 + c) / p.group) * p.a.q_heads + (c0 + c) % p.group;
+    bf16x2 y[2] = {{(__bf16)(x[0] * inv), (__bf16)(x[1] * inv)}, {(__bf16)(x[2] * inv), (__bf16)(x[3] * inv)}};
+    *(uint2 *)((__bf16 *)p.a.out + r * D + d) =
+        uint2{__builtin_bit_cast(uint32_t, y[0]), __builtin_bit_cast(uint32_t, y[1])};
+  };
+  auto put_lse = [&](int c, float mm, float ll) {
+    const int64_t r = row0 + (int64_t)((c0 + c) / p.group) * p.a.q_heads + (c0 + c) % p.group;
+    p.a.lse[r] = ll > 0.f || ll != ll ? (mm + log2f(ll)) * kLn2 : -__builtin_inff();
+  };
+#pragma unroll
+  for (int ct = 0; ct < CT; ++ct) {
+    if (ct * 16 >= cols) break;
+    float top = kLowest;
+#pragma unroll
+    for (int w = 0; w < kDecodeWaves; ++w) top = fmaxf(top, stat[0][w][ct * 16 + n]);
+    const float f = __builtin_amdgcn_exp2f(m[ct] - top);
+    if (ct) __syncthreads();
+#pragma unroll
+    for (int d = 0; d < D / 16; ++d) *(f32x4 *)&osum[wave][n][16 * d + 4 * g] = o[ct][d] * f;
+    __syncthreads();
+    for (int i = tid; i < 16 * (D / 4); i += 64 * kDecodeWaves) {
+      const int col = i / (D / 4), d = i % (D / 4) * 4, c = ct * 16 + col;
+      if (c >= cols) break;
+      float mm = kLowest, ll = 0.f;
+#pragma unroll
+      for (int w = 0; w < kDecodeWaves; ++w) mm = fmaxf(mm, stat[0][w][c]);
+#pragma unroll
+      for (int w = 0; w < kDecodeWaves; ++w) ll += stat[1][w][c] * __builtin_amdgcn_exp2f(stat[0][w][c] - mm);
+      f32x4 x = *(const f32x4 *)&osum[0][col][d];
+#pragma unroll
+      for (int w = 1; w < kDecodeWaves; ++w) x += *(const f32x4 *)&osum[w][col][d];
+      if (nsplit == 1) {
+        put(c, d, x, ll);
+        if (d == 0 && p.a.lse) put_lse(c, mm, ll);
+      } else {
+        const uint32_t off = (uint32_t)((split * kCols + c) * width) * 4u;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) st_coherent(pr, off + (uint32_t)(d + k) * 4u, x[k]);
+        if (d == 0) {
+          st_coherent(pr, off + D * 4u, mm);
+          st_coherent(pr, off + D * 4u + 4u, ll);
+        }
+      }
+    }
+  }
+  if (nsplit == 1) return;
+
+  // ---- join the splits: the last workgroup of the item to arrive
+  wait_all_memory();
+  __syncthreads();
+  if (tid == 0)
+    last_flag = __hip_atomic_fetch_add(&p.counters[item], 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) ==
+                (unsigned)(nsplit - 1);
+  __syncthreads();
+  if (!last_flag) return;
+  for (int i = tid; i < cols * (D / 4); i += 64 * kDecodeWaves) {
+    const int c = i / (D / 4), d = i % (D / 4) * 4;
+    float mm = kLowest, ll = 0.f;
+    f32x4 x = {};
+    for (int t = 0; t < nsplit; ++t) {
+      const uint32_t off = (uint32_t)((t * kCols + c) * width) * 4u;
+      const float mt = ld_coherent(pr, off + D * 4u), lt = ld_coherent(pr, off + D * 4u + 4u);
+      f32x4 y;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) y[k] = ld_coherent(pr, off + (uint32_t)(d + k) * 4u);
+      const float mn = fmaxf(mm, mt), fa = __builtin_amdgcn_exp2f(mm - mn), fb = __builtin_amdgcn_exp2f(mt - mn);
+      x = x * fa + y * fb;
+      ll = ll * fa + lt * fb;
+      mm = mn;
+    }
+    put(c, d, x, ll);
+    if (d == 0 && p.a.lse) put_lse(c, mm, ll);
+  }
+  if (tid == 0) __hip_atomic_store(&p.counters[item], 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
+// ---- accumulated attention weight -----------------------------------------------------
+//
+// A second pass over K with the finished log-sums: a token's sum over rows
+// and heads needs them, and K is the smaller half of the cache.  A wave
+// keeps 64 tokens of one KV head as matrix operands and takes the columns
+// (row, head) that can see them 16 at a time; a lane adds up its tokens over
+// its column of every tile, the 16 columns are joined at the end, and
+// k_kv8_weights_join adds the KV heads in order.  No atomics: a token's sum
+// has one order.
+constexpr int kWeightTokens = 256;  // of a workgroup
+
+struct WeightParams {
+  Kv8Attn a;
+  Kv8Pool c;
+  Kv8Batch s;
+  int group, len_pad;
+  float *part;  // [seq][head][len_pad]
+};
+
+template <int D>
+__global__ __launch_bounds__(256) void k_kv8_weights(WeightParams p) {
+  constexpr int U = 4;  // units of a wave
+  const int h = (int)blockIdx.y, b = (int)blockIdx.z, tid = (int)threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int n = lane & 15, g = lane >> 4, shift = p.c.shift;
+  const Kv8Span sp = kv8_span(p.s, shift, b);
+  const int end = min(sp.len, p.a.max_len);
+  const int t0 = (int)blockIdx.x * kWeightTokens + wave * 16 * U;
+  if (t0 >= end) return;
+  const int rows = min(sp.rows, p.s.max_rows), cols = rows * p.group, pos0 = sp.len - sp.rows;
+
+  bf16x8 k[U][D / 32];
+  float f[U];
+  bool valid[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int t = t0 + 16 * u;
+    const int id = t < end ? kv8_page(p.s, p.c, b, t >> shift) : -1;
+    const size_t ph = (size_t)max(id, 0) * p.c.heads + h;
+    const int in = (t >> 4) & ((1 << (shift - 4)) - 1);
+    valid[u] = id >= 0;
+    f[u] = id >= 0 ? p.a.scale * kLog2e * kv8_scale(p.c.ks[ph]) : 0.f;
+    const uint4 *src = (const uint4 *)(p.c.k + ((ph << (shift - 4)) + in) * (16 * D)) + lane;
+#pragma unroll
+    for (int t4 = 0; t4 < D / 64; ++t4) {
+      const uint4 w = src[64 * t4];
+      k[u][2 * t4] = fp8x8_to_bf16(w.x, w.y, 1.0f);
+      k[u][2 * t4 + 1] = fp8x8_to_bf16(w.z, w.w, 1.0f);
+    }
+  }
+
+  // rows that see a token of the wave
+  const int last = min(t0 + 16 * U, end) - 1;
+  const int row0 = max(t0 - pos0, 0);
+  const int row1 = p.a.window ? min(rows, last + p.a.window - pos0) : rows;
+  float sum[U][4] = {};
+  for (int c0 = row0 * p.group; c0 < row1 * p.group; c0 += 16) {
+    const int c = c0 + n, i = c / p.group;
+    const bool in = c < cols;
+    const int64_t r = (int64_t)(sp.r0 + (in ? i : 0)), u0 = h * p.group + (in ? c % p.group : 0);
+    const __bf16 *qr = (const __bf16 *)p.a.q.ptr + r * p.a.q.row_stride + u0 * p.a.q.head_stride;
+    bf16x8 q[D / 32];
+#pragma unroll
+    for (int t = 0; t < D / 64; ++t)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) q[2 * t + e] = as_bf16x8(*(const uint4 *)(qr + 64 * t + 16 * g + 8 * e));
+    const float z = p.a.lse[r * p.a.q_heads + u0] * kLog2e;
+    const int pos = pos0 + i;
+    const int hi = in ? min(pos, end - 1) : -1, lo = p.a.window ? max(pos - p.a.window + 1, 0) : 0;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      f32x4 s = {};
+#pragma unroll
+      for (int t = 0; t < D / 32; ++t) s = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k[u][t], q[t], s, 0, 0, 0);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int j = t0 + 16 * u + 4 * g + e;
+        const float x = __builtin_amdgcn_exp2f(fmaf(s[e], f[u], -z));
+        sum[u][e] += valid[u] && j >= lo && j <= hi ? x : 0.f;
+      }
+    }
+  }
+  float *out = p.part + ((size_t)b * p.c.heads + h) * p.len_pad;
+#pragma unroll
+  for (int u = 0; u < U; ++u)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      float x = sum[u][e];
+#pragma unroll
+      for (int o = 8; o > 0; o >>= 1) x += __shfl_xor(x, o);
+      if (n == 0) out[t0 + 16 * u + 4 * g + e] = x;
+    }
+}
+
+__global__ __launch_bounds__(256) void k_kv8_weights_join(WeightParams p) {
+  const int b = (int)blockIdx.y, j = (int)(blockIdx.x * 256 + threadIdx.x);
+  const Kv8Span sp = kv8_span(p.s, p.c.shift, b);
+  if (j >= min(sp.len, p.a.max_len)) return;
+  const int id = kv8_page(p.s, p.c, b, j >> p.c.shift);
+  if (id < 0) return;
+  const float *part = p.part + (size_t)b * p.c.heads * p.len_pad + j;
+  float sum = 0.f;
+  for (int h = 0; h < p.c.heads; ++h) sum += part[(size_t)h * p.len_pad];
+  p.c.w[((size_t)id << p.c.shift) + (j & ((1 << p.c.shift) - 1))] += sum;
 }
 
 }  // namespace
 
+// Few rows: as many (row, head) columns of a KV head as one workgroup keeps
+// (64, with head size 256 32).
+constexpr int kv8_few_cols(int dim) { return dim == 256 ? 32 : 64; }
+constexpr int kDecodeGroups = 1024;  // workgroups wanted
+
+size_t kv8_part_bound(const Kv8Attn &a, const Kv8Pool &c, const Kv8Batch &s, int dim) {
+  // fewer tokens or a window: shorter pieces, but (kv8_plan) never twice kDecodeGroups and one per item
+  const Kv8Plan pl = kv8_plan(a, c, s, dim);
+  const size_t cols = pl.few ? 16 * (size_t)pl.ct : (size_t)kv8_few_cols(dim);
+  return std::max(pl.part_floats, (2 * kDecodeGroups + (size_t)s.seqs * c.heads) * cols * (size_t)(dim + 2));
+}
+
+Kv8Plan kv8_plan(const Kv8Attn &a, const Kv8Pool &c, const Kv8Batch &s, int dim) {
+  Kv8Plan pl = {};
+  pl.group = a.q_heads / c.heads;
+  const int cols = (int)std::min<int64_t>((int64_t)s.max_rows * pl.group, 1 << 30);
+  pl.few = cols <= kv8_few_cols(dim);
+  pl.counter_bytes = kKv8MaxItems * 4;
+  if (pl.few) {
+    pl.ct = cols <= 16 ? 1 : cols <= 32 ? 2 : 4;
+    const int items = s.seqs * c.heads;
+    const int64_t seen = a.window ? std::min<int64_t>(a.max_len, (int64_t)a.window + s.max_rows + 31) : a.max_len;
+    const int steps = (int)((seen + 31) / 32) + (a.window ? 1 : 0);
+    // the longest pieces that still give every CU a few workgroups
+    pl.spw = 32;
+    while (pl.spw > 1 && (int64_t)items * ((steps + 4 * pl.spw - 1) / (4 * pl.spw)) < kDecodeGroups) pl.spw /= 2;
+    pl.splits = std::max((steps + 4 * pl.spw - 1) / (4 * pl.spw), 1);
+    if (pl.splits > 1 && items <= kKv8MaxItems)
+      pl.part_floats = (size_t)items * pl.splits * 16 * pl.ct * (dim + 2);
+  }
+  pl.len_pad = (a.max_len + kWeightTokens - 1) / kWeightTokens * kWeightTokens;
+  if (c.w) pl.part_floats = std::max(pl.part_floats, (size_t)s.seqs * c.heads * pl.len_pad);
+  return pl;
+}
+
 hipError_t launch_kv8_attention(const Kv8Attn &a, const Kv8Pool &c, const Kv8Batch &s, int dim,
-                                hipStream_t stream) {
+                                const Kv8Plan &pl, unsigned *counters, float *part, hipStream_t stream) {
+  if (pl.few) {
+    const DecodeParams p{a, c, s, pl.group, 1, pl.spw, pl.splits, part, counters};
+    const dim3 grid((unsigned)pl.splits, (unsigned)c.heads, (unsigned)s.seqs), block(64 * kDecodeWaves);
+    auto k = dim == 64 ? (pl.ct == 1 ? k_kv8_decode<64, 1> : pl.ct == 2 ? k_kv8_decode<64, 2> : k_kv8_decode<64, 4>)
+             : dim == 128
+                 ? (pl.ct == 1 ? k_kv8_decode<128, 1> : pl.ct == 2 ? k_kv8_decode<128, 2> : k_kv8_decode<128, 4>)
+                 : (pl.ct == 1 ? k_kv8_decode<256, 1> : k_kv8_decode<256, 2>);
+    k<<<grid, block, 0, stream>>>(p);
+    return hipGetLastError();
+  }
   const AttnParams p{a, c, s};
   const dim3 grid((unsigned)s.max_rows, (unsigned)a.q_heads, (unsigned)s.seqs);
   auto k = dim == 64 ? k_kv8_attn_row<64> : dim == 128 ? k_kv8_attn_row<128> : k_kv8_attn_row<256>;
@@ -141,11 +618,15 @@ hipError_t launch_kv8_attention(const Kv8Attn &a, const Kv8Pool &c, const Kv8Bat
 }
 
 hipError_t launch_kv8_weights(const Kv8Attn &a, const Kv8Pool &c, const Kv8Batch &s, int dim,
-                              hipStream_t stream) {
-  const AttnParams p{a, c, s};
-  const dim3 grid((unsigned)((a.max_len + 63) / 64), (unsigned)s.seqs);
-  auto k = dim == 64 ? k_kv8_weights_token<64> : dim == 128 ? k_kv8_weights_token<128> : k_kv8_weights_token<256>;
-  k<<<grid, dim3(64), 0, stream>>>(p);
+                              const Kv8Plan &pl, float *part, hipStream_t stream) {
+  if (a.max_len <= 0) return hipSuccess;
+  const WeightParams p{a, c, s, pl.group, pl.len_pad, part};
+  const unsigned blocks = (unsigned)(pl.len_pad / kWeightTokens);
+  const dim3 grid(blocks, (unsigned)c.heads, (unsigned)s.seqs);
+  auto k = dim == 64 ? k_kv8_weights<64> : dim == 128 ? k_kv8_weights<128> : k_kv8_weights<256>;
+  k<<<grid, dim3(256), 0, stream>>>(p);
+  if (hipError_t e = hipGetLastError()) return e;
+  k_kv8_weights_join<<<dim3(blocks, (unsigned)s.seqs), dim3(256), 0, stream>>>(p);
   return hipGetLastError();
 }
 

@@ -306,11 +306,24 @@ struct Kv8Attn {
   void *out;
   float *lse;   // or null
 };
+struct Kv8Plan {
+  int group;    // query heads per KV head
+  bool few;     // the kernel that splits the tokens (few rows)
+  int ct, spw, splits;
+  int len_pad;  // tokens of a part of the weights pass
+  size_t counter_bytes, part_floats;
+};
+constexpr int kKv8MaxItems = 65536;  // arrival counters
+Kv8Plan kv8_plan(const Kv8Attn &a, const Kv8Pool &c, const Kv8Batch &s, int dim);
+// part_floats of any call with these sizes or smaller ones and any window
+size_t kv8_part_bound(const Kv8Attn &a, const Kv8Pool &c, const Kv8Batch &s, int dim);
+// `counters` (counter_bytes, zero on entry, left zero) and `part`
+// (part_floats) as planned.
 hipError_t launch_kv8_attention(const Kv8Attn &a, const Kv8Pool &c, const Kv8Batch &s, int dim,
-                                hipStream_t stream);
+                                const Kv8Plan &pl, unsigned *counters, float *part, hipStream_t stream);
 // Adds each visible token's attention weight, summed over rows and query
 // heads, to c.w, from the lse that the attention wrote.
 hipError_t launch_kv8_weights(const Kv8Attn &a, const Kv8Pool &c, const Kv8Batch &s, int dim,
-                              hipStream_t stream);
+                              const Kv8Plan &pl, float *part, hipStream_t stream);
 
 }  // namespace nvfp4
