@@ -1145,6 +1145,8 @@ int64_t kv8_attention_workspace(int32_t q_heads, const kv8_cache *cache, const k
   if (q_heads <= 0 || q_heads % cache->heads != 0 || q_heads > 65535)
     return fail(NVFP4_ESHAPE, "kv8_attention: q_heads=%d is not a multiple of heads=%d up to 65535", q_heads,
                 cache->heads);
+  if ((int64_t)batch->rows * q_heads > (1 << 30))
+    return fail(NVFP4_ESHAPE, "kv8_attention: %d rows of %d heads exceed 2^30", batch->rows, q_heads);
   Kv8Attn a{};
   a.q_heads = q_heads;
   a.max_len = std::min(batch->max_len, batch->cols * cache->page);

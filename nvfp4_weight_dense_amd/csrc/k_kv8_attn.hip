@@ -17,90 +17,6 @@ namespace {
 
 constexpr float kLog2e = 1.44269504088896341f, kLn2 = 0.693147180559945309f;
 
-struct AttnParams {
-  Kv8Attn a;
-  Kv8Pool c;
-  Kv8Batch s;
-};
-
-// scale * log2(e) * q . k of one token, from fp32 q in LDS
-template <int D>
-__device__ __forceinline__ float dot_token(const float *q, const uint8_t *codes, int slot) {
-  float acc = 0.f;
-  for (int d = 0; d < D; d += 16) {
-    const uint4 v = *(const uint4 *)(codes + kv8_k_at(slot, d, D));
-    const uint32_t u[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int w = 0; w < 4; ++w) {
-      float f[4];
-      kv8_decode4(u[w], f);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) acc = fmaf(q[d + 4 * w + i], f[i], acc);
-    }
-  }
-  return acc;
-}
-
-// One wave: one row and query head; 64 tokens at a time, a lane each for the
-// products with K, a lane per channel for those with V.
-template <int D>
-__global__ __launch_bounds__(64) void k_kv8_attn_row(AttnParams p) {
-  __shared__ float q[D], prob[64];
-  const int i = (int)blockIdx.x, hq = (int)blockIdx.y, b = (int)blockIdx.z, lane = (int)threadIdx.x;
-  const Kv8Span sp = kv8_span(p.s, p.c.shift, b);
-  if (i >= sp.rows) return;
-  const int h = hq / (p.a.q_heads / p.c.heads), page = 1 << p.c.shift;
-  const __bf16 *qr = (const __bf16 *)p.a.q.ptr + (int64_t)(sp.r0 + i) * p.a.q.row_stride +
-                     (int64_t)hq * p.a.q.head_stride;
-  for (int d = lane; d < D; d += 64) q[d] = (float)qr[d];
-  __syncthreads();
-  const int pos = sp.len - sp.rows + i;
-  const int j0 = p.a.window ? max(pos - p.a.window + 1, 0) : 0;
-  float m = -__builtin_inff(), l = 0.f, o[D / 64] = {};
-  const int last = min(pos, p.a.max_len - 1);
-  for (int j = j0 & ~63; j <= last; j += 64) {
-    const int mine = j + lane;
-    float s = -__builtin_inff();
-    if (mine >= j0 && mine <= last) {
-      const int id = kv8_page(p.s, p.c, b, mine >> p.c.shift);
-      if (id >= 0) {
-        const size_t ph = (size_t)id * p.c.heads + h;
-        s = dot_token<D>(q, p.c.k + (ph << p.c.shift) * D, mine & (page - 1)) *
-            (p.a.scale * kLog2e * kv8_scale(p.c.ks[ph]));
-      }
-    }
-    float top = s;
-#pragma unroll
-    for (int x = 32; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor(top, x));
-    const float mn = fmaxf(m, top), base = mn == -__builtin_inff() ? 0.f : mn;
-    const float keep = __builtin_amdgcn_exp2f(m - base), e = __builtin_amdgcn_exp2f(s - base);
-    m = mn;
-    l = l * keep + e;
-    prob[lane] = e;
-    __syncthreads();
-#pragma unroll
-    for (int a = 0; a < D / 64; ++a) o[a] *= keep;
-    for (int t = 0; t < 64 && j + t <= last; ++t) {
-      const int id = kv8_page(p.s, p.c, b, (j + t) >> p.c.shift);
-      if (id < 0 || j + t < j0) continue;
-      const size_t ph = (size_t)id * p.c.heads + h;
-      const uint8_t *codes = p.c.v + (ph << p.c.shift) * D;
-      const float w = prob[t] * kv8_scale(p.c.vs[ph]);
-#pragma unroll
-      for (int a = 0; a < D / 64; ++a)
-        o[a] = fmaf(w, e4m3_to_f32(codes[kv8_v_at((j + t) & (page - 1), 64 * a + lane, D)]), o[a]);
-    }
-    __syncthreads();
-  }
-#pragma unroll
-  for (int x = 32; x > 0; x >>= 1) l += __shfl_xor(l, x);
-  const size_t at = (size_t)(sp.r0 + i) * p.a.q_heads + hq;
-  const float inv = l > 0.f || l != l ? 1.0f / l : 0.f;
-#pragma unroll
-  for (int a = 0; a < D / 64; ++a) ((__bf16 *)p.a.out)[at * D + 64 * a + lane] = (__bf16)(o[a] * inv);
-  if (lane == 0 && p.a.lse) p.a.lse[at] = l > 0.f || l != l ? (m + log2f(l)) * kLn2 : -__builtin_inff();
-}
-
 // ---- few rows: one pass over the cache, split along the tokens ---------------------
 //
 // What bounds it: the bytes of the codes.  A step is 32 tokens of one KV
@@ -455,6 +371,337 @@ __global__ __launch_bounds__(64 * kDecodeWaves) void k_kv8_decode(DecodeParams p
   if (tid == 0) __hip_atomic_store(&p.counters[item], 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
+// ---- many rows ------------------------------------------------------------------------
+//
+// What bounds it: the matrix instructions (4 D operations for each score
+// against about 5 vector instructions of the softmax).  A workgroup takes
+// 32 * CT * NW columns ((row, head) pairs of one KV head, so the heads of a
+// group share its codes) and walks the tokens in tiles of 64: the codes are
+// read one tile ahead into registers, widened to bf16 once by the workgroup
+// (K and V times their scales, exact) and written to LDS as the operands of
+// the 32x32x16 instructions, two tiles in turn, one barrier a tile.  As in
+// the kernel for few rows S^T = K Q^T leaves each lane the probabilities of
+// its column as the next product's operand: accumulator row
+// (r % 4) + 8 (r / 4) + 4 half of a 32-token step is token 16 ks + 8 (e / 4)
+// + 4 half + e % 4 for r = 8 ks + e, so V's operand takes, of unit ks, the
+// token groups `half` and 2 + half.  The maximum is looked at once per tile
+// and raised when a score passes it by 2^8.
+struct PrefillParams {
+  Kv8Attn a;
+  Kv8Pool c;
+  Kv8Batch s;
+  int group, blocks, splits;
+  float *part;  // [item][split][column][D + 2]
+};
+
+template <int D, int CT, int NW>
+__global__ __launch_bounds__(64 * NW, NW / 4) void k_kv8_prefill(PrefillParams p) {
+  constexpr int kCols = 32 * CT * NW;
+  constexpr int KT = D / 16, VT = D / 32;   // operands of a step: K's and (of each 16 tokens) V's
+  constexpr bool kBoth = NW == 4;           // a wave widens K and V of its unit, or one of them
+  __shared__ uint4 kbuf[2][2][KT][64];      // [tile][step][channels 16 t ..][lane]
+  __shared__ uint4 vbuf[2][2][2][VT][64];   // [tile][step][unit][channels 32 t ..][lane]
+  __shared__ __align__(16) int bad[2][4], odd[2][4];      // a unit without a page; with a NaN code of V
+  // heads side by side, so that those of one XCD's workgroups share its L2; the longest first
+  const int h = (int)blockIdx.x % p.c.heads, cb = p.blocks - 1 - (int)blockIdx.x / p.c.heads;
+  const int b = (int)blockIdx.y / p.splits, split = (int)blockIdx.y % p.splits;
+  const int tid = (int)threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int n = lane & 31, half = lane >> 5, shift = p.c.shift;
+  const Kv8Span sp = kv8_span(p.s, shift, b);
+  const int all = min(sp.rows, p.s.max_rows) * p.group, c0 = cb * kCols;
+  if (c0 >= all) return;
+  const int end = min(sp.len, p.a.max_len), pos0 = sp.len - sp.rows;
+  auto low = [&](int pos) { return p.a.window ? max(pos - p.a.window + 1, 0) : 0; };
+
+  // the workgroup's tiles
+  const int wg_first = pos0 + c0 / p.group, wg_final = pos0 + (min(c0 + kCols, all) - 1) / p.group;
+  int tile0 = low(wg_first) >> 6, tile1 = (min(wg_final + 1, end) + 63) >> 6;
+  if (p.splits > 1) {
+    const int per = (max(tile1 - tile0, 0) + p.splits - 1) / p.splits;
+    tile0 += split * per;
+    tile1 = min(tile1, tile0 + per);
+  }
+  // the wave's columns and the tokens that its first and last row see
+  const int w0 = c0 + wave * 32 * CT, cols = min(all - w0, 32 * CT);
+  const int first = pos0 + w0 / p.group, final = pos0 + (w0 + max(cols, 1) - 1) / p.group;
+  const int full_lo = low(final), full_hi = min(first, end - 1);
+  const int any_lo = low(first), any_hi = cols > 0 ? min(final, end - 1) : -1;
+
+  const float cs = fmaxf(fabsf(p.a.scale) * kLog2e, 1.1754944e-38f);  // its sign goes to q
+  const uint32_t flip = p.a.scale < 0.f ? 0x80008000u : 0u;
+  bf16x8 q[CT][KT];
+  int lo[CT], hi[CT];
+#pragma unroll
+  for (int ct = 0; ct < CT; ++ct) {
+    const int c = w0 + ct * 32 + n, i = c / p.group;
+    const bool in = c < all;
+    const __bf16 *qr = (const __bf16 *)p.a.q.ptr + (int64_t)(sp.r0 + (in ? i : 0)) * p.a.q.row_stride +
+                       (int64_t)(h * p.group + (in ? c % p.group : 0)) * p.a.q.head_stride;
+#pragma unroll
+    for (int t = 0; t < KT; ++t) {
+      const uint4 w = *(const uint4 *)(qr + 16 * t + 8 * half);
+      q[ct][t] = as_bf16x8(in ? uint4{w.x ^ flip, w.y ^ flip, w.z ^ flip, w.w ^ flip} : uint4{0, 0, 0, 0});
+    }
+    lo[ct] = low(pos0 + i);
+    hi[ct] = min(pos0 + i, end - 1);
+  }
+
+  // lane i: the wave's unit of tile `meta + i`
+  int meta = tile0 - 64, at = -1;
+  float ksc = 1.f, vsc = 1.f;
+  const int unit = wave & 3;
+  const bool does_k = kBoth || wave < 4, does_v = kBoth || wave >= 4;
+  uint4 kr[D / 64], vr[D / 64];
+  auto load = [&](int tile) {
+    if (tile - meta >= 64) {
+      meta = tile;
+      const int t = (tile + lane) * 64 + unit * 16;
+      at = -1;
+      ksc = vsc = 1.f;
+      if (t < end && tile + lane < tile1) {
+        const int id = kv8_page(p.s, p.c, b, t >> shift);
+        if (id >= 0) {
+          const size_t ph = (size_t)id * p.c.heads + h;
+          at = (int)((ph << (shift - 4)) + ((t >> 4) & ((1 << (shift - 4)) - 1)));
+          ksc = kv8_scale(p.c.ks[ph]);
+          vsc = kv8_scale(p.c.vs[ph]);
+        }
+      }
+    }
+    const uint32_t u = (uint32_t)__builtin_amdgcn_readlane(at, tile - meta);
+    const size_t off = (size_t)(u == 0xFFFFFFFFu ? 0u : u) * (16 * D);
+    if (does_k) {
+      const uint4 *k = (const uint4 *)(p.c.k + off) + lane;
+#pragma unroll
+      for (int t = 0; t < D / 64; ++t) kr[t] = k[64 * t];
+    }
+    if (does_v) {
+      const uint4 *v = (const uint4 *)(p.c.v + off) + lane;
+#pragma unroll
+      for (int t = 0; t < D / 64; ++t) vr[t] = v[64 * t];
+    }
+  };
+  auto widen = [&](int tile, int buf, int a, float sk, float sv) {
+    const int r = lane & 15, g = lane >> 4, step = unit >> 1;
+    if (does_k) {
+#pragma unroll
+      for (int t = 0; t < D / 64; ++t) {  // token r, channels 16 (4 t + g) ..
+        uint4 *to = &kbuf[buf][step][4 * t + g][16 * (unit & 1) + r];
+        to[0] = __builtin_bit_cast(uint4, fp8x8_to_bf16(kr[t].x, kr[t].y, sk));
+        to[32] = __builtin_bit_cast(uint4, fp8x8_to_bf16(kr[t].z, kr[t].w, sk));
+      }
+      if (lane == 0) bad[buf][unit] = a == -1;
+    }
+    if (does_v) {
+      uint32_t any = 0;
+#pragma unroll
+      for (int t = 0; t < D / 64; ++t) {  // tokens 4 g .., channels 64 t + 16 c + r
+        const uint32_t w[4] = {vr[t].x, vr[t].y, vr[t].z, vr[t].w};
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          any |= nan_bytes(w[c]);
+          const bf16x2 x0 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[c], sv, false);
+          const bf16x2 x1 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[c], sv, true);
+          uint2 *to = (uint2 *)&vbuf[buf][step][unit & 1][2 * t + (c >> 1)][32 * (g & 1) + 16 * (c & 1) + r];
+          to[g >> 1] = uint2{__builtin_bit_cast(uint32_t, x0), __builtin_bit_cast(uint32_t, x1)};
+        }
+      }
+      const bool some = __any(any != 0);
+      if (lane == 0) odd[buf][unit] = some;
+    }
+  };
+  int a_next;
+  float k_next, v_next;
+  auto load_next = [&](int tile) {
+    load(tile);
+    a_next = __builtin_amdgcn_readlane(at, tile - meta);
+    k_next = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, ksc), tile - meta));
+    v_next = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, vsc), tile - meta));
+  };
+
+  f32x16 o[CT][VT] = {};
+  float m[CT], l[CT] = {};
+#pragma unroll
+  for (int ct = 0; ct < CT; ++ct) m[ct] = kLowest;
+
+  if (tile0 < tile1) {
+    load_next(tile0);
+    widen(tile0, 0, a_next, k_next, v_next);
+    if (tile0 + 1 < tile1) load_next(tile0 + 1);
+  }
+  lds_barrier();
+  for (int tile = tile0; tile < tile1; ++tile) {
+    const int buf = (tile - tile0) & 1, t0 = tile * 64;
+    const bool in = t0 <= any_hi && t0 + 63 >= any_lo;
+    f32x16 s[CT][2] = {};
+    if (in) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int t = 0; t < KT; ++t) {
+          const bf16x8 k = as_bf16x8(kbuf[buf][j][t][lane]);
+#pragma unroll
+          for (int ct = 0; ct < CT; ++ct)
+            s[ct][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k, q[ct][t], s[ct][j], 0, 0, 0);
+        }
+    }
+    if (tile + 1 < tile1) {
+      widen(tile + 1, buf ^ 1, a_next, k_next, v_next);
+      if (tile + 2 < tile1) load_next(tile + 2);
+    }
+    if (in) {
+      const int4 no = *(const int4 *)bad[buf], od = *(const int4 *)odd[buf];
+      const bool whole = __builtin_amdgcn_readfirstlane(
+          t0 >= full_lo && t0 + 63 <= full_hi && !(no.x | no.y | no.z | no.w));
+      uint32_t seen[CT];  // bit 16 j + r
+      bool nan = false;
+      if (!whole) {
+        const int nos[4] = {no.x, no.y, no.z, no.w};
+#pragma unroll
+        for (int ct = 0; ct < CT; ++ct) {
+          seen[ct] = 0;
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {
+              const int k = t0 + 32 * j + (r & 3) + 8 * (r >> 2) + 4 * half;
+              const bool yes = k >= lo[ct] && k <= hi[ct] && !nos[2 * j + (r >> 3)];
+              seen[ct] |= (yes ? 1u : 0u) << (16 * j + r);
+              s[ct][j][r] = yes ? s[ct][j][r] : -__builtin_inff();
+            }
+        }
+        nan = __builtin_amdgcn_readfirstlane(od.x | od.y | od.z | od.w) != 0;
+      }
+      float top[CT];
+      bool raise = false;
+#pragma unroll
+      for (int ct = 0; ct < CT; ++ct) {
+        float x = kLowest;
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int r = 0; r < 16; r += 2) x = fmaxf(x, fmaxf(s[ct][j][r], s[ct][j][r + 1]));
+        top[ct] = x * cs;
+        raise |= top[ct] > m[ct] + 8.0f;
+      }
+      if (__any(raise)) {
+#pragma unroll
+        for (int ct = 0; ct < CT; ++ct) {
+          const float x = fmaxf(top[ct], __shfl_xor(top[ct], 32));
+          const float mn = fmaxf(m[ct], x), down = __builtin_amdgcn_exp2f(m[ct] - mn);
+          m[ct] = mn;
+          l[ct] *= down;
+#pragma unroll
+          for (int t = 0; t < VT; ++t) o[ct][t] *= down;
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks) {
+          bf16x8 pr[CT];
+#pragma unroll
+          for (int ct = 0; ct < CT; ++ct) {
+            float e[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              e[i] = __builtin_amdgcn_exp2f(fmaf(s[ct][j][8 * ks + i], cs, -m[ct]));
+            l[ct] += ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
+            // (bf16, the type of the product's other operand; l sums the fp32 values)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) pr[ct][i] = (__bf16)e[i];
+          }
+#pragma unroll
+          for (int t = 0; t < VT; ++t) {
+            bf16x8 v = as_bf16x8(vbuf[buf][j][ks][t][lane]);
+            if (nan) {  // NaN codes of tokens that some row does not see: as in the kernel for few rows
+              bf16x8 here;
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                const float x = (float)v[i];
+                here[i] = (__bf16)(x != x ? 1.0f : 0.0f);
+                v[i] = x != x ? (__bf16)0.0f : v[i];
+              }
+#pragma unroll
+              for (int ct = 0; ct < CT; ++ct) {
+                bf16x8 sees;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) sees[i] = (__bf16)(float)((seen[ct] >> (16 * j + 8 * ks + i)) & 1u);
+                f32x16 hit = {};
+                hit = __builtin_amdgcn_mfma_f32_32x32x16_bf16(here, sees, hit, 0, 0, 0);
+#pragma unroll
+                for (int r = 0; r < 16; ++r)
+                  if (hit[r] > 0.f) o[ct][t][r] = __builtin_nanf("");
+              }
+            }
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct)
+              o[ct][t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v, pr[ct], o[ct][t], 0, 0, 0);
+          }
+        }
+    }
+    lds_barrier();
+  }
+
+#pragma unroll
+  for (int ct = 0; ct < CT; ++ct) {
+    const int c = w0 + ct * 32 + n;
+    const float ll = l[ct] + __shfl_xor(l[ct], 32);
+    if (c >= all) continue;
+    if (p.splits > 1) {
+      const int item = ((int)b * p.c.heads + h) * p.blocks + cb;
+      float *to = p.part + (((size_t)item * p.splits + split) * kCols + (c - c0)) * (D + 2);
+#pragma unroll
+      for (int t = 0; t < VT; ++t)
+#pragma unroll
+        for (int r = 0; r < 16; r += 2)
+          *(float2 *)(to + 32 * t + (r & 3) + 8 * (r >> 2) + 4 * half) = float2{o[ct][t][r], o[ct][t][r + 1]};
+      if (half == 0) *(float2 *)(to + D) = float2{m[ct], ll};
+      continue;
+    }
+    const int64_t row = (int64_t)(sp.r0 + c / p.group) * p.a.q_heads + h * p.group + c % p.group;
+    const float inv = ll > 0.f || ll != ll ? 1.0f / ll : 0.f;
+    __bf16 *to = (__bf16 *)p.a.out + row * D;
+#pragma unroll
+    for (int t = 0; t < VT; ++t)
+#pragma unroll
+      for (int r = 0; r < 16; r += 4) {
+        const bf16x2 x = {(__bf16)(o[ct][t][r] * inv), (__bf16)(o[ct][t][r + 1] * inv)};
+        const bf16x2 y = {(__bf16)(o[ct][t][r + 2] * inv), (__bf16)(o[ct][t][r + 3] * inv)};
+        *(uint2 *)(to + 32 * t + 2 * r + 4 * half) =
+            uint2{__builtin_bit_cast(uint32_t, x), __builtin_bit_cast(uint32_t, y)};
+      }
+    if (half == 0 && p.a.lse)
+      p.a.lse[row] = ll > 0.f || ll != ll ? (m[ct] + log2f(ll)) * kLn2 : -__builtin_inff();
+  }
+}
+
+// Joins the splits of the kernel above, in the order of the tokens: a wave per column.
+template <int D>
+__global__ __launch_bounds__(256) void k_kv8_prefill_join(PrefillParams p, int kcols) {
+  const int h = (int)blockIdx.y, b = (int)blockIdx.z, lane = (int)threadIdx.x & 63;
+  const int c = (int)blockIdx.x * 4 + ((int)threadIdx.x >> 6);
+  const Kv8Span sp = kv8_span(p.s, p.c.shift, b);
+  if (c >= min(sp.rows, p.s.max_rows) * p.group) return;
+  const int item = (b * p.c.heads + h) * p.blocks + c / kcols;
+  const float *from = p.part + ((size_t)item * p.splits * kcols + c % kcols) * (D + 2);
+  const size_t step = (size_t)kcols * (D + 2);
+  float m = kLowest, l = 0.f, o[D / 64] = {};
+  for (int s = 0; s < p.splits; ++s) m = fmaxf(m, from[s * step + D]);
+  for (int s = 0; s < p.splits; ++s) {
+    const float f = __builtin_amdgcn_exp2f(from[s * step + D] - m);
+    l = fmaf(from[s * step + D + 1], f, l);
+#pragma unroll
+    for (int a = 0; a < D / 64; ++a) o[a] = fmaf(from[s * step + 64 * a + lane], f, o[a]);
+  }
+  const int64_t row = (int64_t)(sp.r0 + c / p.group) * p.a.q_heads + h * p.group + c % p.group;
+  const float inv = l > 0.f || l != l ? 1.0f / l : 0.f;
+#pragma unroll
+  for (int a = 0; a < D / 64; ++a) ((__bf16 *)p.a.out)[row * D + 64 * a + lane] = (__bf16)(o[a] * inv);
+  if (lane == 0 && p.a.lse) p.a.lse[row] = l > 0.f || l != l ? (m + log2f(l)) * kLn2 : -__builtin_inff();
+}
+
 // ---- accumulated attention weight -----------------------------------------------------
 //
 // A second pass over K with the finished log-sums: a token's sum over rows
@@ -566,19 +813,24 @@ __global__ __launch_bounds__(256) void k_kv8_weights_join(WeightParams p) {
 // Few rows: as many (row, head) columns of a KV head as one workgroup keeps
 // (64, with head size 256 32).
 constexpr int kv8_few_cols(int dim) { return dim == 256 ? 32 : 64; }
+constexpr int kv8_many_cols(int dim) { return dim == 256 ? 128 : 256; }
+constexpr int kManyGroups = 512;
 constexpr int kDecodeGroups = 1024;  // workgroups wanted
+
+int64_t cols_of(const Kv8Batch &s, const Kv8Plan &pl) { return (int64_t)s.max_rows * pl.group; }
 
 size_t kv8_part_bound(const Kv8Attn &a, const Kv8Pool &c, const Kv8Batch &s, int dim) {
   // fewer tokens or a window: shorter pieces, but (kv8_plan) never twice kDecodeGroups and one per item
   const Kv8Plan pl = kv8_plan(a, c, s, dim);
-  const size_t cols = pl.few ? 16 * (size_t)pl.ct : (size_t)kv8_few_cols(dim);
-  return std::max(pl.part_floats, (2 * kDecodeGroups + (size_t)s.seqs * c.heads) * cols * (size_t)(dim + 2));
+  const size_t few = (2 * kDecodeGroups + (size_t)s.seqs * c.heads) * (size_t)kv8_few_cols(dim);
+  const size_t many = pl.few ? 0 : (size_t)kManyGroups * kv8_many_cols(dim);
+  return std::max(pl.part_floats, std::max(few, many) * (size_t)(dim + 2));
 }
 
 Kv8Plan kv8_plan(const Kv8Attn &a, const Kv8Pool &c, const Kv8Batch &s, int dim) {
   Kv8Plan pl = {};
   pl.group = a.q_heads / c.heads;
-  const int cols = (int)std::min<int64_t>((int64_t)s.max_rows * pl.group, 1 << 30);
+  const int64_t cols = cols_of(s, pl);
   pl.few = cols <= kv8_few_cols(dim);
   pl.counter_bytes = kKv8MaxItems * 4;
   if (pl.few) {
@@ -592,6 +844,15 @@ Kv8Plan kv8_plan(const Kv8Attn &a, const Kv8Pool &c, const Kv8Batch &s, int dim)
     pl.splits = std::max((steps + 4 * pl.spw - 1) / (4 * pl.spw), 1);
     if (pl.splits > 1 && items <= kKv8MaxItems)
       pl.part_floats = (size_t)items * pl.splits * 16 * pl.ct * (dim + 2);
+  }
+  if (!pl.few) {
+    const int kc = kv8_many_cols(dim);
+    pl.blocks = (int)((cols + kc - 1) / kc);
+    const int64_t items = (int64_t)s.seqs * c.heads * pl.blocks;
+    const int64_t seen = a.window ? std::min<int64_t>(a.max_len, (int64_t)a.window + s.max_rows) : a.max_len;
+    // one workgroup fills a CU: split the tokens where there are fewer, into pieces of 512 at least
+    pl.splits = (int)std::max<int64_t>(std::min<int64_t>(kManyGroups / items, seen / 512), 1);
+    if (pl.splits > 1) pl.part_floats = (size_t)items * pl.splits * kc * (dim + 2);
   }
   pl.len_pad = (a.max_len + kWeightTokens - 1) / kWeightTokens * kWeightTokens;
   if (c.w) pl.part_floats = std::max(pl.part_floats, (size_t)s.seqs * c.heads * pl.len_pad);
@@ -610,10 +871,15 @@ hipError_t launch_kv8_attention(const Kv8Attn &a, const Kv8Pool &c, const Kv8Bat
     k<<<grid, block, 0, stream>>>(p);
     return hipGetLastError();
   }
-  const AttnParams p{a, c, s};
-  const dim3 grid((unsigned)s.max_rows, (unsigned)a.q_heads, (unsigned)s.seqs);
-  auto k = dim == 64 ? k_kv8_attn_row<64> : dim == 128 ? k_kv8_attn_row<128> : k_kv8_attn_row<256>;
-  k<<<grid, dim3(64), 0, stream>>>(p);
+  const PrefillParams p{a, c, s, pl.group, pl.blocks, pl.splits, part};
+  const dim3 grid((unsigned)c.heads * (unsigned)pl.blocks, (unsigned)(s.seqs * pl.splits));
+  auto k = dim == 64 ? k_kv8_prefill<64, 2, 4> : dim == 128 ? k_kv8_prefill<128, 2, 4> : k_kv8_prefill<256, 1, 4>;
+  k<<<grid, dim3(256), 0, stream>>>(p);
+  if (hipError_t e = hipGetLastError()) return e;
+  if (pl.splits == 1) return hipSuccess;
+  const dim3 jgrid((unsigned)((cols_of(s, pl) + 3) / 4), (unsigned)c.heads, (unsigned)s.seqs);
+  auto kj = dim == 64 ? k_kv8_prefill_join<64> : dim == 128 ? k_kv8_prefill_join<128> : k_kv8_prefill_join<256>;
+  kj<<<jgrid, dim3(256), 0, stream>>>(p, kv8_many_cols(dim));
   return hipGetLastError();
 }
 
