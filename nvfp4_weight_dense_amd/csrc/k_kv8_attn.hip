@@ -7,6 +7,7 @@
 // gives zeros and -inf.  Sums and the softmax's statistics are fp32, powers
 // are of two (log2 e is folded into the scale).
 #include <algorithm>
+#include <type_traits>
 
 #include "kv8_common.h"
 #include "launchers.h"
@@ -384,8 +385,11 @@ __global__ __launch_bounds__(64 * kDecodeWaves) void k_kv8_decode(DecodeParams p
 // its column as the next product's operand: accumulator row
 // (r % 4) + 8 (r / 4) + 4 half of a 32-token step is token 16 ks + 8 (e / 4)
 // + 4 half + e % 4 for r = 8 ks + e, so V's operand takes, of unit ks, the
-// token groups `half` and 2 + half.  The maximum is looked at once per tile
-// and raised when a score passes it by 2^8.
+// token groups `half` and 2 + half.  No maximum is looked for either: the
+// running one stays until a tile's sum of powers passes kRaise (overflow to
+// infinity does), and only then is it found and the powers taken again.
+constexpr float kRaise = 1024.0f;
+
 struct PrefillParams {
   Kv8Attn a;
   Kv8Pool c;
@@ -398,10 +402,14 @@ template <int D, int CT, int NW>
 __global__ __launch_bounds__(64 * NW, NW / 4) void k_kv8_prefill(PrefillParams p) {
   constexpr int kCols = 32 * CT * NW;
   constexpr int KT = D / 16, VT = D / 32;   // operands of a step: K's and (of each 16 tokens) V's
-  constexpr bool kBoth = NW == 4;           // a wave widens K and V of its unit, or one of them
+  // a wave reads and widens its share of one unit: 64-channel parts of both K
+  // and V, or (with one part) K or V
+  constexpr int kShare = NW / 4, kParts = D / 64 >= kShare ? D / 64 / kShare : 1;
+  constexpr bool kBoth = D / 64 >= kShare;
   __shared__ uint4 kbuf[2][2][KT][64];      // [tile][step][channels 16 t ..][lane]
   __shared__ uint4 vbuf[2][2][2][VT][64];   // [tile][step][unit][channels 32 t ..][lane]
-  __shared__ __align__(16) int bad[2][4], odd[2][4];      // a unit without a page; with a NaN code of V
+  __shared__ __align__(16) int bad[2][4];   // a unit without a page
+  __shared__ __align__(16) int odd[2][2][4];  // a unit with a NaN code of V, by the waves that widen it
   // heads side by side, so that those of one XCD's workgroups share its L2; the longest first
   const int h = (int)blockIdx.x % p.c.heads, cb = p.blocks - 1 - (int)blockIdx.x / p.c.heads;
   const int b = (int)blockIdx.y / p.splits, split = (int)blockIdx.y % p.splits;
@@ -450,74 +458,77 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void k_kv8_prefill(PrefillParams p
   // lane i: the wave's unit of tile `meta + i`
   int meta = tile0 - 64, at = -1;
   float ksc = 1.f, vsc = 1.f;
-  const int unit = wave & 3;
-  const bool does_k = kBoth || wave < 4, does_v = kBoth || wave >= 4;
-  uint4 kr[D / 64], vr[D / 64];
-  auto load = [&](int tile) {
-    if (tile - meta >= 64) {
-      meta = tile;
-      const int t = (tile + lane) * 64 + unit * 16;
-      at = -1;
-      ksc = vsc = 1.f;
-      if (t < end && tile + lane < tile1) {
-        const int id = kv8_page(p.s, p.c, b, t >> shift);
-        if (id >= 0) {
-          const size_t ph = (size_t)id * p.c.heads + h;
-          at = (int)((ph << (shift - 4)) + ((t >> 4) & ((1 << (shift - 4)) - 1)));
-          ksc = kv8_scale(p.c.ks[ph]);
-          vsc = kv8_scale(p.c.vs[ph]);
-        }
+  const int unit = wave & 3, share = wave >> 2;
+  const int part0 = kBoth ? share * kParts : 0;
+  const bool does_k = kBoth || share == 0, does_v = kBoth || share == 1;
+  uint4 kr[kParts], vr[kParts];
+  int a_next = -1;  // of the tile in kr and vr
+  float k_next = 1.f, v_next = 1.f;
+  auto look_up = [&](int tile) {  // pages and scales of 64 tiles from here
+    meta = tile;
+    const int t = (tile + lane) * 64 + unit * 16;
+    at = -1;
+    ksc = vsc = 1.f;
+    if (t < end && tile + lane < tile1) {
+      const int id = kv8_page(p.s, p.c, b, t >> shift);
+      if (id >= 0) {
+        const size_t ph = (size_t)id * p.c.heads + h;
+        at = (int)((ph << (shift - 4)) + ((t >> 4) & ((1 << (shift - 4)) - 1)));
+        ksc = kv8_scale(p.c.ks[ph]);
+        vsc = kv8_scale(p.c.vs[ph]);
       }
     }
-    const uint32_t u = (uint32_t)__builtin_amdgcn_readlane(at, tile - meta);
-    const size_t off = (size_t)(u == 0xFFFFFFFFu ? 0u : u) * (16 * D);
+  };
+  auto load = [&](int tile) {
+    if (tile - meta >= 64) look_up(tile);
+    a_next = __builtin_amdgcn_readlane(at, tile - meta);
+    k_next = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, ksc), tile - meta));
+    v_next = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, vsc), tile - meta));
+    // (a unit that no page holds reads the pool's first; its scores are masked)
+    const size_t off = (size_t)(a_next == -1 ? 0u : (uint32_t)a_next) * (16 * D);
     if (does_k) {
-      const uint4 *k = (const uint4 *)(p.c.k + off) + lane;
+      const uint4 *k = (const uint4 *)(p.c.k + off) + 64 * part0 + lane;
 #pragma unroll
-      for (int t = 0; t < D / 64; ++t) kr[t] = k[64 * t];
+      for (int t = 0; t < kParts; ++t) kr[t] = k[64 * t];
     }
     if (does_v) {
-      const uint4 *v = (const uint4 *)(p.c.v + off) + lane;
+      const uint4 *v = (const uint4 *)(p.c.v + off) + 64 * part0 + lane;
 #pragma unroll
-      for (int t = 0; t < D / 64; ++t) vr[t] = v[64 * t];
+      for (int t = 0; t < kParts; ++t) vr[t] = v[64 * t];
     }
   };
-  auto widen = [&](int tile, int buf, int a, float sk, float sv) {
+  auto widen = [&](int buf) {
     const int r = lane & 15, g = lane >> 4, step = unit >> 1;
     if (does_k) {
 #pragma unroll
-      for (int t = 0; t < D / 64; ++t) {  // token r, channels 16 (4 t + g) ..
-        uint4 *to = &kbuf[buf][step][4 * t + g][16 * (unit & 1) + r];
-        to[0] = __builtin_bit_cast(uint4, fp8x8_to_bf16(kr[t].x, kr[t].y, sk));
-        to[32] = __builtin_bit_cast(uint4, fp8x8_to_bf16(kr[t].z, kr[t].w, sk));
+      for (int t = 0; t < kParts; ++t) {  // token r, channels 16 (4 (part0 + t) + g) ..
+        uint4 *to = &kbuf[buf][step][4 * (part0 + t) + g][16 * (unit & 1) + r];
+        to[0] = __builtin_bit_cast(uint4, fp8x8_to_bf16(kr[t].x, kr[t].y, k_next));
+        to[32] = __builtin_bit_cast(uint4, fp8x8_to_bf16(kr[t].z, kr[t].w, k_next));
       }
-      if (lane == 0) bad[buf][unit] = a == -1;
+      if (lane == 0) bad[buf][unit] = a_next == -1;
     }
     if (does_v) {
       uint32_t any = 0;
 #pragma unroll
-      for (int t = 0; t < D / 64; ++t) {  // tokens 4 g .., channels 64 t + 16 c + r
+      for (int t = 0; t < kParts; ++t) {  // tokens 4 g .., channels 64 (part0 + t) + 16 c + r
         const uint32_t w[4] = {vr[t].x, vr[t].y, vr[t].z, vr[t].w};
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           any |= nan_bytes(w[c]);
-          const bf16x2 x0 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[c], sv, false);
-          const bf16x2 x1 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[c], sv, true);
-          uint2 *to = (uint2 *)&vbuf[buf][step][unit & 1][2 * t + (c >> 1)][32 * (g & 1) + 16 * (c & 1) + r];
+          const bf16x2 x0 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[c], v_next, false);
+          const bf16x2 x1 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[c], v_next, true);
+          uint2 *to = (uint2 *)&vbuf[buf][step][unit & 1][2 * (part0 + t) + (c >> 1)]
+                                    [32 * (g & 1) + 16 * (c & 1) + r];
           to[g >> 1] = uint2{__builtin_bit_cast(uint32_t, x0), __builtin_bit_cast(uint32_t, x1)};
         }
       }
       const bool some = __any(any != 0);
-      if (lane == 0) odd[buf][unit] = some;
+      if (lane == 0) {
+        odd[buf][kBoth ? share : 0][unit] = some;
+        if (!kBoth || kShare == 1) odd[buf][1][unit] = 0;
+      }
     }
-  };
-  int a_next;
-  float k_next, v_next;
-  auto load_next = [&](int tile) {
-    load(tile);
-    a_next = __builtin_amdgcn_readlane(at, tile - meta);
-    k_next = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, ksc), tile - meta));
-    v_next = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, vsc), tile - meta));
   };
 
   f32x16 o[CT][VT] = {};
@@ -526,122 +537,174 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void k_kv8_prefill(PrefillParams p
   for (int ct = 0; ct < CT; ++ct) m[ct] = kLowest;
 
   if (tile0 < tile1) {
-    load_next(tile0);
-    widen(tile0, 0, a_next, k_next, v_next);
-    if (tile0 + 1 < tile1) load_next(tile0 + 1);
+    load(tile0);
+    widen(0);
+    load(min(tile0 + 1, tile1 - 1));
   }
   lds_barrier();
-  for (int tile = tile0; tile < tile1; ++tile) {
-    const int buf = (tile - tile0) & 1, t0 = tile * 64;
-    const bool in = t0 <= any_hi && t0 + 63 >= any_lo;
-    f32x16 s[CT][2] = {};
-    if (in) {
+
+  f32x16 s[CT][2];
+  bf16x8 pr[CT][4];
+  float sum[CT];
+  auto scores = [&](int buf) {
+    const f32x16 zero = {};
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
+    for (int j = 0; j < 2; ++j)
 #pragma unroll
-        for (int t = 0; t < KT; ++t) {
-          const bf16x8 k = as_bf16x8(kbuf[buf][j][t][lane]);
+      for (int t = 0; t < KT; ++t) {
+        const bf16x8 k = as_bf16x8(kbuf[buf][j][t][lane]);
 #pragma unroll
-          for (int ct = 0; ct < CT; ++ct)
-            s[ct][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k, q[ct][t], s[ct][j], 0, 0, 0);
-        }
+        for (int ct = 0; ct < CT; ++ct)
+          s[ct][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k, q[ct][t], t ? s[ct][j] : zero, 0, 0, 0);
+      }
+  };
+  // P and its sum (fp32; P itself is rounded to bf16, the type of the product's other operand)
+  auto powers = [&]() {
+#pragma unroll
+    for (int ct = 0; ct < CT; ++ct) {
+      float part[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        float e[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          e[i] = __builtin_amdgcn_exp2f(fmaf(s[ct][u >> 1][8 * (u & 1) + i], cs, -m[ct]));
+        part[u] = ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
+#pragma unroll
+        for (int i = 0; i < 8; ++i) pr[ct][u][i] = (__bf16)e[i];
+      }
+      sum[ct] = (part[0] + part[1]) + (part[2] + part[3]);
     }
-    if (tile + 1 < tile1) {
-      widen(tile + 1, buf ^ 1, a_next, k_next, v_next);
-      if (tile + 2 < tile1) load_next(tile + 2);
+  };
+  // whether every row of the wave sees every token of the tile
+  auto is_whole = [&](int t0, int buf) {
+    const int4 no = *(const int4 *)bad[buf];
+    return (bool)__builtin_amdgcn_readfirstlane(t0 >= full_lo && t0 + 63 <= full_hi &&
+                                                !(no.x | no.y | no.z | no.w));
+  };
+  // bit r of step j: accumulator row r's token is one that the lane's column sees
+  auto sees = [&](int ct, int j, int t0, int buf) {
+    uint32_t bits = 0;
+#pragma unroll
+    for (int r = 0; r < 16; ++r) {
+      const int k = t0 + 32 * j + (r & 3) + 8 * (r >> 2) + 4 * half;
+      bits |= (k >= lo[ct] && k <= hi[ct] ? 1u : 0u) << r;
     }
-    if (in) {
-      const int4 no = *(const int4 *)bad[buf], od = *(const int4 *)odd[buf];
-      const bool whole = __builtin_amdgcn_readfirstlane(
-          t0 >= full_lo && t0 + 63 <= full_hi && !(no.x | no.y | no.z | no.w));
-      uint32_t seen[CT];  // bit 16 j + r
-      bool nan = false;
-      if (!whole) {
-        const int nos[4] = {no.x, no.y, no.z, no.w};
+    return bits & ((bad[buf][2 * j] ? 0u : 0xFFu) | (bad[buf][2 * j + 1] ? 0u : 0xFF00u));
+  };
+  auto mask = [&](int t0, int buf) {
 #pragma unroll
-        for (int ct = 0; ct < CT; ++ct) {
-          seen[ct] = 0;
+    for (int ct = 0; ct < CT; ++ct)
 #pragma unroll
-          for (int j = 0; j < 2; ++j)
+      for (int j = 0; j < 2; ++j) {
+        const uint32_t bits = sees(ct, j, t0, buf);
 #pragma unroll
-            for (int r = 0; r < 16; ++r) {
-              const int k = t0 + 32 * j + (r & 3) + 8 * (r >> 2) + 4 * half;
-              const bool yes = k >= lo[ct] && k <= hi[ct] && !nos[2 * j + (r >> 3)];
-              seen[ct] |= (yes ? 1u : 0u) << (16 * j + r);
-              s[ct][j][r] = yes ? s[ct][j][r] : -__builtin_inff();
-            }
+        for (int r = 0; r < 16; ++r) s[ct][j][r] = bits >> r & 1u ? s[ct][j][r] : -__builtin_inff();
+      }
+  };
+  auto fetch = [&](int tile, int buf) {  // the next tile to LDS, the one after it to registers
+    widen(buf ^ 1);
+    load(min(tile + 2, tile1 - 1));
+  };
+
+  // The loop proper has no rare work in it: it leaves for a tile that raises
+  // the maximum, or where a NaN code of V must not reach a row that does not
+  // see its token, and such a tile is done again from its scores below.
+  int tile = tile0;
+  while (true) {
+    bool again = false;
+    for (; tile < tile1; ++tile) {
+      const int buf = (tile - tile0) & 1, t0 = tile * 64;
+      if (t0 <= any_hi && t0 + 63 >= any_lo) {
+        scores(buf);
+        if (!is_whole(t0, buf)) {
+          mask(t0, buf);
+          const int4 x = *(const int4 *)odd[buf][0], y = *(const int4 *)odd[buf][1];
+          again = __builtin_amdgcn_readfirstlane(x.x | x.y | x.z | x.w | y.x | y.y | y.z | y.w) != 0;
         }
-        nan = __builtin_amdgcn_readfirstlane(od.x | od.y | od.z | od.w) != 0;
-      }
-      float top[CT];
-      bool raise = false;
+        powers();
+        bool raise = false;
 #pragma unroll
-      for (int ct = 0; ct < CT; ++ct) {
-        float x = kLowest;
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-#pragma unroll
-          for (int r = 0; r < 16; r += 2) x = fmaxf(x, fmaxf(s[ct][j][r], s[ct][j][r + 1]));
-        top[ct] = x * cs;
-        raise |= top[ct] > m[ct] + 8.0f;
-      }
-      if (__any(raise)) {
-#pragma unroll
-        for (int ct = 0; ct < CT; ++ct) {
-          const float x = fmaxf(top[ct], __shfl_xor(top[ct], 32));
-          const float mn = fmaxf(m[ct], x), down = __builtin_amdgcn_exp2f(m[ct] - mn);
-          m[ct] = mn;
-          l[ct] *= down;
-#pragma unroll
-          for (int t = 0; t < VT; ++t) o[ct][t] *= down;
+        for (int ct = 0; ct < CT; ++ct) raise |= sum[ct] > kRaise;
+        if (again || __any(raise)) {
+          again = true;
+          break;
         }
-      }
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
+        for (int ct = 0; ct < CT; ++ct) l[ct] += sum[ct];
+        fetch(tile, buf);
 #pragma unroll
-        for (int ks = 0; ks < 2; ++ks) {
-          bf16x8 pr[CT];
-#pragma unroll
-          for (int ct = 0; ct < CT; ++ct) {
-            float e[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-              e[i] = __builtin_amdgcn_exp2f(fmaf(s[ct][j][8 * ks + i], cs, -m[ct]));
-            l[ct] += ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
-            // (bf16, the type of the product's other operand; l sums the fp32 values)
-#pragma unroll
-            for (int i = 0; i < 8; ++i) pr[ct][i] = (__bf16)e[i];
-          }
+        for (int u = 0; u < 4; ++u)
 #pragma unroll
           for (int t = 0; t < VT; ++t) {
-            bf16x8 v = as_bf16x8(vbuf[buf][j][ks][t][lane]);
-            if (nan) {  // NaN codes of tokens that some row does not see: as in the kernel for few rows
-              bf16x8 here;
-#pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                const float x = (float)v[i];
-                here[i] = (__bf16)(x != x ? 1.0f : 0.0f);
-                v[i] = x != x ? (__bf16)0.0f : v[i];
-              }
-#pragma unroll
-              for (int ct = 0; ct < CT; ++ct) {
-                bf16x8 sees;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) sees[i] = (__bf16)(float)((seen[ct] >> (16 * j + 8 * ks + i)) & 1u);
-                f32x16 hit = {};
-                hit = __builtin_amdgcn_mfma_f32_32x32x16_bf16(here, sees, hit, 0, 0, 0);
-#pragma unroll
-                for (int r = 0; r < 16; ++r)
-                  if (hit[r] > 0.f) o[ct][t][r] = __builtin_nanf("");
-              }
-            }
+            const bf16x8 v = as_bf16x8(vbuf[buf][u >> 1][u & 1][t][lane]);
 #pragma unroll
             for (int ct = 0; ct < CT; ++ct)
-              o[ct][t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v, pr[ct], o[ct][t], 0, 0, 0);
+              o[ct][t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v, pr[ct][u], o[ct][t], 0, 0, 0);
+          }
+      } else {
+        fetch(tile, buf);
+      }
+      lds_barrier();
+    }
+    if (!again) break;
+
+    const int buf = (tile - tile0) & 1, t0 = tile * 64;
+    scores(buf);
+    mask(t0, buf);
+#pragma unroll
+    for (int ct = 0; ct < CT; ++ct) {
+      float x = kLowest;
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) x = fmaxf(x, s[ct][j][r]);
+      x *= cs;
+      x = fmaxf(x, __shfl_xor(x, 32));
+      const float mn = fmaxf(m[ct], x), down = __builtin_amdgcn_exp2f(m[ct] - mn);
+      m[ct] = mn;
+      l[ct] *= down;
+#pragma unroll
+      for (int t = 0; t < VT; ++t) o[ct][t] *= down;
+    }
+    powers();
+#pragma unroll
+    for (int ct = 0; ct < CT; ++ct) l[ct] += sum[ct];
+    fetch(tile, buf);
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+#pragma unroll
+      for (int t = 0; t < VT; ++t) {
+        bf16x8 v = as_bf16x8(vbuf[buf][u >> 1][u & 1][t][lane]), here;
+        bool some = false;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float x = (float)v[i];
+          here[i] = (__bf16)(x != x ? 1.0f : 0.0f);
+          v[i] = x != x ? (__bf16)0.0f : v[i];
+          some |= x != x;
+        }
+        if (__any(some)) {  // ones where a code is NaN, against ones where a row sees the token
+#pragma unroll
+          for (int ct = 0; ct < CT; ++ct) {
+            const uint32_t bits = sees(ct, u >> 1, t0, buf) >> (8 * (u & 1));
+            bf16x8 yes;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) yes[i] = (__bf16)(float)((bits >> i) & 1u);
+            f32x16 hit = {};
+            hit = __builtin_amdgcn_mfma_f32_32x32x16_bf16(here, yes, hit, 0, 0, 0);
+#pragma unroll
+            for (int r = 0; r < 16; ++r)
+              if (hit[r] > 0.f) o[ct][t][r] = __builtin_nanf("");
           }
         }
-    }
+#pragma unroll
+        for (int ct = 0; ct < CT; ++ct)
+          o[ct][t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v, pr[ct][u], o[ct][t], 0, 0, 0);
+        __builtin_amdgcn_sched_barrier(0);
+      }
     lds_barrier();
+    ++tile;
   }
 
 #pragma unroll
@@ -873,8 +936,8 @@ hipError_t launch_kv8_attention(const Kv8Attn &a, const Kv8Pool &c, const Kv8Bat
   }
   const PrefillParams p{a, c, s, pl.group, pl.blocks, pl.splits, part};
   const dim3 grid((unsigned)c.heads * (unsigned)pl.blocks, (unsigned)(s.seqs * pl.splits));
-  auto k = dim == 64 ? k_kv8_prefill<64, 2, 4> : dim == 128 ? k_kv8_prefill<128, 2, 4> : k_kv8_prefill<256, 1, 4>;
-  k<<<grid, dim3(256), 0, stream>>>(p);
+  auto k = dim == 64 ? k_kv8_prefill<64, 1, 8> : dim == 128 ? k_kv8_prefill<128, 1, 8> : k_kv8_prefill<256, 1, 4>;
+  k<<<grid, dim3(dim==256?256:512), 0, stream>>>(p);
   if (hipError_t e = hipGetLastError()) return e;
   if (pl.splits == 1) return hipSuccess;
   const dim3 jgrid((unsigned)((cols_of(s, pl) + 3) / 4), (unsigned)c.heads, (unsigned)s.seqs);
