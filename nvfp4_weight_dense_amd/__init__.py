@@ -21,6 +21,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from dataclasses import dataclass
 
 import torch
@@ -193,7 +194,7 @@ def load_library(path: str = LIB_PATH):
     L = ctypes.CDLL(path)
     vp, i32, i64 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64
     wp = ctypes.POINTER(_CWeight)
-    kc, kb, kr = (ctypes.POINTER(t) for t in (_CKv8Cache, _CKv8Batch, _CKv8Rows))
+    kc = kb = kr = vp  # a packed descriptor, or a reference to its ctypes structure
     sig = {
         "nvfp4_gemm_w4a16": [vp, i32, wp, vp, vp],
         "nvfp4_gemm_w4a4": [vp, i32, wp, vp, vp],
@@ -654,49 +655,82 @@ def kv8_cache(pages: int, heads: int, dim: int, page: int = 64, weights: bool = 
     return KV8Cache(*codes, *scales, w)
 
 
-def _ckv8(c: KV8Cache) -> _CKv8Cache:
+# The descriptors of include/nvfp4ffn.h as packed bytes (kv8_cache, kv8_batch,
+# kv8_rows): a decode step is a few microseconds, and ctypes structures take
+# one each to fill.  The ctypes classes above have the same layout.
+_pack_cache = struct.Struct("@5P4i").pack
+_pack_batch = struct.Struct("@3P5i4x").pack
+_pack_rows = struct.Struct("@P2q").pack
+
+
+def _ckv8(c: KV8Cache):
+    """(packed kv8_cache, heads, page, dim, device index)"""
     k, v, ks, vs, w = c.k_codes, c.v_codes, c.k_scales, c.v_scales, c.weights
     if k.dtype != torch.uint8 or k.dim() != 4 or not k.is_contiguous():
         raise ValueError("k_codes: expected a contiguous uint8 [pages, heads, page, dim] tensor")
-    if v.dtype != torch.uint8 or v.shape != k.shape or not v.is_contiguous():
+    shape = k.shape
+    pages, heads, page, dim = shape
+    if v.dtype != torch.uint8 or v.shape != shape or not v.is_contiguous():
         raise ValueError("v_codes: expected a contiguous uint8 tensor of k_codes' shape")
-    pages, heads, page, dim = k.shape
     for t, nm in ((ks, "k_scales"), (vs, "v_scales")):
-        if t.dtype != torch.uint8 or tuple(t.shape) != (pages, heads) or not t.is_contiguous():
+        if t.dtype != torch.uint8 or t.shape != (pages, heads) or not t.is_contiguous():
             raise ValueError(f"{nm}: expected a contiguous uint8 [{pages}, {heads}] tensor")
-    if w is not None and (w.dtype != torch.float32 or tuple(w.shape) != (pages, page) or not w.is_contiguous()):
-        raise ValueError(f"weights: expected a contiguous float32 [{pages}, {page}] tensor")
-    return _CKv8Cache(k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr(),
-                      None if w is None else w.data_ptr(), pages, heads, dim, page)
+    dev = k.get_device()
+    if w is not None:
+        if w.dtype != torch.float32 or w.shape != (pages, page) or not w.is_contiguous():
+            raise ValueError(f"weights: expected a contiguous float32 [{pages}, {page}] tensor")
+        if w.get_device() != dev:
+            raise ValueError("cache tensors on several devices: expected one device")
+    if not (v.get_device() == ks.get_device() == vs.get_device() == dev):
+        raise ValueError("cache tensors on several devices: expected one device")
+    return _pack_cache(k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr(),
+                       0 if w is None else w.data_ptr(), pages, heads, dim, page), heads, page, dim, dev
 
 
-def _ckv8_rows(x: torch.Tensor, name: str, dim: int, heads: int | None = None) -> _CKv8Rows:
+def _ckv8_rows(x: torch.Tensor, name: str, dim: int, heads: int | None = None) -> bytes:
     """A bf16 [rows, heads, dim] array with strides of whole 16-byte pieces."""
     if not isinstance(x, torch.Tensor) or x.dtype != torch.bfloat16 or x.dim() != 3:
         raise ValueError(f"{name}: expected a 3-D bfloat16 tensor [rows, heads, dim]")
-    if x.shape[2] != dim or (heads is not None and x.shape[1] != heads):
-        raise ValueError(f"{name}: has shape {tuple(x.shape)}, the cache has {heads or 'n'} heads of size {dim}")
+    shape = x.shape
+    if shape[2] != dim or (heads is not None and shape[1] != heads):
+        raise ValueError(f"{name}: has shape {tuple(shape)}, the cache has {heads or 'n'} heads of size {dim}")
     rs, hs, ds = x.stride()
     if ds != 1 or rs % 8 or hs % 8:
         raise ValueError(f"{name}: strides {x.stride()}: expected the last 1, the others multiples of 8")
-    return _CKv8Rows(x.data_ptr(), rs, hs)
+    return _pack_rows(x.data_ptr(), rs, hs)
 
 
-def _ckv8_batch(table, lens, starts, rows, max_rows, max_len, page) -> _CKv8Batch:
+def _ckv8_batch(table, lens, starts, rows, max_rows, max_len, page):
+    """(packed kv8_batch, seqs)"""
     if table.dtype != torch.int32 or table.dim() != 2 or not table.is_contiguous():
         raise ValueError("table: expected a contiguous int32 [seqs, cols] tensor")
     seqs, cols = table.shape
-    if lens.dtype != torch.int32 or tuple(lens.shape) != (seqs,) or not lens.is_contiguous():
+    if lens.dtype != torch.int32 or lens.shape != (seqs,) or not lens.is_contiguous():
         raise ValueError(f"lens: expected a contiguous int32 [{seqs}] tensor")
-    if starts is not None and (starts.dtype != torch.int32 or tuple(starts.shape) != (seqs + 1,)
-                               or not starts.is_contiguous()):
-        raise ValueError(f"starts: expected a contiguous int32 [{seqs + 1}] tensor")
-    if max_rows is None or starts is None:
-        max_rows = rows if starts is not None else rows // max(seqs, 1)
-    if max_len is None:
-        max_len = cols * page
-    return _CKv8Batch(table.data_ptr(), lens.data_ptr(), None if starts is None else starts.data_ptr(),
-                      seqs, cols, rows, int(max_rows), int(max_len))
+    at = 0
+    if starts is not None:
+        if starts.dtype != torch.int32 or starts.shape != (seqs + 1,) or not starts.is_contiguous():
+            raise ValueError(f"starts: expected a contiguous int32 [{seqs + 1}] tensor")
+        at = starts.data_ptr()
+        max_rows = rows if max_rows is None else int(max_rows)
+    else:
+        max_rows = rows // max(seqs, 1)
+    return _pack_batch(table.data_ptr(), lens.data_ptr(), at, seqs, cols, rows, max_rows,
+                       cols * page if max_len is None else int(max_len)), seqs
+
+
+def _kv8_on(dev: int, *tensors):
+    """Every tensor on the cache's GPU (checked after the shapes)."""
+    if dev < 0:
+        raise ValueError("expected GPU tensors")
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"tensors on {t.device} and cuda:{dev}: expected one device")
+
+
+def _kv8_stream(stream, dev: int):
+    # (the current stream's handle, without building a torch.cuda.Stream)
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
 
 
 def kv8_append(k: torch.Tensor, v: torch.Tensor, cache: KV8Cache, table: torch.Tensor,
@@ -709,13 +743,14 @@ def kv8_append(k: torch.Tensor, v: torch.Tensor, cache: KV8Cache, table: torch.T
     starts [seqs + 1] gives each sequence's rows; without it every sequence
     has rows / seqs.  max_rows bounds one sequence's rows (default: rows)."""
     L = load_library()
-    cc = _ckv8(cache)
-    ck, cv = _ckv8_rows(k, "k", cc.dim, cc.heads), _ckv8_rows(v, "v", cc.dim, cc.heads)
-    if v.shape[0] != k.shape[0]:
-        raise ValueError(f"v: {v.shape[0]} rows, k has {k.shape[0]}")
-    cb = _ckv8_batch(table, lens, starts, k.shape[0], max_rows, None, cc.page)
-    _gpu(k, v, cache.k_codes, cache.v_codes, cache.k_scales, cache.v_scales, cache.weights, table, lens, starts)
-    _check(L.kv8_append(ctypes.byref(ck), ctypes.byref(cv), ctypes.byref(cc), ctypes.byref(cb), _stream(stream)))
+    cc, heads, page, dim, dev = _ckv8(cache)
+    ck, cv = _ckv8_rows(k, "k", dim, heads), _ckv8_rows(v, "v", dim, heads)
+    rows = k.shape[0]
+    if v.shape[0] != rows:
+        raise ValueError(f"v: {v.shape[0]} rows, k has {rows}")
+    cb, _ = _ckv8_batch(table, lens, starts, rows, max_rows, None, page)
+    _kv8_on(dev, k, v, table, lens, starts)
+    _check(L.kv8_append(ck, cv, cc, cb, _kv8_stream(stream, dev)))
 
 
 def kv8_workspace(q_heads: int, cache: KV8Cache, table: torch.Tensor, lens: torch.Tensor, rows: int,
@@ -724,9 +759,9 @@ def kv8_workspace(q_heads: int, cache: KV8Cache, table: torch.Tensor, lens: torc
     """A workspace for kv8_attention calls of these sizes or smaller ones, for
     one stream (without one, calls share the library's scratch arena)."""
     L = load_library()
-    cc = _ckv8(cache)
-    n = L.kv8_attention_workspace(int(q_heads), ctypes.byref(cc), ctypes.byref(
-        _ckv8_batch(table, lens, starts, int(rows), max_rows, max_len, cc.page)))
+    cc, _, page, _, _ = _ckv8(cache)
+    n = L.kv8_attention_workspace(int(q_heads), cc,
+                                  _ckv8_batch(table, lens, starts, int(rows), max_rows, max_len, page)[0])
     if n < 0:
         _check(int(n))
     return torch.zeros((max(n, 256),), dtype=torch.uint8, device=cache.k_codes.device)
@@ -747,28 +782,29 @@ def kv8_attention(q: torch.Tensor, cache: KV8Cache, table: torch.Tensor, lens: t
     [rows, q_heads] tensor to write to) returns (out, lse).  accumulate adds
     the attention weight each token receives to cache.weights."""
     L = load_library()
-    cc = _ckv8(cache)
-    cq = _ckv8_rows(q, "q", cc.dim)
-    rows, q_heads, dim = q.shape
-    cb = _ckv8_batch(table, lens, starts, rows, max_rows, max_len, cc.page)
+    cc, _, page, dim, dev = _ckv8(cache)
+    cq = _ckv8_rows(q, "q", dim)
+    shape = q.shape
+    rows, q_heads, _ = shape
+    cb, _ = _ckv8_batch(table, lens, starts, rows, max_rows, max_len, page)
     if out is None:
-        out = torch.empty((rows, q_heads, dim), dtype=torch.bfloat16, device=q.device)
-    elif out.dtype != torch.bfloat16 or tuple(out.shape) != (rows, q_heads, dim) or not out.is_contiguous():
+        out = torch.empty(shape, dtype=torch.bfloat16, device=q.device)
+    elif out.dtype != torch.bfloat16 or out.shape != shape or not out.is_contiguous():
         raise ValueError(f"out: expected a contiguous bfloat16 [{rows}, {q_heads}, {dim}] tensor")
     give = lse is not None and lse is not False
     if lse is True or (accumulate and not give):
         lse = torch.empty((rows, q_heads), dtype=torch.float32, device=q.device)
     elif not give:
         lse = None
-    elif lse.dtype != torch.float32 or tuple(lse.shape) != (rows, q_heads) or not lse.is_contiguous():
+    elif lse.dtype != torch.float32 or lse.shape != (rows, q_heads) or not lse.is_contiguous():
         raise ValueError(f"lse: expected a contiguous float32 [{rows}, {q_heads}] tensor")
     if workspace is not None and (workspace.dtype != torch.uint8 or not workspace.is_contiguous()):
         raise ValueError("workspace: expected a contiguous uint8 tensor (kv8_workspace)")
-    _gpu(q, out, lse, workspace, cache.k_codes, cache.v_codes, cache.k_scales, cache.v_scales, cache.weights,
-         table, lens, starts)
-    _check(L.kv8_attention(ctypes.byref(cq), q_heads, dim ** -0.5 if scale is None else float(scale), int(window),
-                           ctypes.byref(cc), ctypes.byref(cb), _ptr(out), _ptr(lse), 1 if accumulate else 0,
-                           _ptr(workspace), 0 if workspace is None else workspace.numel(), _stream(stream)))
+    _kv8_on(dev, q, out, lse, workspace, table, lens, starts)
+    _check(L.kv8_attention(cq, q_heads, dim ** -0.5 if scale is None else float(scale), int(window), cc, cb,
+                           out.data_ptr(), None if lse is None else lse.data_ptr(), 1 if accumulate else 0,
+                           None if workspace is None else workspace.data_ptr(),
+                           0 if workspace is None else workspace.numel(), _kv8_stream(stream, dev)))
     return (out, lse) if give else out
 
 
@@ -780,16 +816,17 @@ def kv8_evict(cache: KV8Cache, table: torch.Tensor, lens: torch.Tensor, new_tabl
     none of them a page of table).  Returns (new lens [seqs], kept positions
     [seqs, keep] padded with -1), int32."""
     L = load_library()
-    cc = _ckv8(cache)
-    cb = _ckv8_batch(table, lens, None, 0, None, max_len, cc.page)
-    if new_table.dtype != torch.int32 or new_table.dim() != 2 or new_table.shape[0] != cb.seqs \
+    cc, _, page, _, dev = _ckv8(cache)
+    cb, seqs = _ckv8_batch(table, lens, None, 0, None, max_len, page)
+    if new_table.dtype != torch.int32 or new_table.dim() != 2 or new_table.shape[0] != seqs \
             or not new_table.is_contiguous():
-        raise ValueError(f"new_table: expected a contiguous int32 [{cb.seqs}, new_cols] tensor")
-    if int(keep) <= 0:
+        raise ValueError(f"new_table: expected a contiguous int32 [{seqs}, new_cols] tensor")
+    keep = int(keep)
+    if keep <= 0:
         raise ValueError(f"keep: {keep}, expected at least 1")
-    _gpu(table, lens, new_table, cache.k_codes, cache.v_codes, cache.k_scales, cache.v_scales, cache.weights)
-    new_lens = torch.empty((cb.seqs,), dtype=torch.int32, device=table.device)
-    kept = torch.empty((cb.seqs, int(keep)), dtype=torch.int32, device=table.device)
-    _check(L.kv8_evict(ctypes.byref(cc), ctypes.byref(cb), _ptr(new_table), new_table.shape[1], int(keep),
-                       int(recent), int(sink), _ptr(new_lens), _ptr(kept), _stream(stream)))
+    _kv8_on(dev, table, lens, new_table)
+    new_lens = torch.empty((seqs,), dtype=torch.int32, device=table.device)
+    kept = torch.empty((seqs, keep), dtype=torch.int32, device=table.device)
+    _check(L.kv8_evict(cc, cb, new_table.data_ptr(), new_table.shape[1], keep, int(recent), int(sink),
+                       new_lens.data_ptr(), kept.data_ptr(), _kv8_stream(stream, dev)))
     return new_lens, kept

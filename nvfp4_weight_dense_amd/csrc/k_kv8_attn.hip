@@ -549,14 +549,21 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void k_kv8_prefill(PrefillParams p
   auto scores = [&](int buf) {
     const f32x16 zero = {};
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
+    for (int t = 0; t < KT; ++t)
 #pragma unroll
-      for (int t = 0; t < KT; ++t) {
+      for (int j = 0; j < 2; ++j) {
         const bf16x8 k = as_bf16x8(kbuf[buf][j][t][lane]);
 #pragma unroll
         for (int ct = 0; ct < CT; ++ct)
           s[ct][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k, q[ct][t], t ? s[ct][j] : zero, 0, 0, 0);
       }
+    __builtin_amdgcn_sched_group_barrier(0x100, 6, 0);
+#pragma unroll
+    for (int i = 0; i < 2 * KT - 6; ++i) {
+      __builtin_amdgcn_sched_group_barrier(0x8, CT, 0);
+      __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+    }
+    __builtin_amdgcn_sched_group_barrier(0x8, 6 * CT, 0);
   };
   // P and its sum (fp32; P itself is rounded to bf16, the type of the product's other operand)
   auto powers = [&]() {
@@ -607,44 +614,51 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void k_kv8_prefill(PrefillParams p
     load(min(tile + 2, tile1 - 1));
   };
 
+  // tiles that some row of the wave sees: [mine0, mine1)
+  const int mine0 = min(max(any_lo >> 6, tile0), tile1), mine1 = max(min((any_hi >> 6) + 1, tile1), mine0);
+  int tile = tile0;
+  for (; tile < mine0; ++tile) {
+    fetch(tile, (tile - tile0) & 1);
+    lds_barrier();
+  }
   // The loop proper has no rare work in it: it leaves for a tile that raises
   // the maximum, or where a NaN code of V must not reach a row that does not
   // see its token, and such a tile is done again from its scores below.
-  int tile = tile0;
   while (true) {
     bool again = false;
-    for (; tile < tile1; ++tile) {
+    for (; tile < mine1; ++tile) {
       const int buf = (tile - tile0) & 1, t0 = tile * 64;
-      if (t0 <= any_hi && t0 + 63 >= any_lo) {
-        scores(buf);
-        if (!is_whole(t0, buf)) {
-          mask(t0, buf);
-          const int4 x = *(const int4 *)odd[buf][0], y = *(const int4 *)odd[buf][1];
-          again = __builtin_amdgcn_readfirstlane(x.x | x.y | x.z | x.w | y.x | y.y | y.z | y.w) != 0;
-        }
-        powers();
-        bool raise = false;
-#pragma unroll
-        for (int ct = 0; ct < CT; ++ct) raise |= sum[ct] > kRaise;
-        if (again || __any(raise)) {
-          again = true;
-          break;
-        }
-#pragma unroll
-        for (int ct = 0; ct < CT; ++ct) l[ct] += sum[ct];
-        fetch(tile, buf);
-#pragma unroll
-        for (int u = 0; u < 4; ++u)
-#pragma unroll
-          for (int t = 0; t < VT; ++t) {
-            const bf16x8 v = as_bf16x8(vbuf[buf][u >> 1][u & 1][t][lane]);
-#pragma unroll
-            for (int ct = 0; ct < CT; ++ct)
-              o[ct][t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v, pr[ct][u], o[ct][t], 0, 0, 0);
-          }
-      } else {
-        fetch(tile, buf);
+      scores(buf);
+      if (!is_whole(t0, buf)) {
+        mask(t0, buf);
+        const int4 x = *(const int4 *)odd[buf][0], y = *(const int4 *)odd[buf][1];
+        again = __builtin_amdgcn_readfirstlane(x.x | x.y | x.z | x.w | y.x | y.y | y.z | y.w) != 0;
       }
+      powers();
+      bool raise = again;
+#pragma unroll
+      for (int ct = 0; ct < CT; ++ct) raise |= sum[ct] > kRaise;
+      again = __any(raise);
+      if (again) break;
+#pragma unroll
+      for (int ct = 0; ct < CT; ++ct) l[ct] += sum[ct];
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+#pragma unroll
+        for (int t = 0; t < VT; ++t) {
+          const bf16x8 v = as_bf16x8(vbuf[buf][u >> 1][u & 1][t][lane]);
+#pragma unroll
+          for (int ct = 0; ct < CT; ++ct)
+            o[ct][t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v, pr[ct][u], o[ct][t], 0, 0, 0);
+        }
+      __builtin_amdgcn_sched_group_barrier(0x100, 6, 1);
+#pragma unroll
+      for (int i = 0; i < 4 * VT - 6; ++i) {
+        __builtin_amdgcn_sched_group_barrier(0x8, CT, 1);
+        __builtin_amdgcn_sched_group_barrier(0x100, 1, 1);
+      }
+      __builtin_amdgcn_sched_group_barrier(0x8, 6 * CT, 1);
+      fetch(tile, buf);
       lds_barrier();
     }
     if (!again) break;
@@ -705,6 +719,10 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void k_kv8_prefill(PrefillParams p
       }
     lds_barrier();
     ++tile;
+  }
+  for (; tile < tile1; ++tile) {
+    fetch(tile, (tile - tile0) & 1);
+    lds_barrier();
   }
 
 #pragma unroll
