@@ -36,6 +36,8 @@ constexpr float kLog2e = 1.44269504088896341f, kLn2 = 0.693147180559945309f;
 // the order of the tokens.
 
 constexpr int kDecodeWaves = 4;
+constexpr int kMaxSplits = 128;
+constexpr int kMaxSteps = 31;  // a wave's, two units a lane; lanes 62 and 63 name none
 constexpr float kLowest = -3.4028234663852886e38f;  // below every finite score
 
 struct DecodeParams {
@@ -43,8 +45,9 @@ struct DecodeParams {
   Kv8Pool c;
   Kv8Batch s;
   int group, blocks;  // query heads per KV head; column blocks
-  int spw, splits;    // steps per wave; workgroups per item at most
-  float *part;        // [item][split][cols][D + 2]
+  int spw, rounds;    // a wave's steps at a time, and times
+  int splits;         // workgroups per item at most
+  float *part;        // [item]: o [split][column][D], then m and l [split][column]
   unsigned *counters;
 };
 
@@ -54,6 +57,17 @@ __device__ __forceinline__ bf16x8 fp8x8_to_bf16(uint32_t lo, uint32_t hi, float 
   const bf16x2 c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, scale, false);
   const bf16x2 d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, scale, true);
   return bf16x8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
+}
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+// 16 bytes that this call reads once: kept from displacing reused lines in the caches
+__device__ __forceinline__ uint4 load_once(const uint4 *p) {
+  return __builtin_bit_cast(uint4, __builtin_nontemporal_load((const u32x4 *)p));
+}
+__device__ __forceinline__ void st16_coherent(__amdgpu_buffer_rsrc_t r, uint32_t off, f32x4 v) {
+  __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), r, off, 0, kCoherent);
+}
+__device__ __forceinline__ f32x4 ld16_coherent(__amdgpu_buffer_rsrc_t r, uint32_t off) {
+  return __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, kCoherent));
 }
 // 0x80 in each byte that is a NaN code
 __device__ __forceinline__ uint32_t nan_bytes(uint32_t w) {
@@ -72,6 +86,7 @@ __global__ __launch_bounds__(64 * kDecodeWaves) void k_kv8_decode(DecodeParams p
   __shared__ __align__(16) float osum[kDecodeWaves][16][kPad];
   __shared__ float stat[2][kDecodeWaves][kCols];
   __shared__ bool last_flag;
+  __shared__ float wsplit[kMaxSplits][16];
   const int split = (int)blockIdx.x, h = (int)blockIdx.y / p.blocks, cb = (int)blockIdx.y % p.blocks;
   const int b = (int)blockIdx.z, tid = (int)threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -85,13 +100,10 @@ __global__ __launch_bounds__(64 * kDecodeWaves) void k_kv8_decode(DecodeParams p
   const int end = min(sp.len, p.a.max_len);
   auto low = [&](int pos) { return p.a.window ? max(pos - p.a.window + 1, 0) : 0; };
   const int step0 = low(first) >> 5, step1 = (min(final + 1, end) + 31) >> 5;
-  const int per = p.spw * kDecodeWaves;
-  const int nsplit = max((step1 - step0 + per - 1) / per, 1);
+  const int per = p.spw * kDecodeWaves, whole_per = per * p.rounds;
+  const int nsplit = max((step1 - step0 + whole_per - 1) / whole_per, 1);
   if (split >= nsplit) return;
   const int full_lo = low(final), full_hi = min(first, end - 1);  // every row sees these
-
-  const int base = step0 + split * per + wave;  // this wave's steps: base + 4 s
-  const int count = min(max((step1 - base + kDecodeWaves - 1) / kDecodeWaves, 0), p.spw);
 
   // columns of this lane
   bf16x8 q[CT][D / 32];
@@ -114,10 +126,14 @@ __global__ __launch_bounds__(64 * kDecodeWaves) void k_kv8_decode(DecodeParams p
     hi[ct] = min(pos, end - 1);
   }
 
-  // lane 2 s + u: unit u of step s
-  int at = -1;
+  // this wave's steps of a round: base + 4 s; lane 2 s + u: unit u of step s
+  int base = 0, count = 0, at = -1;
   float ksc = 1.f, vsc = 1.f;
-  {
+  auto look_up = [&](int round) {
+    base = step0 + split * whole_per + round * per + wave;
+    count = min(max((step1 - base + kDecodeWaves - 1) / kDecodeWaves, 0), p.spw);
+    at = -1;
+    ksc = vsc = 1.f;
     const int t0 = (base + kDecodeWaves * (lane >> 1)) * 32 + (lane & 1) * 16;
     if ((lane >> 1) < count && t0 < end) {
       const int id = kv8_page(p.s, p.c, b, t0 >> shift);
@@ -128,18 +144,18 @@ __global__ __launch_bounds__(64 * kDecodeWaves) void k_kv8_decode(DecodeParams p
         vsc = kv8_scale(p.c.vs[ph]);
       }
     }
-  }
+  };
   auto load = [&](Step<D> &x, int s) {
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-      const uint32_t unit = (uint32_t)__builtin_amdgcn_readlane(at, 2 * s + u);
+      const uint32_t unit = (uint32_t)__builtin_amdgcn_readlane(at, min(2 * s, 62) + u);
       // (a unit that no page holds reads the pool's first; its scores are masked)
       const size_t off = (size_t)(unit == 0xFFFFFFFFu ? 0u : unit) * (16 * D);
       const uint4 *k = (const uint4 *)(p.c.k + off) + lane, *v = (const uint4 *)(p.c.v + off) + lane;
 #pragma unroll
-      for (int t = 0; t < D / 64; ++t) x.k[u][t] = k[64 * t];
+      for (int t = 0; t < D / 64; ++t) x.k[u][t] = load_once(k + 64 * t);
 #pragma unroll
-      for (int t = 0; t < D / 64; ++t) x.v[u][t] = v[64 * t];
+      for (int t = 0; t < D / 64; ++t) x.v[u][t] = load_once(v + 64 * t);
     }
   };
 
@@ -186,7 +202,7 @@ __global__ __launch_bounds__(64 * kDecodeWaves) void k_kv8_decode(DecodeParams p
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           const int j = t0 + 16 * (e >> 2) + 4 * g + (e & 3);
-          const bool yes = valid[e >> 2] && j >= lo[ct] && j <= hi[ct];
+          const bool yes = (valid[e >> 2] != 0) & (j >= lo[ct]) & (j <= hi[ct]);
           seen[ct] |= (yes ? 1u : 0u) << e;
           sc[ct][e >> 2][e & 3] = yes ? sc[ct][e >> 2][e & 3] : -__builtin_inff();
         }
@@ -224,57 +240,67 @@ __global__ __launch_bounds__(64 * kDecodeWaves) void k_kv8_decode(DecodeParams p
           any |= nan_bytes(x.v[u][a].x) | nan_bytes(x.v[u][a].y) | nan_bytes(x.v[u][a].z) | nan_bytes(x.v[u][a].w);
       odd = __any(any != 0);
     }
+    auto product = [&](auto careful) {
 #pragma unroll
-    for (int a = 0; a < D / 64; ++a) {
-      const uint32_t v0[4] = {x.v[0][a].x, x.v[0][a].y, x.v[0][a].z, x.v[0][a].w};
-      const uint32_t v1[4] = {x.v[1][a].x, x.v[1][a].y, x.v[1][a].z, x.v[1][a].w};
+      for (int a = 0; a < D / 64; ++a) {
+        const uint32_t v0[4] = {x.v[0][a].x, x.v[0][a].y, x.v[0][a].z, x.v[0][a].w};
+        const uint32_t v1[4] = {x.v[1][a].x, x.v[1][a].y, x.v[1][a].z, x.v[1][a].w};
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        uint32_t w0 = v0[c], w1 = v1[c];
-        if (odd) {
-          // ones where a code is NaN, against ones where a row sees the token
-          const uint32_t b0 = nan_bytes(w0) >> 7, b1 = nan_bytes(w1) >> 7;
-          w0 &= ~(b0 * 0xFFu);
-          w1 &= ~(b1 * 0xFFu);
-          bf16x8 here;
+        for (int c = 0; c < 4; ++c) {
+          uint32_t w0 = v0[c], w1 = v1[c];
+          if constexpr (decltype(careful)::value) {
+            // ones where a code is NaN, against ones where a row sees the token
+            const uint32_t b0 = nan_bytes(w0) >> 7, b1 = nan_bytes(w1) >> 7;
+            w0 &= ~(b0 * 0xFFu);
+            w1 &= ~(b1 * 0xFFu);
+            bf16x8 here;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            here[i] = (__bf16)(float)((b0 >> (8 * i)) & 1u);
-            here[4 + i] = (__bf16)(float)((b1 >> (8 * i)) & 1u);
+            for (int i = 0; i < 4; ++i) {
+              here[i] = (__bf16)(float)((b0 >> (8 * i)) & 1u);
+              here[4 + i] = (__bf16)(float)((b1 >> (8 * i)) & 1u);
+            }
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct) {
+              bf16x8 sees;
+#pragma unroll
+              for (int i = 0; i < 8; ++i) sees[i] = (__bf16)(float)((seen[ct] >> i) & 1u);
+              f32x4 hit = {};
+              hit = __builtin_amdgcn_mfma_f32_16x16x32_bf16(here, sees, hit, 0, 0, 0);
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                if (hit[i] > 0.f) o[ct][4 * a + c][i] = __builtin_nanf("");
+            }
+            __builtin_amdgcn_sched_barrier(0);  // one at a time: a rare path need not set the registers' number
           }
+          const bf16x2 x0 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w0, vscale[0], false);
+          const bf16x2 x1 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w0, vscale[0], true);
+          const bf16x2 y0 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w1, vscale[1], false);
+          const bf16x2 y1 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w1, vscale[1], true);
+          const bf16x8 vt = {x0[0], x0[1], x1[0], x1[1], y0[0], y0[1], y1[0], y1[1]};
 #pragma unroll
-          for (int ct = 0; ct < CT; ++ct) {
-            bf16x8 sees;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) sees[i] = (__bf16)(float)((seen[ct] >> i) & 1u);
-            f32x4 hit = {};
-            hit = __builtin_amdgcn_mfma_f32_16x16x32_bf16(here, sees, hit, 0, 0, 0);
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              if (hit[i] > 0.f) o[ct][4 * a + c][i] = __builtin_nanf("");
-          }
+          for (int ct = 0; ct < CT; ++ct)
+            o[ct][4 * a + c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vt, pr[ct], o[ct][4 * a + c], 0, 0, 0);
         }
-        const bf16x2 x0 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w0, vscale[0], false);
-        const bf16x2 x1 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w0, vscale[0], true);
-        const bf16x2 y0 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w1, vscale[1], false);
-        const bf16x2 y1 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w1, vscale[1], true);
-        const bf16x8 vt = {x0[0], x0[1], x1[0], x1[1], y0[0], y0[1], y1[0], y1[1]};
-#pragma unroll
-        for (int ct = 0; ct < CT; ++ct)
-          o[ct][4 * a + c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vt, pr[ct], o[ct][4 * a + c], 0, 0, 0);
       }
-    }
+    };
+    if (odd)
+      product(std::true_type{});
+    else
+      product(std::false_type{});
   };
 
-  // two steps' codes in turn: one loads while the other is used
-  Step<D> xa, xb;
-  if (count > 0) load(xa, 0);
-  for (int s = 0; s < count; s += 2) {
-    if (s + 1 < count) load(xb, s + 1);
-    compute(xa, s);
-    if (s + 1 < count) {
-      if (s + 2 < count) load(xa, s + 2);
-      compute(xb, s + 1);
+  // Two steps' codes in turn: one loads while the other is used.  The loads
+  // are not conditional (a wait for the older of the two would otherwise
+  // become one for both); a step past the last is the pool's first unit.
+  for (int round = 0; round < p.rounds; ++round) {
+    Step<D> xa, xb;
+    look_up(round);
+    load(xa, 0);
+    for (int s = 0; s < count; s += 2) {
+      load(xb, s + 1);
+      compute(xa, s);
+      load(xa, s + 2);
+      if (s + 1 < count) compute(xb, s + 1);
     }
   }
 
@@ -290,9 +316,9 @@ __global__ __launch_bounds__(64 * kDecodeWaves) void k_kv8_decode(DecodeParams p
   }
   __syncthreads();
   const int item = ((int)blockIdx.z * p.c.heads + h) * p.blocks + cb;
-  constexpr int width = D + 2;
   const __amdgpu_buffer_rsrc_t pr =  // (not touched when there is one split)
-      rsrc_uniform(p.part + (size_t)item * p.splits * kCols * width, (size_t)nsplit * kCols * width * 4);
+      rsrc_uniform(p.part + (size_t)item * p.splits * kCols * (D + 2), (size_t)p.splits * kCols * (D + 2) * 4);
+  const uint32_t stats = (uint32_t)p.splits * kCols * D * 4u;  // m and l of (split, column)
   const int64_t row0 = (int64_t)sp.r0 * p.a.q_heads + (int64_t)h * p.group;
   auto put = [&](int c, int d, f32x4 x, float ll) {  // four channels of column c, done
     const float inv = ll > 0.f || ll != ll ? 1.0f / ll : 0.f;
@@ -331,12 +357,11 @@ __global__ __launch_bounds__(64 * kDecodeWaves) void k_kv8_decode(DecodeParams p
         put(c, d, x, ll);
         if (d == 0 && p.a.lse) put_lse(c, mm, ll);
       } else {
-        const uint32_t off = (uint32_t)((split * kCols + c) * width) * 4u;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) st_coherent(pr, off + (uint32_t)(d + k) * 4u, x[k]);
+        const uint32_t off = (uint32_t)(split * kCols + c);
+        st16_coherent(pr, (off * D + d) * 4u, x);
         if (d == 0) {
-          st_coherent(pr, off + D * 4u, mm);
-          st_coherent(pr, off + D * 4u + 4u, ll);
+          st_coherent(pr, stats + off * 8u, mm);
+          st_coherent(pr, stats + off * 8u + 4u, ll);
         }
       }
     }
@@ -351,23 +376,64 @@ __global__ __launch_bounds__(64 * kDecodeWaves) void k_kv8_decode(DecodeParams p
                 (unsigned)(nsplit - 1);
   __syncthreads();
   if (!last_flag) return;
-  for (int i = tid; i < cols * (D / 4); i += 64 * kDecodeWaves) {
-    const int c = i / (D / 4), d = i % (D / 4) * 4;
-    float mm = kLowest, ll = 0.f;
-    f32x4 x = {};
-    for (int t = 0; t < nsplit; ++t) {
-      const uint32_t off = (uint32_t)((t * kCols + c) * width) * 4u;
-      const float mt = ld_coherent(pr, off + D * 4u), lt = ld_coherent(pr, off + D * 4u + 4u);
-      f32x4 y;
+  // 16 columns at a time: the statistics first, then the sums, the splits of a
+  // column dealt over as many threads as there are and added in order
+  constexpr int kThreads = 64 * kDecodeWaves;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) y[k] = ld_coherent(pr, off + (uint32_t)(d + k) * 4u);
-      const float mn = fmaxf(mm, mt), fa = __builtin_amdgcn_exp2f(mm - mn), fb = __builtin_amdgcn_exp2f(mt - mn);
-      x = x * fa + y * fb;
-      ll = ll * fa + lt * fb;
-      mm = mn;
+  for (int ct = 0; ct < CT; ++ct) {
+    const int here = min(cols - ct * 16, 16);
+    if (here <= 0) break;
+    if (ct) __syncthreads();
+    for (int i = tid; i < nsplit * here; i += kThreads)
+      wsplit[i / here][i % here] = ld_coherent(pr, stats + (uint32_t)(i / here * kCols + ct * 16 + i % here) * 8u);
+    __syncthreads();
+    float *top = stat[0][0], *total = stat[1][0];  // (done with)
+    for (int c = tid >> 4; c < here; c += kThreads / 16) {
+      float x = kLowest;
+      for (int t = tid & 15; t < nsplit; t += 16) x = fmaxf(x, wsplit[t][c]);
+#pragma unroll
+      for (int k = 8; k > 0; k >>= 1) x = fmaxf(x, __shfl_xor(x, k));
+      float y = 0.f;
+      for (int t = tid & 15; t < nsplit; t += 16) {
+        const float f = __builtin_amdgcn_exp2f(wsplit[t][c] - x);
+        wsplit[t][c] = f;
+        y = fmaf(f, ld_coherent(pr, stats + (uint32_t)(t * kCols + ct * 16 + c) * 8u + 4u), y);
+      }
+#pragma unroll
+      for (int k = 8; k > 0; k >>= 1) y += __shfl_xor(y, k);
+      if ((tid & 15) == 0) {
+        top[c] = x;
+        total[c] = y;
+      }
     }
-    put(c, d, x, ll);
-    if (d == 0 && p.a.lse) put_lse(c, mm, ll);
+    __syncthreads();
+    const int items = here * (D / 4);
+    int deal = 1;  // threads of one item
+    while (deal < 8 && items * deal * 2 <= kThreads) deal *= 2;
+    float *sums = &osum[0][0][0];  // [deal][items] of four
+    for (int i = tid; i < items * deal; i += kThreads) {
+      const int k = i / items, c = i % items / (D / 4), d = i % items % (D / 4) * 4;
+      f32x4 x = {};
+#pragma unroll 8
+      for (int t = k; t < nsplit; t += deal)
+        x += ld16_coherent(pr, (uint32_t)((t * kCols + ct * 16 + c) * D + d) * 4u) * wsplit[t][c];
+      if (deal == 1) {
+        put(ct * 16 + c, d, x, total[c]);
+        if (d == 0 && p.a.lse) put_lse(ct * 16 + c, top[c], total[c]);
+      } else {
+        *(f32x4 *)(sums + 4 * i) = x;
+      }
+    }
+    if (deal > 1) {
+      __syncthreads();
+      for (int i = tid; i < items; i += kThreads) {
+        const int c = i / (D / 4), d = i % (D / 4) * 4;
+        f32x4 x = *(const f32x4 *)(sums + 4 * i);
+        for (int k = 1; k < deal; ++k) x += *(const f32x4 *)(sums + 4 * (i + k * items));
+        put(ct * 16 + c, d, x, total[c]);
+        if (d == 0 && p.a.lse) put_lse(ct * 16 + c, top[c], total[c]);
+      }
+    }
   }
   if (tid == 0) __hip_atomic_store(&p.counters[item], 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
@@ -595,7 +661,7 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void k_kv8_prefill(PrefillParams p
 #pragma unroll
     for (int r = 0; r < 16; ++r) {
       const int k = t0 + 32 * j + (r & 3) + 8 * (r >> 2) + 4 * half;
-      bits |= (k >= lo[ct] && k <= hi[ct] ? 1u : 0u) << r;
+      bits |= (((k >= lo[ct]) & (k <= hi[ct])) ? 1u : 0u) << r;
     }
     return bits & ((bad[buf][2 * j] ? 0u : 0xFFu) | (bad[buf][2 * j + 1] ? 0u : 0xFF00u));
   };
@@ -861,7 +927,7 @@ __global__ __launch_bounds__(256) void k_kv8_weights(WeightParams p) {
       for (int e = 0; e < 4; ++e) {
         const int j = t0 + 16 * u + 4 * g + e;
         const float x = __builtin_amdgcn_exp2f(fmaf(s[e], f[u], -z));
-        sum[u][e] += valid[u] && j >= lo && j <= hi ? x : 0.f;
+        sum[u][e] += (valid[u] & (j >= lo) & (j <= hi)) ? x : 0.f;
       }
     }
   }
@@ -896,7 +962,7 @@ __global__ __launch_bounds__(256) void k_kv8_weights_join(WeightParams p) {
 constexpr int kv8_few_cols(int dim) { return dim == 256 ? 32 : 64; }
 constexpr int kv8_many_cols(int dim) { return dim == 256 ? 128 : 256; }
 constexpr int kManyGroups = 512;
-constexpr int kDecodeGroups = 1024;  // workgroups wanted
+constexpr int kDecodeGroups = 512;  // workgroups wanted
 
 int64_t cols_of(const Kv8Batch &s, const Kv8Plan &pl) { return (int64_t)s.max_rows * pl.group; }
 
@@ -916,14 +982,21 @@ Kv8Plan kv8_plan(const Kv8Attn &a, const Kv8Pool &c, const Kv8Batch &s, int dim)
   pl.counter_bytes = kKv8MaxItems * 4;
   if (pl.few) {
     pl.ct = cols <= 16 ? 1 : cols <= 32 ? 2 : 4;
-    const int items = s.seqs * c.heads;
+    pl.blocks = 1;
+    const int items = s.seqs * c.heads * pl.blocks;
     const int64_t seen = a.window ? std::min<int64_t>(a.max_len, (int64_t)a.window + s.max_rows + 31) : a.max_len;
     const int steps = (int)((seen + 31) / 32) + (a.window ? 1 : 0);
-    // the longest pieces that still give every CU a few workgroups
-    pl.spw = 32;
-    while (pl.spw > 1 && (int64_t)items * ((steps + 4 * pl.spw - 1) / (4 * pl.spw)) < kDecodeGroups) pl.spw /= 2;
-    pl.splits = std::max((steps + 4 * pl.spw - 1) / (4 * pl.spw), 1);
-    if (pl.splits > 1 && items <= kKv8MaxItems)
+    // The longest pieces that still give every CU two workgroups, which is
+    // what its registers hold: shorter ones cost more in the join than they
+    // gain (two sequences of 131000 tokens, 8 KV heads: 35 pieces each 118 us,
+    // 69 pieces 134 us, 137 pieces 169 us).
+    auto pieces = [&](int spw) { return std::max((steps + 4 * spw - 1) / (4 * spw), 1); };
+    pl.spw = kMaxSteps;
+    while (pl.spw > 1 && (int64_t)items * pieces(pl.spw) < kDecodeGroups) pl.spw /= 2;
+    const int most = items <= kKv8MaxItems ? kMaxSplits : 1;
+    pl.rounds = (pieces(pl.spw) + most - 1) / most;
+    pl.splits = (pieces(pl.spw) + pl.rounds - 1) / pl.rounds;
+    if (pl.splits > 1)
       pl.part_floats = (size_t)items * pl.splits * 16 * pl.ct * (dim + 2);
   }
   if (!pl.few) {
@@ -943,13 +1016,13 @@ Kv8Plan kv8_plan(const Kv8Attn &a, const Kv8Pool &c, const Kv8Batch &s, int dim)
 hipError_t launch_kv8_attention(const Kv8Attn &a, const Kv8Pool &c, const Kv8Batch &s, int dim,
                                 const Kv8Plan &pl, unsigned *counters, float *part, hipStream_t stream) {
   if (pl.few) {
-    const DecodeParams p{a, c, s, pl.group, 1, pl.spw, pl.splits, part, counters};
-    const dim3 grid((unsigned)pl.splits, (unsigned)c.heads, (unsigned)s.seqs), block(64 * kDecodeWaves);
+    const DecodeParams p{a, c, s, pl.group, pl.blocks, pl.spw, pl.rounds, pl.splits, part, counters};
+    const dim3 grid((unsigned)pl.splits, (unsigned)(c.heads * pl.blocks), (unsigned)s.seqs);
     auto k = dim == 64 ? (pl.ct == 1 ? k_kv8_decode<64, 1> : pl.ct == 2 ? k_kv8_decode<64, 2> : k_kv8_decode<64, 4>)
              : dim == 128
                  ? (pl.ct == 1 ? k_kv8_decode<128, 1> : pl.ct == 2 ? k_kv8_decode<128, 2> : k_kv8_decode<128, 4>)
                  : (pl.ct == 1 ? k_kv8_decode<256, 1> : k_kv8_decode<256, 2>);
-    k<<<grid, block, 0, stream>>>(p);
+    k<<<grid, dim3(64 * kDecodeWaves), 0, stream>>>(p);
     return hipGetLastError();
   }
   const PrefillParams p{a, c, s, pl.group, pl.blocks, pl.splits, part};

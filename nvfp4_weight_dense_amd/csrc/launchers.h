@@ -309,7 +309,7 @@ struct Kv8Attn {
 struct Kv8Plan {
   int group;    // query heads per KV head
   bool few;     // the kernel that splits the tokens (few rows)
-  int ct, spw;  // its 16-column tiles, 32-token steps per wave
+  int ct, spw, rounds;  // its 16-column tiles, a wave's 32-token steps at a time, and times
   int blocks;   // column blocks of a sequence (many rows)
   int splits;   // parts of a sequence's tokens
   int len_pad;  // tokens of a part of the weights pass

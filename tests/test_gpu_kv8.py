@@ -501,3 +501,14 @@ def test_evict_then_attend():
     got = nv.kv8_attention(q.cuda()[:, :4], dev, new_table.cuda(), n, scale=0.002, lse=True)
     _within(got[0], out, b_out, "out")
     _within(got[1], lse, b_lse, "lse")
+
+
+def test_many_rounds_of_a_very_long_cache():
+    """More tokens than one launch's pieces hold at a time (pages named again and again, so that the pool stays
+    small: the reference sees the same tokens)."""
+    _say("very long cache")
+    dim, page, heads, q_heads, n = 64, 128, 1, 2, 700000
+    c = _filled(9, heads, dim, page, 80)
+    table = torch.randint(0, 9, (1, -(-n // page)), generator=_gen(81), dtype=torch.int32)
+    q = torch.randn(1, q_heads + 3, dim, generator=_gen(82)).bfloat16()
+    _check(c, table, q, q_heads, [n], [1], accumulate=False)
