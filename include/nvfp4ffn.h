@@ -408,7 +408,7 @@ int kv8_attention(const kv8_rows *q, int32_t q_heads, float scale, int32_t windo
  * of at most `keep` tokens is copied whole.  new_lens: device, int32 [seqs];
  * kept: device, int32 [seqs][keep], the kept positions, then -1.  No page of
  * new_table may be one that the batch's table names.  batch's rows are not
- * used. */
+ * used; a length beyond max_len is held to it. */
 int kv8_evict(const kv8_cache *cache, const kv8_batch *batch, const int32_t *new_table,
               int32_t new_cols, int32_t keep, int32_t recent, int32_t sink, int32_t *new_lens,
               int32_t *kept, void *stream);

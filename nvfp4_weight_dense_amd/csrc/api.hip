@@ -180,7 +180,9 @@ int counters_get(size_t words, unsigned **out) {
       (void)hipGetLastError();
       return fail(NVFP4_ENOMEM, "split-K counters: hipMalloc of %zu bytes failed", want);
     }
-    if (hipMemset(a.ptr, 0, want) != hipSuccess) return fail(NVFP4_EHIP, "hipMemset of counters failed");
+    // (the clear runs on the default stream, which the caller's need not wait for)
+    if (hipMemset(a.ptr, 0, want) != hipSuccess || hipDeviceSynchronize() != hipSuccess)
+      return fail(NVFP4_EHIP, "hipMemset of counters failed");
     a.size = want;
   }
   *out = (unsigned *)a.ptr;
@@ -1210,9 +1212,14 @@ int kv8_evict(const kv8_cache *cache, const kv8_batch *batch, const int32_t *new
   if (((uintptr_t)new_table | (uintptr_t)new_lens | (uintptr_t)kept) & 3u)
     return fail(NVFP4_EINVAL, "kv8_evict: arrays must be 4-byte aligned");
   hipStream_t s = (hipStream_t)stream;
+  const int max_len = std::min(batch->max_len, batch->cols * cache->page);
+  const Kv8EvictPlan pl = kv8_evict_plan(kv8_batch_ref(batch), max_len);
+  unsigned *hist = nullptr;
+  void *words = nullptr;
+  if ((rc = counters_get(pl.hist_words, &hist)) || (pl.words && (rc = arena_get(pl.words * 4, &words)))) return rc;
   ProfileScope ps("kv8_evict", batch->seqs, s);
-  return hip_status(launch_kv8_evict(kv8_pool(cache), kv8_batch_ref(batch), cache->dim, new_table, new_cols, keep,
-                                     recent, sink, new_lens, kept, s),
+  return hip_status(launch_kv8_evict(kv8_pool(cache), kv8_batch_ref(batch), cache->dim, max_len, new_table, new_cols,
+                                     keep, recent, sink, new_lens, kept, pl, hist, (uint32_t *)words, s),
                     "kv8_evict launch");
 }
 

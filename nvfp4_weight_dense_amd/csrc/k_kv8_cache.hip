@@ -8,6 +8,8 @@
 // except in the lowest, subnormal codes, and it lets a later token raise
 // the page's scale without a second rounding of the codes that are there
 // (kv8_rescale4).
+#include <type_traits>
+
 #include "kv8_common.h"
 #include "launchers.h"
 
@@ -147,14 +149,31 @@ __global__ void k_kv8_append(AppendParams p) {
 }
 
 // ---- eviction ---------------------------------------------------------------------
+//
+// Which tokens stay: the first `sink`, the last `recent` and of those between
+// them the `need` = keep - sink - recent with the largest weights.  Weights
+// become words of the same order, and the smallest word that stays is found
+// by three digits (11, 11, 10 bits) with a histogram each; of the tokens
+// that share it the first stay.  Counts are whole numbers, so the order of
+// their atomic additions does not show.
 
 struct SelectParams {
   Kv8Pool c;
   Kv8Batch s;
-  int keep, recent, sink;
-  int *new_lens;  // [seqs]
-  int *kept;      // [seqs][keep]
+  int keep, recent, sink, max_len;
+  int *new_lens;     // [seqs]
+  int *kept;         // [seqs][keep]
+  // where a sequence is dealt over workgroups:
+  int chunks;
+  uint32_t *words;   // [seqs][chunks * kChunk]
+  unsigned *hist;    // [seqs][3][kBins], zero on entry, left zero
+  int *counts;       // [seqs][chunks][2]: tokens that stay, tokens with the last word
+  unsigned *limit;   // [seqs][2]: the last word, how many of its tokens stay
 };
+
+constexpr int kBins = 2048, kDealt = 256, kChunk = 4 * kDealt;
+__device__ __forceinline__ int digit_shift(int i) { return i == 0 ? 21 : i == 1 ? 10 : 0; }
+__device__ __forceinline__ uint32_t digit(uint32_t w, int i) { return w >> digit_shift(i) & (i == 2 ? 1023u : 2047u); }
 
 // A weight as an unsigned word with the same order (-0 as +0, NaN above all).
 __device__ __forceinline__ uint32_t order_word(float w) {
@@ -163,84 +182,93 @@ __device__ __forceinline__ uint32_t order_word(float w) {
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
-// One workgroup per sequence.  The tokens between the first `sink` and the
-// last `recent` compete for the remaining places: the smallest word that
-// stays is found digit by digit (8 bits, a histogram each), then the kept
-// positions are written in order; of the tokens that share that word the
-// first stay.  Each wave owns one run of positions, so the order needs one
-// exchange of counts.
-constexpr int kSelThreads = 1024, kSelWaves = kSelThreads / 64;
+struct Span {  // the tokens that compete: [lo, hi)
+  int len, lo, hi, need;
+};
+__device__ __forceinline__ Span select_span(const SelectParams &p, int b) {
+  Span s;
+  s.len = min(kv8_span(p.s, p.c.shift, b).len, p.max_len);
+  s.lo = p.sink;
+  s.hi = s.len - p.recent;
+  s.need = p.keep - p.sink - p.recent;
+  return s;
+}
+__device__ __forceinline__ uint32_t token_word(const SelectParams &p, int b, int j) {
+  const int id = kv8_page(p.s, p.c, b, j >> p.c.shift);
+  return id < 0 ? 0u : order_word(p.c.w[((size_t)id << p.c.shift) + (j & ((1 << p.c.shift) - 1))]);
+}
 
-__global__ __launch_bounds__(kSelThreads) void k_kv8_select(SelectParams p) {
-  __shared__ unsigned hist[256];
-  __shared__ unsigned pick[2];  // digit, places left below it
-  __shared__ int above[kSelWaves], equal[kSelWaves];
-  const int b = (int)blockIdx.x, tid = (int)threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int shift = p.c.shift;
-  const int len = kv8_span(p.s, shift, b).len;
-  int *kept = p.kept + (size_t)b * p.keep;
-  const int stay = min(len, p.keep);
-  if (tid == 0) p.new_lens[b] = stay;
-  if (len <= p.keep) {
-    for (int i = tid; i < p.keep; i += kSelThreads) kept[i] = i < len ? i : -1;
-    return;
+// The digit of the `left`-th largest word from a histogram (1 <= left <= its
+// sum), and which of that digit's words it is.  A thread owns neighbouring
+// bins, the first thread the highest; scratch: LDS of NT / 64 + 2 words.
+template <int NT>
+__device__ __forceinline__ void find_digit(const unsigned *hist, unsigned &left, uint32_t &dig, unsigned *scratch) {
+  constexpr int kPer = kBins / NT;
+  const int tid = (int)threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  unsigned c[kPer], sum = 0;
+#pragma unroll
+  for (int k = 0; k < kPer; ++k) c[k] = hist[kBins - 1 - tid * kPer - k];
+#pragma unroll
+  for (int k = 0; k < kPer; ++k) sum += c[k];
+  unsigned incl = sum;
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    const unsigned x = __shfl_up(incl, o);
+    if (lane >= o) incl += x;
   }
-  const int lo = p.sink, hi = len - p.recent, need = p.keep - p.sink - p.recent;
-  auto word = [&](int j) {
-    const int id = kv8_page(p.s, p.c, b, j >> shift);
-    return id < 0 ? 0u : order_word(p.c.w[((size_t)id << shift) + (j & ((1 << shift) - 1))]);
-  };
-  uint32_t prefix = 0, mask = 0;
-  int left = need;  // places among the words that match the prefix
-  for (int sh = 24; sh >= 0 && need > 0; sh -= 8) {
-    if (tid < 256) hist[tid] = 0;
-    __syncthreads();
-    for (int j = lo + tid; j < hi; j += kSelThreads) {
-      const uint32_t u = word(j);
-      if ((u & mask) == prefix) atomicAdd(&hist[(u >> sh) & 255], 1u);
+  if (lane == 63) scratch[2 + wave] = incl;
+  __syncthreads();
+  for (int i = 0; i < wave; ++i) incl += scratch[2 + i];
+  unsigned run = incl - sum;
+  if (run < left && left <= incl) {
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+      if (run < left && left <= run + c[k]) {
+        scratch[0] = (unsigned)(kBins - 1 - tid * kPer - k);
+        scratch[1] = left - run;
+      }
+      run += c[k];
     }
-    __syncthreads();
-    if (tid == 0) {
-      int d = 255;
-      unsigned sum = 0;
-      while (d > 0 && sum + hist[d] < (unsigned)left) sum += hist[d--];
-      pick[0] = (unsigned)d;
-      pick[1] = (unsigned)left - sum;
-    }
-    __syncthreads();
-    prefix |= pick[0] << sh;
-    mask |= 255u << sh;
-    left = (int)pick[1];
-    __syncthreads();
   }
-  // stays: protected, word > prefix, or one of the first `left` equal ones
-  const int run = (((len + kSelWaves - 1) / kSelWaves) + 63) & ~63;
-  const int j0 = wave * run, j1 = min(j0 + run, len);
-  auto kind = [&](int j) {  // 0 goes, 1 stays, 2 stays if among the first equal ones
-    if (j >= j1) return 0;
-    if (j < lo || j >= hi) return 1;
-    if (need == 0) return 0;
+  __syncthreads();
+  dig = scratch[0];
+  left = scratch[1];
+  __syncthreads();
+}
+
+// Writes the positions that stay of [j0, j1) from kept[at]; `seen` tokens
+// with the last word lie before j0.  Each wave owns one run of positions, so
+// the order needs one exchange of counts.
+template <int NT, typename F>
+__device__ __forceinline__ void emit(const Span &sp, int j0, int j1, uint32_t last, int left, int at, int seen,
+                                     int *kept, int (*part)[2], F word) {
+  const int lane = (int)threadIdx.x & 63, wave = (int)threadIdx.x >> 6;
+  const int run = (((j1 - j0 + NT / 64 - 1) / (NT / 64)) + 63) & ~63;
+  const int a = min(j0 + wave * run, j1), z = min(a + run, j1);
+  auto kind = [&](int j) {  // 0 goes, 1 stays, 2 stays if among the first with the last word
+    if (j >= z) return 0;
+    if (j < sp.lo || j >= sp.hi) return 1;
+    if (sp.need == 0) return 0;
     const uint32_t u = word(j);
-    return u > prefix ? 1 : u == prefix ? 2 : 0;
+    return u > last ? 1 : u == last ? 2 : 0;
   };
   int na = 0, ne = 0;
-  for (int j = j0; j < j1; j += 64) {
+  for (int j = a; j < z; j += 64) {
     const int k = kind(j + lane);
     na += __popcll(__ballot(k == 1));
     ne += __popcll(__ballot(k == 2));
   }
   if (lane == 0) {
-    above[wave] = na;
-    equal[wave] = ne;
+    part[wave][0] = na;
+    part[wave][1] = ne;
   }
   __syncthreads();
-  int at = 0, seen = 0;
   for (int i = 0; i < wave; ++i) {
-    at += above[i] + min(max(left - seen, 0), equal[i]);
-    seen += equal[i];
+    at += part[i][0] + min(max(left - seen, 0), part[i][1]);
+    seen += part[i][1];
   }
   const uint64_t before = (1ull << lane) - 1ull;
-  for (int j = j0; j < j1; j += 64) {
+  for (int j = a; j < z; j += 64) {
     const int k = kind(j + lane);
     const uint64_t eq = __ballot(k == 2);
     const bool in = k == 1 || (k == 2 && seen + __popcll(eq & before) < left);
@@ -251,125 +279,300 @@ __global__ __launch_bounds__(kSelThreads) void k_kv8_select(SelectParams p) {
   }
 }
 
+// Up to kWhole tokens: one workgroup per sequence, the words in LDS.
+constexpr int kWhole = 32768, kWholeThreads = 1024;
+
+__global__ __launch_bounds__(kWholeThreads) void k_kv8_select(SelectParams p) {
+  __shared__ uint32_t words[kWhole];
+  __shared__ unsigned hist[kBins], scratch[2 + kWholeThreads / 64];
+  __shared__ int part[kWholeThreads / 64][2];
+  const int b = (int)blockIdx.x, tid = (int)threadIdx.x;
+  const Span sp = select_span(p, b);
+  int *kept = p.kept + (size_t)b * p.keep;
+  if (tid == 0) p.new_lens[b] = min(sp.len, p.keep);
+  if (sp.len <= p.keep) {
+    for (int i = tid; i < p.keep; i += kWholeThreads) kept[i] = i < sp.len ? i : -1;
+    return;
+  }
+  uint32_t prefix = 0;
+  unsigned left = (unsigned)sp.need;
+  if (sp.need > 0) {
+    for (int i = tid; i < kBins; i += kWholeThreads) hist[i] = 0;
+    __syncthreads();
+    for (int j = sp.lo + tid; j < sp.hi; j += kWholeThreads) {
+      const uint32_t u = token_word(p, b, j);
+      words[j] = u;
+      atomicAdd(&hist[digit(u, 0)], 1u);
+    }
+    __syncthreads();
+    for (int i = 0; i < 3; ++i) {
+      uint32_t d;
+      find_digit<kWholeThreads>(hist, left, d, scratch);
+      prefix |= d << digit_shift(i);
+      if (i == 2) break;
+      for (int k = tid; k < kBins; k += kWholeThreads) hist[k] = 0;
+      __syncthreads();
+      for (int j = sp.lo + tid; j < sp.hi; j += kWholeThreads)
+        if (words[j] >> digit_shift(i) == prefix >> digit_shift(i)) atomicAdd(&hist[digit(words[j], i + 1)], 1u);
+      __syncthreads();
+    }
+  }
+  emit<kWholeThreads>(sp, 0, sp.len, prefix, (int)left, 0, 0, kept, part, [&](int j) { return words[j]; });
+}
+
+// More tokens: chunks of them, a launch for each digit, one for the counts of
+// each chunk and one that writes.
+template <int STAGE>  // 0: words and the first histogram; 1, 2: the next digit's; 3: counts
+__global__ __launch_bounds__(kDealt) void k_kv8_select_stage(SelectParams p) {
+  __shared__ unsigned local[kBins], scratch[2 + kDealt / 64];
+  __shared__ int part[2];
+  const int b = (int)blockIdx.y, tid = (int)threadIdx.x;
+  const Span sp = select_span(p, b);
+  const int j0 = (int)blockIdx.x * kChunk, j1 = min(j0 + kChunk, sp.len);
+  if (sp.len <= p.keep || j0 >= sp.len) return;
+  uint32_t *words = p.words + (size_t)b * p.chunks * kChunk;
+  unsigned *hist = p.hist + (size_t)b * 3 * kBins;
+  uint32_t prefix = 0;
+  unsigned left = (unsigned)sp.need;
+  if (sp.need > 0) {
+#pragma unroll
+    for (int i = 0; i < STAGE; ++i) {
+      uint32_t d;
+      find_digit<kDealt>(hist + i * kBins, left, d, scratch);
+      prefix |= d << digit_shift(i);
+    }
+  }
+  // a thread's four tokens: whether they compete, and their words
+  bool in[4];
+  uint32_t u[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int j = j0 + tid + k * kDealt;
+    in[k] = j < j1 && j >= sp.lo && j < sp.hi && sp.need > 0;
+    u[k] = in[k] ? (STAGE == 0 ? token_word(p, b, j) : words[j]) : 0;
+  }
+  if constexpr (STAGE < 3) {
+    if (sp.need == 0) return;
+    for (int i = tid; i < kBins; i += kDealt) local[i] = 0;
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (!in[k]) continue;
+      if constexpr (STAGE == 0) {
+        words[j0 + tid + k * kDealt] = u[k];
+      } else {
+        if (u[k] >> digit_shift(STAGE - 1) != prefix >> digit_shift(STAGE - 1)) continue;
+      }
+      atomicAdd(&local[digit(u[k], STAGE)], 1u);
+    }
+    __syncthreads();
+    for (int i = tid; i < kBins; i += kDealt)
+      if (local[i]) atomicAdd(&hist[STAGE * kBins + i], local[i]);
+  } else {
+    if (tid < 2) part[tid] = 0;
+    __syncthreads();
+    int above = 0, equal = 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int j = j0 + tid + k * kDealt;
+      if (j < j1 && (j < sp.lo || j >= sp.hi)) ++above;
+      if (in[k]) {
+        above += u[k] > prefix;
+        equal += u[k] == prefix;
+      }
+    }
+    atomicAdd(&part[0], above);
+    atomicAdd(&part[1], equal);
+    __syncthreads();
+    if (tid < 2) p.counts[((size_t)b * p.chunks + blockIdx.x) * 2 + tid] = part[tid];
+    if (blockIdx.x == 0 && tid == 0) {
+      p.limit[2 * b] = prefix;
+      p.limit[2 * b + 1] = left;
+    }
+  }
+}
+
+__global__ __launch_bounds__(kDealt) void k_kv8_select_emit(SelectParams p) {
+  __shared__ int part[kDealt / 64][2];
+  const int b = (int)blockIdx.y, tid = (int)threadIdx.x, chunk = (int)blockIdx.x;
+  const Span sp = select_span(p, b);
+  int *kept = p.kept + (size_t)b * p.keep;
+  if (chunk == 0 && tid == 0) p.new_lens[b] = min(sp.len, p.keep);
+  if (sp.len <= p.keep) {
+    for (int i = chunk * kDealt + tid; i < p.keep; i += p.chunks * kDealt) kept[i] = i < sp.len ? i : -1;
+    return;
+  }
+  if (chunk == 0)  // (the histograms' last reader has ended)
+    for (int i = tid; i < 3 * kBins; i += kDealt) p.hist[(size_t)b * 3 * kBins + i] = 0;
+  const int j0 = chunk * kChunk, j1 = min(j0 + kChunk, sp.len);
+  if (j0 >= sp.len) return;
+  const int left = (int)p.limit[2 * b + 1];
+  const int *counts = p.counts + (size_t)b * p.chunks * 2;
+  __shared__ int before[2];
+  if (tid < 2) before[tid] = 0;
+  __syncthreads();
+  int stays = 0, same = 0;
+  for (int i = tid; i < chunk; i += kDealt) {
+    stays += counts[2 * i];
+    same += counts[2 * i + 1];
+  }
+  if (stays) atomicAdd(&before[0], stays);
+  if (same) atomicAdd(&before[1], same);
+  __syncthreads();
+  const int seen = before[1], at = before[0] + min(seen, left);
+  const uint32_t *words = p.words + (size_t)b * p.chunks * kChunk;
+  emit<kDealt>(sp, j0, j1, p.limit[2 * b], left, at, seen, kept, part, [&](int j) { return words[j]; });
+}
+
 struct MoveParams {
   Kv8Pool c;
   Kv8Batch s;
   const int *new_table;  // [seqs][new_cols]
-  int new_cols, keep;
+  int new_cols, keep, max_len;
   const int *kept;
 };
 
-// One workgroup: one fresh page of one sequence, one KV head, K or V.  The
-// kept tokens' codes are gathered into LDS in the page's order, their
-// largest magnitude gives the new scale, and the codes move to it.
-template <int D>
+// One workgroup: one fresh page of one sequence, one KV head, K or V.  A
+// thread gathers NP 16-byte pieces of the new page (of K one token's 16
+// channels, of V four tokens of four channels: a byte of each dword of four
+// source pieces), the largest magnitude gives the new scale, and the codes
+// move to it in registers.
+template <int D, int NP>
 __global__ __launch_bounds__(256) void k_kv8_move(MoveParams p) {
-  extern __shared__ __align__(16) uint8_t image[];
   __shared__ float part[4];
-  __shared__ int src[128];      // page id of each token, -1: none
+  __shared__ int src[128];  // unit of each token's codes, -1: none
   __shared__ int src_slot[128];
   __shared__ float src_scale[128];
   const int b = (int)blockIdx.z, h = (int)blockIdx.y >> 1, isv = (int)blockIdx.y & 1;
-  const int tid = (int)threadIdx.x, nt = (int)blockDim.x;
+  const int tid = (int)threadIdx.x;
   const int shift = p.c.shift, page = 1 << shift, col = (int)blockIdx.x;
-  const int len = min(kv8_span(p.s, shift, b).len, p.keep);
+  const int len = min(min(kv8_span(p.s, shift, b).len, p.max_len), p.keep);
   const int n = min(len - (col << shift), page);  // tokens of this page
   if (n <= 0) return;
   const int to = p.new_table[(size_t)b * p.new_cols + col];
   if ((unsigned)to >= (unsigned)p.c.pages) return;
-  const uint8_t *codes = isv ? p.c.v : p.c.k;
-  const uint8_t *scales = isv ? p.c.vs : p.c.ks;
-  for (int i = tid; i < n; i += nt) {
-    const int j = p.kept[(size_t)b * p.keep + (col << shift) + i];
-    const int id = kv8_page(p.s, p.c, b, j >> shift);
-    src[i] = id;
-    src_slot[i] = j & (page - 1);
-    src_scale[i] = id < 0 ? 1.0f : kv8_scale(scales[(size_t)id * p.c.heads + h]);
-    if (h == 0 && !isv && p.c.w)
-      p.c.w[((size_t)to << shift) + i] = id < 0 ? 0.f : p.c.w[((size_t)id << shift) + (j & (page - 1))];
+  uint8_t *codes = isv ? p.c.v : p.c.k;
+  uint8_t *scales = isv ? p.c.vs : p.c.ks;
+  if (tid < n) {
+    const int j = p.kept[(size_t)b * p.keep + (col << shift) + tid];
+    const int id = kv8_page(p.s, p.c, b, j >> shift), slot = j & (page - 1);
+    const size_t ph = (size_t)max(id, 0) * p.c.heads + h;
+    src[tid] = id < 0 ? -1 : (int)((ph << (shift - 4)) + (slot >> 4));
+    src_slot[tid] = slot & 15;
+    src_scale[tid] = id < 0 ? 1.0f : kv8_scale(scales[ph]);
+    if (h == 0 && !isv && p.c.w) p.c.w[((size_t)to << shift) + tid] = id < 0 ? 0.f : p.c.w[((size_t)id << shift) + slot];
   }
   __syncthreads();
-  uint8_t *out = (uint8_t *)codes + (((size_t)to * p.c.heads + h) << shift) * D;
-  auto from = [&](int i) { return codes + (((size_t)src[i] * p.c.heads + h) << shift) * D; };
+  uint8_t *out = codes + (((size_t)to * p.c.heads + h) << shift) * D;
+  // (a piece of tokens that no page names is zero)
+  auto from = [&](int t, int at) {
+    const int u = src[t];
+    return u < 0 ? uint4{0, 0, 0, 0} : *(const uint4 *)(codes + (size_t)(uint32_t)u * (16 * D) + at);
+  };
+  uint32_t w[NP][4];
   float amax = 0.f;
   if (!isv) {
-    for (int i = tid; i < n * (D / 16); i += nt) {
-      const int t = i % n, d = i / n * 16;
+#pragma unroll
+    for (int k = 0; k < NP; ++k) {  // piece: channels 16 ch of token t, tokens side by side
+      const int i = tid + 256 * k, t = i % page, ch = i / page;
       uint4 v = uint4{0, 0, 0, 0};
-      if (src[t] >= 0) v = *(const uint4 *)(from(t) + kv8_k_at(src_slot[t], d, D));
-      *(uint4 *)(image + kv8_k_at(t, d, D)) = v;
-      const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+      if (ch < D / 16 && t < n) v = from(t, ch * 256 + src_slot[t] * 16);
+      w[k][0] = v.x, w[k][1] = v.y, w[k][2] = v.z, w[k][3] = v.w;
+    }
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
+    for (int k = 0; k < NP; ++k) {
+      const float s = src_scale[min((tid + 256 * k) % page, n - 1)];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
         float f[4];
-        kv8_decode4(u[q], f);
+        kv8_decode4(w[k][c], f);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) amax = fmaxf(amax, fabsf(f[k]) * src_scale[t]);
+        for (int e = 0; e < 4; ++e) amax = fmaxf(amax, fabsf(f[e]) * s);
       }
     }
   } else {
-    // a dword holds one channel's four tokens: one source byte each
-    const int nw = ((n + 3) >> 2) * D;
-    for (int i = tid; i < nw; i += nt) {
-      const int q = i / D, r = i % D;
-      const int d = (r >> 6) * 64 + (r & 3) * 16 + ((r >> 2) & 15);  // neighbours: the dwords of a piece
-      const int at = kv8_v_at(4 * q, d, D);
-      uint32_t w = 0;
-      if (4 * q + 3 >= n) w = *(const uint32_t *)(out + at);  // places that stay unused keep their bytes
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int t = 4 * q + k;
-        if (t >= n) break;
-        uint32_t c = 0;
-        if (src[t] >= 0) c = from(t)[kv8_v_at(src_slot[t], d, D)];
-        w = (w & ~(0xFFu << (8 * k))) | (c << (8 * k));
-        float f[4];
-        kv8_decode4(c, f);
-        amax = fmaxf(amax, fabsf(f[0]) * src_scale[t]);
+    for (int k = 0; k < NP; ++k) {  // piece: group of four tokens q, channels 64 a + 16 c + r
+      const int i = tid + 256 * k, q = i / (D / 4), ar = i % (D / 4);
+      uint4 v[4];
+      uint32_t sel[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int t = 4 * q + e;
+        v[e] = uint4{0, 0, 0, 0};
+        sel[e] = 0;
+        if (t < n) {
+          v[e] = from(t, (ar >> 4) * 1024 + (src_slot[t] >> 2) * 256 + (ar & 15) * 16);
+          sel[e] = (uint32_t)src_slot[t] & 3u;
+        }
       }
-      *(uint32_t *)(image + at) = w;
+      // bytes sel[0] of v[0], sel[1] of v[1] and so on, of each dword
+      const uint32_t p01 = (4u + sel[0]) | sel[1] << 8, p23 = (4u + sel[2]) | sel[3] << 8;
+      const uint32_t a0[4] = {v[0].x, v[0].y, v[0].z, v[0].w}, a1[4] = {v[1].x, v[1].y, v[1].z, v[1].w};
+      const uint32_t a2[4] = {v[2].x, v[2].y, v[2].z, v[2].w}, a3[4] = {v[3].x, v[3].y, v[3].z, v[3].w};
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const uint32_t lo = __builtin_amdgcn_perm(a0[c], a1[c], p01), hi = __builtin_amdgcn_perm(a2[c], a3[c], p23);
+        w[k][c] = (lo & 0xFFFFu) | hi << 16;
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < NP; ++k) {
+      const int q = (tid + 256 * k) / (D / 4);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        float f[4];
+        kv8_decode4(w[k][c], f);
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (4 * q + e < n) amax = fmaxf(amax, fabsf(f[e]) * src_scale[4 * q + e]);
+      }
     }
   }
   amax = kv8_block_max(amax, part);
-  __syncthreads();
   const int e = kv8_exponent(amax);
   const float inv = kv8_two(-e);
   // a code that is not zero is below 448 * 2^e and at least 2^-9 scales: its
   // factor is under 2^18 (the bound keeps a zero under a huge scale a zero)
   auto factor = [&](int t) { return fminf(src_scale[t] * inv, 0x1p18f); };
   if (!isv) {
-    for (int i = tid; i < n * (D / 16); i += nt) {
-      const int t = i % n, at = kv8_k_at(t, i / n * 16, D);
+#pragma unroll
+    for (int k = 0; k < NP; ++k) {
+      const int i = tid + 256 * k, t = i % page, ch = i / page;
+      if (ch >= D / 16 || t >= n) continue;
       const float f = factor(t);
-      uint4 v = *(const uint4 *)(image + at);
-      v.x = kv8_rescale4(v.x, f);
-      v.y = kv8_rescale4(v.y, f);
-      v.z = kv8_rescale4(v.z, f);
-      v.w = kv8_rescale4(v.w, f);
-      *(uint4 *)(out + at) = v;
+      *(uint4 *)(out + kv8_k_at(t, 16 * ch, D)) = uint4{kv8_rescale4(w[k][0], f), kv8_rescale4(w[k][1], f),
+                                                        kv8_rescale4(w[k][2], f), kv8_rescale4(w[k][3], f)};
     }
   } else {
-    const int nw = ((n + 3) >> 2) * (D / 4);
-    for (int i = tid; i < nw; i += nt) {
-      const int q = i / (D / 4), r = i % (D / 4);
-      const int at = kv8_v_at(4 * q, (r >> 4) * 64 + (r & 15), D);
-      uint4 v = *(const uint4 *)(image + at);
-      uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int k = 0; k < NP; ++k) {
+      const int i = tid + 256 * k, q = i / (D / 4), ar = i % (D / 4);
+      if (4 * q >= n) continue;
+      uint4 *at = (uint4 *)(out + kv8_v_at(4 * q, (ar >> 4) * 64 + (ar & 15), D));
       float f[4];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) f[k] = 4 * q + k < n ? factor(4 * q + k) : 1.0f;
+      for (int x = 0; x < 4; ++x) f[x] = 4 * q + x < n ? factor(4 * q + x) : 1.0f;
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
         float y[4];
-        kv8_decode4(u[c], y);
+        kv8_decode4(w[k][c], y);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) y[k] *= f[k];
-        u[c] = kv8_encode4(y);
+        for (int x = 0; x < 4; ++x) y[x] *= f[x];
+        w[k][c] = kv8_encode4(y);
       }
-      *(uint4 *)(out + at) = uint4{u[0], u[1], u[2], u[3]};
+      if (4 * q + 3 >= n) {  // places that stay unused keep their bytes
+        const uint4 old = *at;
+        const uint32_t keep = 0xFFFFFFFFu << (8 * (n - 4 * q));
+        w[k][0] = (w[k][0] & ~keep) | (old.x & keep);
+        w[k][1] = (w[k][1] & ~keep) | (old.y & keep);
+        w[k][2] = (w[k][2] & ~keep) | (old.z & keep);
+        w[k][3] = (w[k][3] & ~keep) | (old.w & keep);
+      }
+      *at = uint4{w[k][0], w[k][1], w[k][2], w[k][3]};
     }
   }
-  if (tid == 0) ((uint8_t *)scales)[(size_t)to * p.c.heads + h] = (uint8_t)(e + 127);
+  if (tid == 0) scales[(size_t)to * p.c.heads + h] = (uint8_t)(e + 127);
 }
 
 template <typename P>
@@ -404,17 +607,44 @@ hipError_t launch_kv8_append(const Kv8Rows &k, const Kv8Rows &v, const Kv8Pool &
                 (size_t)page * dim, stream);
 }
 
-hipError_t launch_kv8_evict(const Kv8Pool &c, const Kv8Batch &s, int dim, const int *new_table,
+Kv8EvictPlan kv8_evict_plan(const Kv8Batch &s, int max_len) {
+  Kv8EvictPlan pl = {};
+  if (max_len <= kWhole) return pl;  // in LDS
+  pl.chunks = (max_len + kChunk - 1) / kChunk;
+  pl.hist_words = (size_t)s.seqs * 3 * kBins;
+  pl.words = (size_t)s.seqs * pl.chunks * (kChunk + 2) + (size_t)s.seqs * 2;
+  return pl;
+}
+
+hipError_t launch_kv8_evict(const Kv8Pool &c, const Kv8Batch &s, int dim, int max_len, const int *new_table,
                             int new_cols, int keep, int recent, int sink, int *new_lens, int *kept,
-                            hipStream_t stream) {
-  k_kv8_select<<<dim3((unsigned)s.seqs), dim3(kSelThreads), 0, stream>>>(
-      SelectParams{c, s, keep, recent, sink, new_lens, kept});
-  if (hipError_t e = hipGetLastError()) return e;
-  const MoveParams p{c, s, new_table, new_cols, keep, kept};
-  const int page = 1 << c.shift;
+                            const Kv8EvictPlan &pl, unsigned *hist, uint32_t *words, hipStream_t stream) {
+  SelectParams sel{c, s, keep, recent, sink, max_len, new_lens, kept, pl.chunks, words, hist, nullptr, nullptr};
+  if (pl.chunks == 0) {
+    k_kv8_select<<<dim3((unsigned)s.seqs), dim3(kWholeThreads), 0, stream>>>(sel);
+    if (hipError_t e = hipGetLastError()) return e;
+  } else {
+    sel.counts = (int *)(words + (size_t)s.seqs * pl.chunks * kChunk);
+    sel.limit = (unsigned *)(sel.counts + (size_t)s.seqs * pl.chunks * 2);
+    const dim3 grid((unsigned)pl.chunks, (unsigned)s.seqs), block(kDealt);
+    for (auto k : {k_kv8_select_stage<0>, k_kv8_select_stage<1>, k_kv8_select_stage<2>, k_kv8_select_stage<3>,
+                   k_kv8_select_emit}) {
+      k<<<grid, block, 0, stream>>>(sel);
+      if (hipError_t e = hipGetLastError()) return e;
+    }
+  }
+  const MoveParams p{c, s, new_table, new_cols, keep, max_len, kept};
+  const int page = 1 << c.shift, np = page * dim / 4096;  // 16-byte pieces of a thread
   const dim3 grid((unsigned)((keep + page - 1) >> c.shift), (unsigned)(2 * c.heads), (unsigned)s.seqs);
-  return by_dim(dim, k_kv8_move<64>, k_kv8_move<128>, k_kv8_move<256>, p, grid, 256,
-                (size_t)page * dim, stream);
+  auto pick = [&](auto d) {
+    constexpr int D = decltype(d)::value;
+    return np <= 1 ? k_kv8_move<D, 1> : np == 2 ? k_kv8_move<D, 2> : np == 4 ? k_kv8_move<D, D / 32 < 4 ? D / 32 : 4>
+                                                                              : k_kv8_move<D, D / 32>;
+  };
+  auto k = dim == 64 ? pick(std::integral_constant<int, 64>{})
+                     : dim == 128 ? pick(std::integral_constant<int, 128>{}) : pick(std::integral_constant<int, 256>{});
+  k<<<grid, dim3(256), 0, stream>>>(p);
+  return hipGetLastError();
 }
 
 }  // namespace nvfp4

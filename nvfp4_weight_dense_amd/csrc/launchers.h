@@ -291,9 +291,16 @@ struct Kv8Rows {  // bf16 [rows][heads][dim], the last dimension contiguous
 
 hipError_t launch_kv8_append(const Kv8Rows &k, const Kv8Rows &v, const Kv8Pool &c, const Kv8Batch &s,
                              int dim, hipStream_t stream);
-hipError_t launch_kv8_evict(const Kv8Pool &c, const Kv8Batch &s, int dim, const int *new_table,
+// Eviction of sequences of up to max_len tokens (longer ones are held to it).
+// Scratch: `hist` (hist_words, zero on entry, left zero) and `words`.
+struct Kv8EvictPlan {
+  int chunks;  // workgroups that a sequence's tokens are dealt over; 0: one, in LDS
+  size_t hist_words, words;
+};
+Kv8EvictPlan kv8_evict_plan(const Kv8Batch &s, int max_len);
+hipError_t launch_kv8_evict(const Kv8Pool &c, const Kv8Batch &s, int dim, int max_len, const int *new_table,
                             int new_cols, int keep, int recent, int sink, int *new_lens, int *kept,
-                            hipStream_t stream);
+                            const Kv8EvictPlan &pl, unsigned *hist, uint32_t *words, hipStream_t stream);
 
 // Attention of rows over the cache: out bf16 [rows][q_heads][dim], lse fp32
 // [rows][q_heads].  `max_len` bounds the lengths (the grid's size only: a

@@ -512,3 +512,23 @@ def test_many_rounds_of_a_very_long_cache():
     table = torch.randint(0, 9, (1, -(-n // page)), generator=_gen(81), dtype=torch.int32)
     q = torch.randn(1, q_heads + 3, dim, generator=_gen(82)).bfloat16()
     _check(c, table, q, q_heads, [n], [1], accumulate=False)
+
+
+@pytest.mark.parametrize("kind", ["random", "equal", "steps", "odd"])
+def test_evict_long(kind):
+    """More tokens than one workgroup selects from, next to a sequence that is kept whole and one that is not."""
+    _say("evict long", kind)
+    dim, page, heads, lens, keep, recent, sink = 64, 128, 1, [41003, 900, 33000], 1500, 130, 5
+    test_evict(dim, page, heads, lens, keep, recent, sink, kind)
+    test_evict(dim, page, heads, [36000], 4200, 4000, 200, kind)
+
+
+def test_evict_holds_a_length_to_max_len():
+    _say("evict, max_len")
+    c = _filled(12, 1, 64, 64, 90, weights=True)
+    table, new_table = _table([400], 64, 12, 91, spare=3), _i32([[9, 10]])
+    pool, dev = ref.Pool(c), _gpu(c)
+    news, kept = pool.evict(table, [333], new_table, 100, 7, 3)
+    got = nv.kv8_evict(dev, table.cuda(), _i32([400]).cuda(), new_table.cuda(), 100, recent=7, sink=3, max_len=333)
+    assert torch.equal(got[0].cpu(), news) and torch.equal(got[1].cpu(), kept)
+    _same(pool, dev)
