@@ -1179,21 +1179,23 @@ int kv8_attention(const kv8_rows *q, int32_t q_heads, float scale, int32_t windo
                   out, lse};
   const Kv8Pool pool = kv8_pool(cache);
   const Kv8Batch seqs = kv8_batch_ref(batch);
-  const Kv8Plan pl = kv8_plan(a, pool, seqs, cache->dim);
+  Kv8Plan pl = kv8_plan(a, pool, seqs, cache->dim);
+  if (!accumulate) pl.score_cols = 0, pl.score_floats = 0;
   unsigned *counters = (unsigned *)workspace;
   float *part = (float *)((char *)workspace + align256(pl.counter_bytes));
   if (!workspace) {
     void *base = nullptr;
     if ((rc = counters_get(pl.counter_bytes / 4, &counters)) ||
-        (pl.part_floats && (rc = arena_get(pl.part_floats * 4, &base))))
+        (pl.part_floats + pl.score_floats && (rc = arena_get((pl.part_floats + pl.score_floats) * 4, &base))))
       return rc;
     part = (float *)base;
   }
+  float *scores = part + pl.part_floats;
   ProfileScope ps("kv8_attention", batch->rows, s);
-  if ((rc = hip_status(launch_kv8_attention(a, pool, seqs, cache->dim, pl, counters, part, s),
+  if ((rc = hip_status(launch_kv8_attention(a, pool, seqs, cache->dim, pl, counters, part, scores, s),
                        "kv8_attention launch")) || !accumulate)
     return rc;
-  return hip_status(launch_kv8_weights(a, pool, seqs, cache->dim, pl, part, s), "kv8_attention weights launch");
+  return hip_status(launch_kv8_weights(a, pool, seqs, cache->dim, pl, scores, s), "kv8_attention weights launch");
 }
 
 int kv8_evict(const kv8_cache *cache, const kv8_batch *batch, const int32_t *new_table, int32_t new_cols,

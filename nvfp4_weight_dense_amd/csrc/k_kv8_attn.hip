@@ -49,6 +49,8 @@ struct DecodeParams {
   int splits;         // workgroups per item at most
   float *part;        // [item]: o [split][column][D], then m and l [split][column]
   unsigned *counters;
+  float *scores;      // [seq][head][len_pad][cols], or null: not wanted
+  int len_pad, score_cols;
 };
 
 __device__ __forceinline__ bf16x8 fp8x8_to_bf16(uint32_t lo, uint32_t hi, float scale) {
@@ -206,6 +208,13 @@ __global__ __launch_bounds__(64 * kDecodeWaves) void k_kv8_decode(DecodeParams p
           seen[ct] |= (yes ? 1u : 0u) << e;
           sc[ct][e >> 2][e & 3] = yes ? sc[ct][e >> 2][e & 3] : -__builtin_inff();
         }
+      }
+    }
+    if constexpr (CT == 1) {
+      if (p.scores && n < cols) {
+        float *to = p.scores + (((size_t)b * p.c.heads + h) * p.len_pad + t0 + 4 * g) * p.score_cols + n;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) to[(16 * (e >> 2) + (e & 3)) * p.score_cols] = sc[0][e >> 2][e & 3];
       }
     }
     bf16x8 pr[CT];
@@ -851,95 +860,196 @@ __global__ __launch_bounds__(256) void k_kv8_prefill_join(PrefillParams p, int k
 
 // ---- accumulated attention weight -----------------------------------------------------
 //
-// A second pass over K with the finished log-sums: a token's sum over rows
-// and heads needs them, and K is the smaller half of the cache.  A wave
-// keeps 64 tokens of one KV head as matrix operands and takes the columns
-// (row, head) that can see them 16 at a time; a lane adds up its tokens over
-// its column of every tile, the 16 columns are joined at the end, and
-// k_kv8_weights_join adds the KV heads in order.  No atomics: a token's sum
-// has one order.
-constexpr int kWeightTokens = 256;  // of a workgroup
+// A token's sum over rows and heads needs the finished log-sums, so it is a
+// second pass.  With one tile of columns the attention leaves its scores
+// behind (fp32, 4 bytes for each of at most 16 columns against the D bytes
+// of K's codes), and k_kv8_weights_few turns them into weights.  With more,
+// k_kv8_weights_many takes K Q^T again: a wave keeps 64 tokens of one KV
+// head as matrix operands, the workgroup's columns pass through LDS 64 at a
+// time, a lane adds up its tokens over its column of every tile, and the 32
+// columns are joined at the end; where there are few tokens the columns are
+// dealt over workgroups (parts).  No atomics: a token's sum has one order.
 
 struct WeightParams {
   Kv8Attn a;
   Kv8Pool c;
   Kv8Batch s;
-  int group, len_pad;
-  float *part;  // [seq][head][len_pad]
+  int group, parts, len_pad;
+  const float *scores;  // few: [seq][head][len_pad][cols]
+  int cols;
+  float *part;          // many: [part][seq][head][len_pad]
 };
 
-template <int D>
-__global__ __launch_bounds__(256) void k_kv8_weights(WeightParams p) {
-  constexpr int U = 4;  // units of a wave
-  const int h = (int)blockIdx.y, b = (int)blockIdx.z, tid = (int)threadIdx.x, lane = tid & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int n = lane & 15, g = lane >> 4, shift = p.c.shift;
-  const Kv8Span sp = kv8_span(p.s, shift, b);
-  const int end = min(sp.len, p.a.max_len);
-  const int t0 = (int)blockIdx.x * kWeightTokens + wave * 16 * U;
-  if (t0 >= end) return;
-  const int rows = min(sp.rows, p.s.max_rows), cols = rows * p.group, pos0 = sp.len - sp.rows;
+__global__ __launch_bounds__(256) void k_kv8_weights_few(WeightParams p) {
+  const int b = (int)blockIdx.y, j = (int)(blockIdx.x * 256 + threadIdx.x);
+  const Kv8Span sp = kv8_span(p.s, p.c.shift, b);
+  const int rows = min(sp.rows, p.s.max_rows), first = sp.len - sp.rows;
+  const int lo = p.a.window ? max(first - p.a.window + 1, 0) : 0;
+  if (rows <= 0 || j < lo || j > min(first + rows, min(sp.len, p.a.max_len)) - 1) return;
+  const int id = kv8_page(p.s, p.c, b, j >> p.c.shift);
+  if (id < 0) return;
+  float sum = 0.f;
+  const float *x = p.scores + ((size_t)b * p.c.heads * p.len_pad + j) * p.cols;
+  for (int h = 0; h < p.c.heads; ++h, x += (size_t)p.len_pad * p.cols)
+    for (int c = 0; c < rows * p.group; ++c) {
+      const float z = p.a.lse[(size_t)(sp.r0 + c / p.group) * p.a.q_heads + h * p.group + c % p.group];
+      // (a row that sees nothing has -inf there and -inf scores)
+      sum += x[c] == -__builtin_inff() ? 0.f : __builtin_amdgcn_exp2f(x[c] - z * kLog2e);
+    }
+  p.c.w[((size_t)id << p.c.shift) + (j & ((1 << p.c.shift) - 1))] += sum;
+}
 
-  bf16x8 k[U][D / 32];
-  float f[U];
-  bool valid[U];
+constexpr int kWeightWaves = 8, kWeightTokens = 64 * kWeightWaves;  // of a workgroup
+
+template <int D>
+__global__ __launch_bounds__(64 * kWeightWaves, 2) void k_kv8_weights_many(WeightParams p) {
+  constexpr int KT = D / 16, kOps = 2 * KT;                        // operands of 32 columns, of 64
+  constexpr int kMine = (kOps + kWeightWaves - 1) / kWeightWaves;  // brought by a wave
+  __shared__ uint4 qbuf[2][kOps][64];
+  const int h = (int)blockIdx.y, b = (int)blockIdx.z / p.parts, piece = (int)blockIdx.z % p.parts;
+  const int tid = (int)threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int n = lane & 31, half = lane >> 5, shift = p.c.shift;
+  const Kv8Span sp = kv8_span(p.s, shift, b);
+  const int end = min(sp.len, p.a.max_len), wg0 = (int)blockIdx.x * kWeightTokens;
+  if (wg0 >= end) return;
+  const int rows = min(sp.rows, p.s.max_rows), all = rows * p.group, pos0 = sp.len - sp.rows;
+  const int t0 = wg0 + wave * 64;
+
+  // this wave's tokens as operands: row m of step u is token t0 + 32 u + m
+  const float cs = fmaxf(fabsf(p.a.scale) * kLog2e, 1.1754944e-38f);  // its sign goes to q
+  const uint32_t flip = p.a.scale < 0.f ? 0x80008000u : 0u;
+  bf16x8 k[2][KT];
+  uint32_t valid = 0;  // bit i: unit i has a page
 #pragma unroll
-  for (int u = 0; u < U; ++u) {
-    const int t = t0 + 16 * u;
+  for (int i = 0; i < 4; ++i) {
+    const int t = t0 + 16 * i;
     const int id = t < end ? kv8_page(p.s, p.c, b, t >> shift) : -1;
-    const size_t ph = (size_t)max(id, 0) * p.c.heads + h;
-    const int in = (t >> 4) & ((1 << (shift - 4)) - 1);
-    valid[u] = id >= 0;
-    f[u] = id >= 0 ? p.a.scale * kLog2e * kv8_scale(p.c.ks[ph]) : 0.f;
-    const uint4 *src = (const uint4 *)(p.c.k + ((ph << (shift - 4)) + in) * (16 * D)) + lane;
+    valid |= (id >= 0 ? 1u : 0u) << i;
+  }
+  valid = __builtin_amdgcn_readfirstlane(valid);
 #pragma unroll
-    for (int t4 = 0; t4 < D / 64; ++t4) {
-      const uint4 w = src[64 * t4];
-      k[u][2 * t4] = fp8x8_to_bf16(w.x, w.y, 1.0f);
-      k[u][2 * t4 + 1] = fp8x8_to_bf16(w.z, w.w, 1.0f);
+  for (int u = 0; u < 2; ++u) {
+    const int t = t0 + 32 * u + (n & 16);
+    const int id = t < end ? max(kv8_page(p.s, p.c, b, t >> shift), 0) : 0;
+    const size_t ph = (size_t)id * p.c.heads + h;
+    const float f = kv8_scale(p.c.ks[ph]);
+    const uint8_t *src = p.c.k + ((ph << (shift - 4)) + ((t >> 4) & ((1 << (shift - 4)) - 1))) * (16 * D) +
+                         (n & 15) * 16 + half * 8;
+#pragma unroll
+    for (int c = 0; c < KT; ++c) {
+      const uint2 w = *(const uint2 *)(src + c * 256);
+      k[u][c] = fp8x8_to_bf16(w.x, w.y, f);
     }
   }
 
-  // rows that see a token of the wave
-  const int last = min(t0 + 16 * U, end) - 1;
-  const int row0 = max(t0 - pos0, 0);
-  const int row1 = p.a.window ? min(rows, last + p.a.window - pos0) : rows;
-  float sum[U][4] = {};
-  for (int c0 = row0 * p.group; c0 < row1 * p.group; c0 += 16) {
-    const int c = c0 + n, i = c / p.group;
-    const bool in = c < cols;
-    const int64_t r = (int64_t)(sp.r0 + (in ? i : 0)), u0 = h * p.group + (in ? c % p.group : 0);
-    const __bf16 *qr = (const __bf16 *)p.a.q.ptr + r * p.a.q.row_stride + u0 * p.a.q.head_stride;
-    bf16x8 q[D / 32];
+  // the workgroup's columns, in tiles of 64: those of rows that see a token of it
+  const int wg_last = min(wg0 + kWeightTokens, end) - 1;
+  const int row0 = min(max(wg0 - pos0, 0), rows);
+  const int row1 = p.a.window ? max(min(rows, wg_last + p.a.window - pos0), row0) : rows;
+  int tile0 = row0 * p.group >> 6, tile1 = (row1 * p.group + 63) >> 6;
+  const int per = (tile1 - tile0 + p.parts - 1) / p.parts;
+  tile0 += piece * per;
+  tile1 = min(tile1, tile0 + per);
+
+  // column c of tile `tile`: lane n of each half (a column past the last repeats it, unseen)
+  auto q_at = [&](int c, int &i) {
+    c = min(c, all - 1);
+    i = c / p.group;
+    return (int64_t)(sp.r0 + i) * p.a.q.row_stride + (int64_t)(h * p.group + c - i * p.group) * p.a.q.head_stride;
+  };
+  uint4 qr[kMine];
+  float z[2], z_next[2];
+  int row[2], row_next[2];
+  auto load = [&](int tile) {
 #pragma unroll
-    for (int t = 0; t < D / 64; ++t)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) q[2 * t + e] = as_bf16x8(*(const uint4 *)(qr + 64 * t + 16 * g + 8 * e));
-    const float z = p.a.lse[r * p.a.q_heads + u0] * kLog2e;
-    const int pos = pos0 + i;
-    const int hi = in ? min(pos, end - 1) : -1, lo = p.a.window ? max(pos - p.a.window + 1, 0) : 0;
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      f32x4 s = {};
-#pragma unroll
-      for (int t = 0; t < D / 32; ++t) s = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k[u][t], q[t], s, 0, 0, 0);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int j = t0 + 16 * u + 4 * g + e;
-        const float x = __builtin_amdgcn_exp2f(fmaf(s[e], f[u], -z));
-        sum[u][e] += (valid[u] & (j >= lo) & (j <= hi)) ? x : 0.f;
+    for (int e = 0; e < kMine; ++e) {
+      const int op = wave * kMine + e;  // 32 (op / KT) + n of the tile, channels 16 (op % KT) + 8 half
+      int i;
+      if (op < kOps) {
+        const __bf16 *src = (const __bf16 *)p.a.q.ptr + q_at(tile * 64 + op / KT * 32 + n, i) + op % KT * 16 + 8 * half;
+        qr[e] = *(const uint4 *)src;
       }
     }
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int c = tile * 64 + 32 * u + n;
+      q_at(c, row_next[u]);
+      const int last = min(c, all - 1);
+      z_next[u] = p.a.lse[(int64_t)(sp.r0 + row_next[u]) * p.a.q_heads + h * p.group + last - row_next[u] * p.group] *
+                  kLog2e;
+      if (c >= all) row_next[u] = -1 - (1 << 29);  // before every token
+    }
+  };
+  auto store = [&](int buf) {
+#pragma unroll
+    for (int e = 0; e < kMine; ++e) {
+      const int op = wave * kMine + e;
+      if (op < kOps) qbuf[buf][op][lane] = uint4{qr[e].x ^ flip, qr[e].y ^ flip, qr[e].z ^ flip, qr[e].w ^ flip};
+    }
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      z[u] = z_next[u];
+      row[u] = row_next[u];
+    }
+  };
+
+  float sum[2][16] = {};
+  if (tile0 < tile1) {
+    load(tile0);
+    store(0);
   }
-  float *out = p.part + ((size_t)b * p.c.heads + h) * p.len_pad;
+  lds_barrier();
+  for (int tile = tile0; tile < tile1; ++tile) {
+    const int buf = (tile - tile0) & 1;
+    if (tile + 1 < tile1) load(tile + 1);
+    const int first = pos0 + tile * 64 / p.group, final = pos0 + min(tile * 64 + 63, all - 1) / p.group;
+    // some column sees a token of the wave; every column sees all of them
+    const bool some = t0 < end && final >= t0 && (!p.a.window || first - p.a.window < t0 + 63);
+    const bool whole = valid == 15u && first >= t0 + 63 && t0 + 64 <= end && tile * 64 + 64 <= all &&
+                       (!p.a.window || final - p.a.window < t0);
+    if (some) {
 #pragma unroll
-  for (int u = 0; u < U; ++u)
+      for (int c = 0; c < 2; ++c) {  // 32 columns
+        f32x16 s[2];
+        const f32x16 zero = {};
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      float x = sum[u][e];
+        for (int t = 0; t < KT; ++t) {
+          const bf16x8 q = as_bf16x8(qbuf[buf][c * KT + t][lane]);
 #pragma unroll
-      for (int o = 8; o > 0; o >>= 1) x += __shfl_xor(x, o);
-      if (n == 0) out[t0 + 16 * u + 4 * g + e] = x;
+          for (int u = 0; u < 2; ++u)
+            s[u] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k[u][t], q, t ? s[u] : zero, 0, 0, 0);
+        }
+        if (whole) {
+#pragma unroll
+          for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) sum[u][r] += __builtin_amdgcn_exp2f(fmaf(s[u][r], cs, -z[c]));
+        } else {
+          const int pos = pos0 + row[c], hi = min(pos, end - 1), lo = p.a.window ? pos - p.a.window + 1 : 0;
+#pragma unroll
+          for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {
+              const int j = t0 + 32 * u + (r & 3) + 8 * (r >> 2) + 4 * half;
+              const bool yes = ((valid >> (2 * u + (r >> 3)) & 1u) != 0) & (j >= lo) & (j <= hi);
+              sum[u][r] += yes ? __builtin_amdgcn_exp2f(fmaf(s[u][r], cs, -z[c])) : 0.f;
+            }
+        }
+      }
+    }
+    if (tile + 1 < tile1) store(buf ^ 1);
+    lds_barrier();
+  }
+  float *out = p.part + (((size_t)piece * p.s.seqs + b) * p.c.heads + h) * p.len_pad;
+#pragma unroll
+  for (int u = 0; u < 2; ++u)
+#pragma unroll
+    for (int r = 0; r < 16; ++r) {
+      float x = sum[u][r];
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) x += __shfl_xor(x, o);
+      if (n == 0) out[t0 + 32 * u + (r & 3) + 8 * (r >> 2) + 4 * half] = x;
     }
 }
 
@@ -949,9 +1059,10 @@ __global__ __launch_bounds__(256) void k_kv8_weights_join(WeightParams p) {
   if (j >= min(sp.len, p.a.max_len)) return;
   const int id = kv8_page(p.s, p.c, b, j >> p.c.shift);
   if (id < 0) return;
-  const float *part = p.part + (size_t)b * p.c.heads * p.len_pad + j;
   float sum = 0.f;
-  for (int h = 0; h < p.c.heads; ++h) sum += part[(size_t)h * p.len_pad];
+  for (int i = 0; i < p.parts; ++i)
+    for (int h = 0; h < p.c.heads; ++h)
+      sum += p.part[(((size_t)i * p.s.seqs + b) * p.c.heads + h) * p.len_pad + j];
   p.c.w[((size_t)id << p.c.shift) + (j & ((1 << p.c.shift) - 1))] += sum;
 }
 
@@ -971,7 +1082,10 @@ size_t kv8_part_bound(const Kv8Attn &a, const Kv8Pool &c, const Kv8Batch &s, int
   const Kv8Plan pl = kv8_plan(a, c, s, dim);
   const size_t few = (2 * kDecodeGroups + (size_t)s.seqs * c.heads) * (size_t)kv8_few_cols(dim);
   const size_t many = pl.few ? 0 : (size_t)kManyGroups * kv8_many_cols(dim);
-  return std::max(pl.part_floats, std::max(few, many) * (size_t)(dim + 2));
+  size_t floats = std::max(pl.part_floats, std::max(few, many) * (size_t)(dim + 2));
+  // 16 columns' scores, or kManyGroups parts of kWeightTokens
+  if (c.w) floats += std::max((size_t)s.seqs * c.heads * pl.len_pad * 16, (size_t)kManyGroups * kWeightTokens * 2);
+  return floats;
 }
 
 Kv8Plan kv8_plan(const Kv8Attn &a, const Kv8Pool &c, const Kv8Batch &s, int dim) {
@@ -1009,14 +1123,27 @@ Kv8Plan kv8_plan(const Kv8Attn &a, const Kv8Pool &c, const Kv8Batch &s, int dim)
     if (pl.splits > 1) pl.part_floats = (size_t)items * pl.splits * kc * (dim + 2);
   }
   pl.len_pad = (a.max_len + kWeightTokens - 1) / kWeightTokens * kWeightTokens;
-  if (c.w) pl.part_floats = std::max(pl.part_floats, (size_t)s.seqs * c.heads * pl.len_pad);
+  pl.parts = 1;
+  if (c.w) {
+    const size_t tokens = (size_t)s.seqs * c.heads * pl.len_pad;
+    if (pl.few && pl.ct == 1) {
+      pl.score_cols = (int)cols;
+      pl.score_floats = tokens * (size_t)cols;
+    } else {
+      // two workgroups a CU where the columns allow it
+      const int64_t groups = (int64_t)s.seqs * c.heads * (pl.len_pad / kWeightTokens);
+      pl.parts = (int)std::max<int64_t>(std::min<int64_t>(kManyGroups / std::max<int64_t>(groups, 1), cols / 256), 1);
+      pl.score_floats = tokens * (size_t)pl.parts;
+    }
+  }
   return pl;
 }
 
 hipError_t launch_kv8_attention(const Kv8Attn &a, const Kv8Pool &c, const Kv8Batch &s, int dim,
-                                const Kv8Plan &pl, unsigned *counters, float *part, hipStream_t stream) {
+                                const Kv8Plan &pl, unsigned *counters, float *part, float *scores, hipStream_t stream) {
   if (pl.few) {
-    const DecodeParams p{a, c, s, pl.group, pl.blocks, pl.spw, pl.rounds, pl.splits, part, counters};
+    const DecodeParams p{a, c, s, pl.group, pl.blocks, pl.spw, pl.rounds, pl.splits, part, counters,
+                         pl.score_cols ? scores : nullptr, pl.len_pad, pl.score_cols};
     const dim3 grid((unsigned)pl.splits, (unsigned)(c.heads * pl.blocks), (unsigned)s.seqs);
     auto k = dim == 64 ? (pl.ct == 1 ? k_kv8_decode<64, 1> : pl.ct == 2 ? k_kv8_decode<64, 2> : k_kv8_decode<64, 4>)
              : dim == 128
@@ -1038,15 +1165,19 @@ hipError_t launch_kv8_attention(const Kv8Attn &a, const Kv8Pool &c, const Kv8Bat
 }
 
 hipError_t launch_kv8_weights(const Kv8Attn &a, const Kv8Pool &c, const Kv8Batch &s, int dim,
-                              const Kv8Plan &pl, float *part, hipStream_t stream) {
+                              const Kv8Plan &pl, float *scores, hipStream_t stream) {
   if (a.max_len <= 0) return hipSuccess;
-  const WeightParams p{a, c, s, pl.group, pl.len_pad, part};
-  const unsigned blocks = (unsigned)(pl.len_pad / kWeightTokens);
-  const dim3 grid(blocks, (unsigned)c.heads, (unsigned)s.seqs);
-  auto k = dim == 64 ? k_kv8_weights<64> : dim == 128 ? k_kv8_weights<128> : k_kv8_weights<256>;
-  k<<<grid, dim3(256), 0, stream>>>(p);
+  const WeightParams p{a, c, s, pl.group, pl.parts, pl.len_pad, scores, pl.score_cols, scores};
+  const dim3 tokens((unsigned)((a.max_len + 255) / 256), (unsigned)s.seqs);
+  if (pl.score_cols) {
+    k_kv8_weights_few<<<tokens, dim3(256), 0, stream>>>(p);
+    return hipGetLastError();
+  }
+  const dim3 grid((unsigned)(pl.len_pad / kWeightTokens), (unsigned)c.heads, (unsigned)(s.seqs * pl.parts));
+  auto k = dim == 64 ? k_kv8_weights_many<64> : dim == 128 ? k_kv8_weights_many<128> : k_kv8_weights_many<256>;
+  k<<<grid, dim3(64 * kWeightWaves), 0, stream>>>(p);
   if (hipError_t e = hipGetLastError()) return e;
-  k_kv8_weights_join<<<dim3(blocks, (unsigned)s.seqs), dim3(256), 0, stream>>>(p);
+  k_kv8_weights_join<<<tokens, dim3(256), 0, stream>>>(p);
   return hipGetLastError();
 }
 

@@ -319,20 +319,23 @@ struct Kv8Plan {
   int ct, spw, rounds;  // its 16-column tiles, a wave's 32-token steps at a time, and times
   int blocks;   // column blocks of a sequence (many rows)
   int splits;   // parts of a sequence's tokens
-  int len_pad;  // tokens of a part of the weights pass
-  size_t counter_bytes, part_floats;
+  // the weights pass: tokens of a sequence (rounded up); columns whose scores
+  // the attention leaves for it (0: it takes K again), parts of the columns
+  int len_pad, score_cols, parts;
+  size_t counter_bytes, part_floats, score_floats;
 };
 constexpr int kKv8MaxItems = 65536;  // arrival counters
 Kv8Plan kv8_plan(const Kv8Attn &a, const Kv8Pool &c, const Kv8Batch &s, int dim);
 // part_floats of any call with these sizes or smaller ones and any window
 size_t kv8_part_bound(const Kv8Attn &a, const Kv8Pool &c, const Kv8Batch &s, int dim);
 // `counters` (counter_bytes, zero on entry, left zero) and `part`
-// (part_floats) as planned.
+// (part_floats) as planned; `scores` (score_floats), or null where no weights
+// are wanted.
 hipError_t launch_kv8_attention(const Kv8Attn &a, const Kv8Pool &c, const Kv8Batch &s, int dim,
-                                const Kv8Plan &pl, unsigned *counters, float *part, hipStream_t stream);
+                                const Kv8Plan &pl, unsigned *counters, float *part, float *scores, hipStream_t stream);
 // Adds each visible token's attention weight, summed over rows and query
-// heads, to c.w, from the lse that the attention wrote.
+// heads, to c.w, from the lse (and scores) that the attention wrote.
 hipError_t launch_kv8_weights(const Kv8Attn &a, const Kv8Pool &c, const Kv8Batch &s, int dim,
-                              const Kv8Plan &pl, float *part, hipStream_t stream);
+                              const Kv8Plan &pl, float *scores, hipStream_t stream);
 
 }  // namespace nvfp4
