@@ -49,7 +49,7 @@ struct DecodeParams {
   int splits;         // workgroups per item at most
   float *part;        // [item]: o [split][column][D], then m and l [split][column]
   unsigned *counters;
-  float *scores;      // [seq][head][len_pad][cols], or null: not wanted
+  float *scores;      // [seq][head][column][len_pad], or null: not wanted
   int len_pad, score_cols;
 };
 
@@ -212,9 +212,9 @@ __global__ __launch_bounds__(64 * kDecodeWaves) void k_kv8_decode(DecodeParams p
     }
     if constexpr (CT == 1) {
       if (p.scores && n < cols) {
-        float *to = p.scores + (((size_t)b * p.c.heads + h) * p.len_pad + t0 + 4 * g) * p.score_cols + n;
+        float *to = p.scores + (((size_t)b * p.c.heads + h) * p.score_cols + n) * p.len_pad + t0 + 4 * g;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) to[(16 * (e >> 2) + (e & 3)) * p.score_cols] = sc[0][e >> 2][e & 3];
+        for (int u = 0; u < 2; ++u) *(f32x4 *)(to + 16 * u) = sc[0][u];
       }
     }
     bf16x8 pr[CT];
@@ -875,7 +875,7 @@ struct WeightParams {
   Kv8Pool c;
   Kv8Batch s;
   int group, parts, len_pad;
-  const float *scores;  // few: [seq][head][len_pad][cols]
+  const float *scores;  // few: [seq][head][column][len_pad]
   int cols;
   float *part;          // many: [part][seq][head][len_pad]
 };
@@ -889,12 +889,22 @@ __global__ __launch_bounds__(256) void k_kv8_weights_few(WeightParams p) {
   const int id = kv8_page(p.s, p.c, b, j >> p.c.shift);
   if (id < 0) return;
   float sum = 0.f;
-  const float *x = p.scores + ((size_t)b * p.c.heads * p.len_pad + j) * p.cols;
-  for (int h = 0; h < p.c.heads; ++h, x += (size_t)p.len_pad * p.cols)
-    for (int c = 0; c < rows * p.group; ++c) {
-      const float z = p.a.lse[(size_t)(sp.r0 + c / p.group) * p.a.q_heads + h * p.group + c % p.group];
-      // (a row that sees nothing has -inf there and -inf scores)
-      sum += x[c] == -__builtin_inff() ? 0.f : __builtin_amdgcn_exp2f(x[c] - z * kLog2e);
+  const float *x = p.scores + (size_t)b * p.c.heads * p.cols * p.len_pad + j;
+  const float *z = p.a.lse + (size_t)sp.r0 * p.a.q_heads;
+  const int cols = rows * p.group;
+  for (int h = 0; h < p.c.heads; ++h, x += (size_t)p.cols * p.len_pad, z += p.group)
+    for (int c0 = 0; c0 < cols; c0 += 8) {  // eight loads at a time
+      float y[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) y[k] = c0 + k < cols ? x[(size_t)(c0 + k) * p.len_pad] : -__builtin_inff();
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int c = min(c0 + k, cols - 1), i = c / p.group;
+        // (a row that sees nothing has -inf there and -inf scores)
+        sum += y[k] == -__builtin_inff()
+                   ? 0.f
+                   : __builtin_amdgcn_exp2f(y[k] - z[(size_t)i * p.a.q_heads + c - i * p.group] * kLog2e);
+      }
     }
   p.c.w[((size_t)id << p.c.shift) + (j & ((1 << p.c.shift) - 1))] += sum;
 }
@@ -952,33 +962,38 @@ __global__ __launch_bounds__(64 * kWeightWaves, 2) void k_kv8_weights_many(Weigh
   tile0 += piece * per;
   tile1 = min(tile1, tile0 + per);
 
-  // column c of tile `tile`: lane n of each half (a column past the last repeats it, unseen)
-  auto q_at = [&](int c, int &i) {
-    c = min(c, all - 1);
-    i = c / p.group;
-    return (int64_t)(sp.r0 + i) * p.a.q.row_stride + (int64_t)(h * p.group + c - i * p.group) * p.a.q.head_stride;
-  };
+  // the lane's columns of the next tile to load, 64 tile + n and 32 on: row and
+  // head, kept by steps (a division of each would cost more than the products)
+  int row_at = (tile0 * 64 + n) / p.group, head_at = (tile0 * 64 + n) % p.group;
+  const int row64 = 64 / p.group, head64 = 64 % p.group, row32 = 32 / p.group, head32 = 32 % p.group;
   uint4 qr[kMine];
   float z[2], z_next[2];
   int row[2], row_next[2];
-  auto load = [&](int tile) {
-#pragma unroll
-    for (int e = 0; e < kMine; ++e) {
-      const int op = wave * kMine + e;  // 32 (op / KT) + n of the tile, channels 16 (op % KT) + 8 half
-      int i;
-      if (op < kOps) {
-        const __bf16 *src = (const __bf16 *)p.a.q.ptr + q_at(tile * 64 + op / KT * 32 + n, i) + op % KT * 16 + 8 * half;
-        qr[e] = *(const uint4 *)src;
-      }
-    }
+  auto load = [&]() {
+    const __bf16 *src[2];
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-      const int c = tile * 64 + 32 * u + n;
-      q_at(c, row_next[u]);
-      const int last = min(c, all - 1);
-      z_next[u] = p.a.lse[(int64_t)(sp.r0 + row_next[u]) * p.a.q_heads + h * p.group + last - row_next[u] * p.group] *
-                  kLog2e;
-      if (c >= all) row_next[u] = -1 - (1 << 29);  // before every token
+      int i = row_at + (u ? row32 : 0), g = head_at + (u ? head32 : 0);
+      if (g >= p.group) {
+        g -= p.group;
+        ++i;
+      }
+      // (a column past the last stands for one of the last row, before every token)
+      row_next[u] = i < rows ? i : -(1 << 29);
+      const int64_t r = sp.r0 + min(i, rows - 1), head = h * p.group + g;
+      src[u] = (const __bf16 *)p.a.q.ptr + r * p.a.q.row_stride + head * p.a.q.head_stride + 8 * half;
+      z_next[u] = p.a.lse[r * p.a.q_heads + head] * kLog2e;
+    }
+#pragma unroll
+    for (int e = 0; e < kMine; ++e) {
+      const int op = wave * kMine + e;  // column 32 (op / KT) + n, channels 16 (op % KT) + 8 half
+      if (op < kOps) qr[e] = *(const uint4 *)((op / KT ? src[1] : src[0]) + op % KT * 16);
+    }
+    row_at += row64;
+    head_at += head64;
+    if (head_at >= p.group) {
+      head_at -= p.group;
+      ++row_at;
     }
   };
   auto store = [&](int buf) {
@@ -996,13 +1011,13 @@ __global__ __launch_bounds__(64 * kWeightWaves, 2) void k_kv8_weights_many(Weigh
 
   float sum[2][16] = {};
   if (tile0 < tile1) {
-    load(tile0);
+    load();
     store(0);
   }
   lds_barrier();
   for (int tile = tile0; tile < tile1; ++tile) {
     const int buf = (tile - tile0) & 1;
-    if (tile + 1 < tile1) load(tile + 1);
+    if (tile + 1 < tile1) load();
     const int first = pos0 + tile * 64 / p.group, final = pos0 + min(tile * 64 + 63, all - 1) / p.group;
     // some column sees a token of the wave; every column sees all of them
     const bool some = t0 < end && final >= t0 && (!p.a.window || first - p.a.window < t0 + 63);
@@ -1060,9 +1075,11 @@ __global__ __launch_bounds__(256) void k_kv8_weights_join(WeightParams p) {
   const int id = kv8_page(p.s, p.c, b, j >> p.c.shift);
   if (id < 0) return;
   float sum = 0.f;
-  for (int i = 0; i < p.parts; ++i)
-    for (int h = 0; h < p.c.heads; ++h)
-      sum += p.part[(((size_t)i * p.s.seqs + b) * p.c.heads + h) * p.len_pad + j];
+  for (int i = 0; i < p.parts; ++i) {
+    const float *x = p.part + ((size_t)i * p.s.seqs + b) * p.c.heads * p.len_pad + j;
+#pragma unroll 8
+    for (int h = 0; h < p.c.heads; ++h) sum += x[(size_t)h * p.len_pad];
+  }
   p.c.w[((size_t)id << p.c.shift) + (j & ((1 << p.c.shift) - 1))] += sum;
 }
 
