@@ -663,37 +663,51 @@ _pack_batch = struct.Struct("@3P5i4x").pack
 _pack_rows = struct.Struct("@P2q").pack
 
 
+_U8, _I32, _F32, _BF16 = torch.uint8, torch.int32, torch.float32, torch.bfloat16
+
+
+def _kv8_refuse(c: KV8Cache):
+    """Names what is wrong with a cache."""
+    k, w = c.k_codes, c.weights
+    if k.dtype != _U8 or k.dim() != 4 or not k.is_contiguous():
+        raise ValueError("k_codes: expected a contiguous uint8 [pages, heads, page, dim] tensor")
+    pages, heads, page, _ = k.shape
+    if c.v_codes.dtype != _U8 or c.v_codes.shape != k.shape or not c.v_codes.is_contiguous():
+        raise ValueError("v_codes: expected a contiguous uint8 tensor of k_codes' shape")
+    for t, nm in ((c.k_scales, "k_scales"), (c.v_scales, "v_scales")):
+        if t.dtype != _U8 or t.shape != (pages, heads) or not t.is_contiguous():
+            raise ValueError(f"{nm}: expected a contiguous uint8 [{pages}, {heads}] tensor")
+    if w is not None and (w.dtype != _F32 or w.shape != (pages, page) or not w.is_contiguous()):
+        raise ValueError(f"weights: expected a contiguous float32 [{pages}, {page}] tensor")
+    raise ValueError("cache tensors on several devices: expected one device")
+
+
 def _ckv8(c: KV8Cache):
     """(packed kv8_cache, heads, page, dim, device index)"""
     k, v, ks, vs, w = c.k_codes, c.v_codes, c.k_scales, c.v_scales, c.weights
-    if k.dtype != torch.uint8 or k.dim() != 4 or not k.is_contiguous():
-        raise ValueError("k_codes: expected a contiguous uint8 [pages, heads, page, dim] tensor")
-    shape = k.shape
+    shape, dev = k.shape, k.get_device()
+    if not (len(shape) == 4 and k.dtype is _U8 and v.dtype is _U8 and ks.dtype is _U8 and vs.dtype is _U8
+            and v.shape == shape and ks.shape == vs.shape == shape[:2]
+            and k.is_contiguous() and v.is_contiguous() and ks.is_contiguous() and vs.is_contiguous()
+            and v.get_device() == ks.get_device() == vs.get_device() == dev):
+        _kv8_refuse(c)
     pages, heads, page, dim = shape
-    if v.dtype != torch.uint8 or v.shape != shape or not v.is_contiguous():
-        raise ValueError("v_codes: expected a contiguous uint8 tensor of k_codes' shape")
-    for t, nm in ((ks, "k_scales"), (vs, "v_scales")):
-        if t.dtype != torch.uint8 or t.shape != (pages, heads) or not t.is_contiguous():
-            raise ValueError(f"{nm}: expected a contiguous uint8 [{pages}, {heads}] tensor")
-    dev = k.get_device()
+    at = 0
     if w is not None:
-        if w.dtype != torch.float32 or w.shape != (pages, page) or not w.is_contiguous():
-            raise ValueError(f"weights: expected a contiguous float32 [{pages}, {page}] tensor")
-        if w.get_device() != dev:
-            raise ValueError("cache tensors on several devices: expected one device")
-    if not (v.get_device() == ks.get_device() == vs.get_device() == dev):
-        raise ValueError("cache tensors on several devices: expected one device")
-    return _pack_cache(k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr(),
-                       0 if w is None else w.data_ptr(), pages, heads, dim, page), heads, page, dim, dev
+        if w.dtype is not _F32 or w.shape != (pages, page) or not w.is_contiguous() or w.get_device() != dev:
+            _kv8_refuse(c)
+        at = w.data_ptr()
+    return _pack_cache(k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr(), at, pages, heads, dim,
+                       page), heads, page, dim, dev
 
 
 def _ckv8_rows(x: torch.Tensor, name: str, dim: int, heads: int | None = None) -> bytes:
     """A bf16 [rows, heads, dim] array with strides of whole 16-byte pieces."""
-    if not isinstance(x, torch.Tensor) or x.dtype != torch.bfloat16 or x.dim() != 3:
+    if not isinstance(x, torch.Tensor) or x.dtype is not _BF16 or x.dim() != 3:
         raise ValueError(f"{name}: expected a 3-D bfloat16 tensor [rows, heads, dim]")
-    shape = x.shape
-    if shape[2] != dim or (heads is not None and shape[1] != heads):
-        raise ValueError(f"{name}: has shape {tuple(shape)}, the cache has {heads or 'n'} heads of size {dim}")
+    _, h, d = x.shape
+    if d != dim or (heads is not None and h != heads):
+        raise ValueError(f"{name}: has shape {tuple(x.shape)}, the cache has {heads or 'n'} heads of size {dim}")
     rs, hs, ds = x.stride()
     if ds != 1 or rs % 8 or hs % 8:
         raise ValueError(f"{name}: strides {x.stride()}: expected the last 1, the others multiples of 8")
@@ -702,19 +716,19 @@ def _ckv8_rows(x: torch.Tensor, name: str, dim: int, heads: int | None = None) -
 
 def _ckv8_batch(table, lens, starts, rows, max_rows, max_len, page):
     """(packed kv8_batch, seqs)"""
-    if table.dtype != torch.int32 or table.dim() != 2 or not table.is_contiguous():
+    if table.dtype is not _I32 or table.dim() != 2 or not table.is_contiguous():
         raise ValueError("table: expected a contiguous int32 [seqs, cols] tensor")
     seqs, cols = table.shape
-    if lens.dtype != torch.int32 or lens.shape != (seqs,) or not lens.is_contiguous():
+    if lens.dtype is not _I32 or lens.shape != (seqs,) or not lens.is_contiguous():
         raise ValueError(f"lens: expected a contiguous int32 [{seqs}] tensor")
     at = 0
     if starts is not None:
-        if starts.dtype != torch.int32 or starts.shape != (seqs + 1,) or not starts.is_contiguous():
+        if starts.dtype is not _I32 or starts.shape != (seqs + 1,) or not starts.is_contiguous():
             raise ValueError(f"starts: expected a contiguous int32 [{seqs + 1}] tensor")
         at = starts.data_ptr()
         max_rows = rows if max_rows is None else int(max_rows)
     else:
-        max_rows = rows // max(seqs, 1)
+        max_rows = rows // seqs if seqs else 0
     return _pack_batch(table.data_ptr(), lens.data_ptr(), at, seqs, cols, rows, max_rows,
                        cols * page if max_len is None else int(max_len)), seqs
 

@@ -60,11 +60,6 @@ __device__ __forceinline__ bf16x8 fp8x8_to_bf16(uint32_t lo, uint32_t hi, float 
   const bf16x2 d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, scale, true);
   return bf16x8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
 }
-typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-// 16 bytes that this call reads once: kept from displacing reused lines in the caches
-__device__ __forceinline__ uint4 load_once(const uint4 *p) {
-  return __builtin_bit_cast(uint4, __builtin_nontemporal_load((const u32x4 *)p));
-}
 __device__ __forceinline__ void st16_coherent(__amdgpu_buffer_rsrc_t r, uint32_t off, f32x4 v) {
   __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), r, off, 0, kCoherent);
 }

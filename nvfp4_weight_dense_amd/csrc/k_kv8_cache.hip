@@ -24,8 +24,22 @@ struct AppendParams {
   Kv8Batch s;
 };
 
-__device__ __forceinline__ void load8(const __bf16 *p, float *f) {
-  const uint4 v = *(const uint4 *)p;
+typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
+
+// the larger of two packed pairs of bf16 magnitudes (as bits, NaN above infinity)
+__device__ __forceinline__ uint32_t max_bits(uint32_t m, uint32_t v) {
+  return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2, m),
+                                                                __builtin_bit_cast(u16x2, v & 0x7FFF7FFFu)));
+}
+// four bf16 (two packed pairs) over a power of two -> E4M3 bytes, nearest-even, for magnitudes up to 448 scales
+__device__ __forceinline__ uint32_t encode_pairs(uint32_t a, uint32_t b, float scale) {
+  s16x2 w = {0, 0};
+  w = __builtin_amdgcn_cvt_scalef32_pk_fp8_bf16(w, __builtin_bit_cast(bf16x2, a), scale, false);
+  w = __builtin_amdgcn_cvt_scalef32_pk_fp8_bf16(w, __builtin_bit_cast(bf16x2, b), scale, true);
+  return __builtin_bit_cast(uint32_t, w);
+}
+// eight bf16 as fp32
+__device__ __forceinline__ void widen8(uint4 v, float *f) {
   const uint32_t u[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -34,17 +48,20 @@ __device__ __forceinline__ void load8(const __bf16 *p, float *f) {
   }
 }
 
-// One workgroup: one page that a sequence's new tokens touch, one KV head,
-// K or V.  Reads the new tokens twice (amax, then codes; the second time
-// from the caches).  V's codes are put together in LDS, since one 16-byte
-// piece holds four tokens; its pieces that also hold older tokens, or
-// places not yet used, take those bytes from the page.
-template <int D>
-__global__ void k_kv8_append(AppendParams p) {
+// One workgroup of T threads: one page that a sequence's new tokens touch,
+// one KV head, K or V.  Bound by the bytes (4 read for each element of K and
+// V, 2 written): a thread takes all its pieces into registers at once -- of K
+// 2 NU times 16 channels of a token, of V NU times 8 channels of a group of
+// four tokens, whose codes of a channel are one dword -- finds the largest
+// magnitude with the workgroup, and writes codes.  V's codes are put in order
+// in LDS; its 16-byte pieces that also hold older tokens, or places not yet
+// used, take those bytes from the page.
+template <int D, int NU, int T>
+__global__ __launch_bounds__(T) void k_kv8_append(AppendParams p) {
   extern __shared__ __align__(16) uint8_t image[];
-  __shared__ float part[4];
+  __shared__ unsigned part[4];
   const int b = (int)blockIdx.z, h = (int)blockIdx.y >> 1, isv = (int)blockIdx.y & 1;
-  const int tid = (int)threadIdx.x, nt = (int)blockDim.x;
+  const int tid = (int)threadIdx.x;
   const int shift = p.c.shift, page = 1 << shift;
   const Kv8Span sp = kv8_span(p.s, shift, b);
   const int pos0 = sp.len - sp.rows;  // position of row 0 (rows before position 0 are dropped)
@@ -52,33 +69,73 @@ __global__ void k_kv8_append(AppendParams p) {
   const int s0 = max(max(pos0, 0) - (col << shift), 0);
   const int s1 = min(sp.len - (col << shift), page);
   if (s1 <= s0) return;
-  const int id = kv8_page(p.s, p.c, b, col);
-  if (id < 0) return;
 
-  const __bf16 *x = p.x[isv] + (int64_t)h * p.head_stride[isv] +
-                    (int64_t)(sp.r0 + (col << shift) - pos0) * p.row_stride[isv];  // slot 0's row
   const int64_t xs = p.row_stride[isv];
+  const __bf16 *x = p.x[isv] + (int64_t)h * p.head_stride[isv] +
+                    (int64_t)(sp.r0 + (col << shift) - pos0) * xs;  // slot 0's row
+  // K: piece i is channels 16 (i % (D/16)) .. of slot s0 + i / (D/16), two
+  // loads; V: channels 8 (i % (D/8)) .. of slots 4 (q0 + i / (D/8)) .., four
+  const int q0 = s0 >> 2, q1 = (s1 + 3) >> 2;
+  uint4 r[NU][4];
+  if (!isv) {
+#pragma unroll
+    for (int u = 0; u < 2 * NU; ++u) {
+      const int i = tid + T * u, slot = s0 + i / (D / 16);
+      const uint4 *src = (const uint4 *)(x + slot * xs + i % (D / 16) * 16);
+      const bool in = slot < s1;
+      r[u >> 1][2 * (u & 1)] = in ? load_once(src) : uint4{0, 0, 0, 0};
+      r[u >> 1][2 * (u & 1) + 1] = in ? load_once(src + 1) : uint4{0, 0, 0, 0};
+    }
+  } else {
+#pragma unroll
+    for (int u = 0; u < NU; ++u) {
+      const int i = tid + T * u, slot = 4 * (q0 + i / (D / 8));
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        r[u][k] = slot + k >= s0 && slot + k < s1 ? load_once((const uint4 *)(x + (slot + k) * xs + i % (D / 8) * 8))
+                                                  : uint4{0, 0, 0, 0};
+    }
+  }
+  const int id = kv8_page(p.s, p.c, b, col);  // (while the rows are on their way)
+  if (id < 0) return;
   const size_t ph = (size_t)id * p.c.heads + h;
   uint8_t *codes = (isv ? p.c.v : p.c.k) + (ph << shift) * D;
   uint8_t *scale = (isv ? p.c.vs : p.c.ks) + ph;
-
-  float amax = 0.f;
-  for (int i = tid; i < (s1 - s0) * (D / 8); i += nt) {
-    float f[8];
-    load8(x + (s0 + i / (D / 8)) * xs + i % (D / 8) * 8, f);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) amax = kv8_max_finite(amax, f[j]);
-  }
-  amax = kv8_block_max(amax, part);
   const int was = s0 > 0 ? (int)*scale - 127 : kKv8MinExp;
+
+  uint32_t bits = 0;
+#pragma unroll
+  for (int u = 0; u < NU; ++u)
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      bits = max_bits(max_bits(max_bits(max_bits(bits, r[u][k].x), r[u][k].y), r[u][k].z), r[u][k].w);
+  bits = kv8_block_max_u(max(bits & 0xFFFFu, bits >> 16), part);
+  float amax = bf16_bits_to_f32(bits);
+  if (bits >= 0x7F80u) {  // infinities and NaN count for no scale
+    amax = 0.f;
+#pragma unroll
+    for (int u = 0; u < NU; ++u)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        float f[8];
+        widen8(r[u][k], f);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) amax = kv8_max_finite(amax, f[j]);
+      }
+    __syncthreads();
+    amax = __uint_as_float(kv8_block_max_u(__float_as_uint(amax), part));
+  }
   const int e = max(kv8_exponent(amax), was);
   // 2^(was - e): below 2^-126 every code goes to zero either way
   const float move = e > was ? kv8_two(max(was - e, -126)) : 1.0f;
+  // every magnitude is at most 448 scales, and none is NaN: the conversion needs no clamp
+  const bool plain = bits < 0x7F80u && amax <= 448.0f * kv8_two(kKv8MaxExp);
+  const float sc = kv8_two(e);
   const float inv = kv8_two(-e);
 
   if (!isv) {
     if (e > was && s0 > 0)
-      for (int i = tid; i < s0 * (D / 16); i += nt) {
+      for (int i = tid; i < s0 * (D / 16); i += T) {
         uint4 *q = (uint4 *)(codes + kv8_k_at(i % s0, i / s0 * 16, D));
         uint4 v = *q;
         v.x = kv8_rescale4(v.x, move);
@@ -87,30 +144,35 @@ __global__ void k_kv8_append(AppendParams p) {
         v.w = kv8_rescale4(v.w, move);
         *q = v;
       }
-    for (int i = tid; i < (s1 - s0) * (D / 16); i += nt) {
-      const int slot = s0 + i / (D / 16), d = i % (D / 16) * 16;
+#pragma unroll
+    for (int u = 0; u < 2 * NU; ++u) {
+      const int i = tid + T * u, slot = s0 + i / (D / 16);
+      if (slot >= s1) continue;
+      uint4 *to = (uint4 *)(codes + kv8_k_at(slot, i % (D / 16) * 16, D));
+      if (plain) {
+        const uint4 lo = r[u >> 1][2 * (u & 1)], hi = r[u >> 1][2 * (u & 1) + 1];
+        *to = uint4{encode_pairs(lo.x, lo.y, sc), encode_pairs(lo.z, lo.w, sc), encode_pairs(hi.x, hi.y, sc),
+                    encode_pairs(hi.z, hi.w, sc)};
+        continue;
+      }
       float f[16];
-      load8(x + slot * xs + d, f);
-      load8(x + slot * xs + d + 8, f + 8);
+      widen8(r[u >> 1][2 * (u & 1)], f);
+      widen8(r[u >> 1][2 * (u & 1) + 1], f + 8);
 #pragma unroll
       for (int j = 0; j < 16; ++j) f[j] *= inv;
-      *(uint4 *)(codes + kv8_k_at(slot, d, D)) =
-          uint4{kv8_encode4(f), kv8_encode4(f + 4), kv8_encode4(f + 8), kv8_encode4(f + 12)};
+      *to = uint4{kv8_encode4(f), kv8_encode4(f + 4), kv8_encode4(f + 8), kv8_encode4(f + 12)};
     }
     if (h == 0 && p.c.w)
-      for (int i = s0 + tid; i < s1; i += nt) p.c.w[((size_t)id << shift) + i] = 0.f;
+      for (int i = s0 + tid; i < s1; i += T) p.c.w[((size_t)id << shift) + i] = 0.f;
   } else {
-    // pieces of 16 bytes: piece (group of 4 tokens q, a, b) at
-    // 16 * (unit * D + 64 a + 16 g + b); groups from the first that is
-    // written to the last
-    const int q0 = e > was ? 0 : s0 >> 2, q1 = (s1 + 3) >> 2;
-    auto piece = [&](int i) {  // i-th piece of the range -> its byte offset
-      const int q = q0 + i / (D / 4), r = i % (D / 4);
-      return kv8_v_at(4 * q, (r >> 4) * 64 + (r & 15), D);
+    // 16-byte piece i of the groups from `from` on: slots 4 q .., channels 64 a + 16 c + r
+    const int from = e > was ? 0 : q0, np = (q1 - from) * (D / 4);
+    auto piece = [&](int i) {
+      const int q = from + i / (D / 4), ar = i % (D / 4);
+      return kv8_v_at(4 * q, (ar >> 4) * 64 + (ar & 15), D);
     };
-    const int np = (q1 - q0) * (D / 4);
-    for (int i = tid; i < np; i += nt) {
-      const int q = q0 + i / (D / 4);
+    for (int i = tid; i < np; i += T) {
+      const int q = from + i / (D / 4);
       if (4 * q >= s0 && 4 * q + 3 < s1) continue;  // all new
       const int at = piece(i);
       uint4 v = *(const uint4 *)(codes + at);
@@ -125,22 +187,43 @@ __global__ void k_kv8_append(AppendParams p) {
       *(uint4 *)(image + at) = v;
     }
     __syncthreads();
-    for (int i = tid; i < (s1 - s0) * (D / 8); i += nt) {
-      const int slot = s0 + i / (D / 8), d = i % (D / 8) * 8;
-      float f[8];
-      load8(x + slot * xs + d, f);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) f[j] *= inv;
-      const uint32_t c0 = kv8_encode4(f), c1 = kv8_encode4(f + 4);
-      const int at = kv8_v_at(slot, d, D);  // channels d..d+7 are 16 bytes apart
+    for (int u = 0; u < NU; ++u) {
+      const int i = tid + T * u, slot = 4 * (q0 + i / (D / 8)), d = i % (D / 8) * 8;
+      if (slot >= s1) continue;
+      const uint32_t lo = (uint32_t)max(s0 - slot, 0), hi = (uint32_t)min(s1 - slot, 4);  // its new tokens
+      const uint32_t mask = (hi == 4 ? 0xFFFFFFFFu : (1u << (8 * hi)) - 1u) & (0xFFFFFFFFu << (8 * lo));
+      uint32_t w[8];  // a channel's four tokens
+      if (plain) {
+        const uint32_t t[4][4] = {{r[u][0].x, r[u][0].y, r[u][0].z, r[u][0].w},
+                                  {r[u][1].x, r[u][1].y, r[u][1].z, r[u][1].w},
+                                  {r[u][2].x, r[u][2].y, r[u][2].z, r[u][2].w},
+                                  {r[u][3].x, r[u][3].y, r[u][3].z, r[u][3].w}};
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        image[at + 16 * j] = (uint8_t)(c0 >> (8 * j));
-        image[at + 16 * (4 + j)] = (uint8_t)(c1 >> (8 * j));
+        for (int j = 0; j < 8; ++j) {
+          const uint32_t sel = j & 1 ? 0x07060302u : 0x05040100u;
+          w[j] = encode_pairs(__builtin_amdgcn_perm(t[1][j >> 1], t[0][j >> 1], sel),
+                              __builtin_amdgcn_perm(t[3][j >> 1], t[2][j >> 1], sel), sc);
+        }
+      } else {
+        float f[4][8];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) widen8(r[u][k], f[k]);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float y[4] = {f[0][j] * inv, f[1][j] * inv, f[2][j] * inv, f[3][j] * inv};
+          w[j] = kv8_encode4(y);
+        }
+      }
+      const int at = kv8_v_at(slot, d, D);  // channels d .. d + 7 are 16 bytes apart
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        uint32_t *to = (uint32_t *)(image + at + 16 * j);
+        *to = mask == 0xFFFFFFFFu ? w[j] : (w[j] & mask) | (*to & ~mask);
       }
     }
     __syncthreads();
-    for (int i = tid; i < np; i += nt) {
+    for (int i = tid; i < np; i += T) {
       const int at = piece(i);
       *(uint4 *)(codes + at) = *(const uint4 *)(image + at);
     }
@@ -439,7 +522,7 @@ struct MoveParams {
 // move to it in registers.
 template <int D, int NP>
 __global__ __launch_bounds__(256) void k_kv8_move(MoveParams p) {
-  __shared__ float part[4];
+  __shared__ unsigned part[4];
   __shared__ int src[128];  // unit of each token's codes, -1: none
   __shared__ int src_slot[128];
   __shared__ float src_scale[128];
@@ -529,7 +612,7 @@ __global__ __launch_bounds__(256) void k_kv8_move(MoveParams p) {
       }
     }
   }
-  amax = kv8_block_max(amax, part);
+  amax = __uint_as_float(kv8_block_max_u(__float_as_uint(amax), part));
   const int e = kv8_exponent(amax);
   const float inv = kv8_two(-e);
   // a code that is not zero is below 448 * 2^e and at least 2^-9 scales: its
@@ -575,14 +658,6 @@ __global__ __launch_bounds__(256) void k_kv8_move(MoveParams p) {
   if (tid == 0) scales[(size_t)to * p.c.heads + h] = (uint8_t)(e + 127);
 }
 
-template <typename P>
-hipError_t by_dim(int dim, void (*k64)(P), void (*k128)(P), void (*k256)(P), const P &p, dim3 grid,
-                  int threads, size_t lds, hipStream_t stream) {
-  auto k = dim == 64 ? k64 : dim == 128 ? k128 : k256;
-  k<<<grid, dim3((unsigned)threads), lds, stream>>>(p);
-  return hipGetLastError();
-}
-
 }  // namespace
 
 hipError_t launch_kv8_append(const Kv8Rows &k, const Kv8Rows &v, const Kv8Pool &c, const Kv8Batch &s,
@@ -601,10 +676,21 @@ hipError_t launch_kv8_append(const Kv8Rows &k, const Kv8Rows &v, const Kv8Pool &
   const int64_t most = ((int64_t)s.max_rows + 2 * page - 2) >> c.shift;
   const int touched = (int)(most < s.cols ? most : s.cols);
   const dim3 grid((unsigned)touched, (unsigned)(2 * c.heads), (unsigned)s.seqs);
-  // a few tokens are one wave's work
-  const int threads = s.max_rows * dim <= 1024 ? 64 : 256;
-  return by_dim(dim, k_kv8_append<64>, k_kv8_append<128>, k_kv8_append<256>, p, grid, threads,
-                (size_t)page * dim, stream);
+  // A few tokens are one wave's work, and each page's part one load for a
+  // thread; otherwise a page is 8192 elements for each unit of 256 threads.
+  const bool few = s.max_rows * dim <= 1024;
+  const int units = page * dim / 8192;
+  auto pick = [&](auto d) {
+    constexpr int D = decltype(d)::value, kMost = 128 * D / 8192;
+    return few ? k_kv8_append<D, 1, 64>
+               : units <= 1 ? k_kv8_append<D, 1, 256> : units == 2 ? k_kv8_append<D, kMost < 2 ? kMost : 2, 256>
+                                                                   : k_kv8_append<D, kMost, 256>;
+  };
+  auto k_append = dim == 64 ? pick(std::integral_constant<int, 64>{})
+                            : dim == 128 ? pick(std::integral_constant<int, 128>{})
+                                         : pick(std::integral_constant<int, 256>{});
+  k_append<<<grid, dim3(few ? 64 : 256), (size_t)page * dim, stream>>>(p);
+  return hipGetLastError();
 }
 
 Kv8EvictPlan kv8_evict_plan(const Kv8Batch &s, int max_len) {

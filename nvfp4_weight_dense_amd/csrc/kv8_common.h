@@ -45,6 +45,12 @@ __device__ __forceinline__ int kv8_page(const Kv8Batch &s, const Kv8Pool &c, int
   return (unsigned)id < (unsigned)c.pages ? id : -1;
 }
 
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+// 16 bytes that this call reads once: kept from displacing reused lines in the caches
+__device__ __forceinline__ uint4 load_once(const uint4 *p) {
+  return __builtin_bit_cast(uint4, __builtin_nontemporal_load((const u32x4 *)p));
+}
+
 __device__ __forceinline__ float kv8_two(int e) {  // 2^e, e >= -126
   return __uint_as_float((uint32_t)(e + 127) << 23);
 }
@@ -105,16 +111,17 @@ __device__ __forceinline__ float kv8_max_finite(float m, float x) {
   return a < __builtin_inff() ? fmaxf(m, a) : m;
 }
 
-// maximum over a workgroup of whole waves; `part` is LDS of one float per wave
-__device__ __forceinline__ float kv8_block_max(float m, float *part) {
+// maximum over a workgroup of whole waves; `part` is LDS of one word per wave
+// (magnitudes as fp32 bits have their order)
+__device__ __forceinline__ uint32_t kv8_block_max_u(uint32_t m, unsigned *part) {
 #pragma unroll
-  for (int o = 32; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor(m, o));
+  for (int o = 32; o > 0; o >>= 1) m = max(m, (uint32_t)__shfl_xor((int)m, o));
   const int waves = (int)blockDim.x >> 6;
   if (waves > 1) {
     if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = m;
     __syncthreads();
     m = part[0];
-    for (int i = 1; i < waves; ++i) m = fmaxf(m, part[i]);
+    for (int i = 1; i < waves; ++i) m = max(m, part[i]);
   }
   return m;
 }
