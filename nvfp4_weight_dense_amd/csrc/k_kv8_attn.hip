@@ -26,10 +26,11 @@ constexpr float kLog2e = 1.44269504088896341f, kLn2 = 0.693147180559945309f;
 // group's query heads of up to 16 * CT (row, head) pairs) leaves lane
 // (g, n) with tokens 4 g .. 4 g + 3 of each 16-token unit for column n, which
 // is the operand layout that O^T = V^T P^T wants, so P goes from the
-// accumulators to the next product without LDS or shuffles.  The running
-// maximum is raised only when a score passes it by 2^8 (the sums are fp32
-// and P is a floating type, so a factor up to 256 costs nothing), which
-// takes the cross-lane maximum out of almost every step.
+// accumulators to the next product without LDS or shuffles.  No maximum is
+// looked for: the running one stays until a step's sum of powers passes
+// kRaise (the sums are fp32 and P is a floating type, so a factor of some
+// hundred costs nothing; overflow to infinity passes it too), and only then
+// is it found and the powers taken again.
 //
 // A workgroup's four waves take its steps in turn; their results are joined
 // in LDS, those of a sequence's workgroups by the last of them to arrive, in
@@ -38,6 +39,7 @@ constexpr float kLog2e = 1.44269504088896341f, kLn2 = 0.693147180559945309f;
 constexpr int kDecodeWaves = 4;
 constexpr int kMaxSplits = 128;
 constexpr int kMaxSteps = 31;  // a wave's, two units a lane; lanes 62 and 63 name none
+constexpr float kRaise = 1024.0f;  // a step's sum of powers that has the running maximum found anew
 constexpr float kLowest = -3.4028234663852886e38f;  // below every finite score
 
 struct DecodeParams {
@@ -71,21 +73,24 @@ __device__ __forceinline__ uint32_t nan_bytes(uint32_t w) {
   return ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
 }
 
-template <int D>
-struct Step {       // the codes of 32 tokens, as one lane holds them
-  uint4 k[2][D / 64];  // [unit][t]: token lane % 16, channels 64 t + 16 g ..
-  uint4 v[2][D / 64];  // [unit][a]: tokens 4 g .., channels 64 a + 16 c + lane % 16
-};
+// waves a SIMD holds: what the accumulators (D * CT / 4 registers), Q and the codes leave room for
+constexpr int decode_waves(int dim, int ct) { return dim * ct <= 64 ? 4 : dim * ct <= 128 ? 3 : 2; }
 
 template <int D, int CT>
-__global__ __launch_bounds__(64 * kDecodeWaves) void k_kv8_decode(DecodeParams p) {
+__global__ __launch_bounds__(64 * kDecodeWaves, decode_waves(D, CT)) void k_kv8_decode(DecodeParams p) {
   constexpr int kCols = 16 * CT, kPad = D + 4;
   __shared__ __align__(16) float osum[kDecodeWaves][16][kPad];
   __shared__ float stat[2][kDecodeWaves][kCols];
   __shared__ bool last_flag;
   __shared__ float wsplit[kMaxSplits][16];
-  const int split = (int)blockIdx.x, h = (int)blockIdx.y / p.blocks, cb = (int)blockIdx.y % p.blocks;
-  const int b = (int)blockIdx.z, tid = (int)threadIdx.x, lane = tid & 63;
+  // Consecutive workgroups go to the 8 XCDs in turn.  The items (sequence, KV
+  // head, column block) are side by side, a step further for each split: with
+  // the splits side by side, an even number of them would leave the XCDs of
+  // the later ones idle where sequences are short.
+  const int items = p.s.seqs * p.c.heads * p.blocks;
+  const int split = (int)blockIdx.x / items, item = ((int)blockIdx.x % items + split) % items;
+  const int cb = item % p.blocks, h = item / p.blocks % p.c.heads, b = item / p.blocks / p.c.heads;
+  const int tid = (int)threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int n = lane & 15, g = lane >> 4, shift = p.c.shift;
   const Kv8Span sp = kv8_span(p.s, shift, b);
@@ -103,6 +108,8 @@ __global__ __launch_bounds__(64 * kDecodeWaves) void k_kv8_decode(DecodeParams p
   const int full_lo = low(final), full_hi = min(first, end - 1);  // every row sees these
 
   // columns of this lane
+  const float cs = fmaxf(fabsf(p.a.scale) * kLog2e, 1.1754944e-38f);  // its sign goes to q
+  const uint32_t flip = p.a.scale < 0.f ? 0x80008000u : 0u;
   bf16x8 q[CT][D / 32];
   int lo[CT], hi[CT];
 #pragma unroll
@@ -116,7 +123,7 @@ __global__ __launch_bounds__(64 * kDecodeWaves) void k_kv8_decode(DecodeParams p
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const uint4 w = *(const uint4 *)(qr + 64 * t + 16 * g + 8 * e);
-        q[ct][2 * t + e] = as_bf16x8(in ? w : uint4{0, 0, 0, 0});
+        q[ct][2 * t + e] = as_bf16x8(in ? uint4{w.x ^ flip, w.y ^ flip, w.z ^ flip, w.w ^ flip} : uint4{0, 0, 0, 0});
       }
     const int pos = sp.len - sp.rows + i;
     lo[ct] = low(pos);
@@ -137,22 +144,21 @@ __global__ __launch_bounds__(64 * kDecodeWaves) void k_kv8_decode(DecodeParams p
       if (id >= 0) {
         const size_t ph = (size_t)id * p.c.heads + h;
         at = (int)((ph << (shift - 4)) + ((t0 >> 4) & ((1 << (shift - 4)) - 1)));
-        ksc = p.a.scale * kLog2e * kv8_scale(p.c.ks[ph]);
+        ksc = fmaxf(cs * kv8_scale(p.c.ks[ph]), 1.1754944e-38f);
         vsc = kv8_scale(p.c.vs[ph]);
       }
     }
   };
-  auto load = [&](Step<D> &x, int s) {
+  uint4 kx[2][D / 64];  // K of a step [unit][t]: token lane % 16, channels 64 t + 16 g ..
+  uint4 vx[2][D / 64], vy[2][D / 64];  // V [unit][a], this step's and the next's: tokens 4 g .., channels 64 a + 16 c + lane % 16
+  auto load = [&](const uint8_t *codes, uint4 (&x)[2][D / 64], int s) {
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       const uint32_t unit = (uint32_t)__builtin_amdgcn_readlane(at, min(2 * s, 62) + u);
       // (a unit that no page holds reads the pool's first; its scores are masked)
-      const size_t off = (size_t)(unit == 0xFFFFFFFFu ? 0u : unit) * (16 * D);
-      const uint4 *k = (const uint4 *)(p.c.k + off) + lane, *v = (const uint4 *)(p.c.v + off) + lane;
+      const uint4 *src = (const uint4 *)(codes + (size_t)(unit == 0xFFFFFFFFu ? 0u : unit) * (16 * D)) + lane;
 #pragma unroll
-      for (int t = 0; t < D / 64; ++t) x.k[u][t] = load_once(k + 64 * t);
-#pragma unroll
-      for (int t = 0; t < D / 64; ++t) x.v[u][t] = load_once(v + 64 * t);
+      for (int t = 0; t < D / 64; ++t) x[u][t] = load_once(src + 64 * t);
     }
   };
 
@@ -161,100 +167,160 @@ __global__ __launch_bounds__(64 * kDecodeWaves) void k_kv8_decode(DecodeParams p
 #pragma unroll
   for (int ct = 0; ct < CT; ++ct) m[ct] = kLowest;
 
-  auto compute = [&](const Step<D> &x, int s) {
-    const int t0 = (base + kDecodeWaves * s) * 32;
-    f32x4 sc[CT][2] = {};
+  const size_t score_bytes = (size_t)p.score_cols * p.len_pad * 4;  // of an item, below 2^31
+  const __amdgpu_buffer_rsrc_t left =
+      rsrc_uniform((const char *)p.scores + ((size_t)b * p.c.heads + h) * score_bytes, score_bytes);
+  const uint32_t score_at = n < cols ? (uint32_t)(n * p.len_pad + 4 * g) * 4u : kOOB;
+
+  f32x4 sc[CT][2];
+  bf16x8 pr[CT];
+  float sum[CT];
+  auto of_unit = [&](float x, int s, int u) {
+    return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, x), 2 * s + u));
+  };
+  auto has_page = [&](int s, int u) { return __builtin_amdgcn_readlane(at, 2 * s + u) != -1; };
+  auto scores = [&]() {
 #pragma unroll
     for (int u = 0; u < 2; ++u)
 #pragma unroll
       for (int t = 0; t < D / 64; ++t) {
-        const bf16x8 k0 = fp8x8_to_bf16(x.k[u][t].x, x.k[u][t].y, 1.0f);
-        const bf16x8 k1 = fp8x8_to_bf16(x.k[u][t].z, x.k[u][t].w, 1.0f);
+        const bf16x8 k0 = fp8x8_to_bf16(kx[u][t].x, kx[u][t].y, 1.0f);
+        const bf16x8 k1 = fp8x8_to_bf16(kx[u][t].z, kx[u][t].w, 1.0f);
+        const f32x4 zero = {};
 #pragma unroll
         for (int ct = 0; ct < CT; ++ct) {
-          sc[ct][u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k0, q[ct][2 * t], sc[ct][u], 0, 0, 0);
+          sc[ct][u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k0, q[ct][2 * t], t ? sc[ct][u] : zero, 0, 0, 0);
           sc[ct][u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k1, q[ct][2 * t + 1], sc[ct][u], 0, 0, 0);
         }
       }
-    int valid[2];
-    float vscale[2];
+  };
+  auto sees = [&](int ct, int t0, int s) {  // bit e: accumulator e's token is one that the lane's column sees
+    uint32_t bits = 0;
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      const float f = __builtin_bit_cast(
-          float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, ksc), 2 * s + u));
-      vscale[u] = __builtin_bit_cast(
-          float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, vsc), 2 * s + u));
-      valid[u] = __builtin_amdgcn_readlane(at, 2 * s + u) != -1;
-#pragma unroll
-      for (int ct = 0; ct < CT; ++ct) sc[ct][u] *= f;
+    for (int e = 0; e < 8; ++e) {
+      const int j = t0 + 16 * (e >> 2) + 4 * g + (e & 3);
+      bits |= (((j >= lo[ct]) & (j <= hi[ct])) ? 1u : 0u) << e;
     }
-    const bool whole = t0 >= full_lo && t0 + 31 <= full_hi && valid[0] && valid[1];
-    uint32_t seen[CT];
-#pragma unroll
-    for (int ct = 0; ct < CT; ++ct) seen[ct] = 0xFFu;
-    if (!whole) {
-#pragma unroll
-      for (int ct = 0; ct < CT; ++ct) {
-        seen[ct] = 0;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const int j = t0 + 16 * (e >> 2) + 4 * g + (e & 3);
-          const bool yes = (valid[e >> 2] != 0) & (j >= lo[ct]) & (j <= hi[ct]);
-          seen[ct] |= (yes ? 1u : 0u) << e;
-          sc[ct][e >> 2][e & 3] = yes ? sc[ct][e >> 2][e & 3] : -__builtin_inff();
-        }
-      }
-    }
-    if constexpr (CT == 1) {
-      if (p.scores && n < cols) {
-        float *to = p.scores + (((size_t)b * p.c.heads + h) * p.score_cols + n) * p.len_pad + t0 + 4 * g;
-#pragma unroll
-        for (int u = 0; u < 2; ++u) *(f32x4 *)(to + 16 * u) = sc[0][u];
-      }
-    }
-    bf16x8 pr[CT];
+    return bits & ((has_page(s, 0) ? 0xFu : 0u) | (has_page(s, 1) ? 0xF0u : 0u));
+  };
+  // P and its sum (fp32; P itself is rounded to bf16, the type of the product's other operand)
+  auto powers = [&](int s) {
+    const float f0 = of_unit(ksc, s, 0), f1 = of_unit(ksc, s, 1);
 #pragma unroll
     for (int ct = 0; ct < CT; ++ct) {
-      float top = fmaxf(fmaxf(sc[ct][0][0], sc[ct][0][1]), fmaxf(sc[ct][0][2], sc[ct][0][3]));
-      top = fmaxf(top, fmaxf(fmaxf(sc[ct][1][0], sc[ct][1][1]), fmaxf(sc[ct][1][2], sc[ct][1][3])));
-      if (__any(top > m[ct] + 8.0f)) {
-        top = fmaxf(top, __shfl_xor(top, 16));
-        top = fmaxf(top, __shfl_xor(top, 32));
-        const float mn = fmaxf(m[ct], top), down = __builtin_amdgcn_exp2f(m[ct] - mn);
+      float e[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) e[i] = __builtin_amdgcn_exp2f(fmaf(sc[ct][i >> 2][i & 3], i < 4 ? f0 : f1, -m[ct]));
+      sum[ct] = ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
+#pragma unroll
+      for (int i = 0; i < 8; ++i) pr[ct][i] = (__bf16)e[i];
+    }
+  };
+  // V of channels 64 a + 16 c + n of the lane's eight tokens, as an operand
+  auto widen = [&](uint32_t w0, uint32_t w1, float v0, float v1) {
+    const bf16x2 x0 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w0, v0, false);
+    const bf16x2 x1 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w0, v0, true);
+    const bf16x2 y0 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w1, v1, false);
+    const bf16x2 y1 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w1, v1, true);
+    return bf16x8{x0[0], x0[1], x1[0], x1[1], y0[0], y0[1], y1[0], y1[1]};
+  };
+  auto take = [&]() {
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+      for (int a = 0; a < D / 64; ++a) vx[u][a] = vy[u][a];
+  };
+  auto word = [](const uint4 &v, int c) { return c == 0 ? v.x : c == 1 ? v.y : c == 2 ? v.z : v.w; };
+
+  // The next step's codes are loaded when this one's scores are done, K into
+  // the registers that held K.  The loads are not conditional; a step past the
+  // last is the pool's first unit.  The loop proper has no rare work in it,
+  // which keeps the accumulators in place: a step that raises the maximum, or
+  // where a NaN code of V must not reach a row that does not see its token, is
+  // finished below from its scores.
+  for (int round = 0; round < p.rounds; ++round) {
+    look_up(round);
+    load(p.c.k, kx, 0);
+    load(p.c.v, vx, 0);
+    int s = 0;
+    while (s < count) {
+      bool leave;
+      do {
+        const int t0 = (base + kDecodeWaves * s) * 32;
+        scores();
+        load(p.c.k, kx, s + 1);
+        load(p.c.v, vy, s + 1);
+        uint32_t odd = 0;
+        if (t0 < full_lo || t0 + 31 > full_hi || !has_page(s, 0) || !has_page(s, 1)) {
+#pragma unroll
+          for (int ct = 0; ct < CT; ++ct) {
+            const uint32_t bits = sees(ct, t0, s);
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              sc[ct][e >> 2][e & 3] = bits >> e & 1u ? sc[ct][e >> 2][e & 3] : -__builtin_inff();
+          }
+#pragma unroll
+          for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int a = 0; a < D / 64; ++a)
+              odd |= nan_bytes(vx[u][a].x) | nan_bytes(vx[u][a].y) | nan_bytes(vx[u][a].z) | nan_bytes(vx[u][a].w);
+        }
+        if constexpr (CT == 1) {
+          if (p.scores) {  // (lanes past the columns store out of range, that is nowhere)
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+              __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, sc[0][u] * of_unit(ksc, s, u)), left,
+                                                     score_at + (uint32_t)(t0 + 16 * u) * 4u, 0, 0);
+          }
+        }
+        powers(s);
+        bool raise = odd != 0;
+#pragma unroll
+        for (int ct = 0; ct < CT; ++ct) raise |= sum[ct] > kRaise;
+        leave = __any(raise);
+        if (leave) break;
+        const float v0 = of_unit(vsc, s, 0), v1 = of_unit(vsc, s, 1);
+#pragma unroll
+        for (int ct = 0; ct < CT; ++ct) l[ct] += sum[ct];
+#pragma unroll
+        for (int a = 0; a < D / 64; ++a)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const bf16x8 vt = widen(word(vx[0][a], c), word(vx[1][a], c), v0, v1);
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct)
+              o[ct][4 * a + c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vt, pr[ct], o[ct][4 * a + c], 0, 0, 0);
+          }
+        take();
+      } while (++s < count);
+      if (!leave) break;
+
+      const int t0 = (base + kDecodeWaves * s) * 32;
+      const float f0 = of_unit(ksc, s, 0), f1 = of_unit(ksc, s, 1);
+#pragma unroll
+      for (int ct = 0; ct < CT; ++ct) {
+        float x = kLowest;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x = fmaxf(x, sc[ct][e >> 2][e & 3] * (e < 4 ? f0 : f1));
+        x = fmaxf(x, __shfl_xor(x, 16));
+        x = fmaxf(x, __shfl_xor(x, 32));
+        const float mn = fmaxf(m[ct], x), down = __builtin_amdgcn_exp2f(m[ct] - mn);
         m[ct] = mn;
         l[ct] *= down;
 #pragma unroll
         for (int d = 0; d < D / 16; ++d) o[ct][d] *= down;
       }
-      float e[8];
+      powers(s);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) e[i] = __builtin_amdgcn_exp2f(sc[ct][i >> 2][i & 3] - m[ct]);
-      l[ct] += ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
-      // (bf16, the type of the product's other operand; l sums the fp32 values)
+      for (int ct = 0; ct < CT; ++ct) l[ct] += sum[ct];
+      const float v0 = of_unit(vsc, s, 0), v1 = of_unit(vsc, s, 1);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) pr[ct][i] = (__bf16)e[i];
-    }
-    bool odd = false;
-    if (!whole) {  // a NaN code of a token that some row does not see must not reach that row
-      uint32_t any = 0;
-#pragma unroll
-      for (int u = 0; u < 2; ++u)
-#pragma unroll
-        for (int a = 0; a < D / 64; ++a)
-          any |= nan_bytes(x.v[u][a].x) | nan_bytes(x.v[u][a].y) | nan_bytes(x.v[u][a].z) | nan_bytes(x.v[u][a].w);
-      odd = __any(any != 0);
-    }
-    auto product = [&](auto careful) {
-#pragma unroll
-      for (int a = 0; a < D / 64; ++a) {
-        const uint32_t v0[4] = {x.v[0][a].x, x.v[0][a].y, x.v[0][a].z, x.v[0][a].w};
-        const uint32_t v1[4] = {x.v[1][a].x, x.v[1][a].y, x.v[1][a].z, x.v[1][a].w};
+      for (int a = 0; a < D / 64; ++a)
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-          uint32_t w0 = v0[c], w1 = v1[c];
-          if constexpr (decltype(careful)::value) {
-            // ones where a code is NaN, against ones where a row sees the token
-            const uint32_t b0 = nan_bytes(w0) >> 7, b1 = nan_bytes(w1) >> 7;
+          uint32_t w0 = word(vx[0][a], c), w1 = word(vx[1][a], c);
+          const uint32_t b0 = nan_bytes(w0) >> 7, b1 = nan_bytes(w1) >> 7;
+          if (__any((b0 | b1) != 0)) {  // ones where a code is NaN, against ones where a row sees the token
             w0 &= ~(b0 * 0xFFu);
             w1 &= ~(b1 * 0xFFu);
             bf16x8 here;
@@ -265,46 +331,25 @@ __global__ __launch_bounds__(64 * kDecodeWaves) void k_kv8_decode(DecodeParams p
             }
 #pragma unroll
             for (int ct = 0; ct < CT; ++ct) {
-              bf16x8 sees;
+              const uint32_t bits = sees(ct, t0, s);
+              bf16x8 yes;
 #pragma unroll
-              for (int i = 0; i < 8; ++i) sees[i] = (__bf16)(float)((seen[ct] >> i) & 1u);
+              for (int i = 0; i < 8; ++i) yes[i] = (__bf16)(float)((bits >> i) & 1u);
               f32x4 hit = {};
-              hit = __builtin_amdgcn_mfma_f32_16x16x32_bf16(here, sees, hit, 0, 0, 0);
+              hit = __builtin_amdgcn_mfma_f32_16x16x32_bf16(here, yes, hit, 0, 0, 0);
 #pragma unroll
               for (int i = 0; i < 4; ++i)
                 if (hit[i] > 0.f) o[ct][4 * a + c][i] = __builtin_nanf("");
             }
-            __builtin_amdgcn_sched_barrier(0);  // one at a time: a rare path need not set the registers' number
           }
-          const bf16x2 x0 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w0, vscale[0], false);
-          const bf16x2 x1 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w0, vscale[0], true);
-          const bf16x2 y0 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w1, vscale[1], false);
-          const bf16x2 y1 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w1, vscale[1], true);
-          const bf16x8 vt = {x0[0], x0[1], x1[0], x1[1], y0[0], y0[1], y1[0], y1[1]};
+          const bf16x8 vt = widen(w0, w1, v0, v1);
 #pragma unroll
           for (int ct = 0; ct < CT; ++ct)
             o[ct][4 * a + c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vt, pr[ct], o[ct][4 * a + c], 0, 0, 0);
+          __builtin_amdgcn_sched_barrier(0);  // one at a time: rare work need not set the registers' number
         }
-      }
-    };
-    if (odd)
-      product(std::true_type{});
-    else
-      product(std::false_type{});
-  };
-
-  // Two steps' codes in turn: one loads while the other is used.  The loads
-  // are not conditional (a wait for the older of the two would otherwise
-  // become one for both); a step past the last is the pool's first unit.
-  for (int round = 0; round < p.rounds; ++round) {
-    Step<D> xa, xb;
-    look_up(round);
-    load(xa, 0);
-    for (int s = 0; s < count; s += 2) {
-      load(xb, s + 1);
-      compute(xa, s);
-      load(xa, s + 2);
-      if (s + 1 < count) compute(xb, s + 1);
+      take();
+      ++s;
     }
   }
 
@@ -319,8 +364,7 @@ __global__ __launch_bounds__(64 * kDecodeWaves) void k_kv8_decode(DecodeParams p
     }
   }
   __syncthreads();
-  const int item = ((int)blockIdx.z * p.c.heads + h) * p.blocks + cb;
-  const __amdgpu_buffer_rsrc_t pr =  // (not touched when there is one split)
+  const __amdgpu_buffer_rsrc_t parts =  // (not touched when there is one split)
       rsrc_uniform(p.part + (size_t)item * p.splits * kCols * (D + 2), (size_t)p.splits * kCols * (D + 2) * 4);
   const uint32_t stats = (uint32_t)p.splits * kCols * D * 4u;  // m and l of (split, column)
   const int64_t row0 = (int64_t)sp.r0 * p.a.q_heads + (int64_t)h * p.group;
@@ -362,10 +406,10 @@ __global__ __launch_bounds__(64 * kDecodeWaves) void k_kv8_decode(DecodeParams p
         if (d == 0 && p.a.lse) put_lse(c, mm, ll);
       } else {
         const uint32_t off = (uint32_t)(split * kCols + c);
-        st16_coherent(pr, (off * D + d) * 4u, x);
+        st16_coherent(parts, (off * D + d) * 4u, x);
         if (d == 0) {
-          st_coherent(pr, stats + off * 8u, mm);
-          st_coherent(pr, stats + off * 8u + 4u, ll);
+          st_coherent(parts, stats + off * 8u, mm);
+          st_coherent(parts, stats + off * 8u + 4u, ll);
         }
       }
     }
@@ -389,7 +433,7 @@ __global__ __launch_bounds__(64 * kDecodeWaves) void k_kv8_decode(DecodeParams p
     if (here <= 0) break;
     if (ct) __syncthreads();
     for (int i = tid; i < nsplit * here; i += kThreads)
-      wsplit[i / here][i % here] = ld_coherent(pr, stats + (uint32_t)(i / here * kCols + ct * 16 + i % here) * 8u);
+      wsplit[i / here][i % here] = ld_coherent(parts, stats + (uint32_t)(i / here * kCols + ct * 16 + i % here) * 8u);
     __syncthreads();
     float *top = stat[0][0], *total = stat[1][0];  // (done with)
     for (int c = tid >> 4; c < here; c += kThreads / 16) {
@@ -401,7 +445,7 @@ __global__ __launch_bounds__(64 * kDecodeWaves) void k_kv8_decode(DecodeParams p
       for (int t = tid & 15; t < nsplit; t += 16) {
         const float f = __builtin_amdgcn_exp2f(wsplit[t][c] - x);
         wsplit[t][c] = f;
-        y = fmaf(f, ld_coherent(pr, stats + (uint32_t)(t * kCols + ct * 16 + c) * 8u + 4u), y);
+        y = fmaf(f, ld_coherent(parts, stats + (uint32_t)(t * kCols + ct * 16 + c) * 8u + 4u), y);
       }
 #pragma unroll
       for (int k = 8; k > 0; k >>= 1) y += __shfl_xor(y, k);
@@ -420,7 +464,7 @@ __global__ __launch_bounds__(64 * kDecodeWaves) void k_kv8_decode(DecodeParams p
       f32x4 x = {};
 #pragma unroll 8
       for (int t = k; t < nsplit; t += deal)
-        x += ld16_coherent(pr, (uint32_t)((t * kCols + ct * 16 + c) * D + d) * 4u) * wsplit[t][c];
+        x += ld16_coherent(parts, (uint32_t)((t * kCols + ct * 16 + c) * D + d) * 4u) * wsplit[t][c];
       if (deal == 1) {
         put(ct * 16 + c, d, x, total[c]);
         if (d == 0 && p.a.lse) put_lse(ct * 16 + c, top[c], total[c]);
@@ -458,8 +502,6 @@ __global__ __launch_bounds__(64 * kDecodeWaves) void k_kv8_decode(DecodeParams p
 // token groups `half` and 2 + half.  No maximum is looked for either: the
 // running one stays until a tile's sum of powers passes kRaise (overflow to
 // infinity does), and only then is it found and the powers taken again.
-constexpr float kRaise = 1024.0f;
-
 struct PrefillParams {
   Kv8Attn a;
   Kv8Pool c;
@@ -1080,25 +1122,19 @@ __global__ __launch_bounds__(256) void k_kv8_weights_join(WeightParams p) {
 
 }  // namespace
 
-// Few rows: as many (row, head) columns of a KV head as one workgroup keeps
-// (64, with head size 256 32).
-constexpr int kv8_few_cols(int dim) { return dim == 256 ? 32 : 64; }
+// Few rows: up to so many (row, head) columns of a KV head.  Beyond one
+// workgroup's (16, 32 or 64 by head size) its blocks read the codes again,
+// from the caches; at 128 columns of 8 sequences of 16000 tokens the two
+// kernels take 64 and 62 us, at 66 50 and 60 us, at 105 of 13 short ones 21
+// and 29 us (head size 256: at 120 86 and 80 us).
+constexpr int kv8_few_cols(int dim) { return dim == 256 ? 64 : 128; }
 constexpr int kv8_many_cols(int dim) { return dim == 256 ? 128 : 256; }
 constexpr int kManyGroups = 512;
-constexpr int kDecodeGroups = 512;  // workgroups wanted
+// workgroups wanted: those that the CUs hold at a time (bound of a plan's: kDecodeGroups)
+constexpr int kDecodeGroups = 768;
+int decode_groups(int dim, int ct) { return std::min(256 * decode_waves(dim, ct), kDecodeGroups); }
 
 int64_t cols_of(const Kv8Batch &s, const Kv8Plan &pl) { return (int64_t)s.max_rows * pl.group; }
-
-size_t kv8_part_bound(const Kv8Attn &a, const Kv8Pool &c, const Kv8Batch &s, int dim) {
-  // fewer tokens or a window: shorter pieces, but (kv8_plan) never twice kDecodeGroups and one per item
-  const Kv8Plan pl = kv8_plan(a, c, s, dim);
-  const size_t few = (2 * kDecodeGroups + (size_t)s.seqs * c.heads) * (size_t)kv8_few_cols(dim);
-  const size_t many = pl.few ? 0 : (size_t)kManyGroups * kv8_many_cols(dim);
-  size_t floats = std::max(pl.part_floats, std::max(few, many) * (size_t)(dim + 2));
-  // 16 columns' scores, or kManyGroups parts of kWeightTokens
-  if (c.w) floats += std::max((size_t)s.seqs * c.heads * pl.len_pad * 16, (size_t)kManyGroups * kWeightTokens * 2);
-  return floats;
-}
 
 Kv8Plan kv8_plan(const Kv8Attn &a, const Kv8Pool &c, const Kv8Batch &s, int dim) {
   Kv8Plan pl = {};
@@ -1108,17 +1144,20 @@ Kv8Plan kv8_plan(const Kv8Attn &a, const Kv8Pool &c, const Kv8Batch &s, int dim)
   pl.counter_bytes = kKv8MaxItems * 4;
   if (pl.few) {
     pl.ct = cols <= 16 ? 1 : cols <= 32 ? 2 : 4;
-    pl.blocks = 1;
-    const int items = s.seqs * c.heads * pl.blocks;
+    pl.ct = std::min(pl.ct, 256 / dim);  // as many accumulators as leave two waves a SIMD
+    pl.blocks = (int)((cols + 16 * pl.ct - 1) / (16 * pl.ct));
+    const int items = std::max(s.seqs * c.heads * pl.blocks, 1);
     const int64_t seen = a.window ? std::min<int64_t>(a.max_len, (int64_t)a.window + s.max_rows + 31) : a.max_len;
     const int steps = (int)((seen + 31) / 32) + (a.window ? 1 : 0);
-    // The longest pieces that still give every CU two workgroups, which is
-    // what its registers hold: shorter ones cost more in the join than they
-    // gain (two sequences of 131000 tokens, 8 KV heads: 35 pieces each 118 us,
-    // 69 pieces 134 us, 137 pieces 169 us).
+    // Equal pieces of the longest sequence, as many as fill the CUs once, of at
+    // most kMaxSteps steps a wave.  Two sequences of 131000 tokens, 8 KV heads:
+    // 32 pieces each (a part of the CUs' places unused) 107 us, 46 pieces (all
+    // of them) 95 us, 64 pieces 100 us; more cost more in the join.
+    const int even = std::max((steps + 3) / 4, 1);  // steps of a wave if it were one piece
+    int want = std::max((decode_groups(dim, pl.ct) + items - 1) / items, (even + kMaxSteps - 1) / kMaxSteps);
+    want = std::min(want, even);
+    pl.spw = (even + want - 1) / want;
     auto pieces = [&](int spw) { return std::max((steps + 4 * spw - 1) / (4 * spw), 1); };
-    pl.spw = kMaxSteps;
-    while (pl.spw > 1 && (int64_t)items * pieces(pl.spw) < kDecodeGroups) pl.spw /= 2;
     const int most = items <= kKv8MaxItems ? kMaxSplits : 1;
     pl.rounds = (pieces(pl.spw) + most - 1) / most;
     pl.splits = (pieces(pl.spw) + pl.rounds - 1) / pl.rounds;
@@ -1128,7 +1167,7 @@ Kv8Plan kv8_plan(const Kv8Attn &a, const Kv8Pool &c, const Kv8Batch &s, int dim)
   if (!pl.few) {
     const int kc = kv8_many_cols(dim);
     pl.blocks = (int)((cols + kc - 1) / kc);
-    const int64_t items = (int64_t)s.seqs * c.heads * pl.blocks;
+    const int64_t items = std::max<int64_t>((int64_t)s.seqs * c.heads * pl.blocks, 1);
     const int64_t seen = a.window ? std::min<int64_t>(a.max_len, (int64_t)a.window + s.max_rows) : a.max_len;
     // one workgroup fills a CU: split the tokens where there are fewer, into pieces of 512 at least
     pl.splits = (int)std::max<int64_t>(std::min<int64_t>(kManyGroups / items, seen / 512), 1);
@@ -1138,7 +1177,7 @@ Kv8Plan kv8_plan(const Kv8Attn &a, const Kv8Pool &c, const Kv8Batch &s, int dim)
   pl.parts = 1;
   if (c.w) {
     const size_t tokens = (size_t)s.seqs * c.heads * pl.len_pad;
-    if (pl.few && pl.ct == 1) {
+    if (pl.few && cols <= 16 && cols * pl.len_pad < (1 << 29)) {
       pl.score_cols = (int)cols;
       pl.score_floats = tokens * (size_t)cols;
     } else {
@@ -1151,16 +1190,32 @@ Kv8Plan kv8_plan(const Kv8Attn &a, const Kv8Pool &c, const Kv8Batch &s, int dim)
   return pl;
 }
 
+size_t kv8_part_bound(const Kv8Attn &a, const Kv8Pool &c, const Kv8Batch &s, int dim) {
+  const Kv8Plan pl = kv8_plan(a, c, s, dim);
+  // the most rows that are few
+  const size_t few = (size_t)kv8_few_cols(dim), many = (size_t)kv8_many_cols(dim), width = (size_t)dim + 2;
+  Kv8Batch s2 = s;
+  s2.max_rows = std::min(s.max_rows, std::max((int)few / pl.group, 1));
+  size_t floats = std::max(pl.part_floats, kv8_plan(a, c, s2, dim).part_floats);
+  // fewer tokens, or a window: shorter pieces, but no more workgroups than kDecodeGroups and one for each item
+  floats = std::max(floats, (kDecodeGroups * 16 * (size_t)(256 / dim) + (size_t)s.seqs * c.heads * few) * width);
+  if (!pl.few) floats = std::max(floats, kManyGroups * many * width);
+  // 16 columns' scores, or kManyGroups parts of kWeightTokens
+  if (c.w) floats += std::max((size_t)s.seqs * c.heads * pl.len_pad * 16, (size_t)kManyGroups * kWeightTokens * 2);
+  return floats;
+}
+
 hipError_t launch_kv8_attention(const Kv8Attn &a, const Kv8Pool &c, const Kv8Batch &s, int dim,
                                 const Kv8Plan &pl, unsigned *counters, float *part, float *scores, hipStream_t stream) {
   if (pl.few) {
     const DecodeParams p{a, c, s, pl.group, pl.blocks, pl.spw, pl.rounds, pl.splits, part, counters,
                          pl.score_cols ? scores : nullptr, pl.len_pad, pl.score_cols};
-    const dim3 grid((unsigned)pl.splits, (unsigned)(c.heads * pl.blocks), (unsigned)s.seqs);
-    auto k = dim == 64 ? (pl.ct == 1 ? k_kv8_decode<64, 1> : pl.ct == 2 ? k_kv8_decode<64, 2> : k_kv8_decode<64, 4>)
-             : dim == 128
-                 ? (pl.ct == 1 ? k_kv8_decode<128, 1> : pl.ct == 2 ? k_kv8_decode<128, 2> : k_kv8_decode<128, 4>)
-                 : (pl.ct == 1 ? k_kv8_decode<256, 1> : k_kv8_decode<256, 2>);
+    const dim3 grid((unsigned)pl.splits * (unsigned)(s.seqs * c.heads * pl.blocks));
+    auto k = dim == 64    ? (pl.ct == 1   ? k_kv8_decode<64, 1>
+                             : pl.ct == 2 ? k_kv8_decode<64, 2>
+                                          : k_kv8_decode<64, 4>)
+             : dim == 128 ? (pl.ct == 1 ? k_kv8_decode<128, 1> : k_kv8_decode<128, 2>)
+                          : k_kv8_decode<256, 1>;
     k<<<grid, dim3(64 * kDecodeWaves), 0, stream>>>(p);
     return hipGetLastError();
   }

@@ -173,3 +173,12 @@ def test_binding_refusals():
         setattr(c, field, bad)
         with pytest.raises(ValueError, match=field):
             call(cache=c)
+
+
+@pytest.mark.parametrize("kw", [dict(seqs=0, rows=0), dict(rows=0, max_rows=0), dict(max_len=0), dict(cols=1, max_len=1),
+                                dict(rows=1 << 24, max_rows=1 << 23, cols=1 << 24, max_len=1 << 28)])
+def test_workspace_sizes_at_the_ends(kw):
+    L = _lib()
+    small = L.kv8_attention_workspace(4, ctypes.byref(_cache()), ctypes.byref(_batch(seqs=0, rows=0)))
+    got = L.kv8_attention_workspace(4, ctypes.byref(_cache()), ctypes.byref(_batch(**kw)))
+    assert got >= small >= 0
