@@ -491,7 +491,7 @@ __global__ __launch_bounds__(64 * kDecodeWaves, decode_waves(D, CT)) void k_kv8_
 // What bounds it: the matrix instructions (4 D operations for each score
 // against about 5 vector instructions of the softmax).  A workgroup takes
 // 32 * CT * NW columns ((row, head) pairs of one KV head, so the heads of a
-// group share its codes) and walks the tokens in tiles of 64: the codes are
+// group share its codes) and walks the tokens in tiles of 32 * ST: the codes are
 // read one tile ahead into registers, widened to bf16 once by the workgroup
 // (K and V times their scales, exact) and written to LDS as the operands of
 // the 32x32x16 instructions, two tiles in turn, one barrier a tile.  As in
@@ -510,18 +510,19 @@ struct PrefillParams {
   float *part;  // [item][split][column][D + 2]
 };
 
-template <int D, int CT, int NW>
+template <int D, int CT, int NW, int ST>
 __global__ __launch_bounds__(64 * NW, NW / 4) void k_kv8_prefill(PrefillParams p) {
   constexpr int kCols = 32 * CT * NW;
   constexpr int KT = D / 16, VT = D / 32;   // operands of a step: K's and (of each 16 tokens) V's
+  constexpr int kUnits = 2 * ST, kShift = ST == 2 ? 6 : 5, kTile = 32 * ST;
   // a wave reads and widens its share of one unit: 64-channel parts of both K
   // and V, or (with one part) K or V
-  constexpr int kShare = NW / 4, kParts = D / 64 >= kShare ? D / 64 / kShare : 1;
+  constexpr int kShare = NW / kUnits, kParts = D / 64 >= kShare ? D / 64 / kShare : 1;
   constexpr bool kBoth = D / 64 >= kShare;
-  __shared__ uint4 kbuf[2][2][KT][64];      // [tile][step][channels 16 t ..][lane]
-  __shared__ uint4 vbuf[2][2][2][VT][64];   // [tile][step][unit][channels 32 t ..][lane]
-  __shared__ __align__(16) int bad[2][4];   // a unit without a page
-  __shared__ __align__(16) int odd[2][2][4];  // a unit with a NaN code of V, by the waves that widen it
+  __shared__ uint4 kbuf[2][ST][KT][64];     // [tile][step][channels 16 t ..][lane]
+  __shared__ uint4 vbuf[2][ST][2][VT][64];  // [tile][step][unit][channels 32 t ..][lane]
+  __shared__ int bad[2][kUnits];            // a unit without a page
+  __shared__ int odd[2][NW];                // whether a wave met a NaN code of V
   // heads side by side, so that those of one XCD's workgroups share its L2; the longest first
   const int h = (int)blockIdx.x % p.c.heads, cb = p.blocks - 1 - (int)blockIdx.x / p.c.heads;
   const int b = (int)blockIdx.y / p.splits, split = (int)blockIdx.y % p.splits;
@@ -536,7 +537,7 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void k_kv8_prefill(PrefillParams p
 
   // the workgroup's tiles
   const int wg_first = pos0 + c0 / p.group, wg_final = pos0 + (min(c0 + kCols, all) - 1) / p.group;
-  int tile0 = low(wg_first) >> 6, tile1 = (min(wg_final + 1, end) + 63) >> 6;
+  int tile0 = low(wg_first) >> kShift, tile1 = (min(wg_final + 1, end) + kTile - 1) >> kShift;
   if (p.splits > 1) {
     const int per = (max(tile1 - tile0, 0) + p.splits - 1) / p.splits;
     tile0 += split * per;
@@ -570,7 +571,7 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void k_kv8_prefill(PrefillParams p
   // lane i: the wave's unit of tile `meta + i`
   int meta = tile0 - 64, at = -1;
   float ksc = 1.f, vsc = 1.f;
-  const int unit = wave & 3, share = wave >> 2;
+  const int unit = wave % kUnits, share = wave / kUnits;
   const int part0 = kBoth ? share * kParts : 0;
   const bool does_k = kBoth || share == 0, does_v = kBoth || share == 1;
   uint4 kr[kParts], vr[kParts];
@@ -578,7 +579,7 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void k_kv8_prefill(PrefillParams p
   float k_next = 1.f, v_next = 1.f;
   auto look_up = [&](int tile) {  // pages and scales of 64 tiles from here
     meta = tile;
-    const int t = (tile + lane) * 64 + unit * 16;
+    const int t = (tile + lane) * kTile + unit * 16;
     at = -1;
     ksc = vsc = 1.f;
     if (t < end && tile + lane < tile1) {
@@ -636,10 +637,9 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void k_kv8_prefill(PrefillParams p
         }
       }
       const bool some = __any(any != 0);
-      if (lane == 0) {
-        odd[buf][kBoth ? share : 0][unit] = some;
-        if (!kBoth || kShare == 1) odd[buf][1][unit] = 0;
-      }
+      if (lane == 0) odd[buf][wave] = some;
+    } else if (lane == 0) {
+      odd[buf][wave] = 0;
     }
   };
 
@@ -655,15 +655,15 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void k_kv8_prefill(PrefillParams p
   }
   lds_barrier();
 
-  f32x16 s[CT][2];
-  bf16x8 pr[CT][4];
+  f32x16 s[CT][ST];
+  bf16x8 pr[CT][kUnits];
   float sum[CT];
   auto scores = [&](int buf) {
     const f32x16 zero = {};
 #pragma unroll
     for (int t = 0; t < KT; ++t)
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
+      for (int j = 0; j < ST; ++j) {
         const bf16x8 k = as_bf16x8(kbuf[buf][j][t][lane]);
 #pragma unroll
         for (int ct = 0; ct < CT; ++ct)
@@ -671,7 +671,7 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void k_kv8_prefill(PrefillParams p
       }
     __builtin_amdgcn_sched_group_barrier(0x100, 6, 0);
 #pragma unroll
-    for (int i = 0; i < 2 * KT - 6; ++i) {
+    for (int i = 0; i < ST * KT - 6; ++i) {
       __builtin_amdgcn_sched_group_barrier(0x8, CT, 0);
       __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
     }
@@ -681,9 +681,9 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void k_kv8_prefill(PrefillParams p
   auto powers = [&]() {
 #pragma unroll
     for (int ct = 0; ct < CT; ++ct) {
-      float part[4];
+      float part[kUnits];
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
+      for (int u = 0; u < kUnits; ++u) {
         float e[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i)
@@ -692,14 +692,19 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void k_kv8_prefill(PrefillParams p
 #pragma unroll
         for (int i = 0; i < 8; ++i) pr[ct][u][i] = (__bf16)e[i];
       }
-      sum[ct] = (part[0] + part[1]) + (part[2] + part[3]);
+      sum[ct] = part[0] + part[1];
+      if constexpr (ST == 2) sum[ct] += part[2] + part[3];
     }
+  };
+  auto any_of = [](const int *flags, int n) {
+    int x = 0;
+#pragma unroll
+    for (int i = 0; i < n; ++i) x |= flags[i];
+    return __builtin_amdgcn_readfirstlane(x) != 0;
   };
   // whether every row of the wave sees every token of the tile
   auto is_whole = [&](int t0, int buf) {
-    const int4 no = *(const int4 *)bad[buf];
-    return (bool)__builtin_amdgcn_readfirstlane(t0 >= full_lo && t0 + 63 <= full_hi &&
-                                                !(no.x | no.y | no.z | no.w));
+    return t0 >= full_lo && t0 + kTile - 1 <= full_hi && !any_of(bad[buf], kUnits);
   };
   // bit r of step j: accumulator row r's token is one that the lane's column sees
   auto sees = [&](int ct, int j, int t0, int buf) {
@@ -715,7 +720,7 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void k_kv8_prefill(PrefillParams p
 #pragma unroll
     for (int ct = 0; ct < CT; ++ct)
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
+      for (int j = 0; j < ST; ++j) {
         const uint32_t bits = sees(ct, j, t0, buf);
 #pragma unroll
         for (int r = 0; r < 16; ++r) s[ct][j][r] = bits >> r & 1u ? s[ct][j][r] : -__builtin_inff();
@@ -727,7 +732,8 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void k_kv8_prefill(PrefillParams p
   };
 
   // tiles that some row of the wave sees: [mine0, mine1)
-  const int mine0 = min(max(any_lo >> 6, tile0), tile1), mine1 = max(min((any_hi >> 6) + 1, tile1), mine0);
+  const int mine0 = min(max(any_lo >> kShift, tile0), tile1);
+  const int mine1 = max(min((any_hi >> kShift) + 1, tile1), mine0);
   int tile = tile0;
   for (; tile < mine0; ++tile) {
     fetch(tile, (tile - tile0) & 1);
@@ -739,12 +745,11 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void k_kv8_prefill(PrefillParams p
   while (true) {
     bool again = false;
     for (; tile < mine1; ++tile) {
-      const int buf = (tile - tile0) & 1, t0 = tile * 64;
+      const int buf = (tile - tile0) & 1, t0 = tile * kTile;
       scores(buf);
       if (!is_whole(t0, buf)) {
         mask(t0, buf);
-        const int4 x = *(const int4 *)odd[buf][0], y = *(const int4 *)odd[buf][1];
-        again = __builtin_amdgcn_readfirstlane(x.x | x.y | x.z | x.w | y.x | y.y | y.z | y.w) != 0;
+        again = any_of(odd[buf], NW);
       }
       powers();
       bool raise = again;
@@ -755,7 +760,7 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void k_kv8_prefill(PrefillParams p
 #pragma unroll
       for (int ct = 0; ct < CT; ++ct) l[ct] += sum[ct];
 #pragma unroll
-      for (int u = 0; u < 4; ++u)
+      for (int u = 0; u < kUnits; ++u)
 #pragma unroll
         for (int t = 0; t < VT; ++t) {
           const bf16x8 v = as_bf16x8(vbuf[buf][u >> 1][u & 1][t][lane]);
@@ -765,7 +770,7 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void k_kv8_prefill(PrefillParams p
         }
       __builtin_amdgcn_sched_group_barrier(0x100, 6, 1);
 #pragma unroll
-      for (int i = 0; i < 4 * VT - 6; ++i) {
+      for (int i = 0; i < kUnits * VT - 6; ++i) {
         __builtin_amdgcn_sched_group_barrier(0x8, CT, 1);
         __builtin_amdgcn_sched_group_barrier(0x100, 1, 1);
       }
@@ -775,14 +780,14 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void k_kv8_prefill(PrefillParams p
     }
     if (!again) break;
 
-    const int buf = (tile - tile0) & 1, t0 = tile * 64;
+    const int buf = (tile - tile0) & 1, t0 = tile * kTile;
     scores(buf);
     mask(t0, buf);
 #pragma unroll
     for (int ct = 0; ct < CT; ++ct) {
       float x = kLowest;
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
+      for (int j = 0; j < ST; ++j)
 #pragma unroll
         for (int r = 0; r < 16; ++r) x = fmaxf(x, s[ct][j][r]);
       x *= cs;
@@ -798,7 +803,7 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void k_kv8_prefill(PrefillParams p
     for (int ct = 0; ct < CT; ++ct) l[ct] += sum[ct];
     fetch(tile, buf);
 #pragma unroll
-    for (int u = 0; u < 4; ++u)
+    for (int u = 0; u < kUnits; ++u)
 #pragma unroll
       for (int t = 0; t < VT; ++t) {
         bf16x8 v = as_bf16x8(vbuf[buf][u >> 1][u & 1][t][lane]), here;
@@ -948,6 +953,17 @@ __global__ __launch_bounds__(256) void k_kv8_weights_few(WeightParams p) {
 
 constexpr int kWeightWaves = 8, kWeightTokens = 64 * kWeightWaves;  // of a workgroup
 
+// Adds x[i] of the lanes n and n ^ O, and leaves them the halves of the sums.
+template <int O>
+__device__ __forceinline__ void fold(float (&x)[32], int n) {
+  const bool up = (n & O) != 0;
+#pragma unroll
+  for (int i = 0; i < O; ++i) {
+    const float lo = x[i], hi = x[i + O];
+    x[i] = (up ? hi : lo) + __shfl_xor(up ? lo : hi, O);
+  }
+}
+
 template <int D>
 __global__ __launch_bounds__(64 * kWeightWaves, 2) void k_kv8_weights_many(WeightParams p) {
   constexpr int KT = D / 16, kOps = 2 * KT;                        // operands of 32 columns, of 64
@@ -1093,16 +1109,19 @@ __global__ __launch_bounds__(64 * kWeightWaves, 2) void k_kv8_weights_many(Weigh
     if (tile + 1 < tile1) store(buf ^ 1);
     lds_barrier();
   }
+  // The 32 columns' sums of each of a lane's 32 tokens: every exchange halves
+  // the tokens a lane holds, until lane n of each half has the whole sum of one.
+  float x[32];
+#pragma unroll
+  for (int i = 0; i < 32; ++i) x[i] = sum[i >> 4][i & 15];
+  fold<16>(x, n);
+  fold<8>(x, n);
+  fold<4>(x, n);
+  fold<2>(x, n);
+  fold<1>(x, n);
+  const int r = n & 15;
   float *out = p.part + (((size_t)piece * p.s.seqs + b) * p.c.heads + h) * p.len_pad;
-#pragma unroll
-  for (int u = 0; u < 2; ++u)
-#pragma unroll
-    for (int r = 0; r < 16; ++r) {
-      float x = sum[u][r];
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) x += __shfl_xor(x, o);
-      if (n == 0) out[t0 + 32 * u + (r & 3) + 8 * (r >> 2) + 4 * half] = x;
-    }
+  out[t0 + 32 * (n >> 4) + (r & 3) + 8 * (r >> 2) + 4 * half] = x[0];
 }
 
 __global__ __launch_bounds__(256) void k_kv8_weights_join(WeightParams p) {
@@ -1128,8 +1147,9 @@ __global__ __launch_bounds__(256) void k_kv8_weights_join(WeightParams p) {
 // kernels take 64 and 62 us, at 66 50 and 60 us, at 105 of 13 short ones 21
 // and 29 us (head size 256: at 120 86 and 80 us).
 constexpr int kv8_few_cols(int dim) { return dim == 256 ? 64 : 128; }
-constexpr int kv8_many_cols(int dim) { return dim == 256 ? 128 : 256; }
-constexpr int kManyGroups = 512;
+constexpr int kManyCols = 256;  // of a workgroup, many rows
+constexpr int kManyGroups = 256;    // one on each CU
+constexpr int kWeightGroups = 512;  // of the second pass over K
 // workgroups wanted: those that the CUs hold at a time (bound of a plan's: kDecodeGroups)
 constexpr int kDecodeGroups = 768;
 int decode_groups(int dim, int ct) { return std::min(256 * decode_waves(dim, ct), kDecodeGroups); }
@@ -1165,12 +1185,21 @@ Kv8Plan kv8_plan(const Kv8Attn &a, const Kv8Pool &c, const Kv8Batch &s, int dim)
       pl.part_floats = (size_t)items * pl.splits * 16 * pl.ct * (dim + 2);
   }
   if (!pl.few) {
-    const int kc = kv8_many_cols(dim);
+    const int kc = kManyCols;
     pl.blocks = (int)((cols + kc - 1) / kc);
     const int64_t items = std::max<int64_t>((int64_t)s.seqs * c.heads * pl.blocks, 1);
     const int64_t seen = a.window ? std::min<int64_t>(a.max_len, (int64_t)a.window + s.max_rows) : a.max_len;
-    // one workgroup fills a CU: split the tokens where there are fewer, into pieces of 512 at least
-    pl.splits = (int)std::max<int64_t>(std::min<int64_t>(kManyGroups / items, seen / 512), 1);
+    // One workgroup fills a CU.  The tokens are split where there are too few of
+    // them, into pieces of 512 at least (64 rows of 32 heads over 60000 tokens:
+    // 256 workgroups 102 us, 512 131 us, 1024 199 us), and into pieces of 4096 up
+    // to four for each CU, since the lengths may differ; of the numbers that
+    // leave the fewest CUs idle in the last turn if they do not, the largest.
+    const int64_t fill = std::max<int64_t>(std::min<int64_t>(kManyGroups / items, seen / 512), 1);
+    const int64_t most = std::max<int64_t>(std::min<int64_t>(4 * kManyGroups / items, seen / 4096), fill);
+    auto turns = [&](int64_t n) { return (double)((items * n + kManyGroups - 1) / kManyGroups) / (double)n; };
+    pl.splits = 1;
+    for (int64_t n = 2; n <= most; ++n)
+      if (turns(n) <= 1.02 * turns(pl.splits)) pl.splits = (int)n;
     if (pl.splits > 1) pl.part_floats = (size_t)items * pl.splits * kc * (dim + 2);
   }
   pl.len_pad = (a.max_len + kWeightTokens - 1) / kWeightTokens * kWeightTokens;
@@ -1183,7 +1212,7 @@ Kv8Plan kv8_plan(const Kv8Attn &a, const Kv8Pool &c, const Kv8Batch &s, int dim)
     } else {
       // two workgroups a CU where the columns allow it
       const int64_t groups = (int64_t)s.seqs * c.heads * (pl.len_pad / kWeightTokens);
-      pl.parts = (int)std::max<int64_t>(std::min<int64_t>(kManyGroups / std::max<int64_t>(groups, 1), cols / 256), 1);
+      pl.parts = (int)std::max<int64_t>(std::min<int64_t>(kWeightGroups / std::max<int64_t>(groups, 1), cols / 256), 1);
       pl.score_floats = tokens * (size_t)pl.parts;
     }
   }
@@ -1193,15 +1222,15 @@ Kv8Plan kv8_plan(const Kv8Attn &a, const Kv8Pool &c, const Kv8Batch &s, int dim)
 size_t kv8_part_bound(const Kv8Attn &a, const Kv8Pool &c, const Kv8Batch &s, int dim) {
   const Kv8Plan pl = kv8_plan(a, c, s, dim);
   // the most rows that are few
-  const size_t few = (size_t)kv8_few_cols(dim), many = (size_t)kv8_many_cols(dim), width = (size_t)dim + 2;
+  const size_t few = (size_t)kv8_few_cols(dim), many = (size_t)kManyCols, width = (size_t)dim + 2;
   Kv8Batch s2 = s;
   s2.max_rows = std::min(s.max_rows, std::max((int)few / pl.group, 1));
   size_t floats = std::max(pl.part_floats, kv8_plan(a, c, s2, dim).part_floats);
   // fewer tokens, or a window: shorter pieces, but no more workgroups than kDecodeGroups and one for each item
   floats = std::max(floats, (kDecodeGroups * 16 * (size_t)(256 / dim) + (size_t)s.seqs * c.heads * few) * width);
-  if (!pl.few) floats = std::max(floats, kManyGroups * many * width);
-  // 16 columns' scores, or kManyGroups parts of kWeightTokens
-  if (c.w) floats += std::max((size_t)s.seqs * c.heads * pl.len_pad * 16, (size_t)kManyGroups * kWeightTokens * 2);
+  if (!pl.few) floats = std::max(floats, 4 * kManyGroups * many * width);
+  // 16 columns' scores, or kWeightGroups parts of kWeightTokens
+  if (c.w) floats += std::max((size_t)s.seqs * c.heads * pl.len_pad * 16, (size_t)kWeightGroups * kWeightTokens * 2);
   return floats;
 }
 
@@ -1221,13 +1250,13 @@ hipError_t launch_kv8_attention(const Kv8Attn &a, const Kv8Pool &c, const Kv8Bat
   }
   const PrefillParams p{a, c, s, pl.group, pl.blocks, pl.splits, part};
   const dim3 grid((unsigned)c.heads * (unsigned)pl.blocks, (unsigned)(s.seqs * pl.splits));
-  auto k = dim == 64 ? k_kv8_prefill<64, 1, 8> : dim == 128 ? k_kv8_prefill<128, 1, 8> : k_kv8_prefill<256, 1, 4>;
-  k<<<grid, dim3(dim==256?256:512), 0, stream>>>(p);
+  auto k = dim == 64 ? k_kv8_prefill<64, 1, 8, 2> : dim == 128 ? k_kv8_prefill<128, 1, 8, 2> : k_kv8_prefill<256, 1, 8, 1>;
+  k<<<grid, dim3(512), 0, stream>>>(p);
   if (hipError_t e = hipGetLastError()) return e;
   if (pl.splits == 1) return hipSuccess;
   const dim3 jgrid((unsigned)((cols_of(s, pl) + 3) / 4), (unsigned)c.heads, (unsigned)s.seqs);
   auto kj = dim == 64 ? k_kv8_prefill_join<64> : dim == 128 ? k_kv8_prefill_join<128> : k_kv8_prefill_join<256>;
-  kj<<<jgrid, dim3(256), 0, stream>>>(p, kv8_many_cols(dim));
+  kj<<<jgrid, dim3(256), 0, stream>>>(p, kManyCols);
   return hipGetLastError();
 }
 
