@@ -8,6 +8,7 @@
 // except in the lowest, subnormal codes, and it lets a later token raise
 // the page's scale without a second rounding of the codes that are there
 // (kv8_rescale4).
+#include <algorithm>
 #include <type_traits>
 
 #include "kv8_common.h"
@@ -527,7 +528,7 @@ __global__ __launch_bounds__(256) void k_kv8_move(MoveParams p) {
   __shared__ int src_slot[128];
   __shared__ float src_scale[128];
   const int b = (int)blockIdx.z, h = (int)blockIdx.y >> 1, isv = (int)blockIdx.y & 1;
-  const int tid = (int)threadIdx.x;
+  const int tid = (int)threadIdx.x, nt = (int)blockDim.x;
   const int shift = p.c.shift, page = 1 << shift, col = (int)blockIdx.x;
   const int len = min(min(kv8_span(p.s, shift, b).len, p.max_len), p.keep);
   const int n = min(len - (col << shift), page);  // tokens of this page
@@ -557,14 +558,14 @@ __global__ __launch_bounds__(256) void k_kv8_move(MoveParams p) {
   if (!isv) {
 #pragma unroll
     for (int k = 0; k < NP; ++k) {  // piece: channels 16 ch of token t, tokens side by side
-      const int i = tid + 256 * k, t = i % page, ch = i / page;
+      const int i = tid + nt * k, t = i % page, ch = i / page;
       uint4 v = uint4{0, 0, 0, 0};
       if (ch < D / 16 && t < n) v = from(t, ch * 256 + src_slot[t] * 16);
       w[k][0] = v.x, w[k][1] = v.y, w[k][2] = v.z, w[k][3] = v.w;
     }
 #pragma unroll
     for (int k = 0; k < NP; ++k) {
-      const float s = src_scale[min((tid + 256 * k) % page, n - 1)];
+      const float s = src_scale[min((tid + nt * k) % page, n - 1)];
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
         float f[4];
@@ -576,7 +577,7 @@ __global__ __launch_bounds__(256) void k_kv8_move(MoveParams p) {
   } else {
 #pragma unroll
     for (int k = 0; k < NP; ++k) {  // piece: group of four tokens q, channels 64 a + 16 c + r
-      const int i = tid + 256 * k, q = i / (D / 4), ar = i % (D / 4);
+      const int i = tid + nt * k, q = i / (D / 4), ar = i % (D / 4);
       uint4 v[4];
       uint32_t sel[4];
 #pragma unroll
@@ -601,7 +602,7 @@ __global__ __launch_bounds__(256) void k_kv8_move(MoveParams p) {
     }
 #pragma unroll
     for (int k = 0; k < NP; ++k) {
-      const int q = (tid + 256 * k) / (D / 4);
+      const int q = (tid + nt * k) / (D / 4);
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
         float f[4];
@@ -621,7 +622,7 @@ __global__ __launch_bounds__(256) void k_kv8_move(MoveParams p) {
   if (!isv) {
 #pragma unroll
     for (int k = 0; k < NP; ++k) {
-      const int i = tid + 256 * k, t = i % page, ch = i / page;
+      const int i = tid + nt * k, t = i % page, ch = i / page;
       if (ch >= D / 16 || t >= n) continue;
       const float f = factor(t);
       *(uint4 *)(out + kv8_k_at(t, 16 * ch, D)) = uint4{kv8_rescale4(w[k][0], f), kv8_rescale4(w[k][1], f),
@@ -630,7 +631,7 @@ __global__ __launch_bounds__(256) void k_kv8_move(MoveParams p) {
   } else {
 #pragma unroll
     for (int k = 0; k < NP; ++k) {
-      const int i = tid + 256 * k, q = i / (D / 4), ar = i % (D / 4);
+      const int i = tid + nt * k, q = i / (D / 4), ar = i % (D / 4);
       if (4 * q >= n) continue;
       uint4 *at = (uint4 *)(out + kv8_v_at(4 * q, (ar >> 4) * 64 + (ar & 15), D));
       float f[4];
@@ -729,7 +730,7 @@ hipError_t launch_kv8_evict(const Kv8Pool &c, const Kv8Batch &s, int dim, int ma
   };
   auto k = dim == 64 ? pick(std::integral_constant<int, 64>{})
                      : dim == 128 ? pick(std::integral_constant<int, 128>{}) : pick(std::integral_constant<int, 256>{});
-  k<<<grid, dim3(256), 0, stream>>>(p);
+  k<<<grid, dim3((unsigned)std::min(page * dim / 16, 256)), 0, stream>>>(p);  // a small page: a thread a piece
   return hipGetLastError();
 }
 
