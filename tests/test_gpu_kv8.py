@@ -195,11 +195,11 @@ def _problem(dim, page, heads, q_heads, lens, rows, window, seed=11, weights=Tru
     return c, table, q
 
 
-def _check(c, table, q, q_heads, lens, rows, window=0, accumulate=True, max_len=None, **kw):
+def _check(c, table, q, q_heads, lens, rows, window=0, accumulate=True, max_len=None, factor=0.02, **kw):
     """Runs the call and compares out, lse and the weights; returns them."""
     dim = c.k_codes.shape[3]
     pool, dev = ref.Pool(c), _gpu(c)
-    scale = 0.02 / math.sqrt(dim)
+    scale = factor / math.sqrt(dim)
     out, lse, b_out, b_lse, w = pool.attention(q[:, 1:1 + q_heads], table, lens, rows, scale, window, max_len)
     got = nv.kv8_attention(q.cuda()[:, 1:1 + q_heads], dev, table.cuda(), _i32(lens).cuda(), _starts(rows).cuda(),
                            scale=scale, window=window, max_rows=max(rows), lse=True, accumulate=accumulate,
@@ -224,6 +224,84 @@ def test_attention(dim, page, heads, q_heads, lens, rows, window):
     _say("attention", dim, page, heads, q_heads, lens, rows, window)
     c, table, q = _problem(dim, page, heads, q_heads, lens, rows, window)
     _check(c, table, q, q_heads, lens, rows, window)
+
+
+COLUMNS = [  # as CASES; rows times query heads of a KV head around what one workgroup takes, up to the wide kernel
+    (128, 64, 1, 4, [300, 64, 9], [5, 8, 1], 0),
+    (128, 64, 2, 8, [700, 130], [10, 3], 0),
+    (128, 32, 1, 3, [513], [17], 0),
+    (128, 16, 1, 10, [250, 1000], [12, 7], 60),
+    (64, 64, 2, 2, [400, 33], [33, 33], 0),
+    (64, 128, 1, 8, [1500], [16], 200),
+    (64, 16, 1, 3, [90, 50], [43, 2], 0),
+    (64, 32, 1, 16, [4000], [8], 0),
+    (256, 64, 1, 4, [600, 70], [8, 4], 0),
+    (256, 16, 1, 1, [333], [33], 50),
+    (256, 128, 2, 8, [1025, 100], [16, 9], 0),
+    (256, 32, 1, 5, [777], [13], 0),
+    (128, 64, 1, 1, [129], [128], 0),
+    (128, 64, 1, 1, [129], [129], 0),
+    (256, 64, 1, 2, [2000, 1900], [300, 257], 0),
+    (64, 64, 1, 1, [9000], [600], 0),
+    (128, 128, 1, 1, [5000, 64], [400, 64], 1500),
+    (128, 16, 1, 1, [1, 0, 17, 255, 256, 257], [1, 0, 17, 255, 256, 257], 0),
+]
+
+
+@pytest.mark.parametrize("dim,page,heads,q_heads,lens,rows,window", COLUMNS)
+def test_attention_columns(dim, page, heads, q_heads, lens, rows, window):
+    _say("attention", dim, page, heads, q_heads, lens, rows, window)
+    c, table, q = _problem(dim, page, heads, q_heads, lens, rows, window, seed=90)
+    _check(c, table, q, q_heads, lens, rows, window)
+
+
+@pytest.mark.parametrize("factor", [-0.02, 0.0, -1e-30, 1.0])
+@pytest.mark.parametrize("dim,rows", [(128, [1, 3]), (64, [20, 9]), (256, [12, 16]), (128, [100, 60])])
+def test_attention_scales(dim, rows, factor):
+    """Negative scales, and 0: every token counts alike; 1: each row sees little but its largest score."""
+    _say("attention, scale", dim, rows, factor)
+    c, table, q = _problem(dim, 64, 1, 4, [200, 131], rows, 0, seed=100)
+    _, lse, _ = _check(c, table, q, 4, [200, 131], rows, factor=factor)
+    if factor == 0.0:
+        seen = torch.tensor([n - r + 1 + i for n, r in zip([200, 131], rows) for i in range(r)]).double()
+        assert float((lse.cpu().double() - seen.log()[:, None]).abs().max()) <= 2.0 ** -20
+
+
+@pytest.mark.parametrize("dim,rows", [(128, [20, 12]), (64, [9, 31]), (256, [13, 16])])
+def test_attention_columns_with_unnamed_pages_and_far_from_zero(dim, rows):
+    _say("attention, bad pages and large scores", dim, rows)
+    c, table, q = _problem(dim, 16, 1, 4, [150, 90], rows, 0, seed=110)
+    table[0, 2], table[0, 7], table[1, 0] = -1, 2 ** 30, c.k_codes.shape[0]
+    _check(c, table, q * 40, 4, [150, 90], rows)
+    _check(c, table, q, 4, [150, 90], rows, max_len=37)
+    table[:] = -1
+    out, lse, _ = _check(c, table, q, 4, [150, 90], rows)
+    assert not out.any() and bool((lse == NEG).all())
+
+
+@pytest.mark.parametrize("rows", [[1, 1], [6, 5], [50, 70]])
+def test_strides(rows):
+    """K and V of one head shared by several (a head stride of 0), q with its heads outermost, rows far apart."""
+    _say("strides", rows)
+    lens, dim, page = [100, 77], 128, 16
+    c = _filled(12, 3, dim, page, 120, weights=True)
+    pool, dev = ref.Pool(c), _gpu(c)
+    table = _table(lens, page, 12, 121)
+    g = _gen(122)
+    k = torch.randn(sum(rows), 1, dim, generator=g).bfloat16().expand(-1, 3, -1)
+    v = torch.randn(3, sum(rows), dim, generator=g).bfloat16().transpose(0, 1)
+    pool.append(k, v, table, lens, rows)
+    kd = k[:, :1].cuda().expand(-1, 3, -1)
+    vd = v.transpose(0, 1).contiguous().cuda().transpose(0, 1)
+    assert kd.stride(1) == 0 and vd.stride(0) == dim
+    nv.kv8_append(kd, vd, dev, table.cuda(), _i32(lens).cuda(), _starts(rows).cuda(), max_rows=max(rows))
+    _same(pool, dev)
+    q = torch.randn(6, sum(rows), 3 * dim, generator=g).bfloat16()
+    qd = q.cuda().transpose(0, 1)[:, :, dim:2 * dim]
+    out, lse, b_out, b_lse, _ = pool.attention(q.transpose(0, 1)[:, :, dim:2 * dim], table, lens, rows, dim ** -0.5)
+    got = nv.kv8_attention(qd, dev, table.cuda(), _i32(lens).cuda(), _starts(rows).cuda(), max_rows=max(rows), lse=True)
+    _within(got[0], out, b_out, "out")
+    _within(got[1], lse, b_lse, "lse")
 
 
 @pytest.mark.parametrize("rows", [[1, 1], [4, 4], [100, 60]])
@@ -271,7 +349,8 @@ def test_unseen_tokens_have_no_influence(dim, page, rows, window):
 
 @pytest.mark.parametrize("dim,page,rows,window", [(128, 64, [1, 1, 1], 0), (128, 64, [4, 2, 1], 0), (64, 16, [70, 30, 9], 0),
                                                   (256, 32, [5, 90, 33], 40), (128, 32, [3, 1, 2], 21),
-                                                  (128, 128, [90, 130, 35], 0)])
+                                                  (128, 128, [90, 130, 35], 0), (128, 64, [20, 12, 8], 0),
+                                                  (64, 16, [30, 9, 2], 40), (256, 64, [13, 9, 16], 0)])
 def test_finite_where_only_unseen_places_hold_nan(dim, page, rows, window):
     """The same with NaN in every code that no row sees, and in the last token's V, which only the last row sees:
     every other row's result is finite."""
