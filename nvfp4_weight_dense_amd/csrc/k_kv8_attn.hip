@@ -933,21 +933,31 @@ __global__ __launch_bounds__(256) void k_kv8_weights_few(WeightParams p) {
   float sum = 0.f;
   const float *x = p.scores + (size_t)b * p.c.heads * p.cols * p.len_pad + j;
   const float *z = p.a.lse + (size_t)sp.r0 * p.a.q_heads;
-  const int cols = rows * p.group;
-  for (int h = 0; h < p.c.heads; ++h, x += (size_t)p.cols * p.len_pad, z += p.group)
-    for (int c0 = 0; c0 < cols; c0 += 8) {  // eight loads at a time
-      float y[8];
+  // Columns of all heads in turn, kStep loads at a time (16 sequences of 6007
+  // tokens, 8 heads of 4 columns: a head at a time 11.4 us, 16 columns 8.3 us).
+  constexpr int kStep = 16;
+  const int cols = rows * p.group, total = p.c.heads * cols;
+  int h = 0, c = 0, i = 0, u = 0;  // head, its column (row i, query head u of the group)
+  for (int e0 = 0; e0 < total; e0 += kStep) {
+    float y[kStep];
+    // (columns beyond a sequence's own rows are not written)
+    int hh = h, cc = c;
 #pragma unroll
-      for (int k = 0; k < 8; ++k) y[k] = c0 + k < cols ? x[(size_t)(c0 + k) * p.len_pad] : -__builtin_inff();
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const int c = min(c0 + k, cols - 1), i = c / p.group;
-        // (a row that sees nothing has -inf there and -inf scores)
-        sum += y[k] == -__builtin_inff()
-                   ? 0.f
-                   : __builtin_amdgcn_exp2f(y[k] - z[(size_t)i * p.a.q_heads + c - i * p.group] * kLog2e);
-      }
+    for (int k = 0; k < kStep; ++k) {
+      const float *at = x + (size_t)(min(hh, p.c.heads - 1) * p.cols + cc) * p.len_pad;
+      y[k] = *at;
+      if (++cc == cols) cc = 0, ++hh;
     }
+#pragma unroll
+    for (int k = 0; k < kStep; ++k) {
+      // (a row that sees nothing has -inf there and -inf scores)
+      const float lse = z[(size_t)i * p.a.q_heads + min(h, p.c.heads - 1) * p.group + u];
+      const float add = y[k] == -__builtin_inff() ? 0.f : __builtin_amdgcn_exp2f(y[k] - lse * kLog2e);
+      sum += h < p.c.heads ? add : 0.f;
+      if (++u == p.group) u = 0, ++i;
+      if (++c == cols) c = i = u = 0, ++h;
+    }
+  }
   p.c.w[((size_t)id << p.c.shift) + (j & ((1 << p.c.shift) - 1))] += sum;
 }
 

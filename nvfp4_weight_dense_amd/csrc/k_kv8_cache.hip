@@ -277,9 +277,20 @@ __device__ __forceinline__ Span select_span(const SelectParams &p, int b) {
   s.need = p.keep - p.sink - p.recent;
   return s;
 }
-__device__ __forceinline__ uint32_t token_word(const SelectParams &p, int b, int j) {
-  const int id = kv8_page(p.s, p.c, b, j >> p.c.shift);
-  return id < 0 ? 0u : order_word(p.c.w[((size_t)id << p.c.shift) + (j & ((1 << p.c.shift) - 1))]);
+// The words of the tokens j + k * step below hi (all loads in flight together;
+// hi > 0, and places beyond it read its last token).
+template <int N>
+__device__ __forceinline__ void token_words(const SelectParams &p, int b, int j, int step, int hi, uint32_t (&u)[N]) {
+  int id[N];
+#pragma unroll
+  for (int k = 0; k < N; ++k) id[k] = kv8_page(p.s, p.c, b, min(j + k * step, hi - 1) >> p.c.shift);
+#pragma unroll
+  for (int k = 0; k < N; ++k) {
+    const int slot = min(j + k * step, hi - 1) & ((1 << p.c.shift) - 1);
+    u[k] = __float_as_uint(p.c.w[((size_t)max(id[k], 0) << p.c.shift) + slot]);
+  }
+#pragma unroll
+  for (int k = 0; k < N; ++k) u[k] = id[k] < 0 ? 0u : order_word(__uint_as_float(u[k]));
 }
 
 // The digit of the `left`-th largest word from a histogram (1 <= left <= its
@@ -383,10 +394,16 @@ __global__ __launch_bounds__(kWholeThreads) void k_kv8_select(SelectParams p) {
   if (sp.need > 0) {
     for (int i = tid; i < kBins; i += kWholeThreads) hist[i] = 0;
     __syncthreads();
-    for (int j = sp.lo + tid; j < sp.hi; j += kWholeThreads) {
-      const uint32_t u = token_word(p, b, j);
-      words[j] = u;
-      atomicAdd(&hist[digit(u, 0)], 1u);
+    for (int j0 = sp.lo + tid; j0 < sp.hi; j0 += 8 * kWholeThreads) {
+      uint32_t u[8];
+      token_words(p, b, j0, kWholeThreads, sp.hi, u);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int j = j0 + k * kWholeThreads;
+        if (j >= sp.hi) break;
+        words[j] = u[k];
+        atomicAdd(&hist[digit(u[k], 0)], 1u);
+      }
     }
     __syncthreads();
     for (int i = 0; i < 3; ++i) {
@@ -433,8 +450,9 @@ __global__ __launch_bounds__(kDealt) void k_kv8_select_stage(SelectParams p) {
   for (int k = 0; k < 4; ++k) {
     const int j = j0 + tid + k * kDealt;
     in[k] = j < j1 && j >= sp.lo && j < sp.hi && sp.need > 0;
-    u[k] = in[k] ? (STAGE == 0 ? token_word(p, b, j) : words[j]) : 0;
+    if constexpr (STAGE > 0) u[k] = words[min(max(j, sp.lo), max(sp.hi - 1, sp.lo))];
   }
+  if constexpr (STAGE == 0) token_words(p, b, j0 + tid, kDealt, sp.len, u);
   if constexpr (STAGE < 3) {
     if (sp.need == 0) return;
     for (int i = tid; i < kBins; i += kDealt) local[i] = 0;
