@@ -35,6 +35,12 @@ constexpr float kLog2e = 1.44269504088896341f, kLn2 = 0.693147180559945309f;
 // A workgroup's four waves take its steps in turn; their results are joined
 // in LDS, those of a sequence's workgroups by the last of them to arrive, in
 // the order of the tokens.
+//
+// Measured (32 query heads on 8 KV heads of 128 but where said): 48 sequences
+// of up to 8191 tokens 78 us, 5400 GB/s of codes; 2 of 131000 (40 heads) 93 us,
+// 5780 GB/s, which is what reading alone reaches; 24 of 4099 with four rows, a
+// window of 2048 and heads of 64 16 us (40 MB: start, look-ups and join are
+// most of it); one of 521 12 us, of which the call's own 12 us hide the kernel's 9.
 
 constexpr int kDecodeWaves = 4;
 constexpr int kMaxSplits = 128;
@@ -502,15 +508,33 @@ __global__ __launch_bounds__(64 * kDecodeWaves, decode_waves(D, CT)) void k_kv8_
 // token groups `half` and 2 + half.  No maximum is looked for either: the
 // running one stays until a tile's sum of powers passes kRaise (overflow to
 // infinity does), and only then is it found and the powers taken again.
+//
+// An item is a block of columns over all its tokens.  Where there are many, a
+// workgroup takes one.  Where there are few (DEALT) the tiles of all items
+// stand in a row, one KV head after the other, and are dealt in equal runs
+// over one workgroup per CU, whatever the lengths: a run's first and last item
+// may be parts, whose sums and statistics go to memory (two places a
+// workgroup) for a second kernel to join in the order of the tokens.
+//
+// Measured: a prompt of 8192 tokens, 32 heads on 8 of 128, 518 us, 1060
+// TFLOP/s; 3 pieces of up to 1023 rows, 16 heads on 4 of 256, a window of 3000,
+// 177 us, 690 TFLOP/s (its 32-token tiles and one wave's 128 accumulators leave
+// the softmax less to hide behind).
 struct PrefillParams {
   Kv8Attn a;
   Kv8Pool c;
   Kv8Batch s;
-  int group, blocks, splits;
-  float *part;  // [item][split][column][D + 2]
+  int group, blocks;
+  float *part;  // [workgroup][2]: o as the kernel holds it, then m and l
+  int2 *parts;  // [item]: the workgroup with its first part, how many parts (0: whole)
 };
+constexpr int kManyCols = 256;     // of an item
+constexpr int kManyGroups = 256;   // one on each CU
+constexpr int kManyItems = 384;    // most that are dealt
+constexpr int kStart = 6;          // an item's start and end cost as much as so many tiles
+constexpr int many_floats(int dim) { return kManyCols * dim + 4 * kManyCols; }  // of a part
 
-template <int D, int CT, int NW, int ST>
+template <int D, int CT, int NW, int ST, bool DEALT>
 __global__ __launch_bounds__(64 * NW, NW / 4) void k_kv8_prefill(PrefillParams p) {
   constexpr int kCols = 32 * CT * NW;
   constexpr int KT = D / 16, VT = D / 32;   // operands of a step: K's and (of each 16 tokens) V's
@@ -523,381 +547,451 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void k_kv8_prefill(PrefillParams p
   __shared__ uint4 vbuf[2][ST][2][VT][64];  // [tile][step][unit][channels 32 t ..][lane]
   __shared__ int bad[2][kUnits];            // a unit without a page
   __shared__ int odd[2][NW];                // whether a wave met a NaN code of V
-  // heads side by side, so that those of one XCD's workgroups share its L2; the longest first
-  const int h = (int)blockIdx.x % p.c.heads, cb = p.blocks - 1 - (int)blockIdx.x / p.c.heads;
-  const int b = (int)blockIdx.y / p.splits, split = (int)blockIdx.y % p.splits;
+  constexpr int kPairs = 64 * NW;
+  __shared__ int before[DEALT ? kPairs + 1 : 1], wave_sum[NW];  // tiles of one head before each (sequence, block)
+  static_assert(kCols == kManyCols && kPairs >= kManyItems && (kPairs & (kPairs - 1)) == 0, "");
   const int tid = (int)threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int n = lane & 31, half = lane >> 5, shift = p.c.shift;
-  const Kv8Span sp = kv8_span(p.s, shift, b);
-  const int all = min(sp.rows, p.s.max_rows) * p.group, c0 = cb * kCols;
-  if (c0 >= all) return;
-  const int end = min(sp.len, p.a.max_len), pos0 = sp.len - sp.rows;
   auto low = [&](int pos) { return p.a.window ? max(pos - p.a.window + 1, 0) : 0; };
-
-  // the workgroup's tiles
-  const int wg_first = pos0 + c0 / p.group, wg_final = pos0 + (min(c0 + kCols, all) - 1) / p.group;
-  int tile0 = low(wg_first) >> kShift, tile1 = (min(wg_final + 1, end) + kTile - 1) >> kShift;
-  if (p.splits > 1) {
-    const int per = (max(tile1 - tile0, 0) + p.splits - 1) / p.splits;
-    tile0 += split * per;
-    tile1 = min(tile1, tile0 + per);
+  // the tiles of an item: [x, y)
+  auto tiles_of = [&](const Kv8Span &sp, int c0) {
+    const int all = min(sp.rows, p.s.max_rows) * p.group, pos0 = sp.len - sp.rows;
+    const int wg_first = pos0 + c0 / p.group, wg_final = pos0 + (min(c0 + kCols, all) - 1) / p.group;
+    return int2{low(wg_first) >> kShift, (min(min(wg_final + 1, sp.len), p.a.max_len) + kTile - 1) >> kShift};
+  };
+  // heads side by side, so that those of one XCD's workgroups share its L2; the longest first
+  int h = (int)blockIdx.x % p.c.heads, cb = p.blocks - 1 - (int)blockIdx.x / p.c.heads, b = (int)blockIdx.y;
+  // a run [run0, run1) of the tiles of all heads, `row` of them a head's
+  int run0 = 0, run1 = 1, row = 1, per = 1, rank = 0;
+  const int pairs = p.s.seqs * p.blocks;
+  if constexpr (DEALT) {
+    const int seq = min(tid / p.blocks, p.s.seqs - 1), first = (tid - seq * p.blocks) * kCols;
+    const Kv8Span one = kv8_span(p.s, shift, seq);
+    const int2 x = tiles_of(one, first);
+    // (one at least where there are columns: they may see nothing, and have results all the same)
+    const int sum =
+        tid < pairs && first < min(one.rows, p.s.max_rows) * p.group ? kStart + max(x.y - x.x, 1) : 0;
+    int incl = sum;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+      const int x = __shfl_up(incl, o);
+      if (lane >= o) incl += x;
+    }
+    if (lane == 63) wave_sum[wave] = incl;
+    __syncthreads();
+    for (int i = 0; i < wave; ++i) incl += wave_sum[i];
+    before[tid + 1] = incl;
+    if (tid == 0) before[0] = 0;
+    __syncthreads();
+    row = __builtin_amdgcn_readfirstlane(before[pairs]);
+    const int total = row * p.c.heads, groups = (int)gridDim.x;
+    per = max((total + groups - 1) / groups, kStart + 512 / kTile);
+    // neighbouring runs on one XCD (a workgroup's is its number modulo 8): they read the same codes
+    rank = groups % 8 ? (int)blockIdx.x : (int)blockIdx.x % 8 * (groups / 8) + (int)blockIdx.x / 8;
+    run0 = min(rank * per, total);
+    run1 = min(run0 + per, total);
   }
-  // the wave's columns and the tokens that its first and last row see
-  const int w0 = c0 + wave * 32 * CT, cols = min(all - w0, 32 * CT);
-  const int first = pos0 + w0 / p.group, final = pos0 + (w0 + max(cols, 1) - 1) / p.group;
-  const int full_lo = low(final), full_hi = min(first, end - 1);
-  const int any_lo = low(first), any_hi = cols > 0 ? min(final, end - 1) : -1;
-
-  const float cs = fmaxf(fabsf(p.a.scale) * kLog2e, 1.1754944e-38f);  // its sign goes to q
-  const uint32_t flip = p.a.scale < 0.f ? 0x80008000u : 0u;
-  bf16x8 q[CT][KT];
-  int lo[CT], hi[CT];
+  while (run0 < run1) {
+    int part_at = -1, skip = 0, most = 0x7FFFFFFF;  // where a part goes; its first tile and how many
+    if constexpr (DEALT) {
+      h = run0 / row;
+      const int x = run0 - h * row;
+      int pair = 0;  // the last with before[pair] <= x, found bit by bit (equal ones: the last has tiles)
 #pragma unroll
-  for (int ct = 0; ct < CT; ++ct) {
-    const int c = w0 + ct * 32 + n, i = c / p.group;
-    const bool in = c < all;
-    const __bf16 *qr = (const __bf16 *)p.a.q.ptr + (int64_t)(sp.r0 + (in ? i : 0)) * p.a.q.row_stride +
-                       (int64_t)(h * p.group + (in ? c % p.group : 0)) * p.a.q.head_stride;
-#pragma unroll
-    for (int t = 0; t < KT; ++t) {
-      const uint4 w = *(const uint4 *)(qr + 16 * t + 8 * half);
-      q[ct][t] = as_bf16x8(in ? uint4{w.x ^ flip, w.y ^ flip, w.z ^ flip, w.w ^ flip} : uint4{0, 0, 0, 0});
-    }
-    lo[ct] = low(pos0 + i);
-    hi[ct] = min(pos0 + i, end - 1);
-  }
-
-  // lane i: the wave's unit of tile `meta + i`
-  int meta = tile0 - 64, at = -1;
-  float ksc = 1.f, vsc = 1.f;
-  const int unit = wave % kUnits, share = wave / kUnits;
-  const int part0 = kBoth ? share * kParts : 0;
-  const bool does_k = kBoth || share == 0, does_v = kBoth || share == 1;
-  uint4 kr[kParts], vr[kParts];
-  int a_next = -1;  // of the tile in kr and vr
-  float k_next = 1.f, v_next = 1.f;
-  auto look_up = [&](int tile) {  // pages and scales of 64 tiles from here
-    meta = tile;
-    const int t = (tile + lane) * kTile + unit * 16;
-    at = -1;
-    ksc = vsc = 1.f;
-    if (t < end && tile + lane < tile1) {
-      const int id = kv8_page(p.s, p.c, b, t >> shift);
-      if (id >= 0) {
-        const size_t ph = (size_t)id * p.c.heads + h;
-        at = (int)((ph << (shift - 4)) + ((t >> 4) & ((1 << (shift - 4)) - 1)));
-        ksc = kv8_scale(p.c.ks[ph]);
-        vsc = kv8_scale(p.c.vs[ph]);
+      for (int bit = kPairs / 2; bit > 0; bit >>= 1)
+        if (pair + bit < pairs && __builtin_amdgcn_readfirstlane(before[pair + bit]) <= x) pair += bit;
+      b = pair / p.blocks;
+      cb = pair - b * p.blocks;
+      const int from = __builtin_amdgcn_readfirstlane(before[pair]);
+      const int size = __builtin_amdgcn_readfirstlane(before[pair + 1]) - from;
+      skip = x - from;
+      most = min(size - skip, run1 - run0);
+      const bool whole = most == size;
+      if (!whole) part_at = 2 * rank + (skip == 0 ? 1 : 0);
+      if (skip == 0 && tid == 0) {
+        const int w0 = run0 / per, w1 = (run0 + size - 1) / per;
+        p.parts[((size_t)b * p.c.heads + h) * p.blocks + cb] = int2{w0, whole ? 0 : w1 - w0 + 1};
       }
+      run0 += most;
+    } else {
+      run0 = run1;
     }
-  };
-  auto load = [&](int tile) {
-    if (tile - meta >= 64) look_up(tile);
-    a_next = __builtin_amdgcn_readlane(at, tile - meta);
-    k_next = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, ksc), tile - meta));
-    v_next = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, vsc), tile - meta));
-    // (a unit that no page holds reads the pool's first; its scores are masked)
-    const size_t off = (size_t)(a_next == -1 ? 0u : (uint32_t)a_next) * (16 * D);
-    if (does_k) {
-      const uint4 *k = (const uint4 *)(p.c.k + off) + 64 * part0 + lane;
-#pragma unroll
-      for (int t = 0; t < kParts; ++t) kr[t] = k[64 * t];
-    }
-    if (does_v) {
-      const uint4 *v = (const uint4 *)(p.c.v + off) + 64 * part0 + lane;
-#pragma unroll
-      for (int t = 0; t < kParts; ++t) vr[t] = v[64 * t];
-    }
-  };
-  auto widen = [&](int buf) {
-    const int r = lane & 15, g = lane >> 4, step = unit >> 1;
-    if (does_k) {
-#pragma unroll
-      for (int t = 0; t < kParts; ++t) {  // token r, channels 16 (4 (part0 + t) + g) ..
-        uint4 *to = &kbuf[buf][step][4 * (part0 + t) + g][16 * (unit & 1) + r];
-        to[0] = __builtin_bit_cast(uint4, fp8x8_to_bf16(kr[t].x, kr[t].y, k_next));
-        to[32] = __builtin_bit_cast(uint4, fp8x8_to_bf16(kr[t].z, kr[t].w, k_next));
-      }
-      if (lane == 0) bad[buf][unit] = a_next == -1;
-    }
-    if (does_v) {
-      uint32_t any = 0;
-#pragma unroll
-      for (int t = 0; t < kParts; ++t) {  // tokens 4 g .., channels 64 (part0 + t) + 16 c + r
-        const uint32_t w[4] = {vr[t].x, vr[t].y, vr[t].z, vr[t].w};
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          any |= nan_bytes(w[c]);
-          const bf16x2 x0 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[c], v_next, false);
-          const bf16x2 x1 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[c], v_next, true);
-          uint2 *to = (uint2 *)&vbuf[buf][step][unit & 1][2 * (part0 + t) + (c >> 1)]
-                                    [32 * (g & 1) + 16 * (c & 1) + r];
-          to[g >> 1] = uint2{__builtin_bit_cast(uint32_t, x0), __builtin_bit_cast(uint32_t, x1)};
-        }
-      }
-      const bool some = __any(any != 0);
-      if (lane == 0) odd[buf][wave] = some;
-    } else if (lane == 0) {
-      odd[buf][wave] = 0;
-    }
-  };
+    const Kv8Span sp = kv8_span(p.s, shift, b);
+    const int all = min(sp.rows, p.s.max_rows) * p.group, c0 = cb * kCols;
+    if (c0 >= all) return;
+    const int end = min(sp.len, p.a.max_len), pos0 = sp.len - sp.rows;
+    const int2 span = tiles_of(sp, c0);
+    const int tile0 = span.x + max(skip - kStart, 0);
+    const int tile1 = most == 0x7FFFFFFF ? span.y : min(span.x + max(skip + most - kStart, 0), span.y);
+    // the wave's columns and the tokens that its first and last row see
+    const int w0 = c0 + wave * 32 * CT, cols = min(all - w0, 32 * CT);
+    const int first = pos0 + w0 / p.group, final = pos0 + (w0 + max(cols, 1) - 1) / p.group;
+    const int full_lo = low(final), full_hi = min(first, end - 1);
+    const int any_lo = low(first), any_hi = cols > 0 ? min(final, end - 1) : -1;
 
-  f32x16 o[CT][VT] = {};
-  float m[CT], l[CT] = {};
-#pragma unroll
-  for (int ct = 0; ct < CT; ++ct) m[ct] = kLowest;
-
-  if (tile0 < tile1) {
-    load(tile0);
-    widen(0);
-    load(min(tile0 + 1, tile1 - 1));
-  }
-  lds_barrier();
-
-  f32x16 s[CT][ST];
-  bf16x8 pr[CT][kUnits];
-  float sum[CT];
-  auto scores = [&](int buf) {
-    const f32x16 zero = {};
-#pragma unroll
-    for (int t = 0; t < KT; ++t)
-#pragma unroll
-      for (int j = 0; j < ST; ++j) {
-        const bf16x8 k = as_bf16x8(kbuf[buf][j][t][lane]);
-#pragma unroll
-        for (int ct = 0; ct < CT; ++ct)
-          s[ct][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k, q[ct][t], t ? s[ct][j] : zero, 0, 0, 0);
-      }
-    __builtin_amdgcn_sched_group_barrier(0x100, 6, 0);
-#pragma unroll
-    for (int i = 0; i < ST * KT - 6; ++i) {
-      __builtin_amdgcn_sched_group_barrier(0x8, CT, 0);
-      __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-    }
-    __builtin_amdgcn_sched_group_barrier(0x8, 6 * CT, 0);
-  };
-  // P and its sum (fp32; P itself is rounded to bf16, the type of the product's other operand)
-  auto powers = [&]() {
+    const float cs = fmaxf(fabsf(p.a.scale) * kLog2e, 1.1754944e-38f);  // its sign goes to q
+    const uint32_t flip = p.a.scale < 0.f ? 0x80008000u : 0u;
+    bf16x8 q[CT][KT];
+    int lo[CT], hi[CT];
 #pragma unroll
     for (int ct = 0; ct < CT; ++ct) {
-      float part[kUnits];
+      const int c = w0 + ct * 32 + n, i = c / p.group;
+      const bool in = c < all;
+      const __bf16 *qr = (const __bf16 *)p.a.q.ptr + (int64_t)(sp.r0 + (in ? i : 0)) * p.a.q.row_stride +
+                         (int64_t)(h * p.group + (in ? c % p.group : 0)) * p.a.q.head_stride;
 #pragma unroll
-      for (int u = 0; u < kUnits; ++u) {
-        float e[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          e[i] = __builtin_amdgcn_exp2f(fmaf(s[ct][u >> 1][8 * (u & 1) + i], cs, -m[ct]));
-        part[u] = ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
-#pragma unroll
-        for (int i = 0; i < 8; ++i) pr[ct][u][i] = (__bf16)e[i];
+      for (int t = 0; t < KT; ++t) {
+        const uint4 w = *(const uint4 *)(qr + 16 * t + 8 * half);
+        q[ct][t] = as_bf16x8(in ? uint4{w.x ^ flip, w.y ^ flip, w.z ^ flip, w.w ^ flip} : uint4{0, 0, 0, 0});
       }
-      sum[ct] = part[0] + part[1];
-      if constexpr (ST == 2) sum[ct] += part[2] + part[3];
+      lo[ct] = low(pos0 + i);
+      hi[ct] = min(pos0 + i, end - 1);
     }
-  };
-  auto any_of = [](const int *flags, int n) {
-    int x = 0;
-#pragma unroll
-    for (int i = 0; i < n; ++i) x |= flags[i];
-    return __builtin_amdgcn_readfirstlane(x) != 0;
-  };
-  // whether every row of the wave sees every token of the tile
-  auto is_whole = [&](int t0, int buf) {
-    return t0 >= full_lo && t0 + kTile - 1 <= full_hi && !any_of(bad[buf], kUnits);
-  };
-  // bit r of step j: accumulator row r's token is one that the lane's column sees
-  auto sees = [&](int ct, int j, int t0, int buf) {
-    uint32_t bits = 0;
-#pragma unroll
-    for (int r = 0; r < 16; ++r) {
-      const int k = t0 + 32 * j + (r & 3) + 8 * (r >> 2) + 4 * half;
-      bits |= (((k >= lo[ct]) & (k <= hi[ct])) ? 1u : 0u) << r;
-    }
-    return bits & ((bad[buf][2 * j] ? 0u : 0xFFu) | (bad[buf][2 * j + 1] ? 0u : 0xFF00u));
-  };
-  auto mask = [&](int t0, int buf) {
-#pragma unroll
-    for (int ct = 0; ct < CT; ++ct)
-#pragma unroll
-      for (int j = 0; j < ST; ++j) {
-        const uint32_t bits = sees(ct, j, t0, buf);
-#pragma unroll
-        for (int r = 0; r < 16; ++r) s[ct][j][r] = bits >> r & 1u ? s[ct][j][r] : -__builtin_inff();
-      }
-  };
-  auto fetch = [&](int tile, int buf) {  // the next tile to LDS, the one after it to registers
-    widen(buf ^ 1);
-    load(min(tile + 2, tile1 - 1));
-  };
 
-  // tiles that some row of the wave sees: [mine0, mine1)
-  const int mine0 = min(max(any_lo >> kShift, tile0), tile1);
-  const int mine1 = max(min((any_hi >> kShift) + 1, tile1), mine0);
-  int tile = tile0;
-  for (; tile < mine0; ++tile) {
-    fetch(tile, (tile - tile0) & 1);
+    // lane i: the wave's unit of tile `meta + i`
+    int meta = tile0 - 64, at = -1;
+    float ksc = 1.f, vsc = 1.f;
+    const int unit = wave % kUnits, share = wave / kUnits;
+    const int part0 = kBoth ? share * kParts : 0;
+    const bool does_k = kBoth || share == 0, does_v = kBoth || share == 1;
+    uint4 kr[kParts], vr[kParts];
+    int a_next = -1;  // of the tile in kr and vr
+    float k_next = 1.f, v_next = 1.f;
+    auto look_up = [&](int tile) {  // pages and scales of 64 tiles from here
+      meta = tile;
+      const int t = (tile + lane) * kTile + unit * 16;
+      at = -1;
+      ksc = vsc = 1.f;
+      if (t < end && tile + lane < tile1) {
+        const int id = kv8_page(p.s, p.c, b, t >> shift);
+        if (id >= 0) {
+          const size_t ph = (size_t)id * p.c.heads + h;
+          at = (int)((ph << (shift - 4)) + ((t >> 4) & ((1 << (shift - 4)) - 1)));
+          ksc = kv8_scale(p.c.ks[ph]);
+          vsc = kv8_scale(p.c.vs[ph]);
+        }
+      }
+    };
+    auto load = [&](int tile) {
+      if (tile - meta >= 64) look_up(tile);
+      a_next = __builtin_amdgcn_readlane(at, tile - meta);
+      k_next = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, ksc), tile - meta));
+      v_next = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, vsc), tile - meta));
+      // (a unit that no page holds reads the pool's first; its scores are masked)
+      const size_t off = (size_t)(a_next == -1 ? 0u : (uint32_t)a_next) * (16 * D);
+      if (does_k) {
+        const uint4 *k = (const uint4 *)(p.c.k + off) + 64 * part0 + lane;
+#pragma unroll
+        for (int t = 0; t < kParts; ++t) kr[t] = k[64 * t];
+      }
+      if (does_v) {
+        const uint4 *v = (const uint4 *)(p.c.v + off) + 64 * part0 + lane;
+#pragma unroll
+        for (int t = 0; t < kParts; ++t) vr[t] = v[64 * t];
+      }
+    };
+    auto widen = [&](int buf) {
+      const int r = lane & 15, g = lane >> 4, step = unit >> 1;
+      if (does_k) {
+#pragma unroll
+        for (int t = 0; t < kParts; ++t) {  // token r, channels 16 (4 (part0 + t) + g) ..
+          uint4 *to = &kbuf[buf][step][4 * (part0 + t) + g][16 * (unit & 1) + r];
+          to[0] = __builtin_bit_cast(uint4, fp8x8_to_bf16(kr[t].x, kr[t].y, k_next));
+          to[32] = __builtin_bit_cast(uint4, fp8x8_to_bf16(kr[t].z, kr[t].w, k_next));
+        }
+        if (lane == 0) bad[buf][unit] = a_next == -1;
+      }
+      if (does_v) {
+        uint32_t any = 0;
+#pragma unroll
+        for (int t = 0; t < kParts; ++t) {  // tokens 4 g .., channels 64 (part0 + t) + 16 c + r
+          const uint32_t w[4] = {vr[t].x, vr[t].y, vr[t].z, vr[t].w};
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            any |= nan_bytes(w[c]);
+            const bf16x2 x0 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[c], v_next, false);
+            const bf16x2 x1 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[c], v_next, true);
+            uint2 *to = (uint2 *)&vbuf[buf][step][unit & 1][2 * (part0 + t) + (c >> 1)]
+                                      [32 * (g & 1) + 16 * (c & 1) + r];
+            to[g >> 1] = uint2{__builtin_bit_cast(uint32_t, x0), __builtin_bit_cast(uint32_t, x1)};
+          }
+        }
+        const bool some = __any(any != 0);
+        if (lane == 0) odd[buf][wave] = some;
+      } else if (lane == 0) {
+        odd[buf][wave] = 0;
+      }
+    };
+
+    f32x16 o[CT][VT] = {};
+    float m[CT], l[CT] = {};
+#pragma unroll
+    for (int ct = 0; ct < CT; ++ct) m[ct] = kLowest;
+
+    if (tile0 < tile1) {
+      load(tile0);
+      widen(0);
+      load(min(tile0 + 1, tile1 - 1));
+    }
     lds_barrier();
-  }
-  // The loop proper has no rare work in it: it leaves for a tile that raises
-  // the maximum, or where a NaN code of V must not reach a row that does not
-  // see its token, and such a tile is done again from its scores below.
-  while (true) {
-    bool again = false;
-    for (; tile < mine1; ++tile) {
+
+    f32x16 s[CT][ST];
+    bf16x8 pr[CT][kUnits];
+    float sum[CT];
+    auto scores = [&](int buf) {
+      const f32x16 zero = {};
+#pragma unroll
+      for (int t = 0; t < KT; ++t)
+#pragma unroll
+        for (int j = 0; j < ST; ++j) {
+          const bf16x8 k = as_bf16x8(kbuf[buf][j][t][lane]);
+#pragma unroll
+          for (int ct = 0; ct < CT; ++ct)
+            s[ct][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k, q[ct][t], t ? s[ct][j] : zero, 0, 0, 0);
+        }
+      __builtin_amdgcn_sched_group_barrier(0x100, 6, 0);
+#pragma unroll
+      for (int i = 0; i < ST * KT - 6; ++i) {
+        __builtin_amdgcn_sched_group_barrier(0x8, CT, 0);
+        __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+      }
+      __builtin_amdgcn_sched_group_barrier(0x8, 6 * CT, 0);
+    };
+    // P and its sum (fp32; P itself is rounded to bf16, the type of the product's other operand)
+    auto powers = [&]() {
+#pragma unroll
+      for (int ct = 0; ct < CT; ++ct) {
+        float part[kUnits];
+#pragma unroll
+        for (int u = 0; u < kUnits; ++u) {
+          float e[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            e[i] = __builtin_amdgcn_exp2f(fmaf(s[ct][u >> 1][8 * (u & 1) + i], cs, -m[ct]));
+          part[u] = ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
+#pragma unroll
+          for (int i = 0; i < 8; ++i) pr[ct][u][i] = (__bf16)e[i];
+        }
+        sum[ct] = part[0] + part[1];
+        if constexpr (ST == 2) sum[ct] += part[2] + part[3];
+      }
+    };
+    auto any_of = [](const int *flags, int n) {
+      int x = 0;
+#pragma unroll
+      for (int i = 0; i < n; ++i) x |= flags[i];
+      return __builtin_amdgcn_readfirstlane(x) != 0;
+    };
+    // whether every row of the wave sees every token of the tile
+    auto is_whole = [&](int t0, int buf) {
+      return t0 >= full_lo && t0 + kTile - 1 <= full_hi && !any_of(bad[buf], kUnits);
+    };
+    // bit r of step j: accumulator row r's token is one that the lane's column sees
+    auto sees = [&](int ct, int j, int t0, int buf) {
+      uint32_t bits = 0;
+#pragma unroll
+      for (int r = 0; r < 16; ++r) {
+        const int k = t0 + 32 * j + (r & 3) + 8 * (r >> 2) + 4 * half;
+        bits |= (((k >= lo[ct]) & (k <= hi[ct])) ? 1u : 0u) << r;
+      }
+      return bits & ((bad[buf][2 * j] ? 0u : 0xFFu) | (bad[buf][2 * j + 1] ? 0u : 0xFF00u));
+    };
+    auto mask = [&](int t0, int buf) {
+#pragma unroll
+      for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+        for (int j = 0; j < ST; ++j) {
+          const uint32_t bits = sees(ct, j, t0, buf);
+#pragma unroll
+          for (int r = 0; r < 16; ++r) s[ct][j][r] = bits >> r & 1u ? s[ct][j][r] : -__builtin_inff();
+        }
+    };
+    auto fetch = [&](int tile, int buf) {  // the next tile to LDS, the one after it to registers
+      widen(buf ^ 1);
+      load(min(tile + 2, tile1 - 1));
+    };
+
+    // tiles that some row of the wave sees: [mine0, mine1)
+    const int mine0 = min(max(any_lo >> kShift, tile0), tile1);
+    const int mine1 = max(min((any_hi >> kShift) + 1, tile1), mine0);
+    int tile = tile0;
+    for (; tile < mine0; ++tile) {
+      fetch(tile, (tile - tile0) & 1);
+      lds_barrier();
+    }
+    // The loop proper has no rare work in it: it leaves for a tile that raises
+    // the maximum, or where a NaN code of V must not reach a row that does not
+    // see its token, and such a tile is done again from its scores below.
+    while (true) {
+      bool again = false;
+      for (; tile < mine1; ++tile) {
+        const int buf = (tile - tile0) & 1, t0 = tile * kTile;
+        scores(buf);
+        if (!is_whole(t0, buf)) {
+          mask(t0, buf);
+          again = any_of(odd[buf], NW);
+        }
+        powers();
+        bool raise = again;
+#pragma unroll
+        for (int ct = 0; ct < CT; ++ct) raise |= sum[ct] > kRaise;
+        again = __any(raise);
+        if (again) break;
+#pragma unroll
+        for (int ct = 0; ct < CT; ++ct) l[ct] += sum[ct];
+#pragma unroll
+        for (int u = 0; u < kUnits; ++u)
+#pragma unroll
+          for (int t = 0; t < VT; ++t) {
+            const bf16x8 v = as_bf16x8(vbuf[buf][u >> 1][u & 1][t][lane]);
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct)
+              o[ct][t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v, pr[ct][u], o[ct][t], 0, 0, 0);
+          }
+        __builtin_amdgcn_sched_group_barrier(0x100, 6, 1);
+#pragma unroll
+        for (int i = 0; i < kUnits * VT - 6; ++i) {
+          __builtin_amdgcn_sched_group_barrier(0x8, CT, 1);
+          __builtin_amdgcn_sched_group_barrier(0x100, 1, 1);
+        }
+        __builtin_amdgcn_sched_group_barrier(0x8, 6 * CT, 1);
+        fetch(tile, buf);
+        lds_barrier();
+      }
+      if (!again) break;
+
       const int buf = (tile - tile0) & 1, t0 = tile * kTile;
       scores(buf);
-      if (!is_whole(t0, buf)) {
-        mask(t0, buf);
-        again = any_of(odd[buf], NW);
+      mask(t0, buf);
+#pragma unroll
+      for (int ct = 0; ct < CT; ++ct) {
+        float x = kLowest;
+#pragma unroll
+        for (int j = 0; j < ST; ++j)
+#pragma unroll
+          for (int r = 0; r < 16; ++r) x = fmaxf(x, s[ct][j][r]);
+        x *= cs;
+        x = fmaxf(x, __shfl_xor(x, 32));
+        const float mn = fmaxf(m[ct], x), down = __builtin_amdgcn_exp2f(m[ct] - mn);
+        m[ct] = mn;
+        l[ct] *= down;
+#pragma unroll
+        for (int t = 0; t < VT; ++t) o[ct][t] *= down;
       }
       powers();
-      bool raise = again;
-#pragma unroll
-      for (int ct = 0; ct < CT; ++ct) raise |= sum[ct] > kRaise;
-      again = __any(raise);
-      if (again) break;
 #pragma unroll
       for (int ct = 0; ct < CT; ++ct) l[ct] += sum[ct];
+      fetch(tile, buf);
 #pragma unroll
       for (int u = 0; u < kUnits; ++u)
 #pragma unroll
         for (int t = 0; t < VT; ++t) {
-          const bf16x8 v = as_bf16x8(vbuf[buf][u >> 1][u & 1][t][lane]);
+          bf16x8 v = as_bf16x8(vbuf[buf][u >> 1][u & 1][t][lane]), here;
+          bool some = false;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const float x = (float)v[i];
+            here[i] = (__bf16)(x != x ? 1.0f : 0.0f);
+            v[i] = x != x ? (__bf16)0.0f : v[i];
+            some |= x != x;
+          }
+          if (__any(some)) {  // ones where a code is NaN, against ones where a row sees the token
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct) {
+              const uint32_t bits = sees(ct, u >> 1, t0, buf) >> (8 * (u & 1));
+              bf16x8 yes;
+#pragma unroll
+              for (int i = 0; i < 8; ++i) yes[i] = (__bf16)(float)((bits >> i) & 1u);
+              f32x16 hit = {};
+              hit = __builtin_amdgcn_mfma_f32_32x32x16_bf16(here, yes, hit, 0, 0, 0);
+#pragma unroll
+              for (int r = 0; r < 16; ++r)
+                if (hit[r] > 0.f) o[ct][t][r] = __builtin_nanf("");
+            }
+          }
 #pragma unroll
           for (int ct = 0; ct < CT; ++ct)
             o[ct][t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v, pr[ct][u], o[ct][t], 0, 0, 0);
+          __builtin_amdgcn_sched_barrier(0);
         }
-      __builtin_amdgcn_sched_group_barrier(0x100, 6, 1);
-#pragma unroll
-      for (int i = 0; i < kUnits * VT - 6; ++i) {
-        __builtin_amdgcn_sched_group_barrier(0x8, CT, 1);
-        __builtin_amdgcn_sched_group_barrier(0x100, 1, 1);
-      }
-      __builtin_amdgcn_sched_group_barrier(0x8, 6 * CT, 1);
-      fetch(tile, buf);
+      lds_barrier();
+      ++tile;
+    }
+    for (; tile < tile1; ++tile) {
+      fetch(tile, (tile - tile0) & 1);
       lds_barrier();
     }
-    if (!again) break;
 
-    const int buf = (tile - tile0) & 1, t0 = tile * kTile;
-    scores(buf);
-    mask(t0, buf);
 #pragma unroll
     for (int ct = 0; ct < CT; ++ct) {
-      float x = kLowest;
+      const int c = w0 + ct * 32 + n;
+      const float ll = l[ct] + __shfl_xor(l[ct], 32);
+      if (DEALT && part_at >= 0) {  // [wave][32 channels][4 of 8][lane]
+        float *to = p.part + (size_t)part_at * many_floats(D);
 #pragma unroll
-      for (int j = 0; j < ST; ++j)
+        for (int t = 0; t < VT; ++t)
 #pragma unroll
-        for (int r = 0; r < 16; ++r) x = fmaxf(x, s[ct][j][r]);
-      x *= cs;
-      x = fmaxf(x, __shfl_xor(x, 32));
-      const float mn = fmaxf(m[ct], x), down = __builtin_amdgcn_exp2f(m[ct] - mn);
-      m[ct] = mn;
-      l[ct] *= down;
-#pragma unroll
-      for (int t = 0; t < VT; ++t) o[ct][t] *= down;
-    }
-    powers();
-#pragma unroll
-    for (int ct = 0; ct < CT; ++ct) l[ct] += sum[ct];
-    fetch(tile, buf);
-#pragma unroll
-    for (int u = 0; u < kUnits; ++u)
-#pragma unroll
-      for (int t = 0; t < VT; ++t) {
-        bf16x8 v = as_bf16x8(vbuf[buf][u >> 1][u & 1][t][lane]), here;
-        bool some = false;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float x = (float)v[i];
-          here[i] = (__bf16)(x != x ? 1.0f : 0.0f);
-          v[i] = x != x ? (__bf16)0.0f : v[i];
-          some |= x != x;
-        }
-        if (__any(some)) {  // ones where a code is NaN, against ones where a row sees the token
-#pragma unroll
-          for (int ct = 0; ct < CT; ++ct) {
-            const uint32_t bits = sees(ct, u >> 1, t0, buf) >> (8 * (u & 1));
-            bf16x8 yes;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) yes[i] = (__bf16)(float)((bits >> i) & 1u);
-            f32x16 hit = {};
-            hit = __builtin_amdgcn_mfma_f32_32x32x16_bf16(here, yes, hit, 0, 0, 0);
-#pragma unroll
-            for (int r = 0; r < 16; ++r)
-              if (hit[r] > 0.f) o[ct][t][r] = __builtin_nanf("");
-          }
-        }
-#pragma unroll
-        for (int ct = 0; ct < CT; ++ct)
-          o[ct][t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v, pr[ct][u], o[ct][t], 0, 0, 0);
-        __builtin_amdgcn_sched_barrier(0);
+          for (int r = 0; r < 16; r += 4)
+            *(f32x4 *)(to + (((wave * VT + t) * 4 + r / 4) * 64 + lane) * 4) =
+                f32x4{o[ct][t][r], o[ct][t][r + 1], o[ct][t][r + 2], o[ct][t][r + 3]};
+        *(float2 *)(to + kManyCols * D + (wave * 64 + lane) * 2) = float2{m[ct], ll};
+        continue;
       }
-    lds_barrier();
-    ++tile;
-  }
-  for (; tile < tile1; ++tile) {
-    fetch(tile, (tile - tile0) & 1);
-    lds_barrier();
-  }
-
-#pragma unroll
-  for (int ct = 0; ct < CT; ++ct) {
-    const int c = w0 + ct * 32 + n;
-    const float ll = l[ct] + __shfl_xor(l[ct], 32);
-    if (c >= all) continue;
-    if (p.splits > 1) {
-      const int item = ((int)b * p.c.heads + h) * p.blocks + cb;
-      float *to = p.part + (((size_t)item * p.splits + split) * kCols + (c - c0)) * (D + 2);
+      if (c >= all) continue;
+      const int64_t out_row = (int64_t)(sp.r0 + c / p.group) * p.a.q_heads + h * p.group + c % p.group;
+      const float inv = ll > 0.f || ll != ll ? 1.0f / ll : 0.f;
+      __bf16 *to = (__bf16 *)p.a.out + out_row * D;
 #pragma unroll
       for (int t = 0; t < VT; ++t)
 #pragma unroll
-        for (int r = 0; r < 16; r += 2)
-          *(float2 *)(to + 32 * t + (r & 3) + 8 * (r >> 2) + 4 * half) = float2{o[ct][t][r], o[ct][t][r + 1]};
-      if (half == 0) *(float2 *)(to + D) = float2{m[ct], ll};
-      continue;
+        for (int r = 0; r < 16; r += 4) {
+          const bf16x2 x = {(__bf16)(o[ct][t][r] * inv), (__bf16)(o[ct][t][r + 1] * inv)};
+          const bf16x2 y = {(__bf16)(o[ct][t][r + 2] * inv), (__bf16)(o[ct][t][r + 3] * inv)};
+          *(uint2 *)(to + 32 * t + 2 * r + 4 * half) =
+              uint2{__builtin_bit_cast(uint32_t, x), __builtin_bit_cast(uint32_t, y)};
+        }
+      if (half == 0 && p.a.lse)
+        p.a.lse[out_row] = ll > 0.f || ll != ll ? (m[ct] + log2f(ll)) * kLn2 : -__builtin_inff();
     }
-    const int64_t row = (int64_t)(sp.r0 + c / p.group) * p.a.q_heads + h * p.group + c % p.group;
-    const float inv = ll > 0.f || ll != ll ? 1.0f / ll : 0.f;
-    __bf16 *to = (__bf16 *)p.a.out + row * D;
-#pragma unroll
-    for (int t = 0; t < VT; ++t)
-#pragma unroll
-      for (int r = 0; r < 16; r += 4) {
-        const bf16x2 x = {(__bf16)(o[ct][t][r] * inv), (__bf16)(o[ct][t][r + 1] * inv)};
-        const bf16x2 y = {(__bf16)(o[ct][t][r + 2] * inv), (__bf16)(o[ct][t][r + 3] * inv)};
-        *(uint2 *)(to + 32 * t + 2 * r + 4 * half) =
-            uint2{__builtin_bit_cast(uint32_t, x), __builtin_bit_cast(uint32_t, y)};
-      }
-    if (half == 0 && p.a.lse)
-      p.a.lse[row] = ll > 0.f || ll != ll ? (m[ct] + log2f(ll)) * kLn2 : -__builtin_inff();
   }
 }
 
-// Joins the splits of the kernel above, in the order of the tokens: a wave per column.
+// Joins the parts of the kernel above, in the order of the tokens: a workgroup
+// for 32 columns' 32 channels, a wave for 8 of these.
 template <int D>
-__global__ __launch_bounds__(256) void k_kv8_prefill_join(PrefillParams p, int kcols) {
-  const int h = (int)blockIdx.y, b = (int)blockIdx.z, lane = (int)threadIdx.x & 63;
-  const int c = (int)blockIdx.x * 4 + ((int)threadIdx.x >> 6);
+__global__ __launch_bounds__(256) void k_kv8_prefill_join(PrefillParams p) {
+  constexpr int VT = D / 32, NW = kManyCols / 32;
+  const int cb = (int)blockIdx.x / NW, w = (int)blockIdx.x % NW, h = (int)blockIdx.y;
+  const int b = (int)blockIdx.z / VT, t = (int)blockIdx.z % VT;
+  const int lane = (int)threadIdx.x & 63, r4 = (int)threadIdx.x >> 6, n = lane & 31, half = lane >> 5;
   const Kv8Span sp = kv8_span(p.s, p.c.shift, b);
-  if (c >= min(sp.rows, p.s.max_rows) * p.group) return;
-  const int item = (b * p.c.heads + h) * p.blocks + c / kcols;
-  const float *from = p.part + ((size_t)item * p.splits * kcols + c % kcols) * (D + 2);
-  const size_t step = (size_t)kcols * (D + 2);
-  float m = kLowest, l = 0.f, o[D / 64] = {};
-  for (int s = 0; s < p.splits; ++s) m = fmaxf(m, from[s * step + D]);
-  for (int s = 0; s < p.splits; ++s) {
-    const float f = __builtin_amdgcn_exp2f(from[s * step + D] - m);
-    l = fmaf(from[s * step + D + 1], f, l);
-#pragma unroll
-    for (int a = 0; a < D / 64; ++a) o[a] = fmaf(from[s * step + 64 * a + lane], f, o[a]);
+  const int all = min(sp.rows, p.s.max_rows) * p.group, c = cb * kManyCols + 32 * w + n;
+  if (c - n >= all) return;
+  const int2 at = p.parts[((size_t)b * p.c.heads + h) * p.blocks + cb];
+  if (at.y == 0 || c >= all) return;
+  // the first part is its workgroup's last item, the others their workgroups' first
+  auto place = [&](int k) { return p.part + (size_t)(2 * (at.x + k) + (k == 0 ? 1 : 0)) * many_floats(D); };
+  auto stat = [&](int k) { return *(const float2 *)(place(k) + kManyCols * D + (w * 64 + lane) * 2); };
+  const int off = (((w * VT + t) * 4 + r4) * 64 + lane) * 4;
+  float m = kLowest, l = 0.f;
+  f32x4 o = {};
+#pragma unroll 4
+  for (int k = 0; k < at.y; ++k) m = fmaxf(m, stat(k).x);
+#pragma unroll 4
+  for (int k = 0; k < at.y; ++k) {
+    const float2 x = stat(k);
+    const float f = __builtin_amdgcn_exp2f(x.x - m);
+    l = fmaf(x.y, f, l);
+    o += *(const f32x4 *)(place(k) + off) * f;
   }
   const int64_t row = (int64_t)(sp.r0 + c / p.group) * p.a.q_heads + h * p.group + c % p.group;
   const float inv = l > 0.f || l != l ? 1.0f / l : 0.f;
-#pragma unroll
-  for (int a = 0; a < D / 64; ++a) ((__bf16 *)p.a.out)[row * D + 64 * a + lane] = (__bf16)(o[a] * inv);
-  if (lane == 0 && p.a.lse) p.a.lse[row] = l > 0.f || l != l ? (m + log2f(l)) * kLn2 : -__builtin_inff();
+  const bf16x2 y[2] = {{(__bf16)(o[0] * inv), (__bf16)(o[1] * inv)}, {(__bf16)(o[2] * inv), (__bf16)(o[3] * inv)}};
+  *(uint2 *)((__bf16 *)p.a.out + row * D + 32 * t + 8 * r4 + 4 * half) =
+      uint2{__builtin_bit_cast(uint32_t, y[0]), __builtin_bit_cast(uint32_t, y[1])};
+  if (t == 0 && r4 == 0 && half == 0 && p.a.lse)
+    p.a.lse[row] = l > 0.f || l != l ? (m + log2f(l)) * kLn2 : -__builtin_inff();
 }
 
 // ---- accumulated attention weight -----------------------------------------------------
@@ -911,6 +1005,11 @@ __global__ __launch_bounds__(256) void k_kv8_prefill_join(PrefillParams p, int k
 // time, a lane adds up its tokens over its column of every tile, and the 32
 // columns are joined at the end; where there are few tokens the columns are
 // dealt over workgroups (parts).  No atomics: a token's sum has one order.
+//
+// Measured with the attention: 16 sequences of up to 6007 tokens, one row,
+// 44 us (the weights 8 of them); 2 of up to 4093 with 1531 rows of 40 heads
+// 325 us (the weights 154, 340 TFLOP/s: a power for each score, 256 matrix
+// operations, and two turns of workgroups that each first widen their tokens).
 
 struct WeightParams {
   Kv8Attn a;
@@ -1157,8 +1256,6 @@ __global__ __launch_bounds__(256) void k_kv8_weights_join(WeightParams p) {
 // kernels take 64 and 62 us, at 66 50 and 60 us, at 105 of 13 short ones 21
 // and 29 us (head size 256: at 120 86 and 80 us).
 constexpr int kv8_few_cols(int dim) { return dim == 256 ? 64 : 128; }
-constexpr int kManyCols = 256;  // of a workgroup, many rows
-constexpr int kManyGroups = 256;    // one on each CU
 constexpr int kWeightGroups = 512;  // of the second pass over K
 // workgroups wanted: those that the CUs hold at a time (bound of a plan's: kDecodeGroups)
 constexpr int kDecodeGroups = 768;
@@ -1195,22 +1292,15 @@ Kv8Plan kv8_plan(const Kv8Attn &a, const Kv8Pool &c, const Kv8Batch &s, int dim)
       pl.part_floats = (size_t)items * pl.splits * 16 * pl.ct * (dim + 2);
   }
   if (!pl.few) {
-    const int kc = kManyCols;
-    pl.blocks = (int)((cols + kc - 1) / kc);
+    pl.blocks = (int)((cols + kManyCols - 1) / kManyCols);
     const int64_t items = std::max<int64_t>((int64_t)s.seqs * c.heads * pl.blocks, 1);
     const int64_t seen = a.window ? std::min<int64_t>(a.max_len, (int64_t)a.window + s.max_rows) : a.max_len;
-    // One workgroup fills a CU.  The tokens are split where there are too few of
-    // them, into pieces of 512 at least (64 rows of 32 heads over 60000 tokens:
-    // 256 workgroups 102 us, 512 131 us, 1024 199 us), and into pieces of 4096 up
-    // to four for each CU, since the lengths may differ; of the numbers that
-    // leave the fewest CUs idle in the last turn if they do not, the largest.
-    const int64_t fill = std::max<int64_t>(std::min<int64_t>(kManyGroups / items, seen / 512), 1);
-    const int64_t most = std::max<int64_t>(std::min<int64_t>(4 * kManyGroups / items, seen / 4096), fill);
-    auto turns = [&](int64_t n) { return (double)((items * n + kManyGroups - 1) / kManyGroups) / (double)n; };
-    pl.splits = 1;
-    for (int64_t n = 2; n <= most; ++n)
-      if (turns(n) <= 1.02 * turns(pl.splits)) pl.splits = (int)n;
-    if (pl.splits > 1) pl.part_floats = (size_t)items * pl.splits * kc * (dim + 2);
+    // Dealt where items are too few to even out over the CUs, and long enough
+    // for parts to pay.  6 sequences of up to 900 rows and 9000 tokens (384
+    // items) 308 us as items, 257 us dealt; a prompt of 8192 (1024 items) 518
+    // and 613 us: its short items cost more starts than the idle CUs.
+    pl.dealt = items <= kManyItems && seen >= 1024 && items * (a.max_len / 32 + 8) < (1 << 30);
+    if (pl.dealt) pl.part_floats = 2 * kManyGroups * (size_t)many_floats(dim) + 2 * (size_t)items;
   }
   pl.len_pad = (a.max_len + kWeightTokens - 1) / kWeightTokens * kWeightTokens;
   pl.parts = 1;
@@ -1232,13 +1322,13 @@ Kv8Plan kv8_plan(const Kv8Attn &a, const Kv8Pool &c, const Kv8Batch &s, int dim)
 size_t kv8_part_bound(const Kv8Attn &a, const Kv8Pool &c, const Kv8Batch &s, int dim) {
   const Kv8Plan pl = kv8_plan(a, c, s, dim);
   // the most rows that are few
-  const size_t few = (size_t)kv8_few_cols(dim), many = (size_t)kManyCols, width = (size_t)dim + 2;
+  const size_t few = (size_t)kv8_few_cols(dim), width = (size_t)dim + 2;
   Kv8Batch s2 = s;
   s2.max_rows = std::min(s.max_rows, std::max((int)few / pl.group, 1));
   size_t floats = std::max(pl.part_floats, kv8_plan(a, c, s2, dim).part_floats);
   // fewer tokens, or a window: shorter pieces, but no more workgroups than kDecodeGroups and one for each item
   floats = std::max(floats, (kDecodeGroups * 16 * (size_t)(256 / dim) + (size_t)s.seqs * c.heads * few) * width);
-  if (!pl.few) floats = std::max(floats, 4 * kManyGroups * many * width);
+  if (!pl.few) floats = std::max(floats, 2 * kManyGroups * (size_t)many_floats(dim) + 2 * kManyItems);
   // 16 columns' scores, or kWeightGroups parts of kWeightTokens
   if (c.w) floats += std::max((size_t)s.seqs * c.heads * pl.len_pad * 16, (size_t)kWeightGroups * kWeightTokens * 2);
   return floats;
@@ -1258,15 +1348,22 @@ hipError_t launch_kv8_attention(const Kv8Attn &a, const Kv8Pool &c, const Kv8Bat
     k<<<grid, dim3(64 * kDecodeWaves), 0, stream>>>(p);
     return hipGetLastError();
   }
-  const PrefillParams p{a, c, s, pl.group, pl.blocks, pl.splits, part};
-  const dim3 grid((unsigned)c.heads * (unsigned)pl.blocks, (unsigned)(s.seqs * pl.splits));
-  auto k = dim == 64 ? k_kv8_prefill<64, 1, 8, 2> : dim == 128 ? k_kv8_prefill<128, 1, 8, 2> : k_kv8_prefill<256, 1, 8, 1>;
+  const PrefillParams p{a, c, s, pl.group, pl.blocks, part,
+                        (int2 *)(part + 2 * kManyGroups * (size_t)many_floats(dim))};
+  const dim3 grid = pl.dealt ? dim3(kManyGroups) : dim3((unsigned)c.heads * (unsigned)pl.blocks, (unsigned)s.seqs);
+  auto pick = [&](auto dealt) {
+    constexpr bool kDealt = decltype(dealt)::value;
+    return dim == 64    ? k_kv8_prefill<64, 1, 8, 2, kDealt>
+           : dim == 128 ? k_kv8_prefill<128, 1, 8, 2, kDealt>
+                        : k_kv8_prefill<256, 1, 8, 1, kDealt>;
+  };
+  auto k = pl.dealt ? pick(std::true_type{}) : pick(std::false_type{});
   k<<<grid, dim3(512), 0, stream>>>(p);
   if (hipError_t e = hipGetLastError()) return e;
-  if (pl.splits == 1) return hipSuccess;
-  const dim3 jgrid((unsigned)((cols_of(s, pl) + 3) / 4), (unsigned)c.heads, (unsigned)s.seqs);
+  if (!pl.dealt) return hipSuccess;
+  const dim3 jgrid((unsigned)pl.blocks * (kManyCols / 32), (unsigned)c.heads, (unsigned)(s.seqs * (dim / 32)));
   auto kj = dim == 64 ? k_kv8_prefill_join<64> : dim == 128 ? k_kv8_prefill_join<128> : k_kv8_prefill_join<256>;
-  kj<<<jgrid, dim3(256), 0, stream>>>(p, kManyCols);
+  kj<<<jgrid, dim3(256), 0, stream>>>(p);
   return hipGetLastError();
 }
 

@@ -317,8 +317,9 @@ struct Kv8Plan {
   int group;    // query heads per KV head
   bool few;     // the kernel that splits the tokens (few rows)
   int ct, spw, rounds;  // its 16-column tiles, a wave's 32-token steps at a time, and times
-  int blocks;   // column blocks of a sequence (many rows)
-  int splits;   // parts of a sequence's tokens
+  int blocks;   // column blocks of a sequence
+  int splits;   // parts of a sequence's tokens (few rows)
+  bool dealt;   // equal runs of tiles for the workgroups (many rows)
   // the weights pass: tokens of a sequence (rounded up); columns whose scores
   // the attention leaves for it (0: it takes K again), parts of the columns
   int len_pad, score_cols, parts;

@@ -245,6 +245,9 @@ COLUMNS = [  # as CASES; rows times query heads of a KV head around what one wor
     (64, 64, 1, 1, [9000], [600], 0),
     (128, 128, 1, 1, [5000, 64], [400, 64], 1500),
     (128, 16, 1, 1, [1, 0, 17, 255, 256, 257], [1, 0, 17, 255, 256, 257], 0),
+    (128, 64, 2, 2, [3, 1500, 0, 1100], [200, 400, 0, 129], 0),   # long enough to be dealt, some rows see nothing
+    (64, 32, 3, 3, [1300, 1024, 1], [300, 129, 1], 100),
+    (256, 16, 1, 1, [1030, 17], [260, 17], 0),
 ]
 
 
