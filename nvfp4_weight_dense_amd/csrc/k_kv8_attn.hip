@@ -958,12 +958,12 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void k_kv8_prefill(PrefillParams p
 }
 
 // Joins the parts of the kernel above, in the order of the tokens: a workgroup
-// for 32 columns' 32 channels, a wave for 8 of these.
-template <int D>
+// for 32 columns and T times 32 channels, a wave for 8 of each 32.
+template <int D, int T>
 __global__ __launch_bounds__(256) void k_kv8_prefill_join(PrefillParams p) {
   constexpr int VT = D / 32, NW = kManyCols / 32;
   const int cb = (int)blockIdx.x / NW, w = (int)blockIdx.x % NW, h = (int)blockIdx.y;
-  const int b = (int)blockIdx.z / VT, t = (int)blockIdx.z % VT;
+  const int b = (int)blockIdx.z / (VT / T), t0 = (int)blockIdx.z % (VT / T) * T;
   const int lane = (int)threadIdx.x & 63, r4 = (int)threadIdx.x >> 6, n = lane & 31, half = lane >> 5;
   const Kv8Span sp = kv8_span(p.s, p.c.shift, b);
   const int all = min(sp.rows, p.s.max_rows) * p.group, c = cb * kManyCols + 32 * w + n;
@@ -972,25 +972,31 @@ __global__ __launch_bounds__(256) void k_kv8_prefill_join(PrefillParams p) {
   if (at.y == 0 || c >= all) return;
   // the first part is its workgroup's last item, the others their workgroups' first
   auto place = [&](int k) { return p.part + (size_t)(2 * (at.x + k) + (k == 0 ? 1 : 0)) * many_floats(D); };
-  auto stat = [&](int k) { return *(const float2 *)(place(k) + kManyCols * D + (w * 64 + lane) * 2); };
-  const int off = (((w * VT + t) * 4 + r4) * 64 + lane) * 4;
   float m = kLowest, l = 0.f;
-  f32x4 o = {};
-#pragma unroll 4
-  for (int k = 0; k < at.y; ++k) m = fmaxf(m, stat(k).x);
-#pragma unroll 4
+  f32x4 o[T] = {};
+#pragma unroll 2
   for (int k = 0; k < at.y; ++k) {
-    const float2 x = stat(k);
-    const float f = __builtin_amdgcn_exp2f(x.x - m);
-    l = fmaf(x.y, f, l);
-    o += *(const f32x4 *)(place(k) + off) * f;
+    const float *from = place(k);
+    const float2 x = *(const float2 *)(from + kManyCols * D + (w * 64 + lane) * 2);
+    f32x4 y[T];
+#pragma unroll
+    for (int t = 0; t < T; ++t) y[t] = *(const f32x4 *)(from + (((w * VT + t0 + t) * 4 + r4) * 64 + lane) * 4);
+    const float mn = fmaxf(m, x.x), f = __builtin_amdgcn_exp2f(x.x - mn), g = __builtin_amdgcn_exp2f(m - mn);
+    m = mn;
+    l = l * g + x.y * f;
+#pragma unroll
+    for (int t = 0; t < T; ++t) o[t] = o[t] * g + y[t] * f;
   }
   const int64_t row = (int64_t)(sp.r0 + c / p.group) * p.a.q_heads + h * p.group + c % p.group;
   const float inv = l > 0.f || l != l ? 1.0f / l : 0.f;
-  const bf16x2 y[2] = {{(__bf16)(o[0] * inv), (__bf16)(o[1] * inv)}, {(__bf16)(o[2] * inv), (__bf16)(o[3] * inv)}};
-  *(uint2 *)((__bf16 *)p.a.out + row * D + 32 * t + 8 * r4 + 4 * half) =
-      uint2{__builtin_bit_cast(uint32_t, y[0]), __builtin_bit_cast(uint32_t, y[1])};
-  if (t == 0 && r4 == 0 && half == 0 && p.a.lse)
+  __bf16 *to = (__bf16 *)p.a.out + row * D + 32 * t0 + 8 * r4 + 4 * half;
+#pragma unroll
+  for (int t = 0; t < T; ++t) {
+    const bf16x2 y[2] = {{(__bf16)(o[t][0] * inv), (__bf16)(o[t][1] * inv)},
+                         {(__bf16)(o[t][2] * inv), (__bf16)(o[t][3] * inv)}};
+    *(uint2 *)(to + 32 * t) = uint2{__builtin_bit_cast(uint32_t, y[0]), __builtin_bit_cast(uint32_t, y[1])};
+  }
+  if (t0 == 0 && r4 == 0 && half == 0 && p.a.lse)
     p.a.lse[row] = l > 0.f || l != l ? (m + log2f(l)) * kLn2 : -__builtin_inff();
 }
 
@@ -1361,8 +1367,15 @@ hipError_t launch_kv8_attention(const Kv8Attn &a, const Kv8Pool &c, const Kv8Bat
   k<<<grid, dim3(512), 0, stream>>>(p);
   if (hipError_t e = hipGetLastError()) return e;
   if (!pl.dealt) return hipSuccess;
-  const dim3 jgrid((unsigned)pl.blocks * (kManyCols / 32), (unsigned)c.heads, (unsigned)(s.seqs * (dim / 32)));
-  auto kj = dim == 64 ? k_kv8_prefill_join<64> : dim == 128 ? k_kv8_prefill_join<128> : k_kv8_prefill_join<256>;
+  // All channels of 32 columns for a workgroup, unless there are few items of
+  // many parts (8 items of 32 parts: 32 channels at a time 66 us with the
+  // attention, all 256 100 us; 192 items of up to 3 177 and 173 us).
+  const bool wide = (int64_t)s.seqs * c.heads * pl.blocks >= 64;
+  const dim3 jgrid((unsigned)pl.blocks * (kManyCols / 32), (unsigned)c.heads,
+                   (unsigned)(s.seqs * (wide ? 1 : dim / 32)));
+  auto kj = dim == 64    ? (wide ? k_kv8_prefill_join<64, 2> : k_kv8_prefill_join<64, 1>)
+            : dim == 128 ? (wide ? k_kv8_prefill_join<128, 4> : k_kv8_prefill_join<128, 1>)
+                         : (wide ? k_kv8_prefill_join<256, 8> : k_kv8_prefill_join<256, 1>);
   kj<<<jgrid, dim3(256), 0, stream>>>(p);
   return hipGetLastError();
 }
