@@ -473,18 +473,18 @@ __global__ __launch_bounds__(kDealt) void k_kv8_select_stage(SelectParams p) {
   } else {
     if (tid < 2) part[tid] = 0;
     __syncthreads();
-    int above = 0, equal = 0;
+    int above = 0, equal = 0;  // of the wave
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       const int j = j0 + tid + k * kDealt;
-      if (j < j1 && (j < sp.lo || j >= sp.hi)) ++above;
-      if (in[k]) {
-        above += u[k] > prefix;
-        equal += u[k] == prefix;
-      }
+      const bool always = j < j1 && (j < sp.lo || j >= sp.hi);
+      above += __popcll(__ballot(always || (in[k] && u[k] > prefix)));
+      equal += __popcll(__ballot(in[k] && u[k] == prefix));
     }
-    atomicAdd(&part[0], above);
-    atomicAdd(&part[1], equal);
+    if ((tid & 63) == 0) {
+      atomicAdd(&part[0], above);
+      atomicAdd(&part[1], equal);
+    }
     __syncthreads();
     if (tid < 2) p.counts[((size_t)b * p.chunks + blockIdx.x) * 2 + tid] = part[tid];
     if (blockIdx.x == 0 && tid == 0) {
