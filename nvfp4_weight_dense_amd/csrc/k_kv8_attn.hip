@@ -7,6 +7,7 @@
 // gives zeros and -inf.  Sums and the softmax's statistics are fp32, powers
 // are of two (log2 e is folded into the scale).
 #include <algorithm>
+#include <cmath>
 #include <type_traits>
 
 #include "kv8_common.h"
@@ -1287,7 +1288,16 @@ Kv8Plan kv8_plan(const Kv8Attn &a, const Kv8Pool &c, const Kv8Batch &s, int dim)
     // 32 pieces each (a part of the CUs' places unused) 107 us, 46 pieces (all
     // of them) 95 us, 64 pieces 100 us; more cost more in the join.
     const int even = std::max((steps + 3) / 4, 1);  // steps of a wave if it were one piece
-    int want = std::max((decode_groups(dim, pl.ct) + items - 1) / items, (even + kMaxSteps - 1) / kMaxSteps);
+    // One workgroup joins an item's pieces, so where there are few items s
+    // pieces cost steps / s + s of it: no more than in proportion to the root of
+    // the steps, the fewer the larger a piece's sums (1 item, 130000 tokens: 64
+    // pieces 26 us, 128 30 us; 8 items, 16000 tokens: 32 16 us, 96 20 us; 4 items
+    // of 64 columns, 15879 tokens: 16 27 us, 108 63 us), and then as many for
+    // each CU (32 items: 13 32 us, 8 25 us).
+    int filled = (decode_groups(dim, pl.ct) + items - 1) / items;
+    const int joined = std::max((int)(1.25 * std::sqrt(steps * 128.0 / (pl.ct * dim))), 1);
+    if (joined < filled) filled = items * joined >= 256 ? items * joined / 256 * 256 / items : joined;
+    int want = std::max(filled, (even + kMaxSteps - 1) / kMaxSteps);
     want = std::min(want, even);
     pl.spw = (even + want - 1) / want;
     auto pieces = [&](int spw) { return std::max((steps + 4 * spw - 1) / (4 * spw), 1); };
