@@ -157,7 +157,8 @@ __global__ __launch_bounds__(64 * kDecodeWaves, decode_waves(D, CT)) void k_kv8_
     }
   };
   uint4 kx[2][D / 64];  // K of a step [unit][t]: token lane % 16, channels 64 t + 16 g ..
-  uint4 vx[2][D / 64], vy[2][D / 64];  // V [unit][a], this step's and the next's: tokens 4 g .., channels 64 a + 16 c + lane % 16
+  // V [unit][a], this step's and the next's: tokens 4 g .., channels 64 a + 16 c + lane % 16
+  uint4 vx[2][D / 64], vy[2][D / 64];
   auto load = [&](const uint8_t *codes, uint4 (&x)[2][D / 64], int s) {
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
@@ -519,7 +520,7 @@ __global__ __launch_bounds__(64 * kDecodeWaves, decode_waves(D, CT)) void k_kv8_
 //
 // Measured: a prompt of 8192 tokens, 32 heads on 8 of 128, 518 us, 1060
 // TFLOP/s; 3 pieces of up to 1023 rows, 16 heads on 4 of 256, a window of 3000,
-// 177 us, 690 TFLOP/s (its 32-token tiles and one wave's 128 accumulators leave
+// 171 us, 710 TFLOP/s (its 32-token tiles and one wave's 128 accumulators leave
 // the softmax less to hide behind).
 struct PrefillParams {
   Kv8Attn a;
