@@ -375,8 +375,9 @@ typedef struct kv8_rows {
 int kv8_append(const kv8_rows *k, const kv8_rows *v, const kv8_cache *cache,
                const kv8_batch *batch, void *stream);
 
-/* Bytes of workspace that kv8_attention takes for these sizes (an upper
- * bound for smaller max_len and max_rows); negative status on an error. */
+/* Bytes of workspace that kv8_attention takes for these sizes, whatever the
+ * window (an upper bound for fewer sequences and smaller max_len and max_rows
+ * too); negative status on an error. */
 int64_t kv8_attention_workspace(int32_t q_heads, const kv8_cache *cache, const kv8_batch *batch);
 
 /* Attention of the rows over the cache.  Row i of query head u sees the

@@ -1152,8 +1152,7 @@ int64_t kv8_attention_workspace(int32_t q_heads, const kv8_cache *cache, const k
   Kv8Attn a{};
   a.q_heads = q_heads;
   a.max_len = std::min(batch->max_len, batch->cols * cache->page);
-  return (int64_t)(align256(kKv8MaxItems * 4) +
-                   align256(4 * kv8_part_bound(a, kv8_pool(cache), kv8_batch_ref(batch), cache->dim)));
+  return (int64_t)kv8_workspace_bound(a, kv8_pool(cache), kv8_batch_ref(batch), cache->dim);
 }
 
 int kv8_attention(const kv8_rows *q, int32_t q_heads, float scale, int32_t window, const kv8_cache *cache,
@@ -1171,9 +1170,6 @@ int kv8_attention(const kv8_rows *q, int32_t q_heads, float scale, int32_t windo
     return fail(NVFP4_EINVAL, "kv8_attention: out must be 16-byte and lse 4-byte aligned");
   if (accumulate && (!lse || !cache->weights))
     return fail(NVFP4_EINVAL, "kv8_attention: accumulate needs lse and the cache's weights");
-  if (workspace && (workspace_bytes < need || ((uintptr_t)workspace & 255u)))
-    return fail(NVFP4_EINVAL, "kv8_attention: the workspace must be 256-byte aligned and of %lld bytes",
-                (long long)need);
   hipStream_t s = (hipStream_t)stream;
   const Kv8Attn a{kv8_rows_ref(q), q_heads, std::min(batch->max_len, batch->cols * cache->page), window, scale,
                   out, lse};
@@ -1181,8 +1177,12 @@ int kv8_attention(const kv8_rows *q, int32_t q_heads, float scale, int32_t windo
   const Kv8Batch seqs = kv8_batch_ref(batch);
   Kv8Plan pl = kv8_plan(a, pool, seqs, cache->dim);
   if (!accumulate) pl.score_cols = 0, pl.score_floats = 0;
+  // (what this call itself takes, whatever sizes the workspace was made for)
+  if (workspace && (workspace_bytes < (int64_t)kv8_workspace_bytes(pl) || ((uintptr_t)workspace & 255u)))
+    return fail(NVFP4_EINVAL, "kv8_attention: the workspace must be 256-byte aligned and of %lld bytes",
+                (long long)need);
   unsigned *counters = (unsigned *)workspace;
-  float *part = (float *)((char *)workspace + align256(pl.counter_bytes));
+  float *part = (float *)((char *)workspace + kv8_align(pl.counter_bytes));
   if (!workspace) {
     void *base = nullptr;
     if ((rc = counters_get(pl.counter_bytes / 4, &counters)) ||

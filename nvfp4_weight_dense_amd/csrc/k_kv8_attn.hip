@@ -7,7 +7,6 @@
 // gives zeros and -inf.  Sums and the softmax's statistics are fp32, powers
 // are of two (log2 e is folded into the scale).
 #include <algorithm>
-#include <cmath>
 #include <type_traits>
 
 #include "kv8_common.h"
@@ -43,9 +42,6 @@ constexpr float kLog2e = 1.44269504088896341f, kLn2 = 0.693147180559945309f;
 // window of 2048 and heads of 64 16 us (40 MB: start, look-ups and join are
 // most of it); one of 521 12 us, of which the call's own 12 us hide the kernel's 9.
 
-constexpr int kDecodeWaves = 4;
-constexpr int kMaxSplits = 128;
-constexpr int kMaxSteps = 31;  // a wave's, two units a lane; lanes 62 and 63 name none
 constexpr float kRaise = 1024.0f;  // a step's sum of powers that has the running maximum found anew
 constexpr float kLowest = -3.4028234663852886e38f;  // below every finite score
 
@@ -79,9 +75,6 @@ __device__ __forceinline__ f32x4 ld16_coherent(__amdgpu_buffer_rsrc_t r, uint32_
 __device__ __forceinline__ uint32_t nan_bytes(uint32_t w) {
   return ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
 }
-
-// waves a SIMD holds: what the accumulators (D * CT / 4 registers), Q and the codes leave room for
-constexpr int decode_waves(int dim, int ct) { return dim * ct <= 64 ? 4 : dim * ct <= 128 ? 3 : 2; }
 
 template <int D, int CT>
 __global__ __launch_bounds__(64 * kDecodeWaves, decode_waves(D, CT)) void k_kv8_decode(DecodeParams p) {
@@ -530,12 +523,6 @@ struct PrefillParams {
   float *part;  // [workgroup][2]: o as the kernel holds it, then m and l
   int2 *parts;  // [item]: the workgroup with its first part, how many parts (0: whole)
 };
-constexpr int kManyCols = 256;     // of an item
-constexpr int kManyGroups = 256;   // one on each CU
-constexpr int kManyItems = 384;    // most that are dealt
-constexpr int kStart = 6;          // an item's start and end cost as much as so many tiles
-constexpr int many_floats(int dim) { return kManyCols * dim + 4 * kManyCols; }  // of a part
-
 template <int D, int CT, int NW, int ST, bool DEALT>
 __global__ __launch_bounds__(64 * NW, NW / 4) void k_kv8_prefill(PrefillParams p) {
   constexpr int kCols = 32 * CT * NW;
@@ -1068,8 +1055,6 @@ __global__ __launch_bounds__(256) void k_kv8_weights_few(WeightParams p) {
   p.c.w[((size_t)id << p.c.shift) + (j & ((1 << p.c.shift) - 1))] += sum;
 }
 
-constexpr int kWeightWaves = 8, kWeightTokens = 64 * kWeightWaves;  // of a workgroup
-
 // Adds x[i] of the lanes n and n ^ O, and leaves them the halves of the sums.
 template <int O>
 __device__ __forceinline__ void fold(float (&x)[32], int n) {
@@ -1257,99 +1242,6 @@ __global__ __launch_bounds__(256) void k_kv8_weights_join(WeightParams p) {
 }
 
 }  // namespace
-
-// Few rows: up to so many (row, head) columns of a KV head.  Beyond one
-// workgroup's (16, 32 or 64 by head size) its blocks read the codes again,
-// from the caches; at 128 columns of 8 sequences of 16000 tokens the two
-// kernels take 64 and 62 us, at 66 50 and 60 us, at 105 of 13 short ones 21
-// and 29 us (head size 256: at 120 86 and 80 us).
-constexpr int kv8_few_cols(int dim) { return dim == 256 ? 64 : 128; }
-constexpr int kWeightGroups = 512;  // of the second pass over K
-// workgroups wanted: those that the CUs hold at a time (bound of a plan's: kDecodeGroups)
-constexpr int kDecodeGroups = 768;
-int decode_groups(int dim, int ct) { return std::min(256 * decode_waves(dim, ct), kDecodeGroups); }
-
-int64_t cols_of(const Kv8Batch &s, const Kv8Plan &pl) { return (int64_t)s.max_rows * pl.group; }
-
-Kv8Plan kv8_plan(const Kv8Attn &a, const Kv8Pool &c, const Kv8Batch &s, int dim) {
-  Kv8Plan pl = {};
-  pl.group = a.q_heads / c.heads;
-  const int64_t cols = cols_of(s, pl);
-  pl.few = cols <= kv8_few_cols(dim);
-  pl.counter_bytes = kKv8MaxItems * 4;
-  if (pl.few) {
-    pl.ct = cols <= 16 ? 1 : cols <= 32 ? 2 : 4;
-    pl.ct = std::min(pl.ct, 256 / dim);  // as many accumulators as leave two waves a SIMD
-    pl.blocks = (int)((cols + 16 * pl.ct - 1) / (16 * pl.ct));
-    const int items = std::max(s.seqs * c.heads * pl.blocks, 1);
-    const int64_t seen = a.window ? std::min<int64_t>(a.max_len, (int64_t)a.window + s.max_rows + 31) : a.max_len;
-    const int steps = (int)((seen + 31) / 32) + (a.window ? 1 : 0);
-    // Equal pieces of the longest sequence, as many as fill the CUs once, of at
-    // most kMaxSteps steps a wave.  Two sequences of 131000 tokens, 8 KV heads:
-    // 32 pieces each (a part of the CUs' places unused) 107 us, 46 pieces (all
-    // of them) 95 us, 64 pieces 100 us; more cost more in the join.
-    const int even = std::max((steps + 3) / 4, 1);  // steps of a wave if it were one piece
-    // One workgroup joins an item's pieces, so where there are few items s
-    // pieces cost steps / s + s of it: no more than in proportion to the root of
-    // the steps, the fewer the larger a piece's sums (1 item, 130000 tokens: 64
-    // pieces 26 us, 128 30 us; 8 items, 16000 tokens: 32 16 us, 96 20 us; 4 items
-    // of 64 columns, 15879 tokens: 16 27 us, 108 63 us), and then as many for
-    // each CU (32 items: 13 32 us, 8 25 us).
-    int filled = (decode_groups(dim, pl.ct) + items - 1) / items;
-    const int joined = std::max((int)(1.25 * std::sqrt(steps * 128.0 / (pl.ct * dim))), 1);
-    if (joined < filled) filled = items * joined >= 256 ? items * joined / 256 * 256 / items : joined;
-    int want = std::max(filled, (even + kMaxSteps - 1) / kMaxSteps);
-    want = std::min(want, even);
-    pl.spw = (even + want - 1) / want;
-    auto pieces = [&](int spw) { return std::max((steps + 4 * spw - 1) / (4 * spw), 1); };
-    const int most = items <= kKv8MaxItems ? kMaxSplits : 1;
-    pl.rounds = (pieces(pl.spw) + most - 1) / most;
-    pl.splits = (pieces(pl.spw) + pl.rounds - 1) / pl.rounds;
-    if (pl.splits > 1)
-      pl.part_floats = (size_t)items * pl.splits * 16 * pl.ct * (dim + 2);
-  }
-  if (!pl.few) {
-    pl.blocks = (int)((cols + kManyCols - 1) / kManyCols);
-    const int64_t items = std::max<int64_t>((int64_t)s.seqs * c.heads * pl.blocks, 1);
-    const int64_t seen = a.window ? std::min<int64_t>(a.max_len, (int64_t)a.window + s.max_rows) : a.max_len;
-    // Dealt where items are too few to even out over the CUs, and long enough
-    // for parts to pay.  6 sequences of up to 900 rows and 9000 tokens (384
-    // items) 308 us as items, 257 us dealt; a prompt of 8192 (1024 items) 518
-    // and 613 us: its short items cost more starts than the idle CUs.
-    pl.dealt = items <= kManyItems && seen >= 1024 && items * (a.max_len / 32 + 8) < (1 << 30);
-    if (pl.dealt) pl.part_floats = 2 * kManyGroups * (size_t)many_floats(dim) + 2 * (size_t)items;
-  }
-  pl.len_pad = (a.max_len + kWeightTokens - 1) / kWeightTokens * kWeightTokens;
-  pl.parts = 1;
-  if (c.w) {
-    const size_t tokens = (size_t)s.seqs * c.heads * pl.len_pad;
-    if (pl.few && cols <= 16 && cols * pl.len_pad < (1 << 29)) {
-      pl.score_cols = (int)cols;
-      pl.score_floats = tokens * (size_t)cols;
-    } else {
-      // two workgroups a CU where the columns allow it
-      const int64_t groups = (int64_t)s.seqs * c.heads * (pl.len_pad / kWeightTokens);
-      pl.parts = (int)std::max<int64_t>(std::min<int64_t>(kWeightGroups / std::max<int64_t>(groups, 1), cols / 256), 1);
-      pl.score_floats = tokens * (size_t)pl.parts;
-    }
-  }
-  return pl;
-}
-
-size_t kv8_part_bound(const Kv8Attn &a, const Kv8Pool &c, const Kv8Batch &s, int dim) {
-  const Kv8Plan pl = kv8_plan(a, c, s, dim);
-  // the most rows that are few
-  const size_t few = (size_t)kv8_few_cols(dim), width = (size_t)dim + 2;
-  Kv8Batch s2 = s;
-  s2.max_rows = std::min(s.max_rows, std::max((int)few / pl.group, 1));
-  size_t floats = std::max(pl.part_floats, kv8_plan(a, c, s2, dim).part_floats);
-  // fewer tokens, or a window: shorter pieces, but no more workgroups than kDecodeGroups and one for each item
-  floats = std::max(floats, (kDecodeGroups * 16 * (size_t)(256 / dim) + (size_t)s.seqs * c.heads * few) * width);
-  if (!pl.few) floats = std::max(floats, 2 * kManyGroups * (size_t)many_floats(dim) + 2 * kManyItems);
-  // 16 columns' scores, or kWeightGroups parts of kWeightTokens
-  if (c.w) floats += std::max((size_t)s.seqs * c.heads * pl.len_pad * 16, (size_t)kWeightGroups * kWeightTokens * 2);
-  return floats;
-}
 
 hipError_t launch_kv8_attention(const Kv8Attn &a, const Kv8Pool &c, const Kv8Batch &s, int dim,
                                 const Kv8Plan &pl, unsigned *counters, float *part, float *scores, hipStream_t stream) {

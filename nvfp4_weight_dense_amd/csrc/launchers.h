@@ -6,6 +6,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "kv8_plan.h"
+
 namespace nvfp4 {
 
 struct MatRef {
@@ -270,25 +272,6 @@ hipError_t launch_encode_probe(const float *x, int64_t n, float d, float *q, uin
 
 // ---- 8-bit paged KV cache (head size dim 64, 128 or 256; layout: kv8_common.h) ----
 
-struct Kv8Pool {
-  uint8_t *k, *v;    // codes  [pages][heads][page * D]
-  uint8_t *ks, *vs;  // scales [pages][heads]
-  float *w;          // accumulated attention weight [pages][page], or null
-  int pages, heads, shift;
-};
-
-struct Kv8Batch {
-  const int *table;   // [seqs][cols] page of each block of tokens
-  const int *lens;    // [seqs] tokens, the call's own with them
-  const int *starts;  // [seqs + 1] first row of each sequence, or null: rows / seqs each
-  int seqs, cols, rows, max_rows;
-};
-
-struct Kv8Rows {  // bf16 [rows][heads][dim], the last dimension contiguous
-  const void *ptr;
-  int64_t row_stride, head_stride;  // elements
-};
-
 hipError_t launch_kv8_append(const Kv8Rows &k, const Kv8Rows &v, const Kv8Pool &c, const Kv8Batch &s,
                              int dim, hipStream_t stream);
 // Eviction of sequences of up to max_len tokens (longer ones are held to it).
@@ -302,35 +285,8 @@ hipError_t launch_kv8_evict(const Kv8Pool &c, const Kv8Batch &s, int dim, int ma
                             int new_cols, int keep, int recent, int sink, int *new_lens, int *kept,
                             const Kv8EvictPlan &pl, unsigned *hist, uint32_t *words, hipStream_t stream);
 
-// Attention of rows over the cache: out bf16 [rows][q_heads][dim], lse fp32
-// [rows][q_heads].  `max_len` bounds the lengths (the grid's size only: a
-// longer sequence is a caller's error that leaves its further tokens unseen).
-struct Kv8Attn {
-  Kv8Rows q;
-  int q_heads, max_len;
-  int window;   // 0: none
-  float scale;
-  void *out;
-  float *lse;   // or null
-};
-struct Kv8Plan {
-  int group;    // query heads per KV head
-  bool few;     // the kernel that splits the tokens (few rows)
-  int ct, spw, rounds;  // its 16-column tiles, a wave's 32-token steps at a time, and times
-  int blocks;   // column blocks of a sequence
-  int splits;   // parts of a sequence's tokens (few rows)
-  bool dealt;   // equal runs of tiles for the workgroups (many rows)
-  // the weights pass: tokens of a sequence (rounded up); columns whose scores
-  // the attention leaves for it (0: it takes K again), parts of the columns
-  int len_pad, score_cols, parts;
-  size_t counter_bytes, part_floats, score_floats;
-};
-constexpr int kKv8MaxItems = 65536;  // arrival counters
-Kv8Plan kv8_plan(const Kv8Attn &a, const Kv8Pool &c, const Kv8Batch &s, int dim);
-// part_floats of any call with these sizes or smaller ones and any window
-size_t kv8_part_bound(const Kv8Attn &a, const Kv8Pool &c, const Kv8Batch &s, int dim);
 // `counters` (counter_bytes, zero on entry, left zero) and `part`
-// (part_floats) as planned; `scores` (score_floats), or null where no weights
+// (part_floats) as planned by kv8_plan; `scores` (score_floats), or null where no weights
 // are wanted.
 hipError_t launch_kv8_attention(const Kv8Attn &a, const Kv8Pool &c, const Kv8Batch &s, int dim,
                                 const Kv8Plan &pl, unsigned *counters, float *part, float *scores, hipStream_t stream);
