@@ -342,7 +342,8 @@ typedef struct kv8_cache {
  *           starts[b+1] - 1 of the row arrays; null: rows / seqs each.
  *   rows  : rows of the row arrays in all;
  *   max_rows, max_len: bounds on one sequence's rows and tokens.  They size
- *           the launch: rows and tokens beyond them are left out.
+ *           the launch: rows (the sequence's last) and tokens beyond them are
+ *           left out.  (kv8_append has no use for max_len.)
  * Row i of a sequence with n tokens and r rows is its token n - r + i. */
 typedef struct kv8_batch {
   const int32_t *table;

@@ -72,7 +72,8 @@ __global__ __launch_bounds__(T) void k_kv8_append(AppendParams p) {
   const int pos0 = sp.len - sp.rows;  // position of row 0 (rows before position 0 are dropped)
   const int col = (max(pos0, 0) >> shift) + (int)blockIdx.x;
   const int s0 = max(max(pos0, 0) - (col << shift), 0);
-  const int s1 = min(sp.len - (col << shift), page);
+  // (of more rows than max_rows, for which the grid and the pieces are too few, the first are written)
+  const int s1 = min(pos0 + min(sp.rows, p.s.max_rows) - (col << shift), page);
   if (s1 <= s0) return;
 
   const int64_t xs = p.row_stride[isv];

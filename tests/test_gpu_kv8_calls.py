@@ -8,7 +8,7 @@ import torch
 
 import kv8_ref as ref
 import nvfp4_weight_dense_amd as nv
-from test_gpu_kv8 import _gpu, _i32, _problem, _say, _table, _within
+from test_gpu_kv8 import _filled, _gen, _gpu, _i32, _problem, _same, _say, _starts, _table, _within
 
 pytestmark = pytest.mark.gpu
 
@@ -37,3 +37,30 @@ def test_workspace_of_exactly_the_given_size(cols, lens, rows, window):
         _within(out, want[0], want[2], "out")
         _within(lse, want[1], want[3], "lse")
         assert bool((room[size:] == 0x5A).all())
+
+
+# ---- rows beyond max_rows ----------------------------------------------------------------------------
+
+@pytest.mark.parametrize("dim,page,max_rows", [(128, 64, 1), (128, 64, 8), (64, 16, 1), (64, 16, 8), (256, 32, 1),
+                                               (256, 32, 8), (128, 128, 20), (64, 128, 40)])
+def test_append_leaves_rows_beyond_max_rows_out(dim, page, max_rows):
+    """starts that give a sequence more rows than max_rows: its first max_rows rows are written, at their own
+    places, and nothing else changes."""
+    _say("append, max_rows", dim, page, max_rows)
+    heads, lens, rows = 2, [200, 33, 90, 5, 1], [50, 33, 7, 9, 1]
+    c = _filled(sum(-(-n // page) for n in lens) + 2, heads, dim, page, 130, weights=True)
+    pool, dev = ref.Pool(c), _gpu(c)
+    table = _table(lens, page, c.k_codes.shape[0], 131)
+    x = torch.randn(sum(rows), 2 * heads, dim, generator=_gen(132))
+    x = (x * torch.exp(2 * torch.randn(sum(rows), 1, 1, generator=_gen(133)))).bfloat16()
+    held, most, at = [], [], 0
+    for n, r in zip(lens, rows):
+        m = min(r, max_rows)
+        held.append(x[at:at + m])
+        most.append(m)
+        at += r
+    y = torch.cat(held)
+    pool.append(y[:, :heads], y[:, heads:], table, [n - r + m for n, r, m in zip(lens, rows, most)], most)
+    d = x.cuda()
+    nv.kv8_append(d[:, :heads], d[:, heads:], dev, table.cuda(), _i32(lens).cuda(), _starts(rows).cuda(), max_rows=max_rows)
+    _same(pool, dev)
