@@ -815,7 +815,8 @@ def kv8_attention(q: torch.Tensor, cache: KV8Cache, table: torch.Tensor, lens: t
     if workspace is not None and (workspace.dtype != torch.uint8 or not workspace.is_contiguous()):
         raise ValueError("workspace: expected a contiguous uint8 tensor (kv8_workspace)")
     _kv8_on(dev, q, out, lse, workspace, table, lens, starts)
-    _check(L.kv8_attention(cq, q_heads, dim ** -0.5 if scale is None else float(scale), int(window), cc, cb,
+    window = max(min(int(window), 2 ** 31 - 1), -1)  # (ctypes would take it modulo 2^32)
+    _check(L.kv8_attention(cq, q_heads, dim ** -0.5 if scale is None else float(scale), window, cc, cb,
                            out.data_ptr(), None if lse is None else lse.data_ptr(), 1 if accumulate else 0,
                            None if workspace is None else workspace.data_ptr(),
                            0 if workspace is None else workspace.numel(), _kv8_stream(stream, dev)))

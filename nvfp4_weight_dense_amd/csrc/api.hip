@@ -1171,7 +1171,9 @@ int kv8_attention(const kv8_rows *q, int32_t q_heads, float scale, int32_t windo
   if (accumulate && (!lse || !cache->weights))
     return fail(NVFP4_EINVAL, "kv8_attention: accumulate needs lse and the cache's weights");
   hipStream_t s = (hipStream_t)stream;
-  const Kv8Attn a{kv8_rows_ref(q), q_heads, std::min(batch->max_len, batch->cols * cache->page), window, scale,
+  // (a window of all the table's tokens is none, and positions less a window stay within 32 bits)
+  const int tokens = batch->cols * cache->page;
+  const Kv8Attn a{kv8_rows_ref(q), q_heads, std::min(batch->max_len, tokens), std::min(window, tokens), scale,
                   out, lse};
   const Kv8Pool pool = kv8_pool(cache);
   const Kv8Batch seqs = kv8_batch_ref(batch);

@@ -8,7 +8,7 @@ import torch
 
 import kv8_ref as ref
 import nvfp4_weight_dense_amd as nv
-from test_gpu_kv8 import _filled, _gen, _gpu, _i32, _problem, _same, _say, _starts, _table, _within
+from test_gpu_kv8 import _check, _filled, _gen, _gpu, _i32, _problem, _same, _say, _starts, _table, _within
 
 pytestmark = pytest.mark.gpu
 
@@ -64,3 +64,19 @@ def test_append_leaves_rows_beyond_max_rows_out(dim, page, max_rows):
     d = x.cuda()
     nv.kv8_append(d[:, :heads], d[:, heads:], dev, table.cuda(), _i32(lens).cuda(), _starts(rows).cuda(), max_rows=max_rows)
     _same(pool, dev)
+
+
+# ---- windows -----------------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 31 - 40, 2 ** 30, 2 ** 63 - 1, 10 ** 5])
+@pytest.mark.parametrize("dim,page,q_heads,lens,rows", [
+    (128, 64, 4, [300, 77], [1, 1]), (128, 32, 4, [40, 3], [12, 9]), (64, 16, 4, [700, 600], [690, 600]),
+    (128, 64, 2, [40, 3], [60, 150]), (256, 16, 1, [1100, 5], [300, 280]), (64, 64, 8, [20, 700], [16, 16])])
+def test_windows_wider_than_any_cache(dim, page, q_heads, lens, rows, window):
+    """A window past every length is none, also for rows before position 0 (which see nothing) and for weights."""
+    _say("wide window", dim, page, q_heads, lens, rows, window)
+    c, table, q = _problem(dim, page, 1, q_heads, lens, rows, 0, seed=140)
+    got = _check(c, table, q, q_heads, lens, rows, window=window)
+    want = _check(c, table, q, q_heads, lens, rows, window=10 ** 6)
+    for a, b in zip(got, want):
+        assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
