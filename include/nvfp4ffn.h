@@ -390,7 +390,9 @@ int64_t kv8_attention_workspace(int32_t q_heads, const kv8_cache *cache, const k
  *   out: bf16 [rows][q_heads][dim]; lse: fp32 [rows][q_heads] or null.
  * accumulate != 0 (needs lse and the cache's weights) also adds to each
  * token's weight the sum of e^(s_j - lse) over the rows and query heads that
- * see it, in an order that does not change from call to call.
+ * see it, in an order that does not change from call to call.  Sequences may
+ * share pages (a common prefix): a page's weights get the sums of every
+ * sequence that names it, and once for each time it does.
  * fp32 throughout, except that e^(s_j - m) is rounded to bf16 before its
  * product with V (as the other operand of that product is at most bf16).
  * workspace: device memory of kv8_attention_workspace bytes, 256-byte

@@ -794,7 +794,8 @@ def kv8_attention(q: torch.Tensor, cache: KV8Cache, table: torch.Tensor, lens: t
 
     Returns out (bf16 [rows, q_heads, dim]); with lse (True, or a float32
     [rows, q_heads] tensor to write to) returns (out, lse).  accumulate adds
-    the attention weight each token receives to cache.weights."""
+    the attention weight each token receives to cache.weights (of a page that
+    several sequences share, what it receives from each of them)."""
     L = load_library()
     cc, _, page, dim, dev = _ckv8(cache)
     cq = _ckv8_rows(q, "q", dim)

@@ -1178,7 +1178,9 @@ int kv8_attention(const kv8_rows *q, int32_t q_heads, float scale, int32_t windo
   const Kv8Pool pool = kv8_pool(cache);
   const Kv8Batch seqs = kv8_batch_ref(batch);
   Kv8Plan pl = kv8_plan(a, pool, seqs, cache->dim);
-  if (!accumulate) pl.score_cols = 0, pl.score_floats = 0;
+  if (!accumulate) pl.score_cols = 0, pl.score_floats = pl.link_words = 0;
+  if (pl.link_words / 2 > 0xFFFFFFFEu)
+    return fail(NVFP4_ESHAPE, "kv8_attention: accumulate over %zu blocks of tokens, at most 2^32 - 2", pl.link_words / 2);
   // (what this call itself takes, whatever sizes the workspace was made for)
   if (workspace && (workspace_bytes < (int64_t)kv8_workspace_bytes(pl) || ((uintptr_t)workspace & 255u)))
     return fail(NVFP4_EINVAL, "kv8_attention: the workspace must be 256-byte aligned and of %lld bytes",
@@ -1187,17 +1189,17 @@ int kv8_attention(const kv8_rows *q, int32_t q_heads, float scale, int32_t windo
   float *part = (float *)((char *)workspace + kv8_align(pl.counter_bytes));
   if (!workspace) {
     void *base = nullptr;
-    if ((rc = counters_get(pl.counter_bytes / 4, &counters)) ||
-        (pl.part_floats + pl.score_floats && (rc = arena_get((pl.part_floats + pl.score_floats) * 4, &base))))
-      return rc;
+    const size_t words = pl.part_floats + pl.score_floats + pl.link_words;
+    if ((rc = counters_get(pl.counter_bytes / 4, &counters)) || (words && (rc = arena_get(words * 4, &base)))) return rc;
     part = (float *)base;
   }
   float *scores = part + pl.part_floats;
+  const Kv8Links links{counters + kKv8MaxItems, (uint2 *)(scores + pl.score_floats), pl.link_blocks, pl.link_bits};
   ProfileScope ps("kv8_attention", batch->rows, s);
-  if ((rc = hip_status(launch_kv8_attention(a, pool, seqs, cache->dim, pl, counters, part, scores, s),
+  if ((rc = hip_status(launch_kv8_attention(a, pool, seqs, cache->dim, pl, counters, part, scores, links, s),
                        "kv8_attention launch")) || !accumulate)
     return rc;
-  return hip_status(launch_kv8_weights(a, pool, seqs, cache->dim, pl, scores, s), "kv8_attention weights launch");
+  return hip_status(launch_kv8_weights(a, pool, seqs, cache->dim, pl, scores, links, s), "kv8_attention weights launch");
 }
 
 int kv8_evict(const kv8_cache *cache, const kv8_batch *batch, const int32_t *new_table, int32_t new_cols,

@@ -18,6 +18,27 @@ namespace {
 
 constexpr float kLog2e = 1.44269504088896341f, kLn2 = 0.693147180559945309f;
 
+// The tokens of a sequence that some row sees: [lo, hi); its rows and the first.
+struct Kv8Seen {
+  int r0, rows, lo, hi;
+};
+__device__ __forceinline__ Kv8Seen kv8_seen(const Kv8Attn &a, const Kv8Batch &s, int shift, int b) {
+  const Kv8Span sp = kv8_span(s, shift, b);
+  const int rows = min(sp.rows, s.max_rows), first = sp.len - sp.rows;
+  if (rows <= 0) return {0, 0, 0, 0};
+  return {sp.r0, rows, a.window ? max(first - a.window + 1, 0) : 0, min(first + rows, min(sp.len, a.max_len))};
+}
+// Chains block `col` of sequence b to its page's list, where some row sees it.
+__device__ __forceinline__ void kv8_chain(const Kv8Links &links, const Kv8Pool &c, const Kv8Batch &s,
+                                          const Kv8Seen &q, int b, int col) {
+  if (q.hi <= q.lo || col < q.lo >> c.shift || col > (q.hi - 1) >> c.shift) return;
+  const int id = kv8_page(s, c, b, col);
+  if (id < 0) return;
+  const unsigned groups = 1u << links.bits, e = (unsigned)b * (unsigned)links.blocks + (unsigned)col;
+  const unsigned at = ((unsigned)id & (groups - 1u)) + ((((unsigned)id >> links.bits) & (kKv8Chains - 1u)) << links.bits);
+  links.next[e] = uint2{atomicExch(&links.head[at], e + 1u), (unsigned)id};
+}
+
 // ---- few rows: one pass over the cache, split along the tokens ---------------------
 //
 // What bounds it: the bytes of the codes.  A step is 32 tokens of one KV
@@ -56,6 +77,7 @@ struct DecodeParams {
   unsigned *counters;
   float *scores;      // [seq][head][column][len_pad], or null: not wanted
   int len_pad, score_cols;
+  Kv8Links links;     // where scores are wanted
 };
 
 __device__ __forceinline__ bf16x8 fp8x8_to_bf16(uint32_t lo, uint32_t hi, float scale) {
@@ -106,6 +128,14 @@ __global__ __launch_bounds__(64 * kDecodeWaves, decode_waves(D, CT)) void k_kv8_
   const int nsplit = max((step1 - step0 + whole_per - 1) / whole_per, 1);
   if (split >= nsplit) return;
   const int full_lo = low(final), full_hi = min(first, end - 1);  // every row sees these
+  if constexpr (CT == 1) {
+    if (p.scores) {  // a block for a thread of the sequence's workgroups
+      const Kv8Seen seen = kv8_seen(p.a, p.s, shift, b);
+      for (int col = (seen.lo >> shift) + (split * p.c.heads + h) * 64 * kDecodeWaves + tid;
+           col <= (seen.hi - 1) >> shift; col += nsplit * p.c.heads * 64 * kDecodeWaves)
+        kv8_chain(p.links, p.c, p.s, seen, b, col);
+    }
+  }
 
   // columns of this lane
   const float cs = fmaxf(fabsf(p.a.scale) * kLog2e, 1.1754944e-38f);  // its sign goes to q
@@ -994,12 +1024,13 @@ __global__ __launch_bounds__(256) void k_kv8_prefill_join(PrefillParams p) {
 // A token's sum over rows and heads needs the finished log-sums, so it is a
 // second pass.  With one tile of columns the attention leaves its scores
 // behind (fp32, 4 bytes for each of at most 16 columns against the D bytes
-// of K's codes), and k_kv8_weights_few turns them into weights.  With more,
+// of K's codes), and k_kv8_weights_add turns them into weights.  With more,
 // k_kv8_weights_many takes K Q^T again: a wave keeps 64 tokens of one KV
 // head as matrix operands, the workgroup's columns pass through LDS 64 at a
 // time, a lane adds up its tokens over its column of every tile, and the 32
 // columns are joined at the end; where there are few tokens the columns are
-// dealt over workgroups (parts).  No atomics: a token's sum has one order.
+// dealt over workgroups (parts).  A token's sum has one order, and so have
+// those that k_kv8_weights_add adds to a page.
 //
 // Measured with the attention: 16 sequences of up to 6007 tokens, one row,
 // 44 us (the weights 8 of them); 2 of up to 4093 with 1531 rows of 40 heads
@@ -1014,46 +1045,8 @@ struct WeightParams {
   const float *scores;  // few: [seq][head][column][len_pad]
   int cols;
   float *part;          // many: [part][seq][head][len_pad]
+  Kv8Links links;
 };
-
-__global__ __launch_bounds__(256) void k_kv8_weights_few(WeightParams p) {
-  const int b = (int)blockIdx.y, j = (int)(blockIdx.x * 256 + threadIdx.x);
-  const Kv8Span sp = kv8_span(p.s, p.c.shift, b);
-  const int rows = min(sp.rows, p.s.max_rows), first = sp.len - sp.rows;
-  const int lo = p.a.window ? max(first - p.a.window + 1, 0) : 0;
-  if (rows <= 0 || j < lo || j > min(first + rows, min(sp.len, p.a.max_len)) - 1) return;
-  const int id = kv8_page(p.s, p.c, b, j >> p.c.shift);
-  if (id < 0) return;
-  float sum = 0.f;
-  const float *x = p.scores + (size_t)b * p.c.heads * p.cols * p.len_pad + j;
-  const float *z = p.a.lse + (size_t)sp.r0 * p.a.q_heads;
-  // Columns of all heads in turn, kStep loads at a time (16 sequences of 6007
-  // tokens, 8 heads of 4 columns: a head at a time 11.4 us, 16 columns 8.3 us).
-  constexpr int kStep = 16;
-  const int cols = rows * p.group, total = p.c.heads * cols;
-  int h = 0, c = 0, i = 0, u = 0;  // head, its column (row i, query head u of the group)
-  for (int e0 = 0; e0 < total; e0 += kStep) {
-    float y[kStep];
-    // (columns beyond a sequence's own rows are not written)
-    int hh = h, cc = c;
-#pragma unroll
-    for (int k = 0; k < kStep; ++k) {
-      const float *at = x + (size_t)(min(hh, p.c.heads - 1) * p.cols + cc) * p.len_pad;
-      y[k] = *at;
-      if (++cc == cols) cc = 0, ++hh;
-    }
-#pragma unroll
-    for (int k = 0; k < kStep; ++k) {
-      // (a row that sees nothing has -inf there and -inf scores)
-      const float lse = z[(size_t)i * p.a.q_heads + min(h, p.c.heads - 1) * p.group + u];
-      const float add = y[k] == -__builtin_inff() ? 0.f : __builtin_amdgcn_exp2f(y[k] - lse * kLog2e);
-      sum += h < p.c.heads ? add : 0.f;
-      if (++u == p.group) u = 0, ++i;
-      if (++c == cols) c = i = u = 0, ++h;
-    }
-  }
-  p.c.w[((size_t)id << p.c.shift) + (j & ((1 << p.c.shift) - 1))] += sum;
-}
 
 // Adds x[i] of the lanes n and n ^ O, and leaves them the halves of the sums.
 template <int O>
@@ -1080,6 +1073,8 @@ __global__ __launch_bounds__(64 * kWeightWaves, 2) void k_kv8_weights_many(Weigh
   if (wg0 >= end) return;
   const int rows = min(sp.rows, p.s.max_rows), all = rows * p.group, pos0 = sp.len - sp.rows;
   const int t0 = wg0 + wave * 64;
+  if (h == 0 && piece == 0 && tid < kWeightTokens >> shift)
+    kv8_chain(p.links, p.c, p.s, kv8_seen(p.a, p.s, shift, b), b, (wg0 >> shift) + tid);
 
   // this wave's tokens as operands: row m of step u is token t0 + 32 u + m
   const float cs = fmaxf(fabsf(p.a.scale) * kLog2e, 1.1754944e-38f);  // its sign goes to q
@@ -1226,28 +1221,175 @@ __global__ __launch_bounds__(64 * kWeightWaves, 2) void k_kv8_weights_many(Weigh
   out[t0 + 32 * (n >> 4) + (r & 3) + 8 * (r >> 2) + 4 * half] = x[0];
 }
 
-__global__ __launch_bounds__(256) void k_kv8_weights_join(WeightParams p) {
-  const int b = (int)blockIdx.y, j = (int)(blockIdx.x * 256 + threadIdx.x);
-  const Kv8Span sp = kv8_span(p.s, p.c.shift, b);
-  if (j >= min(sp.len, p.a.max_len)) return;
-  const int id = kv8_page(p.s, p.c, b, j >> p.c.shift);
-  if (id < 0) return;
+// A token's sum of the weights pass for one sequence: from the scores that the
+// attention left (FEW), or from the parts of k_kv8_weights_many.
+template <bool FEW>
+__device__ __forceinline__ float token_sum(const WeightParams &p, int b, int r0, int rows, int j) {
   float sum = 0.f;
-  for (int i = 0; i < p.parts; ++i) {
-    const float *x = p.part + ((size_t)i * p.s.seqs + b) * p.c.heads * p.len_pad + j;
+  if constexpr (FEW) {
+    const float *x = p.scores + (size_t)b * p.c.heads * p.cols * p.len_pad + j;
+    const float *z = p.a.lse + (size_t)r0 * p.a.q_heads;
+    // Columns of all heads in turn, kStep loads at a time (16 sequences of 6007
+    // tokens, 8 heads of 4 columns: a head at a time 11.4 us, 16 columns 8.3 us).
+    constexpr int kStep = 16;
+    const int cols = rows * p.group, total = p.c.heads * cols;
+    int h = 0, c = 0, i = 0, u = 0;  // head, its column (row i, query head u of the group)
+    for (int e0 = 0; e0 < total; e0 += kStep) {
+      float y[kStep];
+      // (columns beyond a sequence's own rows are not written)
+      int hh = h, cc = c;
+#pragma unroll
+      for (int k = 0; k < kStep; ++k) {
+        y[k] = x[(size_t)(min(hh, p.c.heads - 1) * p.cols + cc) * p.len_pad];
+        if (++cc == cols) cc = 0, ++hh;
+      }
+#pragma unroll
+      for (int k = 0; k < kStep; ++k) {
+        // (a row that sees nothing has -inf there and -inf scores)
+        const float lse = z[(size_t)i * p.a.q_heads + min(h, p.c.heads - 1) * p.group + u];
+        const float add = y[k] == -__builtin_inff() ? 0.f : __builtin_amdgcn_exp2f(y[k] - lse * kLog2e);
+        sum += h < p.c.heads ? add : 0.f;
+        if (++u == p.group) u = 0, ++i;
+        if (++c == cols) c = i = u = 0, ++h;
+      }
+    }
+  } else {
+    for (int i = 0; i < p.parts; ++i) {
+      const float *x = p.part + ((size_t)i * p.s.seqs + b) * p.c.heads * p.len_pad + j;
 #pragma unroll 8
-    for (int h = 0; h < p.c.heads; ++h) sum += x[(size_t)h * p.len_pad];
+      for (int h = 0; h < p.c.heads; ++h) sum += x[(size_t)h * p.len_pad];
+    }
   }
-  p.c.w[((size_t)id << p.c.shift) + (j & ((1 << p.c.shift) - 1))] += sum;
+  return sum;
+}
+
+// Adds the sums to the pages' weights.  Sequences may share pages (a common
+// prefix) and a table may name one twice, so a page's sums are added by one
+// workgroup, in the order of the tables' blocks: the attention (or the kernel
+// above) has chained each block that some row sees to its page's list, of
+// kChains for each workgroup; the workgroup's threads follow them, the blocks
+// are put in order, and as many as the threads hold are taken at a time.
+// Where there are more than kBlocks (a page that very many share) it looks
+// through the tables instead.
+//
+// Bound by latency: list, lengths, scores, one after the other.  16 sequences
+// of 6007 tokens 58 us with the attention, 78 us where they share 40 of their
+// 94 blocks (one workgroup then takes 16 blocks, four at a time).
+constexpr int kBlocks = 1024, kLook = 4;
+static_assert(kBlocks == 256 * kLook, "");
+
+template <bool FEW>
+__global__ __launch_bounds__(256) void k_kv8_weights_add(WeightParams p) {
+  __shared__ int2 found[kBlocks], list[kBlocks];  // (block's number, page)
+  __shared__ int count, part[kLook][4];
+  __shared__ float sums[256];
+  const int tid = (int)threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int shift = p.c.shift, page = 1 << shift, deal = 256 >> shift;
+  const unsigned mine = blockIdx.x;
+  // this thread's word of the page that is added to (threads of the first `page`)
+  int open = -1;
+  float acc = 0.f;
+  float *const word = p.c.w + (tid & (page - 1));
+  auto close = [&]() {
+    if (open >= 0) word[(size_t)open << shift] = acc;
+  };
+  auto take = [&](int n) {  // the first n of the list
+    for (int i0 = 0; i0 < n; i0 += deal) {
+      const int i = i0 + (tid >> shift);
+      float x = 0.f;
+      if (i < n) {
+        const unsigned e = (unsigned)list[i].x, b = e / (unsigned)p.links.blocks;
+        const Kv8Seen q = kv8_seen(p.a, p.s, shift, (int)b);
+        const int j = (int)((e - b * (unsigned)p.links.blocks) << shift) + (tid & (page - 1));
+        if (j >= q.lo && j < q.hi) x = token_sum<FEW>(p, (int)b, q.r0, q.rows, j);
+      }
+      sums[tid] = x;
+      __syncthreads();
+      if (tid < page) {
+        for (int k = 0; k < deal && i0 + k < n; ++k) {
+          const int id = list[i0 + k].y;
+          if (id != open) {
+            close();
+            open = id;
+            acc = word[(size_t)id << shift];
+          }
+          acc += sums[(k << shift) + tid];
+        }
+      }
+      __syncthreads();
+    }
+  };
+
+  if (tid == 0) count = 0;
+  __syncthreads();
+  if (tid < kKv8Chains) {
+    unsigned *head = p.links.head + ((unsigned)tid << p.links.bits) + mine;
+    unsigned e = *head;
+    if (e) *head = 0;
+    while (e) {
+      const int at = atomicAdd(&count, 1);
+      if (at >= kBlocks) break;
+      const uint2 link = p.links.next[e - 1];
+      found[at] = int2{(int)(e - 1), (int)link.y};
+      e = link.x;
+    }
+  }
+  __syncthreads();
+  const int n = count;
+  if (n == 0) return;
+  if (n <= kBlocks) {
+    for (int i = tid; i < n; i += 256) {
+      const int2 x = found[i];
+      int rank = 0;
+      for (int k = 0; k < n; ++k) rank += (unsigned)found[k].x < (unsigned)x.x ? 1 : 0;
+      list[rank] = x;
+    }
+    __syncthreads();
+    take(n);
+  } else {
+    const unsigned all = (unsigned)p.s.seqs * (unsigned)p.links.blocks;
+    for (unsigned e0 = 0; e0 < all; e0 += kBlocks) {
+      uint64_t hit[kLook];
+      int id[kLook];
+#pragma unroll
+      for (int u = 0; u < kLook; ++u) {
+        const unsigned e = e0 + 256 * u + tid, b = e / (unsigned)p.links.blocks;
+        id[u] = -1;
+        if (e < all) {
+          const Kv8Seen q = kv8_seen(p.a, p.s, shift, (int)b);
+          const int col = (int)(e - b * (unsigned)p.links.blocks);
+          if (q.hi > q.lo && col >= q.lo >> shift && col <= (q.hi - 1) >> shift) id[u] = kv8_page(p.s, p.c, (int)b, col);
+        }
+        hit[u] = __ballot(id[u] >= 0 && ((unsigned)id[u] & ((1u << p.links.bits) - 1u)) == mine);
+        if (lane == 0) part[u][wave] = __popcll(hit[u]);
+      }
+      __syncthreads();
+      int m = 0;
+#pragma unroll
+      for (int u = 0; u < kLook; ++u) {
+        int to = m;
+        for (int w = 0; w < 4; ++w) {
+          if (w < wave) to += part[u][w];
+          m += part[u][w];
+        }
+        if (hit[u] >> lane & 1u)
+          list[to + __popcll(hit[u] & ((1ull << lane) - 1ull))] = int2{(int)(e0 + 256 * u + tid), id[u]};
+      }
+      __syncthreads();
+      take(m);
+    }
+  }
+  close();
 }
 
 }  // namespace
 
 hipError_t launch_kv8_attention(const Kv8Attn &a, const Kv8Pool &c, const Kv8Batch &s, int dim,
-                                const Kv8Plan &pl, unsigned *counters, float *part, float *scores, hipStream_t stream) {
+                                const Kv8Plan &pl, unsigned *counters, float *part, float *scores,
+                                const Kv8Links &links, hipStream_t stream) {
   if (pl.few) {
     const DecodeParams p{a, c, s, pl.group, pl.blocks, pl.spw, pl.rounds, pl.splits, part, counters,
-                         pl.score_cols ? scores : nullptr, pl.len_pad, pl.score_cols};
+                         pl.score_cols ? scores : nullptr, pl.len_pad, pl.score_cols, links};
     const dim3 grid((unsigned)pl.splits * (unsigned)(s.seqs * c.heads * pl.blocks));
     auto k = dim == 64    ? (pl.ct == 1   ? k_kv8_decode<64, 1>
                              : pl.ct == 2 ? k_kv8_decode<64, 2>
@@ -1284,19 +1426,19 @@ hipError_t launch_kv8_attention(const Kv8Attn &a, const Kv8Pool &c, const Kv8Bat
 }
 
 hipError_t launch_kv8_weights(const Kv8Attn &a, const Kv8Pool &c, const Kv8Batch &s, int dim,
-                              const Kv8Plan &pl, float *scores, hipStream_t stream) {
+                              const Kv8Plan &pl, float *scores, const Kv8Links &links, hipStream_t stream) {
   if (a.max_len <= 0) return hipSuccess;
-  const WeightParams p{a, c, s, pl.group, pl.parts, pl.len_pad, scores, pl.score_cols, scores};
-  const dim3 tokens((unsigned)((a.max_len + 255) / 256), (unsigned)s.seqs);
+  const WeightParams p{a, c, s, pl.group, pl.parts, pl.len_pad, scores, pl.score_cols, scores, links};
+  const unsigned groups = 1u << links.bits;
   if (pl.score_cols) {
-    k_kv8_weights_few<<<tokens, dim3(256), 0, stream>>>(p);
+    k_kv8_weights_add<true><<<dim3(groups), dim3(256), 0, stream>>>(p);
     return hipGetLastError();
   }
   const dim3 grid((unsigned)(pl.len_pad / kWeightTokens), (unsigned)c.heads, (unsigned)(s.seqs * pl.parts));
   auto k = dim == 64 ? k_kv8_weights_many<64> : dim == 128 ? k_kv8_weights_many<128> : k_kv8_weights_many<256>;
   k<<<grid, dim3(64 * kWeightWaves), 0, stream>>>(p);
   if (hipError_t e = hipGetLastError()) return e;
-  k_kv8_weights_join<<<tokens, dim3(256), 0, stream>>>(p);
+  k_kv8_weights_add<false><<<dim3(groups), dim3(256), 0, stream>>>(p);
   return hipGetLastError();
 }
 

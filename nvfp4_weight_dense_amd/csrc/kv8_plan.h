@@ -52,9 +52,12 @@ struct Kv8Plan {
   // the weights pass: tokens of a sequence (rounded up); columns whose scores
   // the attention leaves for it (0: it takes K again), parts of the columns
   int len_pad, score_cols, parts;
-  size_t counter_bytes, part_floats, score_floats;
+  int link_bits, link_blocks;  // of the lists of blocks (Kv8Links)
+  size_t counter_bytes, part_floats, score_floats, link_words;
 };
 constexpr int kKv8MaxItems = 65536;  // arrival counters
+
+constexpr int kKv8LinkBits = 11, kKv8Chains = 32;  // at most 2^11 workgroups of so many lists
 
 constexpr int kDecodeWaves = 4;  // of a workgroup (few rows)
 constexpr int kMaxSplits = 128;  // of a sequence's tokens
@@ -91,7 +94,8 @@ inline Kv8Plan kv8_plan(const Kv8Attn &a, const Kv8Pool &c, const Kv8Batch &s, i
   pl.group = a.q_heads / c.heads;
   const int64_t cols = cols_of(s, pl);
   pl.few = cols <= kv8_few_cols(dim);
-  pl.counter_bytes = kKv8MaxItems * 4;
+  // (the same for every call, so that one of other sizes finds its words as they have to be)
+  pl.counter_bytes = (size_t)(kKv8MaxItems + (kKv8Chains << kKv8LinkBits)) * 4;
   if (pl.few) {
     pl.ct = few_tiles(cols, dim);
     pl.blocks = (int)((cols + 16 * pl.ct - 1) / (16 * pl.ct));
@@ -136,6 +140,9 @@ inline Kv8Plan kv8_plan(const Kv8Attn &a, const Kv8Pool &c, const Kv8Batch &s, i
   pl.len_pad = (a.max_len + kWeightTokens - 1) / kWeightTokens * kWeightTokens;
   pl.parts = 1;
   if (c.w) {
+    pl.link_blocks = (int)(((int64_t)a.max_len + (1 << c.shift) - 1) >> c.shift);
+    pl.link_words = 2 * (size_t)s.seqs * pl.link_blocks;
+    while (pl.link_bits < kKv8LinkBits && 1 << pl.link_bits < c.pages) ++pl.link_bits;
     const size_t tokens = (size_t)s.seqs * c.heads * pl.len_pad;
     if (pl.few && cols <= 16 && cols * pl.len_pad < (1 << 29)) {
       pl.score_cols = (int)cols;
@@ -153,7 +160,7 @@ inline Kv8Plan kv8_plan(const Kv8Attn &a, const Kv8Pool &c, const Kv8Batch &s, i
 // Bytes of a workspace: the arrival counters, then the floats.
 inline size_t kv8_align(size_t b) { return (b + 255) & ~(size_t)255; }
 inline size_t kv8_workspace_bytes(const Kv8Plan &pl) {
-  return kv8_align(pl.counter_bytes) + kv8_align(4 * (pl.part_floats + pl.score_floats));
+  return kv8_align(pl.counter_bytes) + kv8_align(4 * (pl.part_floats + pl.score_floats + pl.link_words));
 }
 
 // Those of any call with these sequences or fewer, as many rows and tokens of
@@ -178,7 +185,7 @@ inline size_t kv8_workspace_bound(const Kv8Attn &a, const Kv8Pool &c, const Kv8B
   }
   if (!pl.few) floats = std::max(floats, 2 * kManyGroups * (size_t)many_floats(dim) + 2 * kManyItems);
   // 16 columns' scores, or kWeightGroups parts of kWeightTokens
-  if (c.w) floats += std::max(pairs * pl.len_pad * 16, (size_t)kWeightGroups * kWeightTokens);
+  if (c.w) floats += std::max(pairs * pl.len_pad * 16, (size_t)kWeightGroups * kWeightTokens) + pl.link_words;
   return kv8_align(pl.counter_bytes) + kv8_align(4 * floats);
 }
 

@@ -285,14 +285,26 @@ hipError_t launch_kv8_evict(const Kv8Pool &c, const Kv8Batch &s, int dim, int ma
                             int new_cols, int keep, int recent, int sink, int *new_lens, int *kept,
                             const Kv8EvictPlan &pl, unsigned *hist, uint32_t *words, hipStream_t stream);
 
+// Lists of the blocks of tokens that name each page, for the weights: block
+// col of sequence b is number e = b * blocks + col.  Page id's list starts at
+// head[id % 2^bits + 2^bits * (id / 2^bits % kKv8Chains)] with e + 1 (0: empty)
+// and goes on with next[e].x; next[e].y is the page.  The heads are zero before
+// and after a call.
+struct Kv8Links {
+  unsigned *head;
+  uint2 *next;
+  int blocks, bits;
+};
+
 // `counters` (counter_bytes, zero on entry, left zero) and `part`
 // (part_floats) as planned by kv8_plan; `scores` (score_floats), or null where no weights
 // are wanted.
 hipError_t launch_kv8_attention(const Kv8Attn &a, const Kv8Pool &c, const Kv8Batch &s, int dim,
-                                const Kv8Plan &pl, unsigned *counters, float *part, float *scores, hipStream_t stream);
+                                const Kv8Plan &pl, unsigned *counters, float *part, float *scores,
+                                const Kv8Links &links, hipStream_t stream);
 // Adds each visible token's attention weight, summed over rows and query
 // heads, to c.w, from the lse (and scores) that the attention wrote.
 hipError_t launch_kv8_weights(const Kv8Attn &a, const Kv8Pool &c, const Kv8Batch &s, int dim,
-                              const Kv8Plan &pl, float *scores, hipStream_t stream);
+                              const Kv8Plan &pl, float *scores, const Kv8Links &links, hipStream_t stream);
 
 }  // namespace nvfp4

@@ -80,3 +80,96 @@ def test_windows_wider_than_any_cache(dim, page, q_heads, lens, rows, window):
     want = _check(c, table, q, q_heads, lens, rows, window=10 ** 6)
     for a, b in zip(got, want):
         assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+
+
+# ---- shared pages ------------------------------------------------------------------------------------
+
+def _shared(kind, lens, page, pages, seed):
+    """A table whose sequences share pages: all of a common prefix; at other blocks; within one sequence too."""
+    table = _table(lens, page, pages, seed)
+    g = _gen(seed + 1)
+    if kind == "prefix":
+        for b in range(1, len(lens)):
+            most = min(lens[0], lens[b]) // page
+            table[b, :most] = table[0, :most]
+    elif kind == "anywhere":
+        for b, n in enumerate(lens):
+            for c in range(-(-n // page)):
+                if float(torch.rand((), generator=g)) < 0.5:
+                    table[b, c] = int(torch.randint(0, 3, (), generator=g))
+    else:                                              # every block names one of two pages
+        for b, n in enumerate(lens):
+            table[b, :-(-n // page)] = torch.randint(0, 2, (-(-n // page),), generator=g, dtype=torch.int32)
+    return table
+
+
+SHARED = [  # dim, page, heads, q_heads, lens, rows, window
+    (128, 64, 2, 8, [700, 641, 130, 64, 65, 1, 0, 400], [1, 1, 1, 1, 1, 1, 1, 0], 0),
+    (128, 16, 1, 4, [300, 290, 17, 260, 33], [1, 4, 2, 4, 3], 0),
+    (64, 128, 2, 2, [500, 384, 129], [7, 1, 5], 200),
+    (256, 32, 1, 1, [330, 290, 64], [16, 3, 9], 0),
+    (128, 64, 2, 4, [300, 280, 90], [30, 25, 1], 0),            # more columns than the attention leaves scores for
+    (64, 32, 1, 2, [700, 650, 333, 65], [300, 222, 100, 65], 0),
+    (256, 16, 1, 4, [210, 199, 40], [90, 60, 2], 70),
+    (64, 64, 1, 1, [129 + i for i in range(150)], [1] * 150, 0),  # more sequences than are looked up at a time
+]
+
+
+@pytest.mark.parametrize("kind", ["prefix", "anywhere", "two"])
+@pytest.mark.parametrize("dim,page,heads,q_heads,lens,rows,window", SHARED)
+def test_weights_of_shared_pages(dim, page, heads, q_heads, lens, rows, window, kind):
+    """A page's weights get what the rows of every sequence that names it give, with the same bits each time."""
+    _say("shared pages", kind, dim, page, heads, q_heads, len(lens), max(lens), max(rows), window)
+    pages = sum(-(-n // page) for n in lens) + 3
+    c = _filled(pages, heads, dim, page, 150, weights=True)
+    table = _shared(kind, lens, page, pages, 151)
+    q = torch.randn(sum(rows), q_heads, dim, generator=_gen(152)).bfloat16()
+    pool = ref.Pool(c)
+    out, lse, b_out, b_lse, w = pool.attention(q, table, lens, rows, 0.002, window)
+    want, bound = pool.weights.double(), pool.weights.double() * 2.0 ** -23
+    uses = torch.zeros_like(want)
+    for b, (x, bx) in enumerate(w):
+        at = pool.where(table, b, torch.arange(len(x)))
+        assert bool((at[0] >= 0).all())
+        want.index_put_(at, x, accumulate=True)
+        bound.index_put_(at, bx, accumulate=True)
+        uses.index_put_(at, torch.ones_like(x), accumulate=True)
+    bound += uses * want * 2.0 ** -24                   # one addition for each use
+    first = None
+    for _ in range(4):
+        dev = _gpu(c)
+        got = nv.kv8_attention(q.cuda(), dev, table.cuda(), _i32(lens).cuda(), _starts(rows).cuda(), scale=0.002,
+                               window=window, max_rows=max(rows), lse=True, accumulate=True)
+        _within(got[0], out, b_out, "out")
+        _within(got[1], lse, b_lse, "lse")
+        _within(dev.weights, want, bound + 1e-30, "weights")
+        bits = dev.weights.view(torch.int32).clone()
+        assert first is None or torch.equal(first, bits)
+        first = bits
+
+
+def test_weights_of_a_page_that_every_block_names():
+    """More blocks on one page than are listed at a time."""
+    _say("one page")
+    dim, page, lens = 64, 16, [40000, 17, 20000]
+    c = _filled(3, 1, dim, page, 160, weights=True)
+    table = torch.full((3, 2500), 1, dtype=torch.int32)
+    q = torch.randn(3, 2, dim, generator=_gen(161)).bfloat16()
+    pool = ref.Pool(c)
+    *_, w = pool.attention(q, table, lens, [1, 1, 1], 0.002)
+    want = pool.weights.double()
+    for x, _ in w:
+        want[1] += torch.nn.functional.pad(x, (0, -len(x) % page)).reshape(-1, page).sum(0)
+    dev = _gpu(c)
+    nv.kv8_attention(q.cuda(), dev, table.cuda(), _i32(lens).cuda(), scale=0.002, accumulate=True)
+    # each weight is the sum of some thousand, each of which is off by some 2^-20 of itself
+    _within(dev.weights, want, want * (5000 * 2.0 ** -24 + 2.0 ** -18), "weights")
+
+
+def test_lengths_of_a_table_wider_than_its_sequences():
+    """Weights where the table names pages beyond the lengths: those get none."""
+    _say("wide table")
+    c, table, q = _problem(128, 64, 1, 4, [100, 64, 1], [1, 1, 1], 0, seed=170)
+    wide = torch.randint(0, c.k_codes.shape[0], (3, 700), generator=_gen(171), dtype=torch.int32)
+    wide[:, :2] = table[:, :2].clamp(min=0)
+    _check(c, wide, q, 4, [100, 64, 1], [1, 1, 1])
