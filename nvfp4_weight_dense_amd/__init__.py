@@ -14,7 +14,8 @@ the GPU; a weight is any object with ``codes`` (uint8 ``[n, k/2]``),
 ``[n, k]``, E4M3 bits) and ``scales`` (float32 ``[ceil(n/128),
 ceil(k/128)]``) -- see :class:`FP8Weight`.  The ``kv8_*`` calls take a
 :class:`KV8Cache`, a page table and lengths (int32, on the GPU) and bf16
-``[rows, heads, dim]`` arrays that may be parts of a larger one.
+``[rows, heads, dim]`` arrays that may be parts of a larger one; what they
+return, unless the caller gave it, belongs to the stream they run on.
 """
 
 from __future__ import annotations
@@ -747,6 +748,19 @@ def _kv8_stream(stream, dev: int):
     return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
 
 
+def _kv8_empty(shape, dtype, device, stream):
+    """A tensor of the stream that uses it: memory that the caching allocator
+    hands out belongs to the stream it was asked for on, so one of the current
+    stream's could be taken for other work, when the caller drops it or before
+    its last reader there has ended, while the call's kernels use it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream), device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def kv8_append(k: torch.Tensor, v: torch.Tensor, cache: KV8Cache, table: torch.Tensor,
                lens: torch.Tensor, starts: torch.Tensor | None = None, *, max_rows: int | None = None,
                stream=None) -> None:
@@ -802,20 +816,21 @@ def kv8_attention(q: torch.Tensor, cache: KV8Cache, table: torch.Tensor, lens: t
     shape = q.shape
     rows, q_heads, _ = shape
     cb, _ = _ckv8_batch(table, lens, starts, rows, max_rows, max_len, page)
-    if out is None:
-        out = torch.empty(shape, dtype=torch.bfloat16, device=q.device)
-    elif out.dtype != torch.bfloat16 or out.shape != shape or not out.is_contiguous():
+    if out is not None and (out.dtype != torch.bfloat16 or out.shape != shape or not out.is_contiguous()):
         raise ValueError(f"out: expected a contiguous bfloat16 [{rows}, {q_heads}, {dim}] tensor")
     give = lse is not None and lse is not False
-    if lse is True or (accumulate and not give):
-        lse = torch.empty((rows, q_heads), dtype=torch.float32, device=q.device)
-    elif not give:
+    make = lse is True or (accumulate and not give)
+    if make or not give:
         lse = None
     elif lse.dtype != torch.float32 or lse.shape != (rows, q_heads) or not lse.is_contiguous():
         raise ValueError(f"lse: expected a contiguous float32 [{rows}, {q_heads}] tensor")
     if workspace is not None and (workspace.dtype != torch.uint8 or not workspace.is_contiguous()):
         raise ValueError("workspace: expected a contiguous uint8 tensor (kv8_workspace)")
     _kv8_on(dev, q, out, lse, workspace, table, lens, starts)
+    if out is None:
+        out = _kv8_empty(shape, torch.bfloat16, q.device, stream)
+    if make:
+        lse = _kv8_empty((rows, q_heads), torch.float32, q.device, stream)
     window = max(min(int(window), 2 ** 31 - 1), -1)  # (ctypes would take it modulo 2^32)
     _check(L.kv8_attention(cq, q_heads, dim ** -0.5 if scale is None else float(scale), window, cc, cb,
                            out.data_ptr(), None if lse is None else lse.data_ptr(), 1 if accumulate else 0,
@@ -841,8 +856,8 @@ def kv8_evict(cache: KV8Cache, table: torch.Tensor, lens: torch.Tensor, new_tabl
     if keep <= 0:
         raise ValueError(f"keep: {keep}, expected at least 1")
     _kv8_on(dev, table, lens, new_table)
-    new_lens = torch.empty((seqs,), dtype=torch.int32, device=table.device)
-    kept = torch.empty((seqs, keep), dtype=torch.int32, device=table.device)
+    new_lens = _kv8_empty((seqs,), torch.int32, table.device, stream)
+    kept = _kv8_empty((seqs, keep), torch.int32, table.device, stream)
     _check(L.kv8_evict(cc, cb, new_table.data_ptr(), new_table.shape[1], keep, int(recent), int(sink),
                        new_lens.data_ptr(), kept.data_ptr(), _kv8_stream(stream, dev)))
     return new_lens, kept

@@ -173,3 +173,46 @@ def test_lengths_of_a_table_wider_than_its_sequences():
     wide = torch.randint(0, c.k_codes.shape[0], (3, 700), generator=_gen(171), dtype=torch.int32)
     wide[:, :2] = table[:, :2].clamp(min=0)
     _check(c, wide, q, 4, [100, 64, 1], [1, 1, 1])
+
+
+# ---- streams -----------------------------------------------------------------------------------------
+
+def _others(like):
+    """Takes memory of these tensors' sizes for other work of the current stream, and fills it."""
+    got = [torch.empty_like(x) for x in like for _ in range(8)]
+    for x in got:
+        x.view(torch.uint8).fill_(0xFF)
+    return got
+
+
+@pytest.mark.parametrize("handle", [False, True])
+@pytest.mark.parametrize("rows", [[1, 1, 1, 1], [30, 5, 64, 1]])
+def test_tensors_of_a_call_on_another_stream(rows, handle):
+    """The call's own tensors are not handed out again before its kernels have run: its stream is held up while
+    the current one asks for tensors of the same sizes."""
+    _say("another stream", rows, handle)
+    lens = [900, 333, 64, 1]
+    c, table, q = _problem(128, 64, 2, 8, lens, rows, 0, seed=180)
+    pages = c.k_codes.shape[0]
+    more = _filled(pages + 8, 2, 128, 64, 181, weights=True)
+    for x in ("k_codes", "v_codes", "k_scales", "v_scales", "weights"):
+        getattr(more, x)[:pages] = getattr(c, x)
+    new_table = (pages + torch.randperm(8, generator=_gen(182))).to(torch.int32).reshape(4, 2).cuda()
+    t, n, at, qd = table.cuda(), _i32(lens).cuda(), _starts(rows).cuda(), q.cuda()[:, 1:9]
+    kw = dict(max_rows=max(rows), scale=0.002, accumulate=True)
+    here, there = _gpu(more), _gpu(more)
+    want = nv.kv8_attention(qd, here, t, n, at, **kw), nv.kv8_evict(here, t, n, new_table, 100, recent=9, sink=2)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(200_000_000)                   # about a tenth of a second
+    to = s.cuda_stream if handle else s
+    out = nv.kv8_attention(qd, there, t, n, at, stream=to, **kw)
+    nv.kv8_evict(there, t, n, new_table, 100, recent=9, sink=2, stream=to)      # (what it returns is dropped)
+    held = _others([torch.empty(sum(rows), 8, device="cuda"), *want[1]])
+    assert not s.query()
+    torch.cuda.synchronize()
+    assert torch.equal(out.view(torch.int16), want[0].view(torch.int16))
+    for x in ("k_codes", "v_codes", "k_scales", "v_scales", "weights"):
+        assert torch.equal(getattr(there, x).view(torch.uint8), getattr(here, x).view(torch.uint8)), x
+    assert all(bool((x.view(torch.uint8) == 0xFF).all()) for x in held)
