@@ -310,8 +310,9 @@ int dense_ffn_forward_q2(const void *x, int32_t m, int32_t hidden,
  *
  * A cache is a pool of pages of `page` tokens:
  *   k_codes, v_codes  : device, uint8 [pages][heads][page * dim], E4M3FN;
- *   k_scales, v_scales: device, uint8 [pages][heads], E8M0 (1..254):
- *                       value = e4m3(code) * 2^(scale - 127);
+ *   k_scales, v_scales: device, uint8 [pages][heads], E8M0 (1..246, so that
+ *                       every code's value is a bf16 number; a larger byte
+ *                       acts as 246, 0 as 1): value = e4m3(code) * 2^(scale - 127);
  *   weights           : device, fp32 [pages][page], the attention weight each
  *                       token has received so far; null if not kept.
  * A page's codes of one head are page/16 units of 16 tokens, 16 * dim bytes
@@ -393,8 +394,9 @@ int64_t kv8_attention_workspace(int32_t q_heads, const kv8_cache *cache, const k
  * see it, in an order that does not change from call to call.  Sequences may
  * share pages (a common prefix): a page's weights get the sums of every
  * sequence that names it, and once for each time it does.
- * fp32 throughout, except that e^(s_j - m) is rounded to bf16 before its
- * product with V (as the other operand of that product is at most bf16).
+ * fp32 throughout (sums over V of values up to 2^90 do not overflow), except
+ * that e^(s_j - m) is rounded to bf16 before its product with V (as the other
+ * operand of that product is at most bf16).
  * workspace: device memory of kv8_attention_workspace bytes, 256-byte
  * aligned, all zero before its first use and left as it needs to be for the
  * next; one per stream that calls may overlap on.  Null: the library's

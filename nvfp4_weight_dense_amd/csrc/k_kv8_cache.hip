@@ -107,7 +107,7 @@ __global__ __launch_bounds__(T) void k_kv8_append(AppendParams p) {
   const size_t ph = (size_t)id * p.c.heads + h;
   uint8_t *codes = (isv ? p.c.v : p.c.k) + (ph << shift) * D;
   uint8_t *scale = (isv ? p.c.vs : p.c.ks) + ph;
-  const int was = s0 > 0 ? (int)*scale - 127 : kKv8MinExp;
+  const int was = s0 > 0 ? min((int)*scale - 127, kKv8MaxExp) : kKv8MinExp;
 
   uint32_t bits = 0;
 #pragma unroll

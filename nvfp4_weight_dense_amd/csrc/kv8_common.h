@@ -54,9 +54,11 @@ __device__ __forceinline__ uint4 load_once(const uint4 *p) {
 __device__ __forceinline__ float kv8_two(int e) {  // 2^e, e >= -126
   return __uint_as_float((uint32_t)(e + 127) << 23);
 }
-// the scale of a byte in [1, 254]; 0 and 255, which no append writes, act as 1 and 254
+// The scale of a byte.  One above 246 (2^119, the largest that append and
+// eviction write) acts as 246: 448 * 2^120 is no bf16 number, and an infinite
+// operand times the probability 0 of a row that does not see it would be NaN.
 __device__ __forceinline__ float kv8_scale(uint32_t byte) {
-  return __uint_as_float(min(max(byte, 1u), 254u) << 23);
+  return __uint_as_float(min(max(byte, 1u), (uint32_t)(kKv8MaxExp + 127)) << 23);
 }
 
 // Smallest E in the scales' range with amax <= 448 * 2^E (448 = 1.75 * 2^8).

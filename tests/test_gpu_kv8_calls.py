@@ -216,3 +216,49 @@ def test_tensors_of_a_call_on_another_stream(rows, handle):
     for x in ("k_codes", "v_codes", "k_scales", "v_scales", "weights"):
         assert torch.equal(getattr(there, x).view(torch.uint8), getattr(here, x).view(torch.uint8)), x
     assert all(bool((x.view(torch.uint8) == 0xFF).all()) for x in held)
+
+
+# ---- scales ------------------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("byte", [246, 247, 250, 254, 255, 0])
+@pytest.mark.parametrize("dim,rows", [(128, [3, 1]), (64, [12, 9]), (256, [9, 16]), (128, [70, 40])])
+def test_scale_bytes_beyond_those_that_append_writes(dim, rows, byte):
+    """A byte above 246 acts as 246, whose largest code is still a bf16 number, and 0 as 1: rows that do not see
+    such a page's tokens keep their results, and those that do get the values these bytes stand for."""
+    _say("scale bytes", dim, rows, byte)
+    lens, page = [100, 75], 16
+    c, table, q = _problem(dim, page, 1, 4, lens, rows, 0, seed=190)
+    last = [int(table[b, (n - 1) // page]) for b, n in enumerate(lens)]
+    c.v_scales[last] = byte                               # seen by the last rows only
+    c.k_scales[int(table[0, 2])] = 0                      # scores of next to nothing
+    held = nv.KV8Cache(c.k_codes, c.v_codes, c.k_scales.clamp(1, 246), c.v_scales.clamp(1, 246), c.weights)
+    pool, dev = ref.Pool(held), _gpu(c)
+    want = pool.attention(q[:, 1:5], table, lens, rows, 0.002)
+    got = nv.kv8_attention(q.cuda()[:, 1:5], dev, table.cuda(), _i32(lens).cuda(), _starts(rows).cuda(), scale=0.002,
+                           max_rows=max(rows), lse=True)
+    at = 0
+    for n, r in zip(lens, rows):                          # rows at positions before the last page
+        some = slice(at, at + max(r - (n - (n - 1) // page * page), 0))
+        assert bool(torch.isfinite(got[0][some].float()).all())
+        _within(got[0][some], want[0][some], want[2][some], "out")
+        at += r
+    _within(got[1], want[1], want[3], "lse")
+    _within(got[0], want[0], want[2], "out") if byte < 240 else None
+
+
+@pytest.mark.parametrize("byte", [250, 255])
+def test_append_after_a_scale_byte_beyond_those_it_writes(byte):
+    """Tokens that join a page with such a scale keep their values; the page's byte becomes the one it acted as."""
+    _say("append, scale byte", byte)
+    c, table, _ = _problem(64, 16, 1, 1, [20], [1], 0, seed=200)
+    c.k_scales[:], c.v_scales[:] = byte, byte
+    held = nv.KV8Cache(c.k_codes, c.v_codes, c.k_scales.clamp(1, 246), c.v_scales.clamp(1, 246), c.weights)
+    for x in (torch.full((1, 1, 64), 2.0 ** 120), torch.full((1, 1, 64), -3.0e38)):
+        pool, dev = ref.Pool(held), _gpu(c)
+        x = x.bfloat16()
+        pool.append(x, x, table, [20], [1])
+        nv.kv8_append(x.cuda(), x.cuda(), dev, table.cuda(), _i32([20]).cuda())
+        page = int(table[0, 1])
+        assert int(dev.k_scales[page]) == int(dev.v_scales[page]) == 246
+        for isv, codes in ((0, dev.k_codes), (1, dev.v_codes)):
+            assert torch.equal(codes[page].cpu(), pool.raw(isv)[page])
