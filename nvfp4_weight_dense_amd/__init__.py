@@ -735,9 +735,11 @@ def _ckv8_batch(table, lens, starts, rows, max_rows, max_len, page):
 
 
 def _kv8_on(dev: int, *tensors):
-    """Every tensor on the cache's GPU (checked after the shapes)."""
+    """Every tensor on the cache's GPU, which is the current one (checked after the shapes)."""
     if dev < 0:
         raise ValueError("expected GPU tensors")
+    if torch._C._cuda_getDevice() != dev:  # (the library's launches and scratch are the current device's)
+        raise ValueError(f"tensors on cuda:{dev}, the current device is cuda:{torch._C._cuda_getDevice()}")
     for t in tensors:
         if t is not None and t.get_device() != dev:
             raise ValueError(f"tensors on {t.device} and cuda:{dev}: expected one device")
