@@ -419,6 +419,19 @@ int kv8_evict(const kv8_cache *cache, const kv8_batch *batch, const int32_t *new
               int32_t new_cols, int32_t keep, int32_t recent, int32_t sink, int32_t *new_lens,
               int32_t *kept, void *stream);
 
+/* kv8_evict takes scratch from the arena (see above) where max_len is beyond
+ * 32768 tokens.  kv8_evict_noalloc takes it from the caller instead, so that
+ * such calls may overlap on several streams and a captured one does not depend
+ * on the arena: the same arguments and results, and `workspace`, device memory
+ * of kv8_evict_workspace bytes (0 up to 32768 tokens: it may then be null; an
+ * upper bound for fewer sequences and a smaller max_len), 256-byte aligned, of
+ * any contents, one per stream. */
+int64_t kv8_evict_workspace(const kv8_cache *cache, const kv8_batch *batch);
+int kv8_evict_noalloc(const kv8_cache *cache, const kv8_batch *batch, const int32_t *new_table,
+                      int32_t new_cols, int32_t keep, int32_t recent, int32_t sink,
+                      int32_t *new_lens, int32_t *kept, void *workspace, int64_t workspace_bytes,
+                      void *stream);
+
 /* The calling thread's last error message ("" if none).  The pages' ops
  * return an error value whose message names the failed check (page
  * layers/dense_ffn_fixed.rs, the `ensure!`/`bail!` checks of

@@ -44,6 +44,7 @@ __all__ = [
     "dense_ffn_forward_lora", "FP8Weight", "fp8_quantize_rows", "fp8_gemm_w8a8",
     "dense_ffn_forward_w8a8", "Q2Weight", "q2_gemm_w2a16", "dense_ffn_forward_q2",
     "KV8Cache", "kv8_cache", "kv8_append", "kv8_attention", "kv8_workspace", "kv8_evict",
+    "kv8_evict_workspace",
     "nvfp4_last_error", "nvfp4_release", "nvfp4_abi_version", "load_library",
     "nvfp4_probe_mfma_bf16",
     "nvfp4_probe_read",
@@ -219,6 +220,7 @@ def load_library(path: str = LIB_PATH):
         "kv8_append": [kr, kr, kc, kb, vp],
         "kv8_attention": [kr, i32, ctypes.c_float, i32, kc, kb, vp, vp, i32, vp, i64, vp],
         "kv8_evict": [kc, kb, vp, i32, i32, i32, i32, vp, vp, vp],
+        "kv8_evict_noalloc": [kc, kb, vp, i32, i32, i32, i32, vp, vp, vp, i64, vp],
     }
     for name, args in sig.items():
         f = getattr(L, name)
@@ -232,6 +234,8 @@ def load_library(path: str = LIB_PATH):
     L.nvfp4_probe_encode.restype = ctypes.c_int
     L.kv8_attention_workspace.argtypes = [i32, kc, kb]
     L.kv8_attention_workspace.restype = i64
+    L.kv8_evict_workspace.argtypes = [kc, kb]
+    L.kv8_evict_workspace.restype = i64
     L.nvfp4_last_error.argtypes = []
     L.nvfp4_last_error.restype = ctypes.c_char_p
     L.nvfp4_release.argtypes = []
@@ -841,13 +845,28 @@ def kv8_attention(q: torch.Tensor, cache: KV8Cache, table: torch.Tensor, lens: t
     return (out, lse) if give else out
 
 
+def kv8_evict_workspace(cache: KV8Cache, table: torch.Tensor, lens: torch.Tensor, *,
+                        max_len: int | None = None) -> torch.Tensor:
+    """A workspace for kv8_evict calls of these sizes or smaller ones, for one
+    stream (without one, calls of more than 32768 tokens share the library's
+    scratch arena)."""
+    L = load_library()
+    cc, _, page, _, _ = _ckv8(cache)
+    n = L.kv8_evict_workspace(cc, _ckv8_batch(table, lens, None, 0, None, max_len, page)[0])
+    if n < 0:
+        _check(int(n))
+    return torch.empty((max(n, 256),), dtype=torch.uint8, device=cache.k_codes.device)
+
+
 def kv8_evict(cache: KV8Cache, table: torch.Tensor, lens: torch.Tensor, new_table: torch.Tensor, keep: int, *,
-              recent: int = 0, sink: int = 0, max_len: int | None = None, stream=None):
+              recent: int = 0, sink: int = 0, max_len: int | None = None,
+              workspace: torch.Tensor | None = None, stream=None):
     """Cut each sequence to at most `keep` tokens -- its first `sink`, its last
     `recent` and of the others those with the largest cache.weights -- and
     write them, in order, to the pages of new_table (int32 [seqs, new_cols],
     none of them a page of table).  Returns (new lens [seqs], kept positions
-    [seqs, keep] padded with -1), int32."""
+    [seqs, keep] padded with -1), int32.  workspace: a kv8_evict_workspace,
+    for calls that overlap on several streams or are captured."""
     L = load_library()
     cc, _, page, _, dev = _ckv8(cache)
     cb, seqs = _ckv8_batch(table, lens, None, 0, None, max_len, page)
@@ -857,9 +876,15 @@ def kv8_evict(cache: KV8Cache, table: torch.Tensor, lens: torch.Tensor, new_tabl
     keep = int(keep)
     if keep <= 0:
         raise ValueError(f"keep: {keep}, expected at least 1")
-    _kv8_on(dev, table, lens, new_table)
+    if workspace is not None and (workspace.dtype != torch.uint8 or not workspace.is_contiguous()):
+        raise ValueError("workspace: expected a contiguous uint8 tensor (kv8_evict_workspace)")
+    _kv8_on(dev, table, lens, new_table, workspace)
     new_lens = _kv8_empty((seqs,), torch.int32, table.device, stream)
     kept = _kv8_empty((seqs, keep), torch.int32, table.device, stream)
-    _check(L.kv8_evict(cc, cb, new_table.data_ptr(), new_table.shape[1], keep, int(recent), int(sink),
-                       new_lens.data_ptr(), kept.data_ptr(), _kv8_stream(stream, dev)))
+    args = (cc, cb, new_table.data_ptr(), new_table.shape[1], keep, int(recent), int(sink), new_lens.data_ptr(),
+            kept.data_ptr())
+    if workspace is None:
+        _check(L.kv8_evict(*args, _kv8_stream(stream, dev)))
+    else:
+        _check(L.kv8_evict_noalloc(*args, workspace.data_ptr(), workspace.numel(), _kv8_stream(stream, dev)))
     return new_lens, kept

@@ -553,6 +553,36 @@ Kv8Batch kv8_batch_ref(const kv8_batch *b) {
   return Kv8Batch{b->table, b->lens, b->starts, b->seqs, b->cols, b->rows, std::min(b->max_rows, b->rows)};
 }
 
+// `workspace` (as large as the plan asks, any contents), or null: the arena
+int run_evict(const char *name, const kv8_cache *cache, const kv8_batch *batch, const int32_t *new_table,
+              int32_t new_cols, int32_t keep, int32_t recent, int32_t sink, int32_t *new_lens, int32_t *kept,
+              void *workspace, int64_t need, hipStream_t s) {
+  int rc;
+  if ((rc = check_kv8_cache(cache)) || (rc = check_kv8_batch(batch, cache, false))) return rc;
+  if (!cache->weights) return fail(NVFP4_EINVAL, "%s: the cache keeps no weights", name);
+  if (keep <= 0 || recent < 0 || sink < 0 || (int64_t)recent + sink > keep)
+    return fail(NVFP4_EINVAL, "%s: keep=%d must be positive and hold recent=%d and sink=%d", name, keep, recent, sink);
+  if ((int64_t)new_cols * cache->page < keep || keep > (1 << 28))
+    return fail(NVFP4_ESHAPE, "%s: %d pages of %d tokens do not hold keep=%d", name, new_cols, cache->page, keep);
+  if (batch->seqs == 0) return NVFP4_OK;
+  if (!new_table || !new_lens || !kept) return fail(NVFP4_EINVAL, "%s: null pointer", name);
+  if (((uintptr_t)new_table | (uintptr_t)new_lens | (uintptr_t)kept) & 3u)
+    return fail(NVFP4_EINVAL, "%s: arrays must be 4-byte aligned", name);
+  const int max_len = std::min(batch->max_len, batch->cols * cache->page);
+  const Kv8EvictPlan pl = kv8_evict_plan(kv8_batch_ref(batch), max_len);
+  unsigned *hist = (unsigned *)workspace;
+  void *words = hist + pl.hist_words;
+  if (!workspace || need == 0) {
+    if ((rc = counters_get(pl.hist_words, &hist)) || (pl.words && (rc = arena_get(pl.words * 4, &words)))) return rc;
+  } else if ((rc = hip_status(launch_zero_words(hist, (int)pl.hist_words, s), "eviction histograms' clear"))) {
+    return rc;
+  }
+  ProfileScope ps(name, batch->seqs, s);
+  return hip_status(launch_kv8_evict(kv8_pool(cache), kv8_batch_ref(batch), cache->dim, max_len, new_table, new_cols,
+                                     keep, recent, sink, new_lens, kept, pl, hist, (uint32_t *)words, s),
+                    "eviction launch");
+}
+
 struct NoAllocDev {
   bool ready = false;
   void *ptr = nullptr;
@@ -1205,28 +1235,28 @@ int kv8_attention(const kv8_rows *q, int32_t q_heads, float scale, int32_t windo
 int kv8_evict(const kv8_cache *cache, const kv8_batch *batch, const int32_t *new_table, int32_t new_cols,
               int32_t keep, int32_t recent, int32_t sink, int32_t *new_lens, int32_t *kept, void *stream) {
   g_err.clear();
+  return run_evict("kv8_evict", cache, batch, new_table, new_cols, keep, recent, sink, new_lens, kept, nullptr, 0,
+                   (hipStream_t)stream);
+}
+
+int64_t kv8_evict_workspace(const kv8_cache *cache, const kv8_batch *batch) {
+  g_err.clear();
   int rc;
   if ((rc = check_kv8_cache(cache)) || (rc = check_kv8_batch(batch, cache, false))) return rc;
-  if (!cache->weights) return fail(NVFP4_EINVAL, "kv8_evict: the cache keeps no weights");
-  if (keep <= 0 || recent < 0 || sink < 0 || (int64_t)recent + sink > keep)
-    return fail(NVFP4_EINVAL, "kv8_evict: keep=%d must be positive and hold recent=%d and sink=%d", keep, recent,
-                sink);
-  if ((int64_t)new_cols * cache->page < keep || keep > (1 << 28))
-    return fail(NVFP4_ESHAPE, "kv8_evict: %d pages of %d tokens do not hold keep=%d", new_cols, cache->page, keep);
-  if (batch->seqs == 0) return NVFP4_OK;
-  if (!new_table || !new_lens || !kept) return fail(NVFP4_EINVAL, "kv8_evict: null pointer");
-  if (((uintptr_t)new_table | (uintptr_t)new_lens | (uintptr_t)kept) & 3u)
-    return fail(NVFP4_EINVAL, "kv8_evict: arrays must be 4-byte aligned");
-  hipStream_t s = (hipStream_t)stream;
-  const int max_len = std::min(batch->max_len, batch->cols * cache->page);
-  const Kv8EvictPlan pl = kv8_evict_plan(kv8_batch_ref(batch), max_len);
-  unsigned *hist = nullptr;
-  void *words = nullptr;
-  if ((rc = counters_get(pl.hist_words, &hist)) || (pl.words && (rc = arena_get(pl.words * 4, &words)))) return rc;
-  ProfileScope ps("kv8_evict", batch->seqs, s);
-  return hip_status(launch_kv8_evict(kv8_pool(cache), kv8_batch_ref(batch), cache->dim, max_len, new_table, new_cols,
-                                     keep, recent, sink, new_lens, kept, pl, hist, (uint32_t *)words, s),
-                    "kv8_evict launch");
+  const Kv8EvictPlan pl = kv8_evict_plan(kv8_batch_ref(batch), std::min(batch->max_len, batch->cols * cache->page));
+  return (int64_t)align256(4 * (pl.hist_words + pl.words));
+}
+
+int kv8_evict_noalloc(const kv8_cache *cache, const kv8_batch *batch, const int32_t *new_table, int32_t new_cols,
+                      int32_t keep, int32_t recent, int32_t sink, int32_t *new_lens, int32_t *kept, void *workspace,
+                      int64_t workspace_bytes, void *stream) {
+  const int64_t need = kv8_evict_workspace(cache, batch);  // checks them too
+  if (need < 0) return (int)need;
+  if (need > 0 && (!workspace || workspace_bytes < need || ((uintptr_t)workspace & 255u)))
+    return fail(NVFP4_EINVAL, "kv8_evict_noalloc: the workspace must be 256-byte aligned and of %lld bytes",
+                (long long)need);
+  return run_evict("kv8_evict_noalloc", cache, batch, new_table, new_cols, keep, recent, sink, new_lens, kept,
+                   workspace, need, (hipStream_t)stream);
 }
 
 }  // extern "C"

@@ -262,3 +262,71 @@ def test_append_after_a_scale_byte_beyond_those_it_writes(byte):
         assert int(dev.k_scales[page]) == int(dev.v_scales[page]) == 246
         for isv, codes in ((0, dev.k_codes), (1, dev.v_codes)):
             assert torch.equal(codes[page].cpu(), pool.raw(isv)[page])
+
+
+# ---- eviction with its own workspace -----------------------------------------------------------------
+
+def _long(seed, lens=(41003, 900, 33000), keep=1500):
+    dim, page = 64, 128
+    per = -(-keep // page)
+    pages = sum(-(-n // page) for n in lens) + len(lens) * per
+    c = _filled(pages, 1, dim, page, seed, weights=True)
+    table = _table(list(lens), page, pages, seed + 1, spare=len(lens) * per)
+    new_table = (pages - len(lens) * per + torch.arange(len(lens) * per)).to(torch.int32).reshape(len(lens), per)
+    pool = ref.Pool(c)
+    news, kept = pool.evict(table, list(lens), new_table, keep, 130, 5)
+    return c, pool, news, kept, (table.cuda(), _i32(list(lens)).cuda(), new_table.cuda(), keep)
+
+
+def test_evictions_that_overlap():
+    """Two streams with a workspace each, of any contents and used again for fewer sequences and tokens."""
+    _say("evictions on two streams")
+    jobs = [_long(210), _long(220, lens=(36000, 40000), keep=3000)]
+    streams, spaces = [torch.cuda.Stream() for _ in jobs], []
+    for c, *_, (t, n, nt, keep) in jobs:
+        ws = nv.kv8_evict_workspace(_gpu(c), t, n)
+        spaces.append(ws.random_(0, 256))
+    for again in range(2):
+        devs = [_gpu(c) for c, *_ in jobs]
+        torch.cuda.synchronize()
+        got = []
+        for (c, *_, (t, n, nt, keep)), dev, s, ws in zip(jobs, devs, streams, spaces):
+            with torch.cuda.stream(s):
+                torch.cuda._sleep(2_000_000)
+            got.append(nv.kv8_evict(dev, t, n, nt, keep, recent=130, sink=5, workspace=ws, stream=s))
+        torch.cuda.synchronize()
+        for (c, pool, news, kept, _), dev, g in zip(jobs, devs, got):
+            assert torch.equal(g[0].cpu(), news) and torch.equal(g[1].cpu(), kept)
+            _same(pool, dev)
+    c, pool, news, kept, (t, n, nt, keep) = _long(230, lens=(33000,), keep=200)
+    dev = _gpu(c)
+    got = nv.kv8_evict(dev, t, n, nt, keep, recent=130, sink=5, workspace=spaces[0])
+    assert torch.equal(got[0].cpu(), news) and torch.equal(got[1].cpu(), kept)
+    _same(pool, dev)
+
+
+def test_eviction_in_a_graph_after_the_arena_has_grown():
+    """A captured eviction of a long cache keeps its results when a later call takes a larger arena."""
+    _say("eviction in a graph")
+    c, pool, news, kept, (t, n, nt, keep) = _long(240)
+    dev = _gpu(c)
+    ws = nv.kv8_evict_workspace(dev, t, n)
+    nv.kv8_evict(dev, t, n, nt, keep, recent=130, sink=5, workspace=ws)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        got = nv.kv8_evict(dev, t, n, nt, keep, recent=130, sink=5, workspace=ws)
+    big = _long(250, lens=(200000, 200000, 200000, 200000))
+    for again in range(3):
+        for x in ("k_codes", "v_codes", "k_scales", "v_scales", "weights"):
+            getattr(dev, x).copy_(getattr(c, x))
+        got[0].zero_()
+        got[1].zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(got[0].cpu(), news) and torch.equal(got[1].cpu(), kept)
+        _same(pool, dev)
+        other = _gpu(big[0])                                # eager work between the replays
+        r = nv.kv8_evict(other, *big[4], recent=130, sink=5)
+        torch.cuda.synchronize()
+        assert torch.equal(r[1].cpu(), big[3])
