@@ -719,6 +719,14 @@ def _ckv8_rows(x: torch.Tensor, name: str, dim: int, heads: int | None = None) -
     return _pack_rows(x.data_ptr(), rs, hs)
 
 
+def _i32(x, name: str) -> int:
+    """A whole number that the C ABI's int32 holds (ctypes would take it modulo 2^32)."""
+    x = int(x)
+    if not -2 ** 31 <= x < 2 ** 31:
+        raise ValueError(f"{name}: {x} does not fit 32 bits")
+    return x
+
+
 def _ckv8_batch(table, lens, starts, rows, max_rows, max_len, page):
     """(packed kv8_batch, seqs)"""
     if table.dtype is not _I32 or table.dim() != 2 or not table.is_contiguous():
@@ -731,11 +739,11 @@ def _ckv8_batch(table, lens, starts, rows, max_rows, max_len, page):
         if starts.dtype is not _I32 or starts.shape != (seqs + 1,) or not starts.is_contiguous():
             raise ValueError(f"starts: expected a contiguous int32 [{seqs + 1}] tensor")
         at = starts.data_ptr()
-        max_rows = rows if max_rows is None else int(max_rows)
+        max_rows = rows if max_rows is None else min(int(max_rows), rows)
     else:
         max_rows = rows // seqs if seqs else 0
     return _pack_batch(table.data_ptr(), lens.data_ptr(), at, seqs, cols, rows, max_rows,
-                       cols * page if max_len is None else int(max_len)), seqs
+                       cols * page if max_len is None else min(int(max_len), cols * page)), seqs
 
 
 def _kv8_on(dev: int, *tensors):
@@ -794,8 +802,8 @@ def kv8_workspace(q_heads: int, cache: KV8Cache, table: torch.Tensor, lens: torc
     one stream (without one, calls share the library's scratch arena)."""
     L = load_library()
     cc, _, page, _, _ = _ckv8(cache)
-    n = L.kv8_attention_workspace(int(q_heads), cc,
-                                  _ckv8_batch(table, lens, starts, int(rows), max_rows, max_len, page)[0])
+    n = L.kv8_attention_workspace(_i32(q_heads, "q_heads"), cc, _ckv8_batch(
+        table, lens, starts, _i32(rows, "rows"), max_rows, max_len, page)[0])
     if n < 0:
         _check(int(n))
     return torch.zeros((max(n, 256),), dtype=torch.uint8, device=cache.k_codes.device)
@@ -873,7 +881,7 @@ def kv8_evict(cache: KV8Cache, table: torch.Tensor, lens: torch.Tensor, new_tabl
     if new_table.dtype != torch.int32 or new_table.dim() != 2 or new_table.shape[0] != seqs \
             or not new_table.is_contiguous():
         raise ValueError(f"new_table: expected a contiguous int32 [{seqs}, new_cols] tensor")
-    keep = int(keep)
+    keep, recent, sink = _i32(keep, "keep"), _i32(recent, "recent"), _i32(sink, "sink")
     if keep <= 0:
         raise ValueError(f"keep: {keep}, expected at least 1")
     if workspace is not None and (workspace.dtype != torch.uint8 or not workspace.is_contiguous()):
@@ -881,7 +889,7 @@ def kv8_evict(cache: KV8Cache, table: torch.Tensor, lens: torch.Tensor, new_tabl
     _kv8_on(dev, table, lens, new_table, workspace)
     new_lens = _kv8_empty((seqs,), torch.int32, table.device, stream)
     kept = _kv8_empty((seqs, keep), torch.int32, table.device, stream)
-    args = (cc, cb, new_table.data_ptr(), new_table.shape[1], keep, int(recent), int(sink), new_lens.data_ptr(),
+    args = (cc, cb, new_table.data_ptr(), new_table.shape[1], keep, recent, sink, new_lens.data_ptr(),
             kept.data_ptr())
     if workspace is None:
         _check(L.kv8_evict(*args, _kv8_stream(stream, dev)))

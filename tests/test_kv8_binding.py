@@ -44,3 +44,20 @@ def test_eviction_workspace_sizes_and_refusals():
     assert _noalloc(batch=_batch(seqs=0, table=None, lens=None, rows=0)) == nv.NVFP4_OK
     with pytest.raises(ValueError, match="workspace"):
         nv.kv8_evict(**_py(), new_table=torch.zeros(2, 2, dtype=torch.int32), keep=8, workspace=torch.zeros(4))
+
+
+@pytest.mark.parametrize("kw,text", [(dict(keep=2 ** 32 + 5), "keep"), (dict(recent=2 ** 32), "recent"),
+                                     (dict(sink=2 ** 32 + 1), "sink"), (dict(recent=-2 ** 32), "recent")])
+def test_numbers_past_32_bits_are_refused(kw, text):
+    """(ctypes would take them modulo 2^32)"""
+    with pytest.raises(ValueError, match=text):
+        nv.kv8_evict(**_py(), new_table=torch.zeros(2, 4, dtype=torch.int32), **{"keep": 8, **kw})
+
+
+def test_lengths_past_the_table_are_held_to_it():
+    a = _py()
+    sizes = [nv.kv8_workspace(4, a["cache"], a["table"], a["lens"], 2, max_len=n).numel() for n in (None, 64, 2 ** 40)]
+    assert sizes[0] == sizes[1] == sizes[2]
+    starts = torch.tensor([0, 1, 2], dtype=torch.int32)
+    sizes = [nv.kv8_workspace(4, a["cache"], a["table"], a["lens"], 2, starts, max_rows=n).numel() for n in (None, 2 ** 40)]
+    assert sizes[0] == sizes[1]
