@@ -395,8 +395,9 @@ int64_t kv8_attention_workspace(int32_t q_heads, const kv8_cache *cache, const k
  * share pages (a common prefix): a page's weights get the sums of every
  * sequence that names it, and once for each time it does.
  * fp32 throughout (sums over V of values up to 2^90 do not overflow), except
- * that e^(s_j - m) is rounded to bf16 before its product with V (as the other
- * operand of that product is at most bf16).
+ * for e^(s_j - m) in its product with V: it is off by at most 2^-16 of itself
+ * where max_rows * q_heads / heads is at most 32 (dim 64), 128 (128) or 64
+ * (256), and rounded to bf16, the type of that product's operands, beyond.
  * workspace: device memory of kv8_attention_workspace bytes, 256-byte
  * aligned, all zero before its first use and left as it needs to be for the
  * next; one per stream that calls may overlap on.  Null: the library's

@@ -101,6 +101,7 @@ __device__ __forceinline__ uint32_t nan_bytes(uint32_t w) {
 template <int D, int CT>
 __global__ __launch_bounds__(64 * kDecodeWaves, decode_waves(D, CT)) void k_kv8_decode(DecodeParams p) {
   constexpr int kCols = 16 * CT, kPad = D + 4;
+  constexpr bool kRest = CT < 4;  // P's second part
   __shared__ __align__(16) float osum[kDecodeWaves][16][kPad];
   __shared__ float stat[2][kDecodeWaves][kCols];
   __shared__ bool last_flag;
@@ -204,7 +205,7 @@ __global__ __launch_bounds__(64 * kDecodeWaves, decode_waves(D, CT)) void k_kv8_
   const uint32_t score_at = n < cols ? (uint32_t)(n * p.len_pad + 4 * g) * 4u : kOOB;
 
   f32x4 sc[CT][2];
-  bf16x8 pr[CT];
+  bf16x8 pr[CT], rest[CT];
   float sum[CT];
   auto of_unit = [&](float x, int s, int u) {
     return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, x), 2 * s + u));
@@ -234,7 +235,9 @@ __global__ __launch_bounds__(64 * kDecodeWaves, decode_waves(D, CT)) void k_kv8_
     }
     return bits & ((has_page(s, 0) ? 0xFu : 0u) | (has_page(s, 1) ? 0xF0u : 0u));
   };
-  // P and its sum (fp32; P itself is rounded to bf16, the type of the product's other operand)
+  // P and its sum (fp32); the product with V takes P as the sum of two bf16, off
+  // by 2^-16 of itself, but where there are four column tiles: with one, off by
+  // 2^-8, their 16 sequences of 8000 tokens take 44 us, with two 52 us
   auto powers = [&](int s) {
     const float f0 = of_unit(ksc, s, 0), f1 = of_unit(ksc, s, 1);
 #pragma unroll
@@ -244,7 +247,10 @@ __global__ __launch_bounds__(64 * kDecodeWaves, decode_waves(D, CT)) void k_kv8_
       for (int i = 0; i < 8; ++i) e[i] = __builtin_amdgcn_exp2f(fmaf(sc[ct][i >> 2][i & 3], i < 4 ? f0 : f1, -m[ct]));
       sum[ct] = ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
 #pragma unroll
-      for (int i = 0; i < 8; ++i) pr[ct][i] = (__bf16)e[i];
+      for (int i = 0; i < 8; ++i) {
+        pr[ct][i] = (__bf16)e[i];
+        if constexpr (kRest) rest[ct][i] = (__bf16)(e[i] - (float)pr[ct][i]);
+      }
     }
   };
   // V of channels 64 a + 16 c + n of the lane's eight tokens, as an operand
@@ -321,6 +327,11 @@ __global__ __launch_bounds__(64 * kDecodeWaves, decode_waves(D, CT)) void k_kv8_
 #pragma unroll
             for (int ct = 0; ct < CT; ++ct)
               o[ct][4 * a + c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vt, pr[ct], o[ct][4 * a + c], 0, 0, 0);
+            if constexpr (kRest) {
+#pragma unroll
+              for (int ct = 0; ct < CT; ++ct)
+                o[ct][4 * a + c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vt, rest[ct], o[ct][4 * a + c], 0, 0, 0);
+            }
           }
         take();
       } while (++s < count);
@@ -375,8 +386,11 @@ __global__ __launch_bounds__(64 * kDecodeWaves, decode_waves(D, CT)) void k_kv8_
           }
           const bf16x8 vt = widen(w0, w1, v0, v1);
 #pragma unroll
-          for (int ct = 0; ct < CT; ++ct)
+          for (int ct = 0; ct < CT; ++ct) {
             o[ct][4 * a + c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vt, pr[ct], o[ct][4 * a + c], 0, 0, 0);
+            if constexpr (kRest)
+              o[ct][4 * a + c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vt, rest[ct], o[ct][4 * a + c], 0, 0, 0);
+          }
           __builtin_amdgcn_sched_barrier(0);  // one at a time: rare work need not set the registers' number
         }
       take();
@@ -777,7 +791,9 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void k_kv8_prefill(PrefillParams p
       }
       __builtin_amdgcn_sched_group_barrier(0x8, 6 * CT, 0);
     };
-    // P and its sum (fp32; P itself is rounded to bf16, the type of the product's other operand)
+    // P and its sum (fp32).  P itself is rounded to bf16, off by 2^-8: a second
+    // bf16 for the rest, as the kernel for few rows takes it, makes the prompt
+    // 716 us instead of 524 and the wide chunk 206 instead of 170.
     auto powers = [&]() {
 #pragma unroll
       for (int ct = 0; ct < CT; ++ct) {

@@ -330,3 +330,23 @@ def test_eviction_in_a_graph_after_the_arena_has_grown():
         r = nv.kv8_evict(other, *big[4], recent=130, sink=5)
         torch.cuda.synchronize()
         assert torch.equal(r[1].cpu(), big[3])
+
+
+# ---- precision ---------------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("dim,heads,q_heads,lens,rows", [(128, 2, 8, [3000, 517], [1, 1]), (128, 1, 4, [900, 77], [16, 5]),
+                                                         (128, 1, 2, [700], [64]), (64, 2, 8, [2100, 64], [1, 1]),
+                                                         (64, 1, 4, [600, 300], [8, 7]), (256, 1, 8, [1500], [1]),
+                                                         (256, 1, 4, [800, 90], [16, 3])])
+def test_few_rows_lose_nothing_but_the_rounding_of_their_results(dim, heads, q_heads, lens, rows):
+    """The probabilities' share of the bound is two bf16 (2^-16), not one (2^-8)."""
+    _say("precision", dim, heads, q_heads, lens, rows)
+    c, table, q = _problem(dim, 64, heads, q_heads, lens, rows, 0, seed=260, weights=False)
+    q = q[:, :q_heads]
+    pool, size = ref.Pool(c), ref.Pool(c)
+    size.codes[1] = size.codes[1] & 0x7F                   # |v|
+    want, _, bound, _, _ = pool.attention(q, table, lens, rows, 0.002)
+    mass = size.attention(q, table, lens, rows, 0.002)[0]
+    got = nv.kv8_attention(q.cuda(), _gpu(c), table.cuda(), _i32(lens).cuda(), _starts(rows).cuda(), scale=0.002,
+                           max_rows=max(rows))
+    _say("  %.2f of the bound" % _within(got, want, bound - mass * (2.0 ** -8 - 2.0 ** -16), "out"))
