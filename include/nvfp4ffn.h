@@ -386,7 +386,8 @@ int64_t kv8_attention_workspace(int32_t q_heads, const kv8_cache *cache, const k
  * tokens j <= p of its sequence, p = n - r + i its own position, with
  * window > 0 only j > p - window; u reads KV head u / (q_heads / heads):
  *   s_j = scale * q . k_j,  lse = log sum e^s_j,  out = sum e^(s_j - lse) v_j.
- * A row that sees nothing gives out = 0 and lse = -inf.  Tokens that a row
+ * A row that sees nothing, or only scores of -inf, gives out = 0 and lse =
+ * -inf, and no token any weight.  Tokens that a row
  * does not see have no influence on it, whatever their codes.
  *   out: bf16 [rows][q_heads][dim]; lse: fp32 [rows][q_heads] or null.
  * accumulate != 0 (needs lse and the cache's weights) also adds to each

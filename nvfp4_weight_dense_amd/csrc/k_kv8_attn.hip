@@ -1148,7 +1148,9 @@ __global__ __launch_bounds__(64 * kWeightWaves, 2) void k_kv8_weights_many(Weigh
       row_next[u] = i < rows ? i : -(1 << 29);
       const int64_t r = sp.r0 + min(i, rows - 1), head = h * p.group + g;
       src[u] = (const __bf16 *)p.a.q.ptr + r * p.a.q.row_stride + head * p.a.q.head_stride + 8 * half;
-      z_next[u] = p.a.lse[r * p.a.q_heads + head] * kLog2e;
+      // (a row whose scores are all -inf gives 0 to each of its tokens)
+      const float lse = p.a.lse[r * p.a.q_heads + head];
+      z_next[u] = lse == -__builtin_inff() ? 0.f : lse * kLog2e;
     }
 #pragma unroll
     for (int e = 0; e < kMine; ++e) {

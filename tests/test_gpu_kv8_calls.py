@@ -350,3 +350,28 @@ def test_few_rows_lose_nothing_but_the_rounding_of_their_results(dim, heads, q_h
     got = nv.kv8_attention(q.cuda(), _gpu(c), table.cuda(), _i32(lens).cuda(), _starts(rows).cuda(), scale=0.002,
                            max_rows=max(rows))
     _say("  %.2f of the bound" % _within(got, want, bound - mass * (2.0 ** -8 - 2.0 ** -16), "out"))
+
+
+# ---- infinite scores ---------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("dim,rows", [(128, [1, 3]), (128, [12, 9]), (64, [100, 60]), (256, [30, 41])])
+def test_rows_whose_scores_are_all_minus_infinity(dim, rows):
+    """Such a row gives no token any weight, and leaves those of the other rows as they are."""
+    _say("scores of -inf", dim, rows)
+    lens = [200, 131]
+    c, table, q = _problem(dim, 64, 1, 4, lens, rows, 0, seed=270)
+    flat = c.k_codes.view(c.k_codes.shape[0], -1)
+    flat[:, ref.k_at(torch.arange(64), 5, dim)] = 0x38     # 1.0 in every token's channel 5
+    q = q[:, :4].clone()
+    clean = q.clone()
+    q[0, 1, 5], q[rows[0], 2, 5] = -math.inf, -math.inf
+    t, n, at = table.cuda(), _i32(lens).cuda(), _starts(rows).cuda()
+    devs = [_gpu(c) for _ in range(2)]
+    (out, lse), (ref_out, ref_lse) = (nv.kv8_attention(x.cuda(), dev, t, n, at, scale=0.002, max_rows=max(rows), lse=True,
+                                                       accumulate=True) for x, dev in zip((q, clean), devs))
+    gone = torch.zeros(sum(rows), 4, dtype=torch.bool)
+    gone[0, 1] = gone[rows[0], 2] = True
+    assert not out.cpu()[gone].any() and bool((lse.cpu()[gone] == -math.inf).all())
+    assert torch.equal(out.cpu()[~gone].view(torch.int16), ref_out.cpu()[~gone].view(torch.int16))
+    given = [(d.weights.cpu().double() - c.weights.double()).sum().item() for d in devs]
+    assert abs(given[1] - sum(rows) * 4) < 1e-3 and abs(given[0] - (sum(rows) * 4 - 2)) < 1e-3
