@@ -59,9 +59,10 @@ __device__ __forceinline__ void kv8_chain(const Kv8Links &links, const Kv8Pool &
 //
 // Measured (32 query heads on 8 KV heads of 128 but where said): 48 sequences
 // of up to 8191 tokens 78 us, 5400 GB/s of codes; 2 of 131000 (40 heads) 93 us,
-// 5780 GB/s, which is what reading alone reaches; 24 of 4099 with four rows, a
+// 5750 GB/s of the 5990 that reading alone reaches; 24 of 4099 with four rows, a
 // window of 2048 and heads of 64 16 us (40 MB: start, look-ups and join are
-// most of it); one of 521 12 us, of which the call's own 12 us hide the kernel's 9.
+// most of it); one of 521 9.3 us in a graph, where the call's own 12 us do not
+// hide it.
 
 constexpr float kRaise = 1024.0f;  // a step's sum of powers that has the running maximum found anew
 constexpr float kLowest = -3.4028234663852886e38f;  // below every finite score
@@ -555,8 +556,8 @@ __global__ __launch_bounds__(64 * kDecodeWaves, decode_waves(D, CT)) void k_kv8_
 // may be parts, whose sums and statistics go to memory (two places a
 // workgroup) for a second kernel to join in the order of the tokens.
 //
-// Measured: a prompt of 8192 tokens, 32 heads on 8 of 128, 518 us, 1060
-// TFLOP/s; 3 pieces of up to 1023 rows, 16 heads on 4 of 256, a window of 3000,
+// Measured: a prompt of 8192 tokens, 32 heads on 8 of 128, 520 to 540 us from
+// card to card, 1020 to 1060 TFLOP/s; 3 pieces of up to 1023 rows, 16 heads on 4 of 256, a window of 3000,
 // 171 us, 710 TFLOP/s (its 32-token tiles and one wave's 128 accumulators leave
 // the softmax less to hide behind).
 struct PrefillParams {
@@ -1049,8 +1050,8 @@ __global__ __launch_bounds__(256) void k_kv8_prefill_join(PrefillParams p) {
 // those that k_kv8_weights_add adds to a page.
 //
 // Measured with the attention: 16 sequences of up to 6007 tokens, one row,
-// 44 us (the weights 8 of them); 2 of up to 4093 with 1531 rows of 40 heads
-// 325 us (the weights 154, 340 TFLOP/s: a power for each score, 256 matrix
+// 42 us (the weights 7 of them); 2 of up to 4093 with 1531 rows of 40 heads
+// 326 us (K Q^T again 157, 500 TFLOP/s: a power for each score, 256 matrix
 // operations, and two turns of workgroups that each first widen their tokens).
 
 struct WeightParams {
@@ -1247,28 +1248,27 @@ __device__ __forceinline__ float token_sum(const WeightParams &p, int b, int r0,
   if constexpr (FEW) {
     const float *x = p.scores + (size_t)b * p.c.heads * p.cols * p.len_pad + j;
     const float *z = p.a.lse + (size_t)r0 * p.a.q_heads;
-    // Columns of all heads in turn, kStep loads at a time (16 sequences of 6007
-    // tokens, 8 heads of 4 columns: a head at a time 11.4 us, 16 columns 8.3 us).
+    // Columns of all heads in turn, kStep scores and log-sums in flight together
+    // (columns beyond a sequence's own rows are not written; ones past the last
+    // head read its own again).
     constexpr int kStep = 16;
     const int cols = rows * p.group, total = p.c.heads * cols;
     int h = 0, c = 0, i = 0, u = 0;  // head, its column (row i, query head u of the group)
     for (int e0 = 0; e0 < total; e0 += kStep) {
-      float y[kStep];
-      // (columns beyond a sequence's own rows are not written)
-      int hh = h, cc = c;
+      float y[kStep], lse[kStep];
 #pragma unroll
       for (int k = 0; k < kStep; ++k) {
-        y[k] = x[(size_t)(min(hh, p.c.heads - 1) * p.cols + cc) * p.len_pad];
-        if (++cc == cols) cc = 0, ++hh;
+        const int hh = min(h, p.c.heads - 1);
+        y[k] = x[(size_t)(hh * p.cols + c) * p.len_pad];
+        lse[k] = z[(size_t)i * p.a.q_heads + hh * p.group + u];
+        if (++u == p.group) u = 0, ++i;
+        if (++c == cols) c = i = u = 0, ++h;
       }
 #pragma unroll
       for (int k = 0; k < kStep; ++k) {
         // (a row that sees nothing has -inf there and -inf scores)
-        const float lse = z[(size_t)i * p.a.q_heads + min(h, p.c.heads - 1) * p.group + u];
-        const float add = y[k] == -__builtin_inff() ? 0.f : __builtin_amdgcn_exp2f(y[k] - lse * kLog2e);
-        sum += h < p.c.heads ? add : 0.f;
-        if (++u == p.group) u = 0, ++i;
-        if (++c == cols) c = i = u = 0, ++h;
+        const float add = y[k] == -__builtin_inff() ? 0.f : __builtin_amdgcn_exp2f(y[k] - lse[k] * kLog2e);
+        sum += e0 + k < total ? add : 0.f;
       }
     }
   } else {
@@ -1287,22 +1287,25 @@ __device__ __forceinline__ float token_sum(const WeightParams &p, int b, int r0,
 // above) has chained each block that some row sees to its page's list, of
 // kChains for each workgroup; the workgroup's threads follow them, the blocks
 // are put in order, and as many as the threads hold are taken at a time.
-// Where there are more than kBlocks (a page that very many share) it looks
-// through the tables instead.
+// Where a list is longer than a look through the tables takes (a page that
+// very many share), or all together longer than kBlocks, it does that instead.
 //
-// Bound by latency: list, lengths, scores, one after the other.  16 sequences
-// of 6007 tokens 58 us with the attention, 78 us where they share 40 of their
-// 94 blocks (one workgroup then takes 16 blocks, four at a time).
+// Bound by latency: list, lengths, scores, one after the other.  With the
+// attention, 16 sequences of 6007 tokens (94 blocks) 54 us, and 64 us where they
+// share 40 blocks; 256 of 1000 (16 blocks) 124 us, and 325 us where they share
+// 10, each of them one workgroup's, four uses at a time.
 constexpr int kBlocks = 1024, kLook = 4;
-static_assert(kBlocks == 256 * kLook, "");
 
 template <bool FEW>
 __global__ __launch_bounds__(256) void k_kv8_weights_add(WeightParams p) {
-  __shared__ int2 found[kBlocks], list[kBlocks];  // (block's number, page)
-  __shared__ int count, part[kLook][4];
-  __shared__ float sums[256];
+  constexpr int T = 256;
+  static_assert(T * kLook >= kBlocks, "");
+  __shared__ int2 found[kBlocks], list[T * kLook];  // (block's number, page)
+  __shared__ int count, part[kLook][T / 64];
+  __shared__ float sums[T];
   const int tid = (int)threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int shift = p.c.shift, page = 1 << shift, deal = 256 >> shift;
+  const int shift = p.c.shift, page = 1 << shift, deal = T >> shift;
+  const unsigned all = (unsigned)p.s.seqs * (unsigned)p.links.blocks;
   const unsigned mine = blockIdx.x;
   // this thread's word of the page that is added to (threads of the first `page`)
   int open = -1;
@@ -1312,15 +1315,25 @@ __global__ __launch_bounds__(256) void k_kv8_weights_add(WeightParams p) {
     if (open >= 0) word[(size_t)open << shift] = acc;
   };
   auto take = [&](int n) {  // the first n of the list
+    // a thread's block: sequence, token, and what is seen of it (looked up a step ahead)
+    unsigned b = 0;
+    int j = 0;
+    Kv8Seen q = {0, 0, 0, 0};
+    auto look_up = [&](int i) {
+      const unsigned e = (unsigned)list[min(i, n - 1)].x;
+      b = e / (unsigned)p.links.blocks;
+      j = (int)((e - b * (unsigned)p.links.blocks) << shift) + (tid & (page - 1));
+      q = kv8_seen(p.a, p.s, shift, (int)b);
+      if (i >= n) q.hi = 0;
+    };
+    if (n > 0) look_up(tid >> shift);
     for (int i0 = 0; i0 < n; i0 += deal) {
-      const int i = i0 + (tid >> shift);
+      const unsigned bb = b;
+      const int jj = j;
+      const Kv8Seen now = q;
+      if (i0 + deal < n) look_up(i0 + deal + (tid >> shift));
       float x = 0.f;
-      if (i < n) {
-        const unsigned e = (unsigned)list[i].x, b = e / (unsigned)p.links.blocks;
-        const Kv8Seen q = kv8_seen(p.a, p.s, shift, (int)b);
-        const int j = (int)((e - b * (unsigned)p.links.blocks) << shift) + (tid & (page - 1));
-        if (j >= q.lo && j < q.hi) x = token_sum<FEW>(p, (int)b, q.r0, q.rows, j);
-      }
+      if (jj >= now.lo && jj < now.hi) x = token_sum<FEW>(p, (int)bb, now.r0, now.rows, jj);
       sums[tid] = x;
       __syncthreads();
       if (tid < page) {
@@ -1344,9 +1357,10 @@ __global__ __launch_bounds__(256) void k_kv8_weights_add(WeightParams p) {
     unsigned *head = p.links.head + ((unsigned)tid << p.links.bits) + mine;
     unsigned e = *head;
     if (e) *head = 0;
-    while (e) {
-      const int at = atomicAdd(&count, 1);
-      if (at >= kBlocks) break;
+    // (a link costs half of what T * kLook numbers do)
+    for (unsigned most = max(all / (T * kLook) * 2u, 16u); e; --most) {
+      const int at = atomicAdd(&count, most ? 1 : kBlocks + 1);
+      if (at >= kBlocks || !most) break;
       const uint2 link = p.links.next[e - 1];
       found[at] = int2{(int)(e - 1), (int)link.y};
       e = link.x;
@@ -1356,7 +1370,7 @@ __global__ __launch_bounds__(256) void k_kv8_weights_add(WeightParams p) {
   const int n = count;
   if (n == 0) return;
   if (n <= kBlocks) {
-    for (int i = tid; i < n; i += 256) {
+    for (int i = tid; i < n; i += T) {
       const int2 x = found[i];
       int rank = 0;
       for (int k = 0; k < n; ++k) rank += (unsigned)found[k].x < (unsigned)x.x ? 1 : 0;
@@ -1365,13 +1379,12 @@ __global__ __launch_bounds__(256) void k_kv8_weights_add(WeightParams p) {
     __syncthreads();
     take(n);
   } else {
-    const unsigned all = (unsigned)p.s.seqs * (unsigned)p.links.blocks;
-    for (unsigned e0 = 0; e0 < all; e0 += kBlocks) {
+    for (unsigned e0 = 0; e0 < all; e0 += T * kLook) {
       uint64_t hit[kLook];
       int id[kLook];
 #pragma unroll
       for (int u = 0; u < kLook; ++u) {
-        const unsigned e = e0 + 256 * u + tid, b = e / (unsigned)p.links.blocks;
+        const unsigned e = e0 + T * u + tid, b = e / (unsigned)p.links.blocks;
         id[u] = -1;
         if (e < all) {
           const Kv8Seen q = kv8_seen(p.a, p.s, shift, (int)b);
@@ -1386,12 +1399,12 @@ __global__ __launch_bounds__(256) void k_kv8_weights_add(WeightParams p) {
 #pragma unroll
       for (int u = 0; u < kLook; ++u) {
         int to = m;
-        for (int w = 0; w < 4; ++w) {
+        for (int w = 0; w < T / 64; ++w) {
           if (w < wave) to += part[u][w];
           m += part[u][w];
         }
         if (hit[u] >> lane & 1u)
-          list[to + __popcll(hit[u] & ((1ull << lane) - 1ull))] = int2{(int)(e0 + 256 * u + tid), id[u]};
+          list[to + __popcll(hit[u] & ((1ull << lane) - 1ull))] = int2{(int)(e0 + T * u + tid), id[u]};
       }
       __syncthreads();
       take(m);
