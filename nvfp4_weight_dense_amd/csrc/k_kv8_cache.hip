@@ -58,7 +58,7 @@ __device__ __forceinline__ void widen8(uint4 v, float *f) {
 // in LDS; its 16-byte pieces that also hold older tokens, or places not yet
 // used, take those bytes from the page.
 //
-// Measured (8 heads of 128): 5 prompts of up to 2741 tokens 15.7 us, 4300 GB/s
+// Measured (8 heads of 128): 5 prompts of up to 2741 tokens 15.9 us, 4250 GB/s
 // of the 4750 that a copy reaches; a token of each of 64 sequences 4.9 us,
 // a start and three dependent look-ups.
 template <int D, int NU, int T>
@@ -247,8 +247,8 @@ __global__ __launch_bounds__(T) void k_kv8_append(AppendParams p) {
 // their atomic additions does not show.
 //
 // Bound by latency: 12 sequences of up to 6143 tokens 11.7 us (one workgroup
-// each: look-ups, three scans, the list), one of 130001 tokens 26 us in five
-// launches of 4 to 6.6 us (70 us with the move; one workgroup for it all: 430).
+// each: look-ups, three scans, the list), one of 130001 tokens 27 us in five
+// launches of 4.4 to 7.1 us (72 us with the move; one workgroup for it all: 430).
 
 struct SelectParams {
   Kv8Pool c;
