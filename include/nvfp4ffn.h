@@ -401,7 +401,7 @@ int64_t kv8_attention_workspace(int32_t q_heads, const kv8_cache *cache, const k
  * (256), and rounded to bf16, the type of that product's operands, beyond.
  * workspace: device memory of kv8_attention_workspace bytes, 256-byte
  * aligned, all zero before its first use and left as it needs to be for the
- * next; one per stream that calls may overlap on.  Null: the library's
+ * next, of whatever sizes; one per stream that calls may overlap on.  Null: the library's
  * scratch arena (see above). */
 int kv8_attention(const kv8_rows *q, int32_t q_heads, float scale, int32_t window,
                   const kv8_cache *cache, const kv8_batch *batch, void *out, float *lse,

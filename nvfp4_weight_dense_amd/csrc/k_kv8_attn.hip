@@ -1284,8 +1284,8 @@ __device__ __forceinline__ float token_sum(const WeightParams &p, int b, int r0,
 // Adds the sums to the pages' weights.  Sequences may share pages (a common
 // prefix) and a table may name one twice, so a page's sums are added by one
 // workgroup, in the order of the tables' blocks: the attention (or the kernel
-// above) has chained each block that some row sees to its page's list, of
-// kChains for each workgroup; the workgroup's threads follow them, the blocks
+// above) has chained each block that some row sees to its page's list, one of
+// kKv8Chains of its workgroup; the workgroup's threads follow them, the blocks
 // are put in order, and as many as the threads hold are taken at a time.
 // Where a list is longer than a look through the tables takes (a page that
 // very many share), or all together longer than kBlocks, it does that instead.

@@ -39,6 +39,24 @@ def test_workspace_of_exactly_the_given_size(cols, lens, rows, window):
         assert bool((room[size:] == 0x5A).all())
 
 
+def test_one_workspace_for_calls_of_other_sizes():
+    """What one call leaves in a workspace is no other's trouble: caches of other pools, with and without weights,
+    few rows and many, in turn on one workspace."""
+    _say("one workspace, many sizes")
+    jobs = []
+    for i, (dim, page, heads, q_heads, lens, rows, weights) in enumerate([
+            (128, 64, 2, 8, [700, 64, 300], [1, 1, 1], True), (64, 16, 1, 2, [900, 50], [200, 50], True),
+            (256, 32, 1, 4, [1200], [3], False), (128, 16, 1, 1, [2000, 1999, 5], [1, 2, 3], True),
+            (64, 128, 4, 4, [1500], [400], False)]):
+        c, table, q = _problem(dim, page, heads, q_heads, lens, rows, 0, seed=280 + 5 * i, weights=weights)
+        jobs.append((c, table, q, q_heads, lens, rows, weights))
+    ws = max((nv.kv8_workspace(h, _gpu(c), t.cuda(), _i32(lens).cuda(), sum(rows), _starts(rows).cuda(),
+                               max_rows=max(rows)) for c, t, _, h, lens, rows, _ in jobs), key=lambda x: x.numel())
+    for _ in range(3):
+        for c, table, q, q_heads, lens, rows, weights in jobs:
+            _check(c, table, q, q_heads, lens, rows, accumulate=weights, workspace=ws)
+
+
 # ---- rows beyond max_rows ----------------------------------------------------------------------------
 
 @pytest.mark.parametrize("dim,page,max_rows", [(128, 64, 1), (128, 64, 8), (64, 16, 1), (64, 16, 8), (256, 32, 1),
