@@ -302,6 +302,90 @@ int dense_ffn_forward_q2(const void *x, int32_t m, int32_t hidden,
                          const q2_weight *wu, const q2_weight *wd, void *out,
                          void *stream);
 
+/* ---- 8-bit integers -----------------------------------------------------------
+ * A fixed format beside W4A4 and W8A8 in whole numbers: one scale for each
+ * row of the activations (a token) and one for each row of the weight (an
+ * output channel).  (Not on the pages; the formulas here define it.)
+ *
+ * A row in int8: s = amax / 127 in fp32 (1 for a row of zeros); code = x / s
+ * in fp32, rounded to the nearest whole number, ties to even, so that
+ * |code| <= 127.  A row that holds an infinity or a NaN has s = NaN and codes
+ * of 0, and everything computed from it is NaN. */
+
+/* One matrix W[n][k] (y = x . W^T) = codes[r][c] * scales[r]:
+ *   codes : device, int8 [n][k]; k a positive multiple of 32, at most 131072
+ *           (the sums of products then stay below 2^31), n at most 2^21;
+ *   scales: device, fp32 [n].
+ * codes 16-byte and scales 4-byte aligned.  Codes may be -128.  (int8_quantize_rows
+ * of a bf16 weight gives such a matrix.) */
+typedef struct int8_weight {
+  const int8_t *codes;
+  const float *scales;
+  int32_t n;
+  int32_t k;
+} int8_weight;
+
+/* Per-row int8 quantizer.  x: bf16 [m][k], k a multiple of 8, at most 131072.
+ * Outputs: codes int8 [m][k], row_scale fp32 [m]. */
+int int8_quantize_rows(const void *x, int32_t m, int32_t k, int8_t *codes, float *row_scale, void *stream);
+
+/* Bytes of workspace that int8_gemm_w8a8 takes for these sizes or fewer rows;
+ * negative status on an error. */
+int64_t int8_gemm_workspace(int32_t m, const int8_weight *w);
+
+/* y[r][c] = bf16( s_row[r] * scales[c] * sum_k x[r][k] * codes[c][k] ), the sum
+ * exact.  Row r's bits are the same for every m.
+ *   x: bf16 [m][k], quantized by rows in the call; or, where row_scale is not
+ *   null, int8 [m][k] with the rows' scales fp32 [m] (rms_norm and
+ *   rms_norm_residual write such rows; codes of -127 .. 127).
+ *   y: bf16 [m][n], none of the inputs.
+ * workspace: device memory of int8_gemm_workspace bytes, 256-byte aligned, all
+ * zero before its first use and left as it needs to be for the next call, of
+ * whatever sizes; one per stream that calls may overlap on.  Null: the
+ * library's scratch arena (see above); a call on a stream that is being
+ * captured has to bring a workspace (NVFP4_EINVAL without). */
+int int8_gemm_w8a8(const void *x, const float *row_scale, int32_t m, const int8_weight *w, void *y,
+                   void *workspace, int64_t workspace_bytes, void *stream);
+
+/* Bytes of workspace that dense_ffn_forward_int8 takes for these sizes or
+ * fewer rows. */
+int64_t dense_ffn_int8_workspace(int32_t m, int32_t hidden, int32_t inter);
+
+/* Dense SwiGLU FFN in 8-bit integers: x and act are quantized by rows before
+ * each projection; gate, up and act are rounded to bf16.  Row r's output bits
+ * do not depend on m, and are those of int8_gemm_w8a8 and silu_mul one by one.
+ * x and row_scale, workspace: as in int8_gemm_w8a8.  wg, wu: [inter][hidden];
+ * wd: [hidden][inter]; out: bf16 [m][hidden], none of the inputs. */
+int dense_ffn_forward_int8(const void *x, const float *row_scale, int32_t m, int32_t hidden, int32_t inter,
+                           const int8_weight *wg, const int8_weight *wu, const int8_weight *wd, void *out,
+                           void *workspace, int64_t workspace_bytes, void *stream);
+
+/* ---- norms before and after a block --------------------------------------------
+ * norm(x) = x / sqrt(mean(x^2) + eps) * (offset + weight), over rows of k
+ * values, k a positive multiple of 8 up to 131072; without a weight (null) the
+ * last factor is 1.  offset is 0, or 1 for weights kept as their distance from
+ * one.  1e-18 <= eps <= 1.  Statistics are fp32 and hold for every finite row. */
+
+/* The norm before a block.  x: bf16 [m][k]; weight: bf16 [k] or null.  The
+ * result is rounded to bf16 and written to out (bf16 [m][k]; may be x), or,
+ * where out is null, quantized by rows (see above) to codes (int8 [m][k]) and
+ * row_scale (fp32 [m]) -- the bits of int8_quantize_rows on out. */
+int rms_norm(const void *x, int32_t m, int32_t k, const void *weight, float offset, float eps, void *out,
+             int8_t *codes, float *row_scale, void *stream);
+
+/* The end of a block, y its output, and the start of the next:
+ *   h = bf16( residual + scale * gate * t ),  t = post ? norm(y) : y;
+ *   where next, norm(h) to out or to codes and row_scale, as in rms_norm.
+ * residual, y, h: bf16 [m][k]; h may be residual or y.  post_weight,
+ * next_weight: bf16 [k] or null (no weight).  gate: bf16 [gates][k], gates a
+ * divisor of m: row r takes gate row r / (m / gates) (1: one value for each
+ * channel; m: one for each value; between: one for each sequence of equal
+ * length); null with gates 0: no gate.  fp32 up to the two roundings. */
+int rms_norm_residual(const void *residual, const void *y, int32_t m, int32_t k, int32_t post,
+                      const void *post_weight, const void *gate, int32_t gates, float scale, int32_t next,
+                      const void *next_weight, float offset, float eps, void *h, void *out, int8_t *codes,
+                      float *row_scale, void *stream);
+
 /* ---- 8-bit paged KV cache ----------------------------------------------------
  * The attention half of a decoder layer at serving time, next to the FFN:
  * a cache of K and V in E4M3 with one scale for each page of tokens and KV

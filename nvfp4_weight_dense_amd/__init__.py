@@ -1,5 +1,6 @@
 """Python binding of ``libnvfp4ffn.so``, the MI355X (gfx950) dense SwiGLU FFN
-with NVFP4 weights, and the 8-bit paged KV cache and its attention next to it.
+with NVFP4 weights, the same FFN in 8-bit integers, the norms before and after
+it, and the 8-bit paged KV cache and its attention next to it.
 
 Argument marshalling only: every step of the FFN runs in the library's HIP
 kernels; PyTorch supplies device memory and the current stream.  The names
@@ -12,7 +13,9 @@ the GPU; a weight is any object with ``codes`` (uint8 ``[n, k/2]``),
 ``scales`` (uint8 ``[n, k/16]``, E4M3 bits) and ``tensor_scale`` (or
 ``ts``) -- see :class:`NVFP4Weight`; a W8A8 weight has ``codes`` (uint8
 ``[n, k]``, E4M3 bits) and ``scales`` (float32 ``[ceil(n/128),
-ceil(k/128)]``) -- see :class:`FP8Weight`.  The ``kv8_*`` calls take a
+ceil(k/128)]``) -- see :class:`FP8Weight`; an int8 weight has ``codes`` (int8
+``[n, k]``) and ``scales`` (float32 ``[n]``) -- see :class:`Int8Weight` -- and
+meets bf16 rows or :class:`Int8Rows`.  The ``kv8_*`` calls take a
 :class:`KV8Cache`, a page table and lengths (int32, on the GPU) and bf16
 ``[rows, heads, dim]`` arrays that may be parts of a larger one; what they
 return, unless the caller gave it, belongs to the stream they run on.
@@ -24,6 +27,7 @@ import ctypes
 import os
 import struct
 from dataclasses import dataclass
+from typing import NamedTuple
 
 import torch
 
@@ -43,6 +47,8 @@ __all__ = [
     "nvfp4_gate_up_views", "dense_ffn_forward_fused", "LoraPair", "nvfp4_lora_delta",
     "dense_ffn_forward_lora", "FP8Weight", "fp8_quantize_rows", "fp8_gemm_w8a8",
     "dense_ffn_forward_w8a8", "Q2Weight", "q2_gemm_w2a16", "dense_ffn_forward_q2",
+    "Int8Weight", "Int8Rows", "int8_quantize_rows", "int8_gemm_w8a8", "dense_ffn_forward_int8",
+    "int8_workspace", "rms_norm", "rms_norm_residual",
     "KV8Cache", "kv8_cache", "kv8_append", "kv8_attention", "kv8_workspace", "kv8_evict",
     "kv8_evict_workspace",
     "nvfp4_last_error", "nvfp4_release", "nvfp4_abi_version", "load_library",
@@ -136,6 +142,29 @@ class _CQ2Weight(ctypes.Structure):
 
 
 @dataclass
+class Int8Weight:
+    """One int8 matrix W[n][k] on the GPU with a scale for each output channel
+    (int8_quantize_rows of a bf16 weight gives its fields)."""
+    codes: torch.Tensor   # int8 [n, k]
+    scales: torch.Tensor  # float32 [n]
+
+
+class Int8Rows(NamedTuple):
+    """Activation rows in int8 on the GPU with a scale for each row."""
+    codes: torch.Tensor      # int8 [m, k]
+    row_scale: torch.Tensor  # float32 [m]
+
+
+class _CInt8Weight(ctypes.Structure):
+    _fields_ = [
+        ("codes", ctypes.c_void_p),
+        ("scales", ctypes.c_void_p),
+        ("n", ctypes.c_int32),
+        ("k", ctypes.c_int32),
+    ]
+
+
+@dataclass
 class KV8Cache:
     """A pool of pages of an 8-bit KV cache on the GPU.  A page's codes of one
     head are in the kernels' operand order (include/nvfp4ffn.h), not in
@@ -196,6 +225,8 @@ def load_library(path: str = LIB_PATH):
     L = ctypes.CDLL(path)
     vp, i32, i64 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64
     wp = ctypes.POINTER(_CWeight)
+    f32 = ctypes.c_float
+    w8 = vp  # a packed descriptor, or a reference to its ctypes structure
     kc = kb = kr = vp  # a packed descriptor, or a reference to its ctypes structure
     sig = {
         "nvfp4_gemm_w4a16": [vp, i32, wp, vp, vp],
@@ -217,6 +248,11 @@ def load_library(path: str = LIB_PATH):
         "fp8_gemm_w8a8": [vp, i32, ctypes.POINTER(_CFp8Weight), vp, vp],
         "dense_ffn_forward_w8a8": [vp, i32, i32, i32, ctypes.POINTER(_CFp8Weight),
                                    ctypes.POINTER(_CFp8Weight), ctypes.POINTER(_CFp8Weight), vp, vp],
+        "int8_quantize_rows": [vp, i32, i32, vp, vp, vp],
+        "int8_gemm_w8a8": [vp, vp, i32, w8, vp, vp, i64, vp],
+        "dense_ffn_forward_int8": [vp, vp, i32, i32, i32, w8, w8, w8, vp, vp, i64, vp],
+        "rms_norm": [vp, i32, i32, vp, f32, f32, vp, vp, vp, vp],
+        "rms_norm_residual": [vp, vp, i32, i32, i32, vp, vp, i32, f32, i32, vp, f32, f32, vp, vp, vp, vp, vp],
         "kv8_append": [kr, kr, kc, kb, vp],
         "kv8_attention": [kr, i32, ctypes.c_float, i32, kc, kb, vp, vp, i32, vp, i64, vp],
         "kv8_evict": [kc, kb, vp, i32, i32, i32, i32, vp, vp, vp],
@@ -232,6 +268,10 @@ def load_library(path: str = LIB_PATH):
     L.nvfp4_probe_read.restype = ctypes.c_int
     L.nvfp4_probe_encode.argtypes = [vp, i64, ctypes.c_float, vp, vp, vp, vp]
     L.nvfp4_probe_encode.restype = ctypes.c_int
+    L.int8_gemm_workspace.argtypes = [i32, w8]
+    L.int8_gemm_workspace.restype = i64
+    L.dense_ffn_int8_workspace.argtypes = [i32, i32, i32]
+    L.dense_ffn_int8_workspace.restype = i64
     L.kv8_attention_workspace.argtypes = [i32, kc, kb]
     L.kv8_attention_workspace.restype = i64
     L.kv8_evict_workspace.argtypes = [kc, kb]
@@ -247,6 +287,9 @@ def load_library(path: str = LIB_PATH):
 
 
 # ---- marshalling helpers -------------------------------------------------------
+
+_U8, _I8, _I32, _F32, _BF16 = torch.uint8, torch.int8, torch.int32, torch.float32, torch.bfloat16
+
 
 def _ptr(t: torch.Tensor | None):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
@@ -647,6 +690,216 @@ def dense_ffn_forward_q2(x: torch.Tensor, wg, wu, wd, out: torch.Tensor | None =
     return out
 
 
+# ---- 8-bit integers ------------------------------------------------------------------
+
+_pack_int8 = struct.Struct("@2P2i").pack
+
+
+def _cint8(w):
+    """(packed int8_weight, n, k)"""
+    c, s = w.codes, w.scales
+    if c.dtype is not _I8 or c.dim() != 2 or not c.is_contiguous():
+        raise ValueError("int8 weight codes: expected a contiguous 2-D int8 tensor")
+    n, k = c.shape
+    if s.dtype is not _F32 or s.shape != (n,) or not s.is_contiguous():
+        raise ValueError(f"int8 weight scales: expected a contiguous float32 [{n}] tensor")
+    return _pack_int8(c.data_ptr(), s.data_ptr(), n, k), n, k
+
+
+def _int8_x(x, k: int):
+    """(tensor, its scales' tensor or None) of bf16 rows or Int8Rows with k columns"""
+    if not isinstance(x, Int8Rows):
+        return _act(x, "x", k), None
+    c, s = x
+    if c.dtype is not _I8 or c.dim() != 2 or not c.is_contiguous():
+        raise ValueError("x codes: expected a contiguous 2-D int8 tensor")
+    if c.shape[1] != k:
+        raise ValueError(f"x: has {c.shape[1]} columns, the weight has k={k}")
+    if s.dtype is not _F32 or s.shape != c.shape[:1] or not s.is_contiguous():
+        raise ValueError(f"x row_scale: expected a contiguous float32 [{c.shape[0]}] tensor")
+    return c, s
+
+
+def _on_current(first: torch.Tensor, *rest):
+    """_gpu, and that GPU is the current one (the library's launches and scratch are the current device's)."""
+    _gpu(first, *rest)
+    if first.get_device() != torch._C._cuda_getDevice():
+        raise ValueError(f"tensors on {first.device}, the current device is cuda:{torch._C._cuda_getDevice()}")
+
+
+def _rows_workspace(t):
+    if t is not None and (t.dtype != torch.uint8 or not t.is_contiguous()):
+        raise ValueError("workspace: expected a contiguous uint8 tensor (int8_workspace)")
+    return (None, 0) if t is None else (t.data_ptr(), t.numel())
+
+
+def _bf16_out(t, shape, name):
+    """A caller's bf16 output (checked); None for one to be made."""
+    if t is not None and (not isinstance(t, torch.Tensor) or t.dtype is not _BF16 or t.shape != shape
+                          or not t.is_contiguous()):
+        raise ValueError(f"{name}: expected a contiguous bfloat16 {list(shape)} tensor")
+    return t
+
+
+def int8_quantize_rows(x: torch.Tensor, stream=None) -> Int8Rows:
+    """Per-row int8 quantizer: Int8Rows(codes int8 [m, k], row_scale float32
+    [m]) of bf16 rows (activations, or a weight by its output channels)."""
+    L = load_library()
+    x = _act(x, "x")
+    _on_current(x)
+    m, k = x.shape
+    dev = x.get_device()
+    codes = _kv8_empty((m, k), _I8, x.device, stream)
+    rs = _kv8_empty((m,), _F32, x.device, stream)
+    _check(L.int8_quantize_rows(x.data_ptr(), m, k, codes.data_ptr(), rs.data_ptr(), _kv8_stream(stream, dev)))
+    return Int8Rows(codes, rs)
+
+
+def int8_workspace(m: int, *weights) -> torch.Tensor:
+    """A workspace for calls of int8_gemm_w8a8 (one weight) or
+    dense_ffn_forward_int8 (wg, wu, wd) with these weights and m rows or fewer,
+    for one stream.  Without one, calls share the library's scratch arena; a
+    captured call has to bring one."""
+    L = load_library()
+    c = [_cint8(w) for w in weights]
+    m = _i32(m, "m")
+    if len(c) == 1:
+        n = L.int8_gemm_workspace(m, c[0][0])
+    elif len(c) == 3:
+        n = L.dense_ffn_int8_workspace(m, c[0][2], c[0][1])
+    else:
+        raise ValueError(f"{len(c)} weights: expected one, or wg, wu and wd")
+    if n < 0:
+        _check(int(n))
+    return torch.zeros((max(n, 256),), dtype=torch.uint8, device=weights[0].codes.device)
+
+
+def int8_gemm_w8a8(x, w, y: torch.Tensor | None = None, *, workspace: torch.Tensor | None = None, stream=None):
+    """Projection in 8-bit integers: y = bf16(s_row * s_col * (x8 . W8^T)).
+    x: bf16 [m, k], quantized by rows in the call, or Int8Rows."""
+    L = load_library()
+    cw, n, k = _cint8(w)
+    xt, xs = _int8_x(x, k)
+    m = xt.shape[0]
+    y = _bf16_out(y, (m, n), "y")
+    ws, nbytes = _rows_workspace(workspace)
+    _on_current(xt, xs, y, workspace, w.codes, w.scales)
+    if y is None:
+        y = _kv8_empty((m, n), _BF16, xt.device, stream)
+    _check(L.int8_gemm_w8a8(xt.data_ptr(), None if xs is None else xs.data_ptr(), m, cw, y.data_ptr(), ws, nbytes,
+                            _kv8_stream(stream, xt.get_device())))
+    return y
+
+
+def dense_ffn_forward_int8(x, wg, wu, wd, out: torch.Tensor | None = None, *,
+                           workspace: torch.Tensor | None = None, stream=None):
+    """Dense SwiGLU FFN in 8-bit integers (x and act quantized by rows before
+    each projection).  x: bf16 [m, hidden] or Int8Rows."""
+    L = load_library()
+    (cg, inter, hidden), (cu, nu, ku), (cd, nd, kd) = _cint8(wg), _cint8(wu), _cint8(wd)
+    if (nu, ku) != (inter, hidden) or (nd, kd) != (hidden, inter):
+        raise ValueError(f"wg {[inter, hidden]}, wu {[nu, ku]}, wd {[nd, kd]}: expected wg/wu "
+                         f"[inter, hidden] and wd [hidden, inter]")
+    xt, xs = _int8_x(x, hidden)
+    m = xt.shape[0]
+    out = _bf16_out(out, (m, hidden), "out")
+    ws, nbytes = _rows_workspace(workspace)
+    _on_current(xt, xs, out, workspace, wg.codes, wg.scales, wu.codes, wu.scales, wd.codes, wd.scales)
+    if out is None:
+        out = _kv8_empty((m, hidden), _BF16, xt.device, stream)
+    _check(L.dense_ffn_forward_int8(xt.data_ptr(), None if xs is None else xs.data_ptr(), m, hidden, inter, cg, cu, cd,
+                                    out.data_ptr(), ws, nbytes, _kv8_stream(stream, xt.get_device())))
+    return out
+
+
+# ---- norms before and after a block -----------------------------------------------------
+
+def _norm_weight(w, k: int, name: str):
+    """(whether there is a norm, its weight's tensor or None); w: None (no norm), True (no weight) or bf16 [k]"""
+    if w is None or w is False:
+        return 0, None
+    if w is True:
+        return 1, None
+    if not isinstance(w, torch.Tensor) or w.dtype is not _BF16 or w.shape != (k,) or not w.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous bfloat16 [{k}] tensor")
+    return 1, w
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
+
+
+def rms_norm(x: torch.Tensor, weight: torch.Tensor | None = None, *, eps: float = 1e-6, weight_offset: float = 0.0,
+             int8: bool = False, out: torch.Tensor | None = None, stream=None):
+    """x / sqrt(mean(x^2) + eps) * (weight_offset + weight) over the rows of x
+    (bf16 [m, k]): bf16 [m, k] (out, which may be x), or with int8 the Int8Rows
+    that int8_quantize_rows makes of it."""
+    L = load_library()
+    x = _act(x, "x")
+    m, k = x.shape
+    _, w = _norm_weight(weight, k, "weight")
+    out = _bf16_out(out, (m, k), "out")
+    if int8 and out is not None:
+        raise ValueError("out: int8 rows are returned anew")
+    _on_current(x, w, out)
+    dev = x.get_device()
+    q = None
+    if int8:
+        q = Int8Rows(_kv8_empty((m, k), _I8, x.device, stream), _kv8_empty((m,), _F32, x.device, stream))
+    elif out is None:
+        out = _kv8_empty((m, k), _BF16, x.device, stream)
+    _check(L.rms_norm(x.data_ptr(), m, k, _at(w), float(weight_offset), float(eps), _at(out),
+                      q and q.codes.data_ptr(), q and q.row_scale.data_ptr(), _kv8_stream(stream, dev)))
+    return q if int8 else out
+
+
+def rms_norm_residual(residual: torch.Tensor, y: torch.Tensor, *, post=None, gate: torch.Tensor | None = None,
+                      scale: float = 1.0, norm=None, eps: float = 1e-6, weight_offset: float = 0.0,
+                      int8: bool = False, h: torch.Tensor | None = None, out: torch.Tensor | None = None, stream=None):
+    """The end of a block, y its output (bf16 [m, k]), and the start of the next:
+
+        h = bf16(residual + scale * gate * post_norm(y)),  n = norm(h)
+
+    post and norm: None (no such norm), True (one without a weight) or the
+    norm's weight (bf16 [k]; with weight_offset as in rms_norm).  gate: bf16
+    [k], or [gates, k] with gates a divisor of m, each row for m / gates rows.
+    h may be residual or y.  Returns (h, n); n is bf16, Int8Rows with int8, or
+    None without a norm."""
+    L = load_library()
+    residual, y = _act(residual, "residual"), _act(y, "y")
+    m, k = residual.shape
+    if y.shape != residual.shape:
+        raise ValueError(f"y: has shape {tuple(y.shape)}, residual {tuple(residual.shape)}")
+    post, pw = _norm_weight(post, k, "post")
+    nxt, nw = _norm_weight(norm, k, "norm")
+    gates = 0
+    if gate is not None:
+        if not isinstance(gate, torch.Tensor) or gate.dtype is not _BF16 or not gate.is_contiguous() \
+                or gate.dim() not in (1, 2) or gate.shape[-1] != k:
+            raise ValueError(f"gate: expected a contiguous bfloat16 [{k}] or [gates, {k}] tensor")
+        gates = 1 if gate.dim() == 1 else gate.shape[0]
+        if gates == 0 or m % gates:
+            raise ValueError(f"gate: {gates} rows do not divide {m}")
+    h, out = _bf16_out(h, (m, k), "h"), _bf16_out(out, (m, k), "out")
+    if out is not None and (int8 or not nxt):
+        raise ValueError("out: only the bf16 result of a norm is written to it")
+    if int8 and not nxt:
+        raise ValueError("int8: there is no norm to quantize")
+    _on_current(residual, y, pw, nw, gate, h, out)
+    if h is None:
+        h = _kv8_empty((m, k), _BF16, y.device, stream)
+    q = None
+    if int8:
+        q = Int8Rows(_kv8_empty((m, k), _I8, y.device, stream), _kv8_empty((m,), _F32, y.device, stream))
+    elif nxt and out is None:
+        out = _kv8_empty((m, k), _BF16, y.device, stream)
+    _check(L.rms_norm_residual(residual.data_ptr(), y.data_ptr(), m, k, post, _at(pw), _at(gate), gates, float(scale),
+                               nxt, _at(nw), float(weight_offset), float(eps), h.data_ptr(), _at(out),
+                               q and q.codes.data_ptr(), q and q.row_scale.data_ptr(),
+                               _kv8_stream(stream, y.get_device())))
+    return h, q if int8 else out
+
+
 # ---- 8-bit paged KV cache -----------------------------------------------------------
 
 def kv8_cache(pages: int, heads: int, dim: int, page: int = 64, weights: bool = False,
@@ -666,9 +919,6 @@ def kv8_cache(pages: int, heads: int, dim: int, page: int = 64, weights: bool = 
 _pack_cache = struct.Struct("@5P4i").pack
 _pack_batch = struct.Struct("@3P5i4x").pack
 _pack_rows = struct.Struct("@P2q").pack
-
-
-_U8, _I32, _F32, _BF16 = torch.uint8, torch.int32, torch.float32, torch.bfloat16
 
 
 def _kv8_refuse(c: KV8Cache):

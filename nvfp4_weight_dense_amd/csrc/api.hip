@@ -583,6 +583,104 @@ int run_evict(const char *name, const kv8_cache *cache, const kv8_batch *batch, 
                     "eviction launch");
 }
 
+// ---- 8-bit integers -----------------------------------------------------------------
+
+int check_int8_weight(const int8_weight *w, const char *name) {
+  if (!w) return fail(NVFP4_EINVAL, "%s: null weight descriptor", name);
+  if (!w->codes || !w->scales) return fail(NVFP4_EINVAL, "%s: null codes or scales pointer", name);
+  if (w->n <= 0 || w->k <= 0) return fail(NVFP4_ESHAPE, "%s: n=%d k=%d must be positive", name, w->n, w->k);
+  if (w->k % 32 != 0) return fail(NVFP4_ESHAPE, "%s: k=%d is not a multiple of 32", name, w->k);
+  // (127 * 128 * k stays below 2^31)
+  if (w->k > kInt8MaxK || w->n > kMaxDim)
+    return fail(NVFP4_ESHAPE, "%s: n=%d k=%d exceed %d and %d", name, w->n, w->k, kMaxDim, kInt8MaxK);
+  if (misaligned(w->codes) || ((uintptr_t)w->scales & 3u))
+    return fail(NVFP4_EINVAL, "%s: codes must be 16-byte and scales 4-byte aligned", name);
+  return NVFP4_OK;
+}
+
+Int8MatRef int8_mat(const int8_weight *w) { return Int8MatRef{w->codes, w->scales}; }
+
+// Parts of a workspace, one behind the other.  Offsets are found first; with
+// a base they become pointers.
+struct Parts {
+  size_t bytes = 0;
+  size_t take(size_t n) {
+    const size_t at = bytes;
+    bytes += align256(n);
+    return at;
+  }
+};
+
+// A call's rows in int8: the caller's own, or quantized into the workspace.
+struct Int8RowsPlan {
+  bool own;
+  size_t codes = 0, scales = 0;
+  Int8RowsPlan(bool own, int m, int k, Parts &at) : own(own) {
+    if (own) return;
+    codes = at.take((size_t)m * k);
+    scales = at.take((size_t)m * 4);
+  }
+};
+int int8_rows_of(const void *x, const float *row_scale, int m, int k, const Int8RowsPlan &pl, char *base, Int8ActRef *a,
+                 hipStream_t s) {
+  if (pl.own) {
+    *a = Int8ActRef{(const int8_t *)x, row_scale};
+    return NVFP4_OK;
+  }
+  *a = Int8ActRef{(const int8_t *)(base + pl.codes), (const float *)(base + pl.scales)};
+  return hip_status(launch_int8_rows(x, m, k, (int8_t *)(base + pl.codes), (float *)(base + pl.scales), s),
+                    "int8 quantize launch");
+}
+
+// The workspace of a call that takes `need` bytes: the caller's (checked), or
+// the arena, which a captured call may not use: it can move, and other graphs
+// and eager calls share it.
+int int8_scratch(const char *name, void *workspace, int64_t workspace_bytes, size_t need, hipStream_t s, char **base) {
+  if (workspace) {
+    if (workspace_bytes < (int64_t)need || ((uintptr_t)workspace & 255u))
+      return fail(NVFP4_EINVAL, "%s: the workspace must be 256-byte aligned and of %zu bytes", name, need);
+    *base = (char *)workspace;
+    return NVFP4_OK;
+  }
+  hipStreamCaptureStatus st = hipStreamCaptureStatusNone;
+  if (hipStreamIsCapturing(s, &st) != hipSuccess || st != hipStreamCaptureStatusNone) {
+    (void)hipGetLastError();
+    return fail(NVFP4_EINVAL, "%s: a captured call needs a workspace of its own", name);
+  }
+  void *p = nullptr;
+  int rc;
+  if (need && (rc = arena_get(need, &p))) return rc;
+  *base = (char *)p;
+  return NVFP4_OK;
+}
+
+int check_row_k(int k, const char *name) {
+  if (k <= 0 || k % 8 != 0 || k > kMaxRowK)
+    return fail(NVFP4_ESHAPE, "%s: k=%d must be a positive multiple of 8 up to %d", name, k, kMaxRowK);
+  return NVFP4_OK;
+}
+
+// where a pass leaves its rows: out, or codes and row_scale
+int check_rows_out(const void *out, const int8_t *codes, const float *row_scale, const char *name) {
+  if (!out == !codes || !codes != !row_scale)
+    return fail(NVFP4_EINVAL, "%s: expected out, or codes and row_scale", name);
+  if (misaligned(out) || misaligned(codes) || ((uintptr_t)row_scale & 3u))
+    return fail(NVFP4_EINVAL, "%s: out and codes must be 16-byte and row_scale 4-byte aligned", name);
+  return NVFP4_OK;
+}
+
+int check_norm(const void *weight, float offset, float eps, const char *name) {
+  if (misaligned(weight)) return fail(NVFP4_EINVAL, "%s: weights must be 16-byte aligned", name);
+  if (!(fabsf(offset) < INFINITY)) return fail(NVFP4_EINVAL, "%s: offset is not finite", name);
+  if (!(eps >= 1e-18f && eps <= 1.0f)) return fail(NVFP4_EINVAL, "%s: eps=%g is not in 1e-18 .. 1", name, (double)eps);
+  return NVFP4_OK;
+}
+
+int check_int8_x(const void *x, const float *row_scale, int m) {
+  if ((uintptr_t)row_scale & 3u) return fail(NVFP4_EINVAL, "row_scale: must be 4-byte aligned");
+  return check_act(x, m, "x");
+}
+
 struct NoAllocDev {
   bool ready = false;
   void *ptr = nullptr;
@@ -1152,6 +1250,133 @@ int dense_ffn_forward_q2(const void *x, int32_t m, int32_t hidden, int32_t inter
   Q2MatRef w2[2] = {mg, mu};
   if ((rc = run_q2(x, m, hidden, inter, gsg, 2, w2, act, scr, s))) return rc;
   return run_q2(act, m, inter, hidden, gsd, 1, &md, out, scr, s);
+}
+
+// ---- 8-bit integers -----------------------------------------------------------------
+
+int int8_quantize_rows(const void *x, int32_t m, int32_t k, int8_t *codes, float *row_scale, void *stream) {
+  g_err.clear();
+  int rc;
+  if ((rc = check_act(x, m, "x")) || (rc = check_row_k(k, "int8_quantize_rows"))) return rc;
+  if (m == 0) return NVFP4_OK;
+  if (!codes || !row_scale) return fail(NVFP4_EINVAL, "int8_quantize_rows: null output pointer");
+  if ((rc = check_rows_out(nullptr, codes, row_scale, "int8_quantize_rows"))) return rc;
+  return hip_status(launch_int8_rows(x, m, k, codes, row_scale, (hipStream_t)stream), "int8_quantize_rows launch");
+}
+
+int64_t int8_gemm_workspace(int32_t m, const int8_weight *w) {
+  g_err.clear();
+  int rc;
+  if (m < 0 || m > 4194240) return fail(NVFP4_EINVAL, "int8_gemm_workspace: m=%d is not in 0 .. 4194240", m);
+  if ((rc = check_int8_weight(w, "w"))) return rc;
+  Parts at;
+  Int8RowsPlan(false, m, w->k, at);
+  return (int64_t)at.bytes;
+}
+
+int int8_gemm_w8a8(const void *x, const float *row_scale, int32_t m, const int8_weight *w, void *y, void *workspace,
+                   int64_t workspace_bytes, void *stream) {
+  g_err.clear();
+  int rc;
+  if ((rc = check_int8_x(x, row_scale, m)) || (rc = check_act(y, m, "y")) || (rc = check_int8_weight(w, "w")))
+    return rc;
+  if (m == 0) return NVFP4_OK;
+  hipStream_t s = (hipStream_t)stream;
+  Parts at;
+  const Int8RowsPlan rows(row_scale != nullptr, m, w->k, at);
+  char *base = nullptr;
+  if ((rc = int8_scratch("int8_gemm_w8a8", workspace, workspace_bytes, at.bytes, s, &base))) return rc;
+  ProfileScope ps("gemm_int8", m, s);
+  Int8ActRef a;
+  if ((rc = int8_rows_of(x, row_scale, m, w->k, rows, base, &a, s))) return rc;
+  const Int8MatRef wm = int8_mat(w);
+  return hip_status(launch_int8_gemm(a, m, w->k, w->n, 1, &wm, y, s), "int8 projection launch");
+}
+
+int64_t dense_ffn_int8_workspace(int32_t m, int32_t hidden, int32_t inter) {
+  g_err.clear();
+  if (m < 0 || m > 4194240) return fail(NVFP4_EINVAL, "dense_ffn_int8_workspace: m=%d is not in 0 .. 4194240", m);
+  if (hidden <= 0 || inter <= 0 || hidden % 32 != 0 || inter % 32 != 0 || hidden > kInt8MaxK || inter > kInt8MaxK)
+    return fail(NVFP4_ESHAPE, "hidden=%d inter=%d must be positive multiples of 32 up to %d", hidden, inter, kInt8MaxK);
+  Parts at;
+  Int8RowsPlan(false, m, hidden, at);
+  Int8RowsPlan(false, m, inter, at);
+  at.take((size_t)2 * m * inter);
+  return (int64_t)at.bytes;
+}
+
+int dense_ffn_forward_int8(const void *x, const float *row_scale, int32_t m, int32_t hidden, int32_t inter,
+                           const int8_weight *wg, const int8_weight *wu, const int8_weight *wd, void *out,
+                           void *workspace, int64_t workspace_bytes, void *stream) {
+  g_err.clear();
+  int rc;
+  if ((rc = check_int8_x(x, row_scale, m)) || (rc = check_act(out, m, "out"))) return rc;
+  if (hidden <= 0 || inter <= 0)
+    return fail(NVFP4_ESHAPE, "hidden=%d inter=%d must be positive", hidden, inter);
+  if ((rc = check_int8_weight(wg, "wg")) || (rc = check_int8_weight(wu, "wu")) || (rc = check_int8_weight(wd, "wd")))
+    return rc;
+  if (wg->n != inter || wg->k != hidden || wu->n != inter || wu->k != hidden)
+    return fail(NVFP4_ESHAPE, "wg/wu must be [inter=%d][hidden=%d], got [%d][%d] and [%d][%d]",
+                inter, hidden, wg->n, wg->k, wu->n, wu->k);
+  if (wd->n != hidden || wd->k != inter)
+    return fail(NVFP4_ESHAPE, "wd must be [hidden=%d][inter=%d], got [%d][%d]", hidden, inter, wd->n, wd->k);
+  if (m == 0) return NVFP4_OK;
+  hipStream_t s = (hipStream_t)stream;
+  Parts at;
+  const Int8RowsPlan rows(row_scale != nullptr, m, hidden, at), mid(false, m, inter, at);
+  const size_t act_at = at.take((size_t)2 * m * inter);
+  char *base = nullptr;
+  if ((rc = int8_scratch("dense_ffn_forward_int8", workspace, workspace_bytes, at.bytes, s, &base))) return rc;
+  ProfileScope ps("dense_total int8", m, s);
+  Int8ActRef a, b;
+  if ((rc = int8_rows_of(x, row_scale, m, hidden, rows, base, &a, s))) return rc;
+  const Int8MatRef w2[2] = {int8_mat(wg), int8_mat(wu)}, wdm = int8_mat(wd);
+  char *act = base + act_at;
+  if ((rc = hip_status(launch_int8_gemm(a, m, hidden, inter, 2, w2, act, s), "int8 projection launch")) ||
+      (rc = int8_rows_of(act, nullptr, m, inter, mid, base, &b, s)))
+    return rc;
+  return hip_status(launch_int8_gemm(b, m, inter, hidden, 1, &wdm, out, s), "int8 projection launch");
+}
+
+// ---- norms before and after a block -------------------------------------------------
+
+int rms_norm(const void *x, int32_t m, int32_t k, const void *weight, float offset, float eps, void *out,
+             int8_t *codes, float *row_scale, void *stream) {
+  g_err.clear();
+  int rc;
+  if ((rc = check_act(x, m, "x")) || (rc = check_row_k(k, "rms_norm")) ||
+      (rc = check_norm(weight, offset, eps, "rms_norm")))
+    return rc;
+  if (m == 0) return NVFP4_OK;
+  if ((rc = check_rows_out(out, codes, row_scale, "rms_norm"))) return rc;
+  return hip_status(launch_rms_norm(x, m, k, NormRef{weight, offset, true}, eps, RowsOut{out, codes, row_scale},
+                                    (hipStream_t)stream),
+                    "rms_norm launch");
+}
+
+int rms_norm_residual(const void *residual, const void *y, int32_t m, int32_t k, int32_t post,
+                      const void *post_weight, const void *gate, int32_t gates, float scale, int32_t next,
+                      const void *next_weight, float offset, float eps, void *h, void *out, int8_t *codes,
+                      float *row_scale, void *stream) {
+  g_err.clear();
+  int rc;
+  const char *name = "rms_norm_residual";
+  if ((rc = check_act(residual, m, "residual")) || (rc = check_act(y, m, "y")) || (rc = check_act(h, m, "h")) ||
+      (rc = check_row_k(k, name)) || (rc = check_norm(post_weight, offset, eps, name)) ||
+      (rc = check_norm(next_weight, offset, eps, name)))
+    return rc;
+  if (!(fabsf(scale) < INFINITY)) return fail(NVFP4_EINVAL, "%s: scale is not finite", name);
+  if (!gate != (gates == 0) || gates < 0)
+    return fail(NVFP4_EINVAL, "%s: gates=%d does not go with the gate pointer", name, gates);
+  if (misaligned(gate)) return fail(NVFP4_EINVAL, "%s: gate must be 16-byte aligned", name);
+  if (m == 0) return NVFP4_OK;
+  if (gate && m % gates != 0) return fail(NVFP4_ESHAPE, "%s: gates=%d does not divide m=%d", name, gates, m);
+  if (next && (rc = check_rows_out(out, codes, row_scale, name))) return rc;
+  if (!next && (out || codes || row_scale)) return fail(NVFP4_EINVAL, "%s: an output without a next norm", name);
+  const ResidualArgs a{residual, y, gate, gate ? m / gates : 1, scale, {post_weight, offset, post != 0},
+                       {next_weight, offset, next != 0}, h};
+  return hip_status(launch_rms_norm_residual(a, m, k, eps, RowsOut{out, codes, row_scale}, (hipStream_t)stream),
+                    "rms_norm_residual launch");
 }
 
 // ---- 8-bit paged KV cache ---------------------------------------------------------

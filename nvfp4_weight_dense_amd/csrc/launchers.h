@@ -261,6 +261,46 @@ hipError_t launch_fixed_tall_w8a8(const Fp8ActRef &a, int m, int k, int n, int n
                                   unsigned *counters, const StreamPlan &pl,
                                   hipStream_t stream);
 
+// ---- passes over bf16 rows of k values (k % 8 == 0, k <= kMaxRowK): k_rows.hip ----
+constexpr int kMaxRowK = 131072;
+// Where a pass leaves its rows: bf16, or (out null) int8 codes and a scale
+// for each row.
+struct RowsOut {
+  void *out;
+  int8_t *codes;
+  float *row_scale;
+};
+struct NormRef {
+  const void *weight;  // bf16 [k], or null: no weight
+  float offset;        // added to the weight
+  bool on;
+};
+struct ResidualArgs {
+  const void *residual, *y;  // bf16 [m][k]
+  const void *gate;          // bf16 [m / rows_per_gate][k], or null
+  int rows_per_gate;
+  float scale;
+  NormRef post, next;  // of y, and of h
+  void *h;             // bf16 [m][k]
+};
+hipError_t launch_int8_rows(const void *x, int m, int k, int8_t *codes, float *row_scale, hipStream_t s);
+hipError_t launch_rms_norm(const void *x, int m, int k, const NormRef &n, float eps, const RowsOut &o, hipStream_t s);
+hipError_t launch_rms_norm_residual(const ResidualArgs &a, int m, int k, float eps, const RowsOut &o, hipStream_t s);
+
+// ---- products in 8-bit integers (k % 32 == 0, k <= kInt8MaxK: the sums stay below 2^31) ----
+constexpr int kInt8MaxK = 131072;
+struct Int8MatRef {
+  const int8_t *codes;  // [n][k]
+  const float *scales;  // [n]
+};
+struct Int8ActRef {
+  const int8_t *codes;     // [m][k]
+  const float *row_scale;  // [m]
+};
+// y = x . w0^T (nmat 1), or bf16(silu(bf16(x . w0^T)) * bf16(x . w1^T)) (nmat 2)
+hipError_t launch_int8_gemm(const Int8ActRef &a, int m, int k, int n, int nmat, const Int8MatRef *w, void *y,
+                            hipStream_t s);
+
 // Register-only bf16 MFMA loop (a measurement aid): `workgroups` groups of
 // four waves, each wave iters x 4 v_mfma_f32_32x32x16_bf16.  sink: 256
 // floats, never written in practice.
