@@ -611,35 +611,61 @@ struct Parts {
   }
 };
 
-// A call's rows in int8: the caller's own, or quantized into the workspace.
-struct Int8RowsPlan {
-  bool own;
-  size_t codes = 0, scales = 0;
-  Int8RowsPlan(bool own, int m, int k, Parts &at) : own(own) {
-    if (own) return;
-    codes = at.take((size_t)m * k);
-    scales = at.take((size_t)m * 4);
+// One product: where its rows, if they are to be quantized first, and its
+// partial sums lie behind a base.  (1 to 4 rows take a kernel that quantizes
+// them itself and splits no sum over workgroups.)
+struct Int8Product {
+  bool gemv, quantize;
+  Int8Plan plan{};
+  size_t codes = 0, scales = 0, partial = 0, bytes = 0;
+  Int8Product(bool own_rows, int m, int n, int k, int nmat) {
+    gemv = int8_gemv_eligible(m, k) && (own_rows || int8_gemv_quantizes(m, k));
+    quantize = !own_rows && !gemv;
+    Parts at;
+    if (quantize) codes = at.take((size_t)m * k), scales = at.take((size_t)m * 4);
+    if (!gemv) {
+      plan = int8_plan(m, n, k, nmat);
+      partial = at.take(plan.partial_bytes);
+    }
+    bytes = at.bytes;
   }
 };
-int int8_rows_of(const void *x, const float *row_scale, int m, int k, const Int8RowsPlan &pl, char *base, Int8ActRef *a,
-                 hipStream_t s) {
-  if (pl.own) {
-    *a = Int8ActRef{(const int8_t *)x, row_scale};
-    return NVFP4_OK;
+int run_int8(const Int8Product &pr, const void *x, const float *row_scale, int m, int k, int n, int nmat,
+             const Int8MatRef *w, void *y, unsigned *counters, char *base, hipStream_t s) {
+  if (pr.gemv) return hip_status(launch_int8_gemv(x, row_scale, m, k, n, nmat, w, y, s), "int8 projection launch");
+  int rc;
+  Int8ActRef a{(const int8_t *)x, row_scale};
+  if (pr.quantize) {
+    a = Int8ActRef{(const int8_t *)(base + pr.codes), (const float *)(base + pr.scales)};
+    if ((rc = hip_status(launch_int8_rows(x, m, k, (int8_t *)(base + pr.codes), (float *)(base + pr.scales), s),
+                         "int8 quantize launch")))
+      return rc;
   }
-  *a = Int8ActRef{(const int8_t *)(base + pl.codes), (const float *)(base + pl.scales)};
-  return hip_status(launch_int8_rows(x, m, k, (int8_t *)(base + pl.codes), (float *)(base + pl.scales), s),
-                    "int8 quantize launch");
+  return hip_status(launch_int8_gemm(a, m, k, n, nmat, w, y, pr.plan, counters, (int *)(base + pr.partial), s),
+                    "int8 projection launch");
+}
+// Bytes for up to m rows: the plans' partial sums do not all grow with the
+// rows, so every step of theirs below m counts.
+size_t int8_product_bound(int m, int n, int k, int nmat) {
+  size_t most = 0;
+  for (int rows : {1, 4, 5, 16, 17, 32, 33, 64, 65, 128, 129, 256, 257})
+    if (rows < m) most = std::max(most, Int8Product(false, rows, n, k, nmat).bytes);
+  return m ? std::max(most, Int8Product(false, m, n, k, nmat).bytes) : 0;
 }
 
-// The workspace of a call that takes `need` bytes: the caller's (checked), or
-// the arena, which a captured call may not use: it can move, and other graphs
-// and eager calls share it.
-int int8_scratch(const char *name, void *workspace, int64_t workspace_bytes, size_t need, hipStream_t s, char **base) {
+// The counters and the scratch of a call that takes `need` bytes of it: the
+// caller's workspace (checked), counters first, or the library's, which a
+// captured call may not use: they can move, and other graphs and eager calls
+// share them.
+constexpr size_t kInt8CounterBytes = kInt8Counters * 4;
+int int8_scratch(const char *name, void *workspace, int64_t workspace_bytes, size_t need, hipStream_t s,
+                 unsigned **counters, char **base) {
   if (workspace) {
-    if (workspace_bytes < (int64_t)need || ((uintptr_t)workspace & 255u))
-      return fail(NVFP4_EINVAL, "%s: the workspace must be 256-byte aligned and of %zu bytes", name, need);
-    *base = (char *)workspace;
+    if (workspace_bytes < (int64_t)(need + kInt8CounterBytes) || ((uintptr_t)workspace & 255u))
+      return fail(NVFP4_EINVAL, "%s: the workspace must be 256-byte aligned and of %zu bytes", name,
+                  need + kInt8CounterBytes);
+    *counters = (unsigned *)workspace;
+    *base = (char *)workspace + kInt8CounterBytes;
     return NVFP4_OK;
   }
   hipStreamCaptureStatus st = hipStreamCaptureStatusNone;
@@ -649,7 +675,7 @@ int int8_scratch(const char *name, void *workspace, int64_t workspace_bytes, siz
   }
   void *p = nullptr;
   int rc;
-  if (need && (rc = arena_get(need, &p))) return rc;
+  if ((rc = counters_get(kInt8Counters, counters)) || (need && (rc = arena_get(need, &p)))) return rc;
   *base = (char *)p;
   return NVFP4_OK;
 }
@@ -1269,9 +1295,7 @@ int64_t int8_gemm_workspace(int32_t m, const int8_weight *w) {
   int rc;
   if (m < 0 || m > 4194240) return fail(NVFP4_EINVAL, "int8_gemm_workspace: m=%d is not in 0 .. 4194240", m);
   if ((rc = check_int8_weight(w, "w"))) return rc;
-  Parts at;
-  Int8RowsPlan(false, m, w->k, at);
-  return (int64_t)at.bytes;
+  return (int64_t)(kInt8CounterBytes + int8_product_bound(m, w->n, w->k, 1));
 }
 
 int int8_gemm_w8a8(const void *x, const float *row_scale, int32_t m, const int8_weight *w, void *y, void *workspace,
@@ -1282,15 +1306,13 @@ int int8_gemm_w8a8(const void *x, const float *row_scale, int32_t m, const int8_
     return rc;
   if (m == 0) return NVFP4_OK;
   hipStream_t s = (hipStream_t)stream;
-  Parts at;
-  const Int8RowsPlan rows(row_scale != nullptr, m, w->k, at);
+  const Int8Product pr(row_scale != nullptr, m, w->n, w->k, 1);
+  unsigned *counters = nullptr;
   char *base = nullptr;
-  if ((rc = int8_scratch("int8_gemm_w8a8", workspace, workspace_bytes, at.bytes, s, &base))) return rc;
+  if ((rc = int8_scratch("int8_gemm_w8a8", workspace, workspace_bytes, pr.bytes, s, &counters, &base))) return rc;
   ProfileScope ps("gemm_int8", m, s);
-  Int8ActRef a;
-  if ((rc = int8_rows_of(x, row_scale, m, w->k, rows, base, &a, s))) return rc;
   const Int8MatRef wm = int8_mat(w);
-  return hip_status(launch_int8_gemm(a, m, w->k, w->n, 1, &wm, y, s), "int8 projection launch");
+  return run_int8(pr, x, row_scale, m, w->k, w->n, 1, &wm, y, counters, base, s);
 }
 
 int64_t dense_ffn_int8_workspace(int32_t m, int32_t hidden, int32_t inter) {
@@ -1298,11 +1320,8 @@ int64_t dense_ffn_int8_workspace(int32_t m, int32_t hidden, int32_t inter) {
   if (m < 0 || m > 4194240) return fail(NVFP4_EINVAL, "dense_ffn_int8_workspace: m=%d is not in 0 .. 4194240", m);
   if (hidden <= 0 || inter <= 0 || hidden % 32 != 0 || inter % 32 != 0 || hidden > kInt8MaxK || inter > kInt8MaxK)
     return fail(NVFP4_ESHAPE, "hidden=%d inter=%d must be positive multiples of 32 up to %d", hidden, inter, kInt8MaxK);
-  Parts at;
-  Int8RowsPlan(false, m, hidden, at);
-  Int8RowsPlan(false, m, inter, at);
-  at.take((size_t)2 * m * inter);
-  return (int64_t)at.bytes;
+  return (int64_t)(kInt8CounterBytes + align256((size_t)2 * m * inter) +
+                   std::max(int8_product_bound(m, inter, hidden, 2), int8_product_bound(m, hidden, inter, 1)));
 }
 
 int dense_ffn_forward_int8(const void *x, const float *row_scale, int32_t m, int32_t hidden, int32_t inter,
@@ -1322,20 +1341,19 @@ int dense_ffn_forward_int8(const void *x, const float *row_scale, int32_t m, int
     return fail(NVFP4_ESHAPE, "wd must be [hidden=%d][inter=%d], got [%d][%d]", hidden, inter, wd->n, wd->k);
   if (m == 0) return NVFP4_OK;
   hipStream_t s = (hipStream_t)stream;
-  Parts at;
-  const Int8RowsPlan rows(row_scale != nullptr, m, hidden, at), mid(false, m, inter, at);
-  const size_t act_at = at.take((size_t)2 * m * inter);
+  // act, then the rows and partial sums of either product
+  const Int8Product up(row_scale != nullptr, m, inter, hidden, 2), down(false, m, hidden, inter, 1);
+  const size_t act_b = align256((size_t)2 * m * inter);
+  unsigned *counters = nullptr;
   char *base = nullptr;
-  if ((rc = int8_scratch("dense_ffn_forward_int8", workspace, workspace_bytes, at.bytes, s, &base))) return rc;
-  ProfileScope ps("dense_total int8", m, s);
-  Int8ActRef a, b;
-  if ((rc = int8_rows_of(x, row_scale, m, hidden, rows, base, &a, s))) return rc;
-  const Int8MatRef w2[2] = {int8_mat(wg), int8_mat(wu)}, wdm = int8_mat(wd);
-  char *act = base + act_at;
-  if ((rc = hip_status(launch_int8_gemm(a, m, hidden, inter, 2, w2, act, s), "int8 projection launch")) ||
-      (rc = int8_rows_of(act, nullptr, m, inter, mid, base, &b, s)))
+  if ((rc = int8_scratch("dense_ffn_forward_int8", workspace, workspace_bytes, act_b + std::max(up.bytes, down.bytes), s,
+                         &counters, &base)))
     return rc;
-  return hip_status(launch_int8_gemm(b, m, inter, hidden, 1, &wdm, out, s), "int8 projection launch");
+  ProfileScope ps("dense_total int8", m, s);
+  const Int8MatRef w2[2] = {int8_mat(wg), int8_mat(wu)}, wdm = int8_mat(wd);
+  char *act = base, *rest = base + act_b;
+  if ((rc = run_int8(up, x, row_scale, m, hidden, inter, 2, w2, act, counters, rest, s))) return rc;
+  return run_int8(down, act, nullptr, m, inter, hidden, 1, &wdm, out, counters, rest, s);
 }
 
 // ---- norms before and after a block -------------------------------------------------

@@ -14,6 +14,7 @@ namespace nvfp4 {
 
 typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
 typedef int i32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
 typedef int i32x16 __attribute__((ext_vector_type(16)));
 
 // Magnitudes of bf16 values compare as their bits do, infinities above the

@@ -6,6 +6,7 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "int8_plan.h"
 #include "kv8_plan.h"
 
 namespace nvfp4 {
@@ -297,9 +298,18 @@ struct Int8ActRef {
   const int8_t *codes;     // [m][k]
   const float *row_scale;  // [m]
 };
-// y = x . w0^T (nmat 1), or bf16(silu(bf16(x . w0^T)) * bf16(x . w1^T)) (nmat 2)
+// A product is y = x . w0^T (nmat 1), or bf16(silu(bf16(x . w0^T)) * bf16(x . w1^T)) (nmat 2).
+//
+// 1 to 4 rows, bf16 (row_scale null; where the kernel can quantize them) or int8:
+bool int8_gemv_eligible(int m, int k);
+bool int8_gemv_quantizes(int m, int k);
+hipError_t launch_int8_gemv(const void *x, const float *row_scale, int m, int k, int n, int nmat, const Int8MatRef *w,
+                            void *y, hipStream_t s);
+// Any number of rows, int8.  `counters`: kInt8Counters words, zero on entry,
+// left zero; `partial`: pl.partial_bytes.
+constexpr int kInt8Counters = 256;
 hipError_t launch_int8_gemm(const Int8ActRef &a, int m, int k, int n, int nmat, const Int8MatRef *w, void *y,
-                            hipStream_t s);
+                            const Int8Plan &pl, unsigned *counters, int *partial, hipStream_t s);
 
 // Register-only bf16 MFMA loop (a measurement aid): `workgroups` groups of
 // four waves, each wave iters x 4 v_mfma_f32_32x32x16_bf16.  sink: 256
