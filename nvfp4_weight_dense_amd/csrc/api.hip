@@ -615,8 +615,9 @@ struct Parts {
 // partial sums lie behind a base.  (1 to 4 rows take a kernel that quantizes
 // them itself and splits no sum over workgroups.)
 struct Int8Product {
-  bool gemv, quantize;
+  bool gemv, quantize, tiled = false;
   Int8Plan plan{};
+  Int8TilePlan tile{};
   size_t codes = 0, scales = 0, partial = 0, bytes = 0;
   Int8Product(bool own_rows, int m, int n, int k, int nmat) {
     gemv = int8_gemv_eligible(m, k) && (own_rows || int8_gemv_quantizes(m, k));
@@ -624,8 +625,10 @@ struct Int8Product {
     Parts at;
     if (quantize) codes = at.take((size_t)m * k), scales = at.take((size_t)m * 4);
     if (!gemv) {
-      plan = int8_plan(m, n, k, nmat);
-      partial = at.take(plan.partial_bytes);
+      tiled = m > 256;
+      if (tiled) tile = int8_tile_plan(m, n, k, nmat);
+      else plan = int8_plan(m, n, k, nmat);
+      partial = at.take(tiled ? tile.partial_bytes : plan.partial_bytes);
     }
     bytes = at.bytes;
   }
@@ -641,16 +644,14 @@ int run_int8(const Int8Product &pr, const void *x, const float *row_scale, int m
                          "int8 quantize launch")))
       return rc;
   }
-  return hip_status(launch_int8_gemm(a, m, k, n, nmat, w, y, pr.plan, counters, (int *)(base + pr.partial), s),
+  int *partial = (int *)(base + pr.partial);
+  return hip_status(pr.tiled ? launch_int8_tile(a, m, k, n, nmat, w, y, pr.tile, counters, partial, s)
+                             : launch_int8_gemm(a, m, k, n, nmat, w, y, pr.plan, counters, partial, s),
                     "int8 projection launch");
 }
-// Bytes for up to m rows: the plans' partial sums do not all grow with the
-// rows, so every step of theirs below m counts.
+// Bytes that hold an Int8Product of up to m rows.
 size_t int8_product_bound(int m, int n, int k, int nmat) {
-  size_t most = 0;
-  for (int rows : {1, 4, 5, 16, 17, 32, 33, 64, 65, 128, 129, 256, 257})
-    if (rows < m) most = std::max(most, Int8Product(false, rows, n, k, nmat).bytes);
-  return m ? std::max(most, Int8Product(false, m, n, k, nmat).bytes) : 0;
+  return m ? align256((size_t)m * k) + align256((size_t)m * 4) + align256(int8_partial_bound(m, n, k, nmat)) : 0;
 }
 
 // The counters and the scratch of a call that takes `need` bytes of it: the

@@ -14,8 +14,8 @@ namespace nvfp4 {
 
 typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
 typedef int i32x4 __attribute__((ext_vector_type(4)));
-typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
 typedef int i32x16 __attribute__((ext_vector_type(16)));
+typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
 
 // Magnitudes of bf16 values compare as their bits do, infinities above the
 // finite ones and NaN above those, so a row's largest is found on the bits,
@@ -80,6 +80,48 @@ __device__ __forceinline__ Int8Scale int8_scale(float s) {
 }
 __device__ __forceinline__ float int8_scaled(int sum, const Int8Scale &row, const Int8Scale &col) {
   return __builtin_ldexpf((float)sum * row.f * col.f, row.e + col.e);
+}
+
+// ---- rings in LDS --------------------------------------------------------------
+// 16 bytes a lane from memory to LDS at `lds` + 16 lane; lanes out of the
+// range write zeros.  The compiler does not see the transfer, so it places no
+// waits for it: the kernel's own waits count it, and every transfer has to be
+// complete before its workgroup ends.
+__device__ __forceinline__ void to_lds(u32x4_t r, uint32_t lds, uint32_t voff, uint32_t soff) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+               :
+               : "s"(lds), "v"(voff), "s"(r), "s"(soff)
+               : "memory");
+}
+__device__ __forceinline__ u32x4_t range_of(const void *base, size_t bytes) {
+  const uint64_t a = (uint64_t)base;
+  return u32x4_t{(uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)a),
+                 (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)(a >> 32)),
+                 (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)bytes), 0x00020000u};
+}
+__device__ __forceinline__ uint32_t lds_address(const void *p) {
+  return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const void *)p;
+}
+// This wave's transfers but the youngest N are complete, and its LDS reads.
+template <int N>
+__device__ __forceinline__ void wait_transfers() {
+  static_assert(N < 64, "the counter has six bits");
+  __atomic_signal_fence(__ATOMIC_SEQ_CST);
+  __builtin_amdgcn_s_waitcnt(0x0070 | (N & 15) | ((N >> 4) << 14));
+  __atomic_signal_fence(__ATOMIC_SEQ_CST);
+}
+__device__ __forceinline__ void ring_barrier() {
+  __builtin_amdgcn_s_barrier();
+  __atomic_signal_fence(__ATOMIC_SEQ_CST);
+}
+
+// Pieces of sums handed from workgroup to workgroup, past the caches
+// (kCoherent in nvfp4_common.h).
+__device__ __forceinline__ void st16_coherent(__amdgpu_buffer_rsrc_t r, uint32_t off, i32x4 v) {
+  __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, v), r, off, 0, kCoherent);
+}
+__device__ __forceinline__ i32x4 ld16_coherent(__amdgpu_buffer_rsrc_t r, uint32_t off) {
+  return __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, kCoherent));
 }
 
 }  // namespace nvfp4

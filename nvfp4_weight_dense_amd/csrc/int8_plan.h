@@ -40,6 +40,75 @@ inline Int8Plan int8_plan(int m, int n, int k, int nmat) {
   return p;
 }
 
+// Many rows: tiles of the output.  Whole rounds of tiles go one to a
+// workgroup; the tiles of the last round, where they do not fill it, may be
+// cut along K into equal runs over all workgroups, as above.
+struct Int8TilePlan {
+  int shape;           // of a tile: kInt8Tiles[shape]
+  int row_blocks, groups, units;  // tiles along rows and columns, units of K
+  int nwg;
+  int whole;           // tiles that go whole, the first ones
+  size_t partial_bytes;
+};
+struct Int8Tile {
+  int rows, cols;  // (cols: half of them gate and half up, with two matrices)
+  double unit;     // cost of a unit of K of one tile, in microseconds
+};
+constexpr int kInt8TileK = 64;
+constexpr int kInt8Shapes = 4;
+constexpr Int8Tile kInt8Tiles[kInt8Shapes] = {{256, 256, 0.70}, {256, 128, 0.42}, {128, 256, 0.42}, {128, 128, 0.26}};
+
+inline Int8TilePlan int8_tile_plan_of(int shape, bool split, int m, int n, int k, int nmat) {
+  const Int8Tile t = kInt8Tiles[shape];
+  Int8TilePlan p{};
+  p.shape = shape;
+  p.row_blocks = (m + t.rows - 1) / t.rows;
+  p.groups = (n + t.cols / nmat - 1) / (t.cols / nmat);
+  p.units = (k + kInt8TileK - 1) / kInt8TileK;
+  const int64_t tiles = (int64_t)p.row_blocks * p.groups;
+  // (every workgroup has to have units of a split: the last to end counts them all)
+  int64_t rest = split ? tiles % kInt8MaxWG : 0;
+  if (tiles >= kInt8MaxWG && rest * p.units < (int64_t)kInt8MaxWG * kInt8MinUnits) rest = 0;
+  p.whole = (int)(tiles - rest);
+  int64_t nwg = tiles;
+  if (rest) nwg = p.whole ? kInt8MaxWG : (rest * p.units + kInt8MinUnits - 1) / kInt8MinUnits;
+  p.nwg = (int)(nwg < kInt8MaxWG ? nwg : kInt8MaxWG);
+  p.partial_bytes = rest ? (size_t)p.nwg * 2 * t.rows * t.cols * 4 : 0;
+  return p;
+}
+
+// The shape, and whether to split, by what they cost: units that the busiest
+// workgroup does, and for a split the pieces that are written and read again.
+inline Int8TilePlan int8_tile_plan(int m, int n, int k, int nmat) {
+  Int8TilePlan best{};
+  double least = 0;
+  for (int shape = 0; shape < kInt8Shapes; ++shape)
+    for (int split = 0; split < 2; ++split) {
+      const Int8TilePlan p = int8_tile_plan_of(shape, split, m, n, k, nmat);
+      const Int8Tile t = kInt8Tiles[shape];
+      const int64_t rest = (int64_t)p.row_blocks * p.groups - p.whole;
+      double cost = (double)((p.whole + p.nwg - 1) / p.nwg) * p.units * t.unit;
+      if (rest) cost += (double)rest * p.units / p.nwg * t.unit + 4.0 + 20.0 * t.rows * t.cols / 65536;
+      if ((shape == 0 && !split) || cost < least) best = p, least = cost;
+    }
+  return best;
+}
+
+// No plan for m rows or fewer has more partial sums than these.
+inline size_t int8_partial_bound(int m, int n, int k, int nmat) {
+  size_t most = 0;
+  auto more = [&](size_t b) { most = b > most ? b : most; };
+  for (int rows = 16; rows <= 256; rows *= 2)
+    if (rows == 16 || rows / 2 < m) more(int8_plan(rows, n, k, nmat).partial_bytes);
+  for (int shape = 0; shape < kInt8Shapes && m > 256; ++shape) {
+    const Int8TilePlan p = int8_tile_plan_of(shape, false, m, n, k, nmat);
+    const int64_t tiles = (int64_t)p.row_blocks * p.groups;
+    const int64_t wgs = ((tiles < kInt8MaxWG ? tiles : kInt8MaxWG) * p.units + kInt8MinUnits - 1) / kInt8MinUnits;
+    more((size_t)(wgs < kInt8MaxWG ? wgs : kInt8MaxWG) * 2 * kInt8Tiles[shape].rows * kInt8Tiles[shape].cols * 4);
+  }
+  return most;
+}
+
 // first pair of workgroup w's run, and the workgroup whose run holds pair u
 #if defined(__HIPCC__)
 #define INT8_PLAN_FN __host__ __device__ inline

@@ -44,35 +44,6 @@ struct Int8Args {
   int units, all, nwg; // units of a group, pairs in all, workgroups
 };
 
-// 16 bytes a lane from memory to LDS at `lds` + 16 lane.  The compiler does
-// not see the transfer, so it places no waits for it: the kernel's own waits
-// count it.
-__device__ __forceinline__ void to_lds(u32x4_t r, uint32_t lds, uint32_t voff, uint32_t soff) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
-               :
-               : "s"(lds), "v"(voff), "s"(r), "s"(soff)
-               : "memory");
-}
-__device__ __forceinline__ u32x4_t range_of(const void *base, size_t bytes) {
-  const uint64_t a = (uint64_t)base;
-  return u32x4_t{(uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)a),
-                 (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)(a >> 32)),
-                 (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)bytes), 0x00020000u};
-}
-// this wave's transfers but the youngest N are complete, its LDS reads too
-template <int N>
-__device__ __forceinline__ void wait_transfers() {
-  __atomic_signal_fence(__ATOMIC_SEQ_CST);
-  __builtin_amdgcn_s_waitcnt(0x0070 | (N & 15) | ((N >> 4) << 14));
-  __atomic_signal_fence(__ATOMIC_SEQ_CST);
-}
-__device__ __forceinline__ void st16_coherent(__amdgpu_buffer_rsrc_t r, uint32_t off, i32x4 v) {
-  __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, v), r, off, 0, kCoherent);
-}
-__device__ __forceinline__ i32x4 ld16_coherent(__amdgpu_buffer_rsrc_t r, uint32_t off) {
-  return __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, kCoherent));
-}
-
 // MT: 16-row tiles of the workgroup
 template <int MT>
 struct Cfg {
@@ -104,7 +75,7 @@ __global__ __launch_bounds__(kWaves * 64, 2) void k_int8_gemm(Int8Args p) {
   const int c = lane & 15, g = lane >> 4;
   const int me = (int)blockIdx.x;
   const int begin = int8_run_begin(p.all, p.nwg, me), count = int8_run_begin(p.all, p.nwg, me + 1) - begin;
-  const uint32_t ring_at = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t *)ring;
+  const uint32_t ring_at = lds_address(ring);
 
   // ---- requests: weight rows 16 wave + 8 j + lane / 8 of the group (gate for
   // waves 0..3 and up for the others, with two matrices), activation rows
@@ -266,8 +237,7 @@ __global__ __launch_bounds__(kWaves * 64, 2) void k_int8_gemm(Int8Args p) {
       wait_transfers<(S - 2) * (2 + C::kX)>();
     else
       wait_transfers<(S - 2) * 2>();
-    __builtin_amdgcn_s_barrier();
-    __atomic_signal_fence(__ATOMIC_SEQ_CST);
+    ring_barrier();
     request(stage == 0 ? S - 1 : stage - 1);
     compute(stage);
     stage = stage == S - 1 ? 0 : stage + 1;

@@ -1,0 +1,306 @@
+// k_int8_tile.hip -- the int8 projection of many rows (gfx950), bound by the
+// matrix cores (the formula and why any split of K gives the same bits:
+// k_int8_gemm.hip).
+//
+// A workgroup of eight waves computes tiles of the output.  Both operands go
+// from memory straight into a ring in LDS, 64 codes of K (a unit) at a time;
+// a wave's part of a tile is MT x 2 blocks of v_mfma_i32_32x32x32_i8, for
+// which it reads MT + 2 operands of 1 KB from LDS for each half of a unit.
+// The halves alternate between two sets of registers: the reads of the next
+// half are issued before the products of this one, across units too.  The
+// barrier of a unit lies between its halves: it says that the next unit has
+// arrived for all waves, and that this unit's last operands are in registers
+// everywhere, so its place in the ring is free.
+//
+// A row of a unit is 64 bytes, four chunks of 16; chunk q of row r is stored
+// at q ^ (r / 4 % 4), so that the rows that are read together lie in
+// different banks.
+#include "int8_common.h"
+
+namespace nvfp4 {
+
+namespace {
+
+constexpr int kWaves = 8;
+
+struct TileArgs {
+  const int8_t *x;
+  const float *xs;
+  int m, k, n;
+  const int8_t *w0, *w1;
+  const float *s0, *s1;
+  void *y;
+  int *partial;        // [nwg][2][8 waves][2 MT][4][64 lanes][4]
+  unsigned *counters;  // [nwg], zero between calls
+  int row_blocks, groups, units, whole;
+};
+
+// WM: waves along the rows (8 / WM along the columns); MT: 32-row blocks of a wave
+template <int WM, int MT>
+struct Cfg {
+  static constexpr int kRows = WM * MT * 32, kCols = 8 / WM * 64;
+  static constexpr uint32_t kXBytes = kRows * kInt8TileK, kStage = (kRows + kCols) * kInt8TileK;
+  static constexpr int kStages = 131072 / kStage > 8 ? 8 : 131072 / kStage;
+  static constexpr int kX = kRows / 16 / kWaves, kW = kCols / 16 / kWaves;  // transfers of a wave for a unit
+  static constexpr uint32_t kWavePiece = 2u * MT * 16u * 256u;
+};
+
+template <int WM, int MT, int NMAT>
+__global__ __launch_bounds__(kWaves * 64, 2) void k_int8_tile(TileArgs p) {
+  typedef Cfg<WM, MT> C;
+  constexpr int S = C::kStages, X = C::kX + C::kW;
+  constexpr int kCols = C::kCols / NMAT;
+  static_assert(kWaves * C::kWavePiece == C::kRows * C::kCols * 4, "a piece");
+  __shared__ __attribute__((aligned(1024))) uint8_t ring[S * C::kStage];
+  __shared__ unsigned last_flag;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave % WM, wn = wave / WM;
+  const int c = lane & 31, h = lane >> 5;
+  const uint32_t ring_at = lds_address(ring);
+  // Workgroups go to the eight XCDs in turn; each XCD takes a contiguous run
+  // of the workgroups' numbers, so that neighbouring tiles, which share rows
+  // or columns, are read through one L2.
+  const int nwg = (int)gridDim.x;
+  const int me = [&] {
+    const int q = nwg >> 3, rem = nwg & 7, xcd = (int)blockIdx.x & 7;
+    return xcd * q + min(xcd, rem) + ((int)blockIdx.x >> 3);
+  }();
+
+  // ---- this workgroup's work: tiles me, me + nwg, .. of the whole ones, then
+  // units rest_begin .. of the others'
+  const int tiles = p.row_blocks * p.groups, rest = (tiles - p.whole) * p.units;
+  const int mine = me < p.whole ? (p.whole - me + nwg - 1) / nwg : 0;
+  const int rest_begin = rest ? int8_run_begin(rest, nwg, me) : 0;
+  const int rest_end = rest ? int8_run_begin(rest, nwg, me + 1) : 0;
+  const int count = mine * p.units + rest_end - rest_begin;
+  // the tile and unit of this workgroup's i-th unit, for i in order
+  struct At {
+    int tile, unit, done;
+  };
+  auto start = [&](At &a) __attribute__((always_inline)) {
+    a.done = 0;
+    if (mine) a.tile = me, a.unit = 0;
+    else a.tile = p.whole + rest_begin / p.units, a.unit = rest_begin % p.units;
+  };
+  auto next_tile = [&](At &a) __attribute__((always_inline)) {  // a.done counts tiles
+    if (++a.done < mine) a.tile += nwg, a.unit = 0;
+    else if (a.done == mine) a.tile = p.whole + rest_begin / p.units, a.unit = rest_begin % p.units;
+    else ++a.tile, a.unit = 0;
+  };
+  // Row blocks of eight, columns within them, rows fastest: 32 tiles in a row
+  // are eight row blocks of four column groups.
+  auto place = [&](int tile, int &rb, int &cg) __attribute__((always_inline)) {
+    const int super = tile / (8 * p.groups), in = tile - super * 8 * p.groups;
+    const int high = min(8, p.row_blocks - 8 * super);
+    cg = in / high;
+    rb = 8 * super + in - cg * high;
+  };
+
+  // ---- requests: activation rows 16 t + lane / 4; weight rows 16 t + lane / 4
+  // of the tile's columns (with two matrices 32 of gate and 32 of up in turn)
+  const uint32_t line = (uint32_t)lane >> 2;
+  const uint32_t lk = 16u * ((lane & 3u) ^ (line >> 2));
+  const uint32_t voff = line * (uint32_t)p.k + lk;
+  At la;
+  start(la);
+  int requested = 0;
+  u32x4_t xr, wr[C::kW];
+  auto ranges = [&]() __attribute__((always_inline)) {
+    int rb, cg;
+    place(min(la.tile, tiles - 1), rb, cg);
+    const int row0 = rb * C::kRows, col0 = cg * kCols;
+    xr = range_of(p.x + (size_t)row0 * p.k, (size_t)min(C::kRows, p.m - row0) * p.k);
+#pragma unroll
+    for (int j = 0; j < C::kW; ++j) {
+      const int t = wave * C::kW + j;
+      const int at = col0 + (NMAT > 1 ? (t >> 2) * 32 + (t & 1) * 16 : 16 * t);
+      wr[j] = range_of((NMAT > 1 && (t & 2) ? p.w1 : p.w0) + (size_t)min(at, p.n) * p.k,
+                       (size_t)max(min(16, p.n - at), 0) * p.k);
+    }
+  };
+  ranges();
+  auto request = [&](uint32_t stage) __attribute__((always_inline)) {
+    const bool live = requested < count;
+    // (0 past the run: an offset of its own must not pass a range that is empty there)
+    const uint32_t k0 = live ? (uint32_t)la.unit * kInt8TileK : 0u;
+    const uint32_t to = ring_at + stage * C::kStage;
+    const uint32_t xo = live && k0 + lk < (uint32_t)p.k ? voff : kOOB, wo = live ? voff : kOOB;
+#pragma unroll
+    for (int j = 0; j < C::kX; ++j) {
+      const uint32_t t = (uint32_t)(wave * C::kX + j);
+      to_lds(xr, to + t * 1024u, xo == kOOB ? kOOB : xo + 16u * t * (uint32_t)p.k, k0);
+    }
+#pragma unroll
+    for (int j = 0; j < C::kW; ++j) {
+      // (a range without rows takes no offset either)
+      to_lds(wr[j], to + C::kXBytes + (uint32_t)(wave * C::kW + j) * 1024u, wo, wr[j][2] ? k0 : 0u);
+    }
+    ++requested;
+    if (++la.unit == p.units) {
+      next_tile(la);
+      ranges();
+    }
+  };
+
+  i32x16 acc[2][MT];
+  auto clear = [&]() __attribute__((always_inline)) {
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int t = 0; t < MT; ++t)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) acc[j][t][e] = 0;
+  };
+  struct Half {
+    i32x4 a[MT], b[2];
+  };
+  const uint32_t swz = ((uint32_t)c >> 2) & 3u;
+  auto read = [&](uint32_t stage, int kk, Half &f) __attribute__((always_inline)) {
+    const uint8_t *at = ring + stage * C::kStage + (uint32_t)c * 64u + 16u * ((uint32_t)(2 * kk + h) ^ swz);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) f.b[j] = *(const i32x4 *)(at + C::kXBytes + (uint32_t)(wn * 64 + j * 32) * 64u);
+#pragma unroll
+    for (int t = 0; t < MT; ++t) f.a[t] = *(const i32x4 *)(at + (uint32_t)((wm * MT + t) * 32) * 64u);
+  };
+  auto multiply = [&](const Half &f) __attribute__((always_inline)) {
+#pragma unroll
+    for (int t = 0; t < MT; ++t)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) acc[j][t] = __builtin_amdgcn_mfma_i32_32x32x32_i8(f.a[t], f.b[j], acc[j][t], 0, 0, 0);
+    // a read after each of the first products
+#pragma unroll
+    for (int i = 0; i < 2 * MT; ++i) {
+      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+      if (i < MT + 2) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+    }
+  };
+
+  // element e of block t: row 32 (wm MT + t) + 8 (e / 4) + 4 h + e % 4
+  auto epilogue = [&](int tile) __attribute__((always_inline)) {
+    int rb, cg;
+    place(tile, rb, cg);
+    const int row0 = rb * C::kRows + wm * MT * 32 + 4 * h;
+#pragma unroll
+    for (int j = 0; j < (NMAT > 1 ? 1 : 2); ++j) {
+      const int col = cg * kCols + (NMAT > 1 ? wn * 32 : wn * 64 + j * 32) + c;
+      const bool in = col < p.n;
+      const Int8Scale s0 = int8_scale(in ? p.s0[col] : 0.0f);
+      const Int8Scale s1 = NMAT > 1 ? int8_scale(in ? p.s1[col] : 0.0f) : s0;
+#pragma unroll
+      for (int t = 0; t < MT; ++t)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const int r = row0 + 32 * t + 8 * (e >> 2) + (e & 3);
+          if (r >= p.m || !in) continue;
+          const Int8Scale rs = int8_scale(p.xs[r]);
+          const float v = int8_scaled(acc[j][t][e], rs, s0);
+          ((__bf16 *)p.y)[(size_t)r * p.n + col] =
+              NMAT > 1 ? swiglu_bf16(v, int8_scaled(acc[1][t][e], rs, s1)) : (__bf16)v;
+        }
+    }
+  };
+  auto piece = [&](int wg, int which) __attribute__((always_inline)) {
+    const size_t at = (size_t)(wg * 2 + which) * kWaves + wave;
+    return rsrc_uniform((const uint8_t *)p.partial + at * C::kWavePiece, C::kWavePiece);
+  };
+  auto each_part = [&](auto &&f) __attribute__((always_inline)) {
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int t = 0; t < MT; ++t)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) f(acc[j][t], q, (uint32_t)((j * MT + t) * 4 + q) * 1024u + 16u * (uint32_t)lane);
+  };
+  // the end of this run's part of a tile
+  auto flush = [&](int tile, bool whole) __attribute__((always_inline)) {
+    bool finish = whole;
+    if (!whole) {
+      const int u0 = (tile - p.whole) * p.units;
+      const int v0 = int8_run_owner(rest, nwg, u0), v1 = int8_run_owner(rest, nwg, u0 + p.units - 1);
+      const __amdgpu_buffer_rsrc_t out = piece(me, u0 <= rest_begin ? 0 : 1);
+      each_part([&](const i32x16 &v, int q, uint32_t off) __attribute__((always_inline)) {
+        st16_coherent(out, off, i32x4{v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]});
+      });
+      wait_all_memory();
+      __syncthreads();
+      if (tid == 0)
+        last_flag = __hip_atomic_fetch_add(&p.counters[v0], 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) ==
+                    (unsigned)(v1 - v0);
+      __syncthreads();
+      finish = last_flag != 0;
+      if (finish) {
+        for (int v = v0; v <= v1; ++v) {
+          if (v == me) continue;  // (still in registers)
+          const __amdgpu_buffer_rsrc_t r = piece(v, u0 <= int8_run_begin(rest, nwg, v) ? 0 : 1);
+          each_part([&](i32x16 &s, int q, uint32_t off) __attribute__((always_inline)) {
+            const i32x4 w = ld16_coherent(r, off);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[4 * q + e] += w[e];
+          });
+        }
+        if (tid == 0) __hip_atomic_store(&p.counters[v0], 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      }
+    }
+    if (finish) epilogue(tile);
+    clear();
+    // (the waits of the unit loop count transfers alone again)
+    wait_all_memory();
+  };
+
+#pragma unroll
+  for (int i = 0; i < S; ++i) request((uint32_t)i);
+  clear();
+  At at;
+  start(at);
+  int from = at.unit;
+  uint32_t stage = 0;
+  Half f0, f1;
+  wait_transfers<(S - 1) * X>();
+  ring_barrier();
+  read(0, 0, f0);
+  for (int i = 0; i < count; ++i) {
+    read(stage, 1, f1);
+    multiply(f0);
+    wait_transfers<(S - 2) * X>();
+    ring_barrier();
+    request(stage);
+    stage = stage == S - 1 ? 0 : stage + 1;
+    read(stage, 0, f0);
+    multiply(f1);
+    if (++at.unit == p.units || i == count - 1) {
+      flush(at.tile, from == 0 && at.unit == p.units);
+      next_tile(at);
+      from = at.unit;
+    }
+  }
+  wait_all_memory();
+}
+
+template <int WM, int MT>
+hipError_t launch_shape(const TileArgs &p, int shape, int nmat, int nwg, hipStream_t s) {
+  static_assert(Cfg<WM, MT>::kStages >= 3, "a ring of three units at least");
+  if (Cfg<WM, MT>::kRows != kInt8Tiles[shape].rows || Cfg<WM, MT>::kCols != kInt8Tiles[shape].cols)
+    return hipErrorInvalidValue;
+  if (nmat == 1)
+    hipLaunchKernelGGL((k_int8_tile<WM, MT, 1>), dim3(nwg), dim3(kWaves * 64), 0, s, p);
+  else
+    hipLaunchKernelGGL((k_int8_tile<WM, MT, 2>), dim3(nwg), dim3(kWaves * 64), 0, s, p);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_int8_tile(const Int8ActRef &a, int m, int k, int n, int nmat, const Int8MatRef *w, void *y,
+                            const Int8TilePlan &pl, unsigned *counters, int *partial, hipStream_t s) {
+  const TileArgs p{a.codes, a.row_scale, m, k, n, w[0].codes, nmat > 1 ? w[1].codes : nullptr, w[0].scales,
+                   nmat > 1 ? w[1].scales : nullptr, y, partial, counters, pl.row_blocks, pl.groups, pl.units, pl.whole};
+  switch (pl.shape) {
+    case 0: return launch_shape<2, 4>(p, 0, nmat, pl.nwg, s);
+    case 1: return launch_shape<4, 2>(p, 1, nmat, pl.nwg, s);
+    case 2: return launch_shape<2, 2>(p, 2, nmat, pl.nwg, s);
+    default: return launch_shape<4, 1>(p, 3, nmat, pl.nwg, s);
+  }
+}
+
+}  // namespace nvfp4

@@ -305,11 +305,14 @@ bool int8_gemv_eligible(int m, int k);
 bool int8_gemv_quantizes(int m, int k);
 hipError_t launch_int8_gemv(const void *x, const float *row_scale, int m, int k, int n, int nmat, const Int8MatRef *w,
                             void *y, hipStream_t s);
-// Any number of rows, int8.  `counters`: kInt8Counters words, zero on entry,
-// left zero; `partial`: pl.partial_bytes.
+// Up to 256 rows, int8.  `counters`: kInt8Counters words, zero on entry, left
+// zero; `partial`: pl.partial_bytes.
 constexpr int kInt8Counters = 256;
 hipError_t launch_int8_gemm(const Int8ActRef &a, int m, int k, int n, int nmat, const Int8MatRef *w, void *y,
                             const Int8Plan &pl, unsigned *counters, int *partial, hipStream_t s);
+// More rows, likewise.
+hipError_t launch_int8_tile(const Int8ActRef &a, int m, int k, int n, int nmat, const Int8MatRef *w, void *y,
+                            const Int8TilePlan &pl, unsigned *counters, int *partial, hipStream_t s);
 
 // Register-only bf16 MFMA loop (a measurement aid): `workgroups` groups of
 // four waves, each wave iters x 4 v_mfma_f32_32x32x16_bf16.  sink: 256
