@@ -54,9 +54,9 @@ struct Int8Tile {
   int rows, cols;  // (cols: half of them gate and half up, with two matrices)
   double unit;     // cost of a unit of K of one tile, in microseconds
 };
-constexpr int kInt8TileK = 64;
+constexpr int kInt8TileK = 128;
 constexpr int kInt8Shapes = 4;
-constexpr Int8Tile kInt8Tiles[kInt8Shapes] = {{256, 256, 0.70}, {256, 128, 0.42}, {128, 256, 0.42}, {128, 128, 0.26}};
+constexpr Int8Tile kInt8Tiles[kInt8Shapes] = {{256, 256, 2.0}, {256, 128, 1.3}, {128, 256, 1.3}, {128, 128, 0.75}};
 
 inline Int8TilePlan int8_tile_plan_of(int shape, bool split, int m, int n, int k, int nmat) {
   const Int8Tile t = kInt8Tiles[shape];

@@ -40,8 +40,8 @@ template <int WM, int MT>
 struct Cfg {
   static constexpr int kRows = WM * MT * 32, kCols = 8 / WM * 64;
   static constexpr uint32_t kXBytes = kRows * kInt8TileK, kStage = (kRows + kCols) * kInt8TileK;
-  static constexpr int kStages = 131072 / kStage > 8 ? 8 : 131072 / kStage;
-  static constexpr int kX = kRows / 16 / kWaves, kW = kCols / 16 / kWaves;  // transfers of a wave for a unit
+  static constexpr int kStages = (160 * 1024 - 256) / kStage;
+  static constexpr int kX = kRows / 8 / kWaves, kW = kCols / 8 / kWaves;  // transfers of a wave for a unit
   static constexpr uint32_t kWavePiece = 2u * MT * 16u * 256u;
 };
 
@@ -97,11 +97,15 @@ __global__ __launch_bounds__(kWaves * 64, 2) void k_int8_tile(TileArgs p) {
     rb = 8 * super + in - cg * high;
   };
 
-  // ---- requests: activation rows 16 t + lane / 4; weight rows 16 t + lane / 4
+  // ---- requests: activation rows 8 t + lane / 8; weight rows 8 t + lane / 8
   // of the tile's columns (with two matrices 32 of gate and 32 of up in turn)
-  const uint32_t line = (uint32_t)lane >> 2;
-  const uint32_t lk = 16u * ((lane & 3u) ^ (line >> 2));
-  const uint32_t voff = line * (uint32_t)p.k + lk;
+  const uint32_t line = (uint32_t)lane >> 3;
+  uint32_t lk[2], voff[2];  // for even and odd t
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    lk[j] = 16u * ((lane & 7u) ^ (4u * j + (line >> 1)));
+    voff[j] = line * (uint32_t)p.k + lk[j];
+  }
   At la;
   start(la);
   int requested = 0;
@@ -114,9 +118,9 @@ __global__ __launch_bounds__(kWaves * 64, 2) void k_int8_tile(TileArgs p) {
 #pragma unroll
     for (int j = 0; j < C::kW; ++j) {
       const int t = wave * C::kW + j;
-      const int at = col0 + (NMAT > 1 ? (t >> 2) * 32 + (t & 1) * 16 : 16 * t);
-      wr[j] = range_of((NMAT > 1 && (t & 2) ? p.w1 : p.w0) + (size_t)min(at, p.n) * p.k,
-                       (size_t)max(min(16, p.n - at), 0) * p.k);
+      const int at = col0 + (NMAT > 1 ? (t >> 3) * 32 + (t & 3) * 8 : 8 * t);
+      wr[j] = range_of((NMAT > 1 && (t & 4) ? p.w1 : p.w0) + (size_t)min(at, p.n) * p.k,
+                       (size_t)max(min(8, p.n - at), 0) * p.k);
     }
   };
   ranges();
@@ -125,17 +129,17 @@ __global__ __launch_bounds__(kWaves * 64, 2) void k_int8_tile(TileArgs p) {
     // (0 past the run: an offset of its own must not pass a range that is empty there)
     const uint32_t k0 = live ? (uint32_t)la.unit * kInt8TileK : 0u;
     const uint32_t to = ring_at + stage * C::kStage;
-    const uint32_t xo = live && k0 + lk < (uint32_t)p.k ? voff : kOOB, wo = live ? voff : kOOB;
 #pragma unroll
     for (int j = 0; j < C::kX; ++j) {
       const uint32_t t = (uint32_t)(wave * C::kX + j);
-      to_lds(xr, to + t * 1024u, xo == kOOB ? kOOB : xo + 16u * t * (uint32_t)p.k, k0);
+      to_lds(xr, to + t * 1024u,
+             live && k0 + lk[j & 1] < (uint32_t)p.k ? voff[j & 1] + 8u * t * (uint32_t)p.k : kOOB, k0);
     }
 #pragma unroll
-    for (int j = 0; j < C::kW; ++j) {
+    for (int j = 0; j < C::kW; ++j)
       // (a range without rows takes no offset either)
-      to_lds(wr[j], to + C::kXBytes + (uint32_t)(wave * C::kW + j) * 1024u, wo, wr[j][2] ? k0 : 0u);
-    }
+      to_lds(wr[j], to + C::kXBytes + (uint32_t)(wave * C::kW + j) * 1024u, live ? voff[j & 1] : kOOB,
+             wr[j][2] ? k0 : 0u);
     ++requested;
     if (++la.unit == p.units) {
       next_tile(la);
@@ -152,22 +156,22 @@ __global__ __launch_bounds__(kWaves * 64, 2) void k_int8_tile(TileArgs p) {
 #pragma unroll
         for (int e = 0; e < 16; ++e) acc[j][t][e] = 0;
   };
-  struct Half {
+  struct Step {
     i32x4 a[MT], b[2];
   };
-  const uint32_t swz = ((uint32_t)c >> 2) & 3u;
-  auto read = [&](uint32_t stage, int kk, Half &f) __attribute__((always_inline)) {
-    const uint8_t *at = ring + stage * C::kStage + (uint32_t)c * 64u + 16u * ((uint32_t)(2 * kk + h) ^ swz);
+  const uint32_t swz = ((uint32_t)c >> 1) & 7u;
+  auto read = [&](uint32_t stage, int kk, Step &f) __attribute__((always_inline)) {
+    const uint8_t *at = ring + stage * C::kStage + (uint32_t)c * 128u + 16u * ((uint32_t)(2 * kk + h) ^ swz);
 #pragma unroll
-    for (int j = 0; j < 2; ++j) f.b[j] = *(const i32x4 *)(at + C::kXBytes + (uint32_t)(wn * 64 + j * 32) * 64u);
+    for (int j = 0; j < 2; ++j) f.b[j] = *(const i32x4 *)(at + C::kXBytes + (uint32_t)(wn * 64 + j * 32) * 128u);
 #pragma unroll
-    for (int t = 0; t < MT; ++t) f.a[t] = *(const i32x4 *)(at + (uint32_t)((wm * MT + t) * 32) * 64u);
+    for (int t = 0; t < MT; ++t) f.a[t] = *(const i32x4 *)(at + (uint32_t)((wm * MT + t) * 32) * 128u);
   };
-  auto multiply = [&](const Half &f) __attribute__((always_inline)) {
+  auto multiply = [&](const Step &f) __attribute__((always_inline)) {
 #pragma unroll
     for (int t = 0; t < MT; ++t)
 #pragma unroll
-      for (int j = 0; j < 2; ++j) acc[j][t] = __builtin_amdgcn_mfma_i32_32x32x32_i8(f.a[t], f.b[j], acc[j][t], 0, 0, 0);
+      for (int j = 0; j < 2; ++j) acc[j][t] = __builtin_amdgcn_mfma_i32_32x32x32_i8(f.b[j], f.a[t], acc[j][t], 0, 0, 0);
     // a read after each of the first products
 #pragma unroll
     for (int i = 0; i < 2 * MT; ++i) {
@@ -176,29 +180,57 @@ __global__ __launch_bounds__(kWaves * 64, 2) void k_int8_tile(TileArgs p) {
     }
   };
 
-  // element e of block t: row 32 (wm MT + t) + 8 (e / 4) + 4 h + e % 4
+  // Element e of block (j, t): row 32 (wm MT + t) + c of the tile, column
+  // 8 (e / 4) + 4 h + e % 4 of the block's 32.
   auto epilogue = [&](int tile) __attribute__((always_inline)) {
     int rb, cg;
     place(tile, rb, cg);
-    const int row0 = rb * C::kRows + wm * MT * 32 + 4 * h;
+    const int row0 = rb * C::kRows + wm * MT * 32 + c;
+    const bool pieces = (p.n & 7) == 0;
 #pragma unroll
-    for (int j = 0; j < (NMAT > 1 ? 1 : 2); ++j) {
-      const int col = cg * kCols + (NMAT > 1 ? wn * 32 : wn * 64 + j * 32) + c;
-      const bool in = col < p.n;
-      const Int8Scale s0 = int8_scale(in ? p.s0[col] : 0.0f);
-      const Int8Scale s1 = NMAT > 1 ? int8_scale(in ? p.s1[col] : 0.0f) : s0;
+    for (int j = 0; j < (NMAT > 1 ? 1 : 2); ++j)
 #pragma unroll
-      for (int t = 0; t < MT; ++t)
+      for (int q = 0; q < 2; ++q) {  // sixteen of the block's columns: elements 8 q ..
+        const int col0 = cg * kCols + (NMAT > 1 ? wn * 32 : wn * 64 + j * 32) + 16 * q;
+        Int8Scale s0[8], s1[8];
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const int r = row0 + 32 * t + 8 * (e >> 2) + (e & 3);
-          if (r >= p.m || !in) continue;
-          const Int8Scale rs = int8_scale(p.xs[r]);
-          const float v = int8_scaled(acc[j][t][e], rs, s0);
-          ((__bf16 *)p.y)[(size_t)r * p.n + col] =
-              NMAT > 1 ? swiglu_bf16(v, int8_scaled(acc[1][t][e], rs, s1)) : (__bf16)v;
+        for (int e = 0; e < 8; ++e) {
+          const int col = min(col0 + 8 * (e >> 2) + 4 * h + (e & 3), p.n - 1);
+          s0[e] = int8_scale(p.s0[col]);
+          if (NMAT > 1) s1[e] = int8_scale(p.s1[col]);
         }
-    }
+#pragma unroll
+        for (int t = 0; t < MT; ++t) {
+          const int r = row0 + 32 * t;
+          const Int8Scale rs = int8_scale(p.xs[min(r, p.m - 1)]);
+          uint32_t v[4];  // two columns each
+#pragma unroll
+          for (int e = 0; e < 8; e += 2) {
+            bf16x2 two;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const float f = int8_scaled(acc[j][t][8 * q + e + i], rs, s0[e + i]);
+              two[i] = NMAT > 1 ? swiglu_bf16(f, int8_scaled(acc[1][t][8 * q + e + i], rs, s1[e + i])) : (__bf16)f;
+            }
+            v[e >> 1] = __builtin_bit_cast(uint32_t, two);
+          }
+          __bf16 *to = (__bf16 *)p.y + (size_t)r * p.n + col0;
+          if (pieces) {
+            // Lane (c, 0) holds columns 0..3 of either eight and lane (c, 1)
+            // columns 4..7: they trade halves, and each has a whole eight.
+            const auto lo = __builtin_amdgcn_permlane32_swap(v[0], v[2], false, false);
+            const auto hi = __builtin_amdgcn_permlane32_swap(v[1], v[3], false, false);
+            if (r < p.m && col0 + 8 * h < p.n) *(uint4 *)(to + 8 * h) = uint4{lo[0], hi[0], lo[1], hi[1]};
+          } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const int at = 8 * (e >> 2) + 4 * h + (e & 3);
+              if (r < p.m && col0 + at < p.n)
+                to[at] = __builtin_bit_cast(__bf16, (uint16_t)(e & 1 ? v[e >> 1] >> 16 : v[e >> 1]));
+            }
+          }
+        }
+      }
   };
   auto piece = [&](int wg, int which) __attribute__((always_inline)) {
     const size_t at = (size_t)(wg * 2 + which) * kWaves + wave;
@@ -255,12 +287,16 @@ __global__ __launch_bounds__(kWaves * 64, 2) void k_int8_tile(TileArgs p) {
   start(at);
   int from = at.unit;
   uint32_t stage = 0;
-  Half f0, f1;
+  Step f0, f1;
   wait_transfers<(S - 1) * X>();
   ring_barrier();
   read(0, 0, f0);
   for (int i = 0; i < count; ++i) {
     read(stage, 1, f1);
+    multiply(f0);
+    read(stage, 2, f0);
+    multiply(f1);
+    read(stage, 3, f1);
     multiply(f0);
     wait_transfers<(S - 2) * X>();
     ring_barrier();
@@ -279,7 +315,7 @@ __global__ __launch_bounds__(kWaves * 64, 2) void k_int8_tile(TileArgs p) {
 
 template <int WM, int MT>
 hipError_t launch_shape(const TileArgs &p, int shape, int nmat, int nwg, hipStream_t s) {
-  static_assert(Cfg<WM, MT>::kStages >= 3, "a ring of three units at least");
+  static_assert(Cfg<WM, MT>::kStages >= 2, "a ring of two units at least");
   if (Cfg<WM, MT>::kRows != kInt8Tiles[shape].rows || Cfg<WM, MT>::kCols != kInt8Tiles[shape].cols)
     return hipErrorInvalidValue;
   if (nmat == 1)
