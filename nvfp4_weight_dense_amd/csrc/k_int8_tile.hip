@@ -3,18 +3,21 @@
 // k_int8_gemm.hip).
 //
 // A workgroup of eight waves computes tiles of the output.  Both operands go
-// from memory straight into a ring in LDS, 64 codes of K (a unit) at a time;
-// a wave's part of a tile is MT x 2 blocks of v_mfma_i32_32x32x32_i8, for
-// which it reads MT + 2 operands of 1 KB from LDS for each half of a unit.
-// The halves alternate between two sets of registers: the reads of the next
-// half are issued before the products of this one, across units too.  The
-// barrier of a unit lies between its halves: it says that the next unit has
-// arrived for all waves, and that this unit's last operands are in registers
-// everywhere, so its place in the ring is free.
+// from memory straight into a ring in LDS, 128 codes of K (a unit) at a time,
+// as whole lines; a wave's part of a tile is MT x 2 blocks of
+// v_mfma_i32_32x32x32_i8, for which it reads MT + 2 operands of 1 KB from LDS
+// for each quarter of a unit.  The quarters alternate between two sets of
+// registers: the reads of the next are issued before the products of this
+// one, across units too.  The barrier of a unit lies before its last quarter:
+// it says that the next unit has arrived for all waves, and that this unit's
+// last operands are in registers everywhere, so its place in the ring is free.
 //
-// A row of a unit is 64 bytes, four chunks of 16; chunk q of row r is stored
-// at q ^ (r / 4 % 4), so that the rows that are read together lie in
-// different banks.
+// A row of a unit is 128 bytes, eight chunks of 16; chunk q of row r is stored
+// at q ^ (r / 2 % 8), so that the rows that are read together lie in different
+// banks.  The weights are the first operand: a lane then holds four
+// neighbouring columns of one row, and after a trade between lanes stores
+// eight of them at once.  The scales come into LDS with a tile's first unit,
+// so that a tile's end waits for no memory.
 #include "int8_common.h"
 
 namespace nvfp4 {
@@ -40,7 +43,12 @@ template <int WM, int MT>
 struct Cfg {
   static constexpr int kRows = WM * MT * 32, kCols = 8 / WM * 64;
   static constexpr uint32_t kXBytes = kRows * kInt8TileK, kStage = (kRows + kCols) * kInt8TileK;
-  static constexpr int kStages = (160 * 1024 - 256) / kStage;
+  // The scales of a tile, its rows' and then its columns', come with its first
+  // unit, 64 to a wave.  A unit is requested kStages ahead, which may be as many tiles.
+  static constexpr uint32_t kScaleBytes = kWaves * 64 * 4;
+  static constexpr int kStages = (160 * 1024 - 256) / (kStage + kScaleBytes) > 4 ? 4 : (160 * 1024 - 256) / (kStage + kScaleBytes);
+  static constexpr int kScales = kStages + 1;
+  static_assert(kRows + kCols <= kWaves * 64 && kRows % 64 == 0 && kCols / 2 % 64 == 0, "scales of a wave");
   static constexpr int kX = kRows / 8 / kWaves, kW = kCols / 8 / kWaves;  // transfers of a wave for a unit
   static constexpr uint32_t kWavePiece = 2u * MT * 16u * 256u;
 };
@@ -52,6 +60,7 @@ __global__ __launch_bounds__(kWaves * 64, 2) void k_int8_tile(TileArgs p) {
   constexpr int kCols = C::kCols / NMAT;
   static_assert(kWaves * C::kWavePiece == C::kRows * C::kCols * 4, "a piece");
   __shared__ __attribute__((aligned(1024))) uint8_t ring[S * C::kStage];
+  __shared__ __attribute__((aligned(256))) float scales[C::kScales][kWaves * 64];
   __shared__ unsigned last_flag;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -109,11 +118,21 @@ __global__ __launch_bounds__(kWaves * 64, 2) void k_int8_tile(TileArgs p) {
   At la;
   start(la);
   int requested = 0;
-  u32x4_t xr, wr[C::kW];
+  bool fresh = true;  // the next request is a tile's first
+  u32x4_t xr, wr[C::kW], sr;
+  int scale_set = 0;
+  const uint32_t scales_at = lds_address(scales) + (uint32_t)wave * 256u;
   auto ranges = [&]() __attribute__((always_inline)) {
     int rb, cg;
     place(min(la.tile, tiles - 1), rb, cg);
     const int row0 = rb * C::kRows, col0 = cg * kCols;
+    // this wave's scales: 64 rows', or 64 columns' of a matrix
+    const int at = (wave * 64 - C::kRows) & (kCols - 1);
+    const bool up = NMAT > 1 && wave * 64 >= C::kRows + kCols;
+    if (wave * 64 < C::kRows)
+      sr = range_of(p.xs + min(row0 + wave * 64, p.m), (size_t)max(min(64, p.m - row0 - wave * 64), 0) * 4);
+    else
+      sr = range_of((up ? p.s1 : p.s0) + min(col0 + at, p.n), (size_t)max(min(64, p.n - col0 - at), 0) * 4);
     xr = range_of(p.x + (size_t)row0 * p.k, (size_t)min(C::kRows, p.m - row0) * p.k);
 #pragma unroll
     for (int j = 0; j < C::kW; ++j) {
@@ -129,6 +148,11 @@ __global__ __launch_bounds__(kWaves * 64, 2) void k_int8_tile(TileArgs p) {
     // (0 past the run: an offset of its own must not pass a range that is empty there)
     const uint32_t k0 = live ? (uint32_t)la.unit * kInt8TileK : 0u;
     const uint32_t to = ring_at + stage * C::kStage;
+    if (live && fresh) {
+      words_to_lds(sr, scales_at + (uint32_t)scale_set * C::kScaleBytes, 4u * (uint32_t)lane);
+      scale_set = scale_set == C::kScales - 1 ? 0 : scale_set + 1;
+    }
+    fresh = false;
 #pragma unroll
     for (int j = 0; j < C::kX; ++j) {
       const uint32_t t = (uint32_t)(wave * C::kX + j);
@@ -144,6 +168,7 @@ __global__ __launch_bounds__(kWaves * 64, 2) void k_int8_tile(TileArgs p) {
     if (++la.unit == p.units) {
       next_tile(la);
       ranges();
+      fresh = true;
     }
   };
 
@@ -182,9 +207,11 @@ __global__ __launch_bounds__(kWaves * 64, 2) void k_int8_tile(TileArgs p) {
 
   // Element e of block (j, t): row 32 (wm MT + t) + c of the tile, column
   // 8 (e / 4) + 4 h + e % 4 of the block's 32.
+  int epilogue_set = 0;
   auto epilogue = [&](int tile) __attribute__((always_inline)) {
     int rb, cg;
     place(tile, rb, cg);
+    const float *set = scales[epilogue_set];
     const int row0 = rb * C::kRows + wm * MT * 32 + c;
     const bool pieces = (p.n & 7) == 0;
 #pragma unroll
@@ -195,14 +222,14 @@ __global__ __launch_bounds__(kWaves * 64, 2) void k_int8_tile(TileArgs p) {
         Int8Scale s0[8], s1[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          const int col = min(col0 + 8 * (e >> 2) + 4 * h + (e & 3), p.n - 1);
-          s0[e] = int8_scale(p.s0[col]);
-          if (NMAT > 1) s1[e] = int8_scale(p.s1[col]);
+          const float *col = set + C::kRows + (col0 - cg * kCols) + 8 * (e >> 2) + 4 * h + (e & 3);
+          s0[e] = int8_scale(col[0]);
+          if (NMAT > 1) s1[e] = int8_scale(col[kCols]);
         }
 #pragma unroll
         for (int t = 0; t < MT; ++t) {
           const int r = row0 + 32 * t;
-          const Int8Scale rs = int8_scale(p.xs[min(r, p.m - 1)]);
+          const Int8Scale rs = int8_scale(set[wm * MT * 32 + 32 * t + c]);
           uint32_t v[4];  // two columns each
 #pragma unroll
           for (int e = 0; e < 8; e += 2) {
@@ -275,9 +302,10 @@ __global__ __launch_bounds__(kWaves * 64, 2) void k_int8_tile(TileArgs p) {
       }
     }
     if (finish) epilogue(tile);
+    epilogue_set = epilogue_set == C::kScales - 1 ? 0 : epilogue_set + 1;
     clear();
-    // (the waits of the unit loop count transfers alone again)
-    wait_all_memory();
+    // (Memory operations end in order, so with stores among the youngest the
+    // waits of the unit loop cover more transfers than they ask for, never fewer.)
   };
 
 #pragma unroll
