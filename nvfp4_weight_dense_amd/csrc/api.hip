@@ -617,7 +617,7 @@ struct Parts {
 struct Int8Product {
   bool gemv, quantize, tiled = false;
   Int8Plan plan{};
-  Int8TilePlan tile{};
+  Int8TilePlans tile{};
   size_t codes = 0, scales = 0, partial = 0, bytes = 0;
   Int8Product(bool own_rows, int m, int n, int k, int nmat) {
     gemv = int8_gemv_eligible(m, k) && (own_rows || int8_gemv_quantizes(m, k));
@@ -628,7 +628,7 @@ struct Int8Product {
       tiled = m > 256;
       if (tiled) tile = int8_tile_plan(m, n, k, nmat);
       else plan = int8_plan(m, n, k, nmat);
-      partial = at.take(tiled ? tile.partial_bytes : plan.partial_bytes);
+      partial = at.take(tiled ? int8_tile_partial_bytes(tile) : plan.partial_bytes);
     }
     bytes = at.bytes;
   }

@@ -45,23 +45,31 @@ inline Int8Plan int8_plan(int m, int n, int k, int nmat) {
 // cut along K into equal runs over all workgroups, as above.
 struct Int8TilePlan {
   int shape;           // of a tile: kInt8Tiles[shape]
+  int columns;         // of the output, from the first that is not planned before
   int row_blocks, groups, units;  // tiles along rows and columns, units of K
   int nwg;
   int whole;           // tiles that go whole, the first ones
   size_t partial_bytes;
 };
+// What a round of tiles costs, and a split of one, in microseconds (measured
+// at K of 4096 to 17408): a unit of K, the rest of a tile (its first unit's
+// way from memory, its end), and the pieces' way to the workgroup that joins
+// them.
 struct Int8Tile {
   int rows, cols;  // (cols: half of them gate and half up, with two matrices)
-  double unit;     // cost of a unit of K of one tile, in microseconds
+  double unit, tile, join;
 };
 constexpr int kInt8TileK = 128;
 constexpr int kInt8Shapes = 4;
-constexpr Int8Tile kInt8Tiles[kInt8Shapes] = {{256, 256, 2.0}, {256, 128, 1.3}, {128, 256, 1.3}, {128, 128, 0.75}};
+constexpr Int8Tile kInt8Tiles[kInt8Shapes] = {
+    {256, 256, 1.75, 7.3, 55}, {256, 128, 0.95, 6.9, 25}, {128, 256, 0.96, 6.1, 25}, {128, 128, 0.53, 6.4, 12}};
+constexpr double kInt8Launch = 4;  // one more launch
 
 inline Int8TilePlan int8_tile_plan_of(int shape, bool split, int m, int n, int k, int nmat) {
   const Int8Tile t = kInt8Tiles[shape];
   Int8TilePlan p{};
   p.shape = shape;
+  p.columns = n;
   p.row_blocks = (m + t.rows - 1) / t.rows;
   p.groups = (n + t.cols / nmat - 1) / (t.cols / nmat);
   p.units = (k + kInt8TileK - 1) / kInt8TileK;
@@ -76,22 +84,52 @@ inline Int8TilePlan int8_tile_plan_of(int shape, bool split, int m, int n, int k
   p.partial_bytes = rest ? (size_t)p.nwg * 2 * t.rows * t.cols * 4 : 0;
   return p;
 }
+inline double int8_tile_cost(const Int8TilePlan &p) {
+  const Int8Tile t = kInt8Tiles[p.shape];
+  const int64_t rest = (int64_t)p.row_blocks * p.groups - p.whole;
+  double cost = (double)((p.whole + p.nwg - 1) / p.nwg) * (p.units * t.unit + t.tile);
+  if (rest) cost += (double)rest * p.units / p.nwg * t.unit + t.tile + t.join;
+  return cost;
+}
 
-// The shape, and whether to split, by what they cost: units that the busiest
-// workgroup does, and for a split the pieces that are written and read again.
-inline Int8TilePlan int8_tile_plan(int m, int n, int k, int nmat) {
-  Int8TilePlan best{};
+// One launch, or two: whole rounds of tiles of one shape for the first
+// columns, and the others in a shape (and split) of their own.
+struct Int8TilePlans {
+  int count;
+  Int8TilePlan part[2];
+};
+inline Int8TilePlans int8_tile_plan(int m, int n, int k, int nmat) {
+  Int8TilePlans best{};
   double least = 0;
-  for (int shape = 0; shape < kInt8Shapes; ++shape)
-    for (int split = 0; split < 2; ++split) {
-      const Int8TilePlan p = int8_tile_plan_of(shape, split, m, n, k, nmat);
-      const Int8Tile t = kInt8Tiles[shape];
-      const int64_t rest = (int64_t)p.row_blocks * p.groups - p.whole;
-      double cost = (double)((p.whole + p.nwg - 1) / p.nwg) * p.units * t.unit;
-      if (rest) cost += (double)rest * p.units / p.nwg * t.unit + 4.0 + 20.0 * t.rows * t.cols / 65536;
-      if ((shape == 0 && !split) || cost < least) best = p, least = cost;
-    }
+  auto one = [&](int columns, double *cost) {
+    Int8TilePlan p{};
+    for (int shape = 0; shape < kInt8Shapes; ++shape)
+      for (int split = 0; split < 2; ++split) {
+        const Int8TilePlan q = int8_tile_plan_of(shape, split, m, columns, k, nmat);
+        const double c = int8_tile_cost(q);
+        if ((shape == 0 && !split) || c < *cost) p = q, *cost = c;
+      }
+    return p;
+  };
+  best.count = 1;
+  best.part[0] = one(n, &least);
+  for (int shape = 0; shape < kInt8Shapes; ++shape) {
+    const Int8TilePlan all = int8_tile_plan_of(shape, false, m, n, k, nmat);
+    const int64_t tiles = (int64_t)all.row_blocks * all.groups, rounds = tiles / kInt8MaxWG;
+    const int64_t groups = rounds * kInt8MaxWG / all.row_blocks;
+    if (groups == 0 || groups >= all.groups) continue;
+    const int columns = (int)groups * (kInt8Tiles[shape].cols / nmat);
+    const Int8TilePlan first = int8_tile_plan_of(shape, false, m, columns, k, nmat);
+    double cost = 0;
+    const Int8TilePlan second = one(n - columns, &cost);
+    cost += int8_tile_cost(first) + kInt8Launch;
+    if (cost < least) least = cost, best.count = 2, best.part[0] = first, best.part[1] = second;
+  }
   return best;
+}
+inline size_t int8_tile_partial_bytes(const Int8TilePlans &p) {
+  const size_t a = p.part[0].partial_bytes, b = p.count > 1 ? p.part[1].partial_bytes : 0;
+  return a > b ? a : b;
 }
 
 // No plan for m rows or fewer has more partial sums than these.

@@ -33,6 +33,7 @@ struct TileArgs {
   const int8_t *w0, *w1;
   const float *s0, *s1;
   void *y;
+  int ldy;             // columns of y, of which this launch's are the first n
   int *partial;        // [nwg][2][8 waves][2 MT][4][64 lanes][4]
   unsigned *counters;  // [nwg], zero between calls
   int row_blocks, groups, units, whole;
@@ -213,7 +214,7 @@ __global__ __launch_bounds__(kWaves * 64, 2) void k_int8_tile(TileArgs p) {
     place(tile, rb, cg);
     const float *set = scales[epilogue_set];
     const int row0 = rb * C::kRows + wm * MT * 32 + c;
-    const bool pieces = (p.n & 7) == 0;
+    const bool pieces = (p.ldy & 7) == 0;
 #pragma unroll
     for (int j = 0; j < (NMAT > 1 ? 1 : 2); ++j)
 #pragma unroll
@@ -241,7 +242,7 @@ __global__ __launch_bounds__(kWaves * 64, 2) void k_int8_tile(TileArgs p) {
             }
             v[e >> 1] = __builtin_bit_cast(uint32_t, two);
           }
-          __bf16 *to = (__bf16 *)p.y + (size_t)r * p.n + col0;
+          __bf16 *to = (__bf16 *)p.y + (size_t)r * p.ldy + col0;
           if (pieces) {
             // Lane (c, 0) holds columns 0..3 of either eight and lane (c, 1)
             // columns 4..7: they trade halves, and each has a whole eight.
@@ -356,15 +357,25 @@ hipError_t launch_shape(const TileArgs &p, int shape, int nmat, int nwg, hipStre
 }  // namespace
 
 hipError_t launch_int8_tile(const Int8ActRef &a, int m, int k, int n, int nmat, const Int8MatRef *w, void *y,
-                            const Int8TilePlan &pl, unsigned *counters, int *partial, hipStream_t s) {
-  const TileArgs p{a.codes, a.row_scale, m, k, n, w[0].codes, nmat > 1 ? w[1].codes : nullptr, w[0].scales,
-                   nmat > 1 ? w[1].scales : nullptr, y, partial, counters, pl.row_blocks, pl.groups, pl.units, pl.whole};
-  switch (pl.shape) {
-    case 0: return launch_shape<2, 4>(p, 0, nmat, pl.nwg, s);
-    case 1: return launch_shape<4, 2>(p, 1, nmat, pl.nwg, s);
-    case 2: return launch_shape<2, 2>(p, 2, nmat, pl.nwg, s);
-    default: return launch_shape<4, 1>(p, 3, nmat, pl.nwg, s);
+                            const Int8TilePlans &pl, unsigned *counters, int *partial, hipStream_t s) {
+  int col0 = 0;
+  for (int i = 0; i < pl.count; ++i) {
+    const Int8TilePlan &q = pl.part[i];
+    auto codes = [&](int j) { return w[j].codes + (size_t)col0 * k; };
+    const TileArgs p{a.codes, a.row_scale, m, k, q.columns, codes(0), nmat > 1 ? codes(1) : nullptr, w[0].scales + col0,
+                     nmat > 1 ? w[1].scales + col0 : nullptr, (__bf16 *)y + col0, n, partial, counters, q.row_blocks,
+                     q.groups, q.units, q.whole};
+    hipError_t e;
+    switch (q.shape) {
+      case 0: e = launch_shape<2, 4>(p, 0, nmat, q.nwg, s); break;
+      case 1: e = launch_shape<4, 2>(p, 1, nmat, q.nwg, s); break;
+      case 2: e = launch_shape<2, 2>(p, 2, nmat, q.nwg, s); break;
+      default: e = launch_shape<4, 1>(p, 3, nmat, q.nwg, s); break;
+    }
+    if (e != hipSuccess) return e;
+    col0 += q.columns;
   }
+  return hipSuccess;
 }
 
 }  // namespace nvfp4

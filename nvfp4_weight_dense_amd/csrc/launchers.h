@@ -312,7 +312,7 @@ hipError_t launch_int8_gemm(const Int8ActRef &a, int m, int k, int n, int nmat, 
                             const Int8Plan &pl, unsigned *counters, int *partial, hipStream_t s);
 // More rows, likewise.
 hipError_t launch_int8_tile(const Int8ActRef &a, int m, int k, int n, int nmat, const Int8MatRef *w, void *y,
-                            const Int8TilePlan &pl, unsigned *counters, int *partial, hipStream_t s);
+                            const Int8TilePlans &pl, unsigned *counters, int *partial, hipStream_t s);
 
 // Register-only bf16 MFMA loop (a measurement aid): `workgroups` groups of
 // four waves, each wave iters x 4 v_mfma_f32_32x32x16_bf16.  sink: 256

@@ -84,7 +84,7 @@ static void tiles(const Int8TilePlan &p, int m, int n, int k, int nmat) {
 static void bound(int few, int many, int n, int k, int nmat) {
   if (few > many) return;
   const size_t most = int8_partial_bound(many, n, k, nmat);
-  const size_t need = few <= 256 ? int8_plan(few, n, k, nmat).partial_bytes : int8_tile_plan(few, n, k, nmat).partial_bytes;
+  const size_t need = few <= 256 ? int8_plan(few, n, k, nmat).partial_bytes : int8_tile_partial_bytes(int8_tile_plan(few, n, k, nmat));
   CHECK(need <= most, "m %d of %d, n %d k %d: %zu of %zu", few, many, n, k, need, most);
   CHECK(int8_partial_bound(few, n, k, nmat) <= most, "bound of m %d and %d", few, many);
 }
@@ -102,7 +102,15 @@ int main(int argc, char **argv) {
     const int n = pick(1 << 17), k = 32 * pick(4096), nmat = 1 + rand() % 2;
     ring(1 + rand() % 256, n, k, nmat);
     const int m = 257 + pick(1 << 15);
-    tiles(int8_tile_plan(m, n, k, nmat), m, n, k, nmat);
+    const Int8TilePlans two = int8_tile_plan(m, n, k, nmat);
+    int columns = 0;
+    for (int j = 0; j < two.count; ++j) {
+      // (a second launch's first column starts 16 bytes of y, and a whole group of columns)
+      if (columns % 64) ++bad, printf("column %d\n", columns);
+      tiles(two.part[j], m, two.part[j].columns, k, nmat);
+      columns += two.part[j].columns;
+    }
+    if (columns != n || two.count < 1 || two.count > 2) ++bad, printf("columns %d of %d\n", columns, n);
     const int shape = rand() % kInt8Shapes;
     tiles(int8_tile_plan_of(shape, true, m, n, k, nmat), m, n, k, nmat);
     tiles(int8_tile_plan_of(shape, false, m, n, k, nmat), m, n, k, nmat);
