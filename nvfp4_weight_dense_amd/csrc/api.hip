@@ -625,7 +625,7 @@ struct Int8Product {
     Parts at;
     if (quantize) codes = at.take((size_t)m * k), scales = at.take((size_t)m * 4);
     if (!gemv) {
-      tiled = m > 256;
+      tiled = m > kInt8RingRows;
       if (tiled) tile = int8_tile_plan(m, n, k, nmat);
       else plan = int8_plan(m, n, k, nmat);
       partial = at.take(tiled ? int8_tile_partial_bytes(tile) : plan.partial_bytes);

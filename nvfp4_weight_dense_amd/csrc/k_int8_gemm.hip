@@ -1,28 +1,31 @@
-// k_int8_gemm.hip -- the int8 projection (gfx950) up to 256 rows a pass,
-// bound by reading the weight once:
+// k_int8_gemm.hip -- the int8 projection of up to 64 rows (gfx950), bound by
+// reading the weight once:
 //
 //   y[r][c] = bf16( s_row[r] * s_col[c] * sum_k x[r][k] * w[c][k] )
 //
 // The sum is of whole numbers, |x| <= 127 and |w| <= 128, below 2^31 for the
 // k that are allowed: every order of summation gives the same bits, so a
-// row's result does not depend on the rows beside it or on how K is split,
-// and K is split wherever that fills the CUs.
+// row's result does not depend on the rows beside it or on how K is split.
 //
-// One workgroup of eight waves per CU walks an equal run of (column group,
-// K unit) pairs (int8_plan.h).  A unit is 128 codes of 128 weight rows and of
-// every activation row: whole 128-byte lines, moved from memory straight into
-// a ring in LDS by 16-byte lanes, as many units ahead as LDS holds (two
-// thirds of it are weights under way; registers hold none).  One barrier a
-// unit: it says that a unit has arrived for all waves and that the one before
-// it has been read by all, so its place is free for the unit that is
-// requested next.
+// A workgroup of eight waves computes groups of P slots of columns (32 of one
+// matrix, or 16 of gate and the same 16 of up): a part of K of one that is
+// split, then whole ones; P and the parts are chosen so that the CUs have
+// equal work (int8_plan.h).  A part's sums are left in memory before the whole
+// groups, and are joined behind them by the last of the parts' workgroups, so
+// nothing waits for them on the way.  K goes by units of 128: the weight
+// rows and all activation rows of a unit, whole lines, are moved from memory
+// straight into a ring in LDS that holds as many units as fit, all but the
+// one in work under way.  One barrier a unit: it says that the next unit has
+// arrived for all waves and that the last operands of this one are in
+// registers everywhere, so its place in the ring is free.  Half a unit's
+// operands are read while the half before is multiplied: read, multiplied and
+// only then waited for, a unit took 0.5 us whatever its bytes.
 //
-// Wave (s, h) = (wave % 4, wave / 4) owns columns 32 s .. of the group -- or
-// gate and up columns 16 s .. -- for half of the rows, or with one row tile
-// for half of each unit's K.  Operands are read from LDS in 16-byte lanes
-// (v_mfma_i32_16x16x64_i8: lane (c, g) holds row c, K 16 g ..); the eight
-// chunks of a line are stored at chunk ^ (row / 2 % 8), so that the sixteen
-// rows of a read lie in different banks.
+// Wave s < P multiplies slot s with all rows (v_mfma_i32_16x16x64_i8, operands
+// from LDS in 16-byte lanes: lane (c, g) reads row c, K 16 g ..); it is idle
+// most of the time.  Chunk q of a line of row r is stored at q ^ (r / 2 % 8),
+// so that the sixteen rows of a read lie in different banks.  The weights are
+// the first operand: a lane then holds four neighbouring columns of one row.
 #include "int8_common.h"
 
 namespace nvfp4 {
@@ -30,7 +33,6 @@ namespace nvfp4 {
 namespace {
 
 constexpr int kWaves = 8;
-constexpr uint32_t kWeightBytes = kInt8GroupCols * kInt8UnitK;
 
 struct Int8Args {
   const int8_t *x;  // [m][k]
@@ -39,243 +41,312 @@ struct Int8Args {
   const int8_t *w0, *w1;  // gate and up, or the matrix and null
   const float *s0, *s1;
   void *y;
-  int *partial;        // [nwg][2][waves with sums][2 kTiles][64 lanes][4]
-  unsigned *counters;  // [nwg], zero between calls
-  int units, all, nwg; // units of a group, pairs in all, workgroups
+  int *partial;        // [split group][part][P waves][2 MT][64 lanes][4]
+  unsigned *counters;  // [split group], zero between calls
+  int groups, units, whole, parts;
 };
 
-// MT: 16-row tiles of the workgroup
-template <int MT>
+// MT: 16-row tiles; P: slots
+template <int MT, int P>
 struct Cfg {
-  static constexpr uint32_t kStage = kWeightBytes + 2048u * MT;
-  static constexpr int kStages = MT == 1 ? 8 : MT == 2 ? 7 : MT == 4 ? 6 : MT == 8 ? 4 : 3;
-  static constexpr bool kSplitK = MT == 1;          // the wave halves: of K, else of the rows
-  static constexpr int kTiles = kSplitK ? 1 : MT / 2;  // row tiles of a wave
-  // transfers of a wave for a unit: two of weights, and of the 2 MT of
-  // activations that many, for waves below kXWaves
-  static constexpr int kX = MT >= 4 ? MT / 4 : 1;
-  static constexpr int kXWaves = MT >= 4 ? kWaves : 2 * MT;
-  // a piece of a split group: what each wave (of a split K: of half 0) holds
-  static constexpr uint32_t kWavePiece = 2u * kTiles * 1024u;
-  static constexpr int kPieceWaves = kSplitK ? 4 : kWaves;
+  static constexpr uint32_t kWeights = 32u * P * kInt8UnitK;  // bytes of a unit
+  static constexpr uint32_t kStage = kWeights + 16u * MT * kInt8UnitK;
+  // transfers of a wave for a unit: of weights, eight rows each, wave, wave +
+  // 8, .. of 4 P, and one of the 2 MT of activations (those past the last go
+  // nowhere: all waves count alike)
+  static constexpr int kW = (P + 1) / 2, kX = kW + 1;
+  // The scales of a group come with its first unit, 64 to a wave: rows,
+  // columns.  A unit is requested kStages ahead, which may be as many
+  // groups; a part's stay until its end, in a set of their own.
+  static constexpr uint32_t kScaleBytes = 5 * 64 * 4;
+  static constexpr int kFit = (160 * 1024 - 1024 - 256 - 2 * kScaleBytes) / (kStage + kScaleBytes);
+  static constexpr int kStages = kFit > 16 ? 16 : kFit;
+  static constexpr int kScales = kStages + 2;
+  static constexpr uint32_t kWavePiece = 2u * MT * 1024u;
+  static_assert(kStages >= 3, "a ring of three units at least");
 };
 
-template <int MT, int NMAT>
+template <int MT, int P, int NMAT>
 __global__ __launch_bounds__(kWaves * 64, 2) void k_int8_gemm(Int8Args p) {
-  typedef Cfg<MT> C;
-  constexpr int T = C::kTiles, S = C::kStages;
-  constexpr int kCols = kInt8GroupCols / NMAT;
-  static_assert(C::kPieceWaves * C::kWavePiece == kInt8GroupCols * 16 * MT * 4, "int8_piece_bytes");
+  typedef Cfg<MT, P> C;
+  constexpr int S = C::kStages, kCols = 32 * P / NMAT;
+  static_assert(P * C::kWavePiece == int8_piece_bytes(MT, P), "a piece");
   __shared__ __attribute__((aligned(1024))) uint8_t ring[S * C::kStage];
-  __shared__ i32x4 halves[C::kSplitK ? 4 * 2 * 64 : 1];
+  __shared__ __attribute__((aligned(1024))) uint8_t nowhere[1024];
+  __shared__ __attribute__((aligned(256))) float scales[C::kScales][C::kScaleBytes / 4];
   __shared__ unsigned last_flag;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int slot = wave & 3, half = wave >> 2;
   const int c = lane & 15, g = lane >> 4;
-  const int me = (int)blockIdx.x;
-  const int begin = int8_run_begin(p.all, p.nwg, me), count = int8_run_begin(p.all, p.nwg, me + 1) - begin;
-  const uint32_t ring_at = lds_address(ring);
+  const uint32_t ring_at = lds_address(ring), nowhere_at = lds_address(nowhere);
 
-  // ---- requests: weight rows 16 wave + 8 j + lane / 8 of the group (gate for
-  // waves 0..3 and up for the others, with two matrices), activation rows
-  // 8 t + lane / 8
-  const uint32_t line = (uint32_t)lane >> 3;
-  uint32_t wvoff[2], xvoff[C::kX], xk[C::kX];
-  const uint32_t wrow = NMAT > 1 ? 16u * (uint32_t)(wave & 3) : 16u * (uint32_t)wave;
-#pragma unroll
-  for (int j = 0; j < 2; ++j)
-    wvoff[j] = (wrow + 8u * j + line) * (uint32_t)p.k + 16u * ((lane & 7u) ^ (4u * j + (line >> 1)));
-#pragma unroll
-  for (int j = 0; j < C::kX; ++j) {
-    const uint32_t t = (uint32_t)(wave * C::kX + j);
-    xk[j] = 16u * ((lane & 7u) ^ (4u * (t & 1u) + (line >> 1)));
-    xvoff[j] = (8u * t + line) * (uint32_t)p.k + xk[j];
-  }
-  const u32x4_t xr = range_of(p.x, (size_t)p.m * p.k);
-  const int8_t *wmat = NMAT > 1 && wave >= 4 ? p.w1 : p.w0;
-  int lgroup = begin / p.units, lunit = begin - lgroup * p.units, requested = 0;
-  u32x4_t wr;
-  auto group_range = [&]() __attribute__((always_inline)) {
-    const int at = lgroup * kCols;
-    wr = range_of(wmat + (size_t)at * p.k, (size_t)max(min(kCols, p.n - at), 0) * p.k);
+  // ---- this workgroup's work: pair `me` of the split groups and their parts,
+  // numbered part by part, then whole groups me, me + nwg, ..
+  const int me = (int)blockIdx.x, nwg = (int)gridDim.x, split = p.groups - p.whole, pairs = split * p.parts;
+  const bool has_part = me < pairs;
+  const int part = has_part ? me / split : 0, part_group = p.whole + me - part * split;
+  const int part_begin = p.units * part / p.parts, part_end = p.units * (part + 1) / p.parts;
+  const int mine = me < p.whole ? (p.whole - me + nwg - 1) / nwg : 0;
+  const int count = (has_part ? part_end - part_begin : 0) + mine * p.units;
+  struct At {
+    int group, unit, end, scales;
   };
-  group_range();
+  auto start = [&](At &a) __attribute__((always_inline)) {
+    if (has_part) a = At{part_group, part_begin, part_end, 0};
+    else a = At{me, 0, p.units, 1};
+  };
+  auto next = [&](At &a) __attribute__((always_inline)) {
+    a.group = a.scales == 0 ? me : a.group + nwg;
+    a.unit = 0, a.end = p.units;
+    a.scales = a.scales == C::kScales - 1 ? 1 : a.scales + 1;
+    if (a.group >= p.whole) a.group = 0;  // (past the work: not used)
+  };
+
+  // ---- requests: row 8 t + lane / 8 of transfer t, of the group's weights
+  // (with two matrices the gate's rows first) and of the activations
+  const uint32_t line = (uint32_t)lane >> 3;
+  // (t is wave + 8 j: its row's swizzle goes by wave alone)
+  const uint32_t lk = 16u * ((lane & 7u) ^ (4u * (wave & 1u) + (line >> 1)));
+  const uint32_t voff = line * (uint32_t)p.k + lk;
+  At la;
+  start(la);
+  int requested = 0;
+  bool fresh = true;  // the next request is a group's first
+  u32x4_t wr[C::kW], sr;
+  const u32x4_t xr = range_of(p.x + (size_t)min(8 * wave, p.m) * p.k, (size_t)max(min(8, p.m - 8 * wave), 0) * p.k);
+  const uint32_t scales_at = wave < 5 ? lds_address(scales) + (uint32_t)wave * 256u : nowhere_at;
+  auto ranges = [&]() __attribute__((always_inline)) {
+    const int col0 = la.group * kCols;
+#pragma unroll
+    for (int j = 0; j < C::kW; ++j) {
+      const int row = 8 * (wave + 8 * j);
+      const bool up = NMAT > 1 && row >= kCols;
+      const int at = col0 + (up ? row - kCols : row);
+      wr[j] = range_of((up ? p.w1 : p.w0) + (size_t)min(at, p.n) * p.k,
+                       (size_t)(row < 32 * P ? max(min(8, p.n - at), 0) : 0) * p.k);
+    }
+    // wave 0: the rows' scales; waves 1 .. 4: 64 columns' each, or with two
+    // matrices waves 1 and 2 the gate's and 3 and 4 the up's
+    const int at = col0 + 64 * (NMAT > 1 ? (wave - 1) & 1 : wave - 1);
+    if (wave == 0) sr = range_of(p.xs, (size_t)p.m * 4);
+    else
+      sr = range_of((NMAT > 1 && wave > 2 ? p.s1 : p.s0) + min(at, p.n),
+                    (size_t)(wave < 5 ? max(min(64, p.n - at), 0) : 0) * 4);
+  };
+  ranges();
   auto request = [&](uint32_t stage) __attribute__((always_inline)) {
     const bool live = requested < count;
-    // (0 past the run: an offset of its own must not pass a range that is empty there)
-    const uint32_t k0 = live ? (uint32_t)lunit * kInt8UnitK : 0u;
+    const uint32_t k0 = live ? (uint32_t)la.unit * kInt8UnitK : 0u;
     const uint32_t to = ring_at + stage * C::kStage;
-#pragma unroll
-    for (int j = 0; j < 2; ++j) to_lds(wr, to + (uint32_t)(wave * 2 + j) * 1024u, live ? wvoff[j] : kOOB, k0);
-    if (wave < C::kXWaves) {
-#pragma unroll
-      for (int j = 0; j < C::kX; ++j)
-        to_lds(xr, to + kWeightBytes + (uint32_t)(wave * C::kX + j) * 1024u,
-               live && k0 + xk[j] < (uint32_t)p.k ? xvoff[j] : kOOB, k0);
+    if (live && fresh) {
+      words_to_lds(sr, scales_at + (wave < 5 ? (uint32_t)la.scales * C::kScaleBytes : 0u), 4u * (uint32_t)lane);
     }
+    fresh = false;
+#pragma unroll
+    for (int j = 0; j < C::kW; ++j) {
+      const int t = wave + 8 * j;
+      // (a range without rows takes no offset either)
+      to_lds(wr[j], t < 4 * P ? to + (uint32_t)t * 1024u : nowhere_at, live ? voff : kOOB, wr[j][2] ? k0 : 0u);
+    }
+    to_lds(xr, wave < 2 * MT ? to + C::kWeights + (uint32_t)wave * 1024u : nowhere_at,
+           live && wave < 2 * MT && k0 + lk < (uint32_t)p.k ? voff : kOOB, xr[2] ? k0 : 0u);
     ++requested;
-    if (++lunit == p.units) {
-      lunit = 0, ++lgroup;
-      group_range();
+    if (++la.unit == la.end) {
+      next(la);
+      ranges();
+      fresh = true;
     }
   };
 
-  i32x4 acc[2][T] = {};
-  // operands of a unit: column tile j at weight rows 64 j + 16 slot or
-  // 32 slot + 16 j, K chunk 4 kk + g
-  const uint32_t swz = ((uint32_t)c >> 1) & 7u;
-  auto compute = [&](uint32_t stage) __attribute__((always_inline)) {
-    const uint8_t *at = ring + stage * C::kStage;
-    constexpr int kSteps = C::kSplitK ? 1 : 2;
-#pragma unroll
-    for (int kk = 0; kk < kSteps; ++kk) {
-      const uint32_t chunk = 16u * (((uint32_t)((C::kSplitK ? half : kk) * 4 + g)) ^ swz);
-      i32x4 b[2];
-#pragma unroll
-      for (int j = 0; j < 2; ++j)
-        b[j] = *(const i32x4 *)(at + (uint32_t)((NMAT > 1 ? 64 * j + 16 * slot : 32 * slot + 16 * j) + c) * 128u + chunk);
-#pragma unroll
-      for (int t = 0; t < T; ++t) {
-        const int row = 16 * ((C::kSplitK ? 0 : half * T) + t) + c;
-        const i32x4 a = *(const i32x4 *)(at + kWeightBytes + (uint32_t)row * 128u + chunk);
-#pragma unroll
-        for (int j = 0; j < 2; ++j) acc[j][t] = __builtin_amdgcn_mfma_i32_16x16x64_i8(a, b[j], acc[j][t], 0, 0, 0);
-      }
-    }
-  };
-
-  // element e of row tile t: row 16 (half T + t) + 4 g + e
-  auto epilogue = [&](int group) __attribute__((always_inline)) {
-    const int row0 = C::kSplitK ? 0 : 16 * half * T;
-    if (C::kSplitK && half) return;
-#pragma unroll
-    for (int j = 0; j < (NMAT > 1 ? 1 : 2); ++j) {
-      const int col = group * kCols + (NMAT > 1 ? 16 * slot : 32 * slot + 16 * j) + c;
-      const bool in = col < p.n;
-      const Int8Scale s0 = int8_scale(in ? p.s0[col] : 0.0f);
-      const Int8Scale s1 = NMAT > 1 ? int8_scale(in ? p.s1[col] : 0.0f) : s0;
-#pragma unroll
-      for (int t = 0; t < T; ++t)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int r = row0 + 16 * t + 4 * g + e;
-          if (r >= p.m || !in) continue;
-          const Int8Scale rs = int8_scale(p.xs[r]);
-          const float v = int8_scaled(acc[j][t][e], rs, s0);
-          ((__bf16 *)p.y)[(size_t)r * p.n + col] =
-              NMAT > 1 ? swiglu_bf16(v, int8_scaled(acc[1][t][e], rs, s1)) : (__bf16)v;
-        }
-    }
-  };
-  auto piece = [&](int wg, int which) __attribute__((always_inline)) {
-    const size_t at = (size_t)(wg * 2 + which) * C::kPieceWaves + (C::kSplitK ? slot : wave);
-    return rsrc_uniform((const uint8_t *)p.partial + at * C::kWavePiece, C::kWavePiece);
-  };
-  // the end of this run's part of a group
-  auto flush = [&](int group, bool whole) __attribute__((always_inline)) {
-    if constexpr (C::kSplitK) {
-      if (half) {
-#pragma unroll
-        for (int j = 0; j < 2; ++j) halves[(slot * 2 + j) * 64 + lane] = acc[j][0];
-      }
-      lds_barrier();
-      if (!half) {
-#pragma unroll
-        for (int j = 0; j < 2; ++j) acc[j][0] += halves[(slot * 2 + j) * 64 + lane];
-      }
-    }
-    if (whole) {
-      epilogue(group);
-    } else {
-      const int v0 = int8_run_owner(p.all, p.nwg, group * p.units);
-      const int v1 = int8_run_owner(p.all, p.nwg, group * p.units + p.units - 1);
-      const __amdgpu_buffer_rsrc_t mine = piece(me, group == begin / p.units ? 0 : 1);
-      if (!C::kSplitK || !half) {
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-#pragma unroll
-          for (int t = 0; t < T; ++t) st16_coherent(mine, (uint32_t)(j * T + t) * 1024u + 16u * lane, acc[j][t]);
-      }
-      wait_all_memory();
-      __syncthreads();
-      if (tid == 0)
-        last_flag = __hip_atomic_fetch_add(&p.counters[v0], 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) ==
-                    (unsigned)(v1 - v0);
-      __syncthreads();
-      if (last_flag) {
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-#pragma unroll
-          for (int t = 0; t < T; ++t) acc[j][t] = i32x4{0, 0, 0, 0};
-        for (int v = v0; v <= v1; ++v) {
-          const __amdgpu_buffer_rsrc_t r = piece(v, group == int8_run_begin(p.all, p.nwg, v) / p.units ? 0 : 1);
-#pragma unroll
-          for (int j = 0; j < 2; ++j)
-#pragma unroll
-            for (int t = 0; t < T; ++t) acc[j][t] += ld16_coherent(r, (uint32_t)(j * T + t) * 1024u + 16u * lane);
-        }
-        epilogue(group);
-        if (tid == 0) __hip_atomic_store(&p.counters[v0], 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-      }
-    }
+  i32x4 acc[2][MT];
+  auto clear = [&]() __attribute__((always_inline)) {
 #pragma unroll
     for (int j = 0; j < 2; ++j)
 #pragma unroll
-      for (int t = 0; t < T; ++t) acc[j][t] = i32x4{0, 0, 0, 0};
-    // (the waits of the unit loop count transfers alone again)
-    wait_all_memory();
+      for (int t = 0; t < MT; ++t) acc[j][t] = i32x4{0, 0, 0, 0};
+  };
+  clear();
+  // Operands of half a unit; column tile j of slot `wave` is weight rows
+  // 32 wave + 16 j, or of gate and of up 16 wave.
+  struct Half {
+    i32x4 a[MT], b[2];
+  };
+  const uint32_t swz = ((uint32_t)c >> 1) & 7u;
+  auto read = [&](uint32_t stage, int kk, Half &f) __attribute__((always_inline)) {
+    const uint8_t *at = ring + stage * C::kStage + (uint32_t)c * 128u + 16u * ((uint32_t)(kk * 4 + g) ^ swz);
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+      f.b[j] = *(const i32x4 *)(at + (uint32_t)(NMAT > 1 ? kCols * j + 16 * wave : 32 * wave + 16 * j) * 128u);
+#pragma unroll
+    for (int t = 0; t < MT; ++t) f.a[t] = *(const i32x4 *)(at + C::kWeights + (uint32_t)(16 * t) * 128u);
+  };
+  auto multiply = [&](const Half &f) __attribute__((always_inline)) {
+#pragma unroll
+    for (int t = 0; t < MT; ++t)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) acc[j][t] = __builtin_amdgcn_mfma_i32_16x16x64_i8(f.b[j], f.a[t], acc[j][t], 0, 0, 0);
+  };
+
+  // element e of tile (j, t): row 16 t + c, column 4 g + e of the tile
+  auto epilogue = [&](int group, int scale_set) __attribute__((always_inline)) {
+    const float *set = scales[scale_set];
+#pragma unroll
+    for (int j = 0; j < (NMAT > 1 ? 1 : 2); ++j) {
+      const int in = (NMAT > 1 ? 16 * wave : 32 * wave + 16 * j) + 4 * g, col = group * kCols + in;
+      Int8Scale s0[4], s1[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        s0[e] = int8_scale(set[64 + in + e]);
+        if (NMAT > 1) s1[e] = int8_scale(set[192 + in + e]);
+      }
+#pragma unroll
+      for (int t = 0; t < MT; ++t) {
+        const int r = 16 * t + c;
+        const Int8Scale rs = int8_scale(set[r]);
+        __bf16 v[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float f = int8_scaled(acc[j][t][e], rs, s0[e]);
+          v[e] = NMAT > 1 ? swiglu_bf16(f, int8_scaled(acc[1][t][e], rs, s1[e])) : (__bf16)f;
+        }
+        __bf16 *to = (__bf16 *)p.y + (size_t)r * p.n + col;
+        if (r >= p.m) continue;
+        if ((p.n & 3) == 0) {
+          if (col < p.n)
+            *(uint2 *)to = uint2{__builtin_bit_cast(uint32_t, bf16x2{v[0], v[1]}),
+                                 __builtin_bit_cast(uint32_t, bf16x2{v[2], v[3]})};
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (col + e < p.n) to[e] = v[e];
+        }
+      }
+    }
+  };
+  auto piece = [&](int v) __attribute__((always_inline)) {
+    const size_t at = ((size_t)(part_group - p.whole) * p.parts + v) * P + wave;
+    return rsrc_uniform((const uint8_t *)p.partial + at * C::kWavePiece, C::kWavePiece);
+  };
+  unsigned *const counter = p.counters + (part_group - p.whole);
+  unsigned before = 0;   // parts that had arrived before this one (thread 0)
+  int arrive_at = -1;    // unit at which this part's sums are known to be in memory
+  auto arrive = [&]() __attribute__((always_inline)) {
+    if (tid == 0) before = __hip_atomic_fetch_add(counter, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    arrive_at = -1;
   };
 
 #pragma unroll
-  for (int i = 0; i < S - 1; ++i) request((uint32_t)i);
-  int group = begin / p.units, unit = begin - group * p.units, from = unit;
+  for (int i = 0; i < S; ++i) request((uint32_t)i);
+  At at;
+  start(at);
   uint32_t stage = 0;
+  Half f0, f1;
+  wait_transfers<(S - 1) * C::kX>();
+  ring_barrier();
+  if (wave < P) read(0, 0, f0);
   for (int i = 0; i < count; ++i) {
-    // the S - 2 units behind this one may be under way
-    if (wave < C::kXWaves)
-      wait_transfers<(S - 2) * (2 + C::kX)>();
-    else
-      wait_transfers<(S - 2) * 2>();
+    if (wave < P) {
+      read(stage, 1, f1);
+      multiply(f0);
+    }
+    // the S - 2 units behind the next may be under way
+    wait_transfers<(S - 2) * C::kX>();
     ring_barrier();
-    request(stage == 0 ? S - 1 : stage - 1);
-    compute(stage);
+    if (i == arrive_at) arrive();
+    request(stage);
     stage = stage == S - 1 ? 0 : stage + 1;
-    if (++unit == p.units || i == count - 1) {
-      flush(group, from == 0 && unit == p.units);
-      unit = 0, from = 0, ++group;
+    if (wave < P) {
+      read(stage, 0, f0);
+      multiply(f1);
+    }
+    // (Memory operations end in order, so with stores among the youngest the
+    // waits above cover more transfers than they ask for, never fewer; and
+    // S - 1 units later this wave's stores here are among those waited for.)
+    if (++at.unit == at.end) {
+      if (at.scales == 0) {
+        if (wave < P) {
+          const __amdgpu_buffer_rsrc_t out = piece(part);
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int t = 0; t < MT; ++t) st16_coherent(out, (uint32_t)(j * MT + t) * 1024u + 16u * lane, acc[j][t]);
+        }
+        arrive_at = i + S;
+      } else if (wave < P) {
+        epilogue(at.group, at.scales);
+      }
+      clear();
+      next(at);
     }
   }
+  wait_all_memory();
+  if (!has_part) return;
+
+  // ---- the part's group, if no other part is still to come
+  __syncthreads();
+  if (arrive_at >= 0) arrive();
+  if (tid == 0) last_flag = before == (unsigned)(p.parts - 1);
+  __syncthreads();
+  if (!last_flag) return;
+  if (tid == 0) __hip_atomic_store(counter, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  if (wave >= P) return;
+  constexpr int kAtOnce = 8 / MT;  // pieces in flight
+  for (int v = 0; v < p.parts; v += kAtOnce) {
+    i32x4 w[kAtOnce][2][MT];
+#pragma unroll
+    for (int d = 0; d < kAtOnce; ++d) {
+      const __amdgpu_buffer_rsrc_t r = piece(min(v + d, p.parts - 1));
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int t = 0; t < MT; ++t)
+          w[d][j][t] = ld16_coherent(r, v + d < p.parts ? (uint32_t)(j * MT + t) * 1024u + 16u * lane : kOOB);
+    }
+#pragma unroll
+    for (int d = 0; d < kAtOnce; ++d)
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int t = 0; t < MT; ++t) acc[j][t] += w[d][j][t];
+  }
+  epilogue(part_group, 0);
 }
 
-template <int MT>
-hipError_t launch_mt(const Int8Args &p, int nmat, hipStream_t s) {
+template <int MT, int P>
+hipError_t launch_p(const Int8Args &p, int nmat, int nwg, hipStream_t s) {
   if (nmat == 1)
-    hipLaunchKernelGGL((k_int8_gemm<MT, 1>), dim3(p.nwg), dim3(kWaves * 64), 0, s, p);
+    hipLaunchKernelGGL((k_int8_gemm<MT, P, 1>), dim3(nwg), dim3(kWaves * 64), 0, s, p);
   else
-    hipLaunchKernelGGL((k_int8_gemm<MT, 2>), dim3(p.nwg), dim3(kWaves * 64), 0, s, p);
+    hipLaunchKernelGGL((k_int8_gemm<MT, P, 2>), dim3(nwg), dim3(kWaves * 64), 0, s, p);
   return hipGetLastError();
+}
+template <int MT>
+hipError_t launch_mt(const Int8Args &p, int slots, int nmat, int nwg, hipStream_t s) {
+  static_assert(kInt8MaxSlots == 6, "the slots below");
+  switch (slots) {
+    case 1: return launch_p<MT, 1>(p, nmat, nwg, s);
+    case 2: return launch_p<MT, 2>(p, nmat, nwg, s);
+    case 3: return launch_p<MT, 3>(p, nmat, nwg, s);
+    case 4: return launch_p<MT, 4>(p, nmat, nwg, s);
+    case 5: return launch_p<MT, 5>(p, nmat, nwg, s);
+    case 6: return launch_p<MT, 6>(p, nmat, nwg, s);
+    default: return hipErrorInvalidValue;
+  }
 }
 
 }  // namespace
 
 hipError_t launch_int8_gemm(const Int8ActRef &a, int m, int k, int n, int nmat, const Int8MatRef *w, void *y,
                             const Int8Plan &pl, unsigned *counters, int *partial, hipStream_t s) {
-  for (int r0 = 0; r0 < m; r0 += 256) {
-    const Int8Args p{a.codes + (size_t)r0 * k, a.row_scale + r0, m - r0 < 256 ? m - r0 : 256, k, n, w[0].codes,
-                     nmat > 1 ? w[1].codes : nullptr, w[0].scales, nmat > 1 ? w[1].scales : nullptr,
-                     (__bf16 *)y + (size_t)r0 * n, partial, counters, pl.units, pl.groups * pl.units, pl.nwg};
-    hipError_t e;
-    switch (pl.mt) {
-      case 1: e = launch_mt<1>(p, nmat, s); break;
-      case 2: e = launch_mt<2>(p, nmat, s); break;
-      case 4: e = launch_mt<4>(p, nmat, s); break;
-      case 8: e = launch_mt<8>(p, nmat, s); break;
-      default: e = launch_mt<16>(p, nmat, s); break;
-    }
-    if (e != hipSuccess) return e;
+  const Int8Args p{a.codes, a.row_scale, m, k, n, w[0].codes, nmat > 1 ? w[1].codes : nullptr, w[0].scales,
+                   nmat > 1 ? w[1].scales : nullptr, y, partial, counters, pl.groups, pl.units, pl.whole, pl.parts};
+  if (m > 16 * pl.mt) return hipErrorInvalidValue;
+  switch (pl.mt) {
+    case 1: return launch_mt<1>(p, pl.slots, nmat, pl.nwg, s);
+    case 2: return launch_mt<2>(p, pl.slots, nmat, pl.nwg, s);
+    case 4: return launch_mt<4>(p, pl.slots, nmat, pl.nwg, s);
+    default: return hipErrorInvalidValue;
   }
-  return hipSuccess;
 }
 
 }  // namespace nvfp4

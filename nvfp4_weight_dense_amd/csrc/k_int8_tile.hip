@@ -34,9 +34,9 @@ struct TileArgs {
   const float *s0, *s1;
   void *y;
   int ldy;             // columns of y, of which this launch's are the first n
-  int *partial;        // [nwg][2][8 waves][2 MT][4][64 lanes][4]
-  unsigned *counters;  // [nwg], zero between calls
-  int row_blocks, groups, units, whole;
+  int *partial;        // [split tile][part][8 waves][2 MT][4][64 lanes][4]
+  unsigned *counters;  // [split tile], zero between calls
+  int row_blocks, groups, units, whole, parts;
 };
 
 // WM: waves along the rows (8 / WM along the columns); MT: 32-row blocks of a wave
@@ -78,25 +78,28 @@ __global__ __launch_bounds__(kWaves * 64, 2) void k_int8_tile(TileArgs p) {
   }();
 
   // ---- this workgroup's work: tiles me, me + nwg, .. of the whole ones, then
-  // units rest_begin .. of the others'
-  const int tiles = p.row_blocks * p.groups, rest = (tiles - p.whole) * p.units;
+  // pairs me, me + nwg, .. of the others and their parts (int8_plan.h)
+  const int tiles = p.row_blocks * p.groups, split = tiles - p.whole, pairs = split * p.parts;
   const int mine = me < p.whole ? (p.whole - me + nwg - 1) / nwg : 0;
-  const int rest_begin = rest ? int8_run_begin(rest, nwg, me) : 0;
-  const int rest_end = rest ? int8_run_begin(rest, nwg, me + 1) : 0;
-  const int count = mine * p.units + rest_end - rest_begin;
-  // the tile and unit of this workgroup's i-th unit, for i in order
+  auto part_begin = [&](int part) __attribute__((always_inline)) { return p.units * part / p.parts; };
+  int count = mine * p.units;  // units of this workgroup
+  for (int i = me; i < pairs; i += nwg) count += part_begin(i / split + 1) - part_begin(i / split);
+  // a place in its work: tile, part, unit of K and the part's end, tiles done
   struct At {
-    int tile, unit, done;
+    int tile, part, unit, end, done;
   };
-  auto start = [&](At &a) __attribute__((always_inline)) {
-    a.done = 0;
-    if (mine) a.tile = me, a.unit = 0;
-    else a.tile = p.whole + rest_begin / p.units, a.unit = rest_begin % p.units;
-  };
-  auto next_tile = [&](At &a) __attribute__((always_inline)) {  // a.done counts tiles
-    if (++a.done < mine) a.tile += nwg, a.unit = 0;
-    else if (a.done == mine) a.tile = p.whole + rest_begin / p.units, a.unit = rest_begin % p.units;
-    else ++a.tile, a.unit = 0;
+  auto go = [&](At &a) __attribute__((always_inline)) {
+    if (a.done < mine) {
+      a.tile = me + a.done * nwg, a.part = 0, a.unit = 0, a.end = p.units;
+    } else {
+      const int i = me + (a.done - mine) * nwg;
+      if (i < pairs) {
+        a.part = i / split, a.tile = p.whole + i - a.part * split;
+        a.unit = part_begin(a.part), a.end = part_begin(a.part + 1);
+      } else {
+        a.tile = 0, a.part = 0, a.unit = 0, a.end = p.units;  // (past the work: not used)
+      }
+    }
   };
   // Row blocks of eight, columns within them, rows fastest: 32 tiles in a row
   // are eight row blocks of four column groups.
@@ -117,7 +120,8 @@ __global__ __launch_bounds__(kWaves * 64, 2) void k_int8_tile(TileArgs p) {
     voff[j] = line * (uint32_t)p.k + lk[j];
   }
   At la;
-  start(la);
+  la.done = 0;
+  go(la);
   int requested = 0;
   bool fresh = true;  // the next request is a tile's first
   u32x4_t xr, wr[C::kW], sr;
@@ -125,7 +129,7 @@ __global__ __launch_bounds__(kWaves * 64, 2) void k_int8_tile(TileArgs p) {
   const uint32_t scales_at = lds_address(scales) + (uint32_t)wave * 256u;
   auto ranges = [&]() __attribute__((always_inline)) {
     int rb, cg;
-    place(min(la.tile, tiles - 1), rb, cg);
+    place(la.tile, rb, cg);
     const int row0 = rb * C::kRows, col0 = cg * kCols;
     // this wave's scales: 64 rows', or 64 columns' of a matrix
     const int at = (wave * 64 - C::kRows) & (kCols - 1);
@@ -166,8 +170,9 @@ __global__ __launch_bounds__(kWaves * 64, 2) void k_int8_tile(TileArgs p) {
       to_lds(wr[j], to + C::kXBytes + (uint32_t)(wave * C::kW + j) * 1024u, live ? voff[j & 1] : kOOB,
              wr[j][2] ? k0 : 0u);
     ++requested;
-    if (++la.unit == p.units) {
-      next_tile(la);
+    if (++la.unit == la.end) {
+      ++la.done;
+      go(la);
       ranges();
       fresh = true;
     }
@@ -260,8 +265,8 @@ __global__ __launch_bounds__(kWaves * 64, 2) void k_int8_tile(TileArgs p) {
         }
       }
   };
-  auto piece = [&](int wg, int which) __attribute__((always_inline)) {
-    const size_t at = (size_t)(wg * 2 + which) * kWaves + wave;
+  auto piece = [&](int tile, int part) __attribute__((always_inline)) {
+    const size_t at = ((size_t)(tile - p.whole) * p.parts + part) * kWaves + wave;
     return rsrc_uniform((const uint8_t *)p.partial + at * C::kWavePiece, C::kWavePiece);
   };
   auto each_part = [&](auto &&f) __attribute__((always_inline)) {
@@ -272,34 +277,33 @@ __global__ __launch_bounds__(kWaves * 64, 2) void k_int8_tile(TileArgs p) {
 #pragma unroll
         for (int q = 0; q < 4; ++q) f(acc[j][t], q, (uint32_t)((j * MT + t) * 4 + q) * 1024u + 16u * (uint32_t)lane);
   };
-  // the end of this run's part of a tile
-  auto flush = [&](int tile, bool whole) __attribute__((always_inline)) {
-    bool finish = whole;
-    if (!whole) {
-      const int u0 = (tile - p.whole) * p.units;
-      const int v0 = int8_run_owner(rest, nwg, u0), v1 = int8_run_owner(rest, nwg, u0 + p.units - 1);
-      const __amdgpu_buffer_rsrc_t out = piece(me, u0 <= rest_begin ? 0 : 1);
+  // the end of a tile, or of a part of one
+  auto flush = [&](int tile, int part) __attribute__((always_inline)) {
+    bool finish = true;
+    if (tile >= p.whole) {
+      const __amdgpu_buffer_rsrc_t out = piece(tile, part);
       each_part([&](const i32x16 &v, int q, uint32_t off) __attribute__((always_inline)) {
         st16_coherent(out, off, i32x4{v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]});
       });
       wait_all_memory();
       __syncthreads();
       if (tid == 0)
-        last_flag = __hip_atomic_fetch_add(&p.counters[v0], 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) ==
-                    (unsigned)(v1 - v0);
+        last_flag = __hip_atomic_fetch_add(&p.counters[tile - p.whole], 1u, __ATOMIC_RELAXED,
+                                           __HIP_MEMORY_SCOPE_AGENT) == (unsigned)(p.parts - 1);
       __syncthreads();
       finish = last_flag != 0;
       if (finish) {
-        for (int v = v0; v <= v1; ++v) {
-          if (v == me) continue;  // (still in registers)
-          const __amdgpu_buffer_rsrc_t r = piece(v, u0 <= int8_run_begin(rest, nwg, v) ? 0 : 1);
+        for (int v = 0; v < p.parts; ++v) {
+          if (v == part) continue;  // (still in registers)
+          const __amdgpu_buffer_rsrc_t r = piece(tile, v);
           each_part([&](i32x16 &s, int q, uint32_t off) __attribute__((always_inline)) {
             const i32x4 w = ld16_coherent(r, off);
 #pragma unroll
             for (int e = 0; e < 4; ++e) s[4 * q + e] += w[e];
           });
         }
-        if (tid == 0) __hip_atomic_store(&p.counters[v0], 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        if (tid == 0)
+          __hip_atomic_store(&p.counters[tile - p.whole], 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
       }
     }
     if (finish) epilogue(tile);
@@ -313,8 +317,8 @@ __global__ __launch_bounds__(kWaves * 64, 2) void k_int8_tile(TileArgs p) {
   for (int i = 0; i < S; ++i) request((uint32_t)i);
   clear();
   At at;
-  start(at);
-  int from = at.unit;
+  at.done = 0;
+  go(at);
   uint32_t stage = 0;
   Step f0, f1;
   wait_transfers<(S - 1) * X>();
@@ -333,10 +337,10 @@ __global__ __launch_bounds__(kWaves * 64, 2) void k_int8_tile(TileArgs p) {
     stage = stage == S - 1 ? 0 : stage + 1;
     read(stage, 0, f0);
     multiply(f1);
-    if (++at.unit == p.units || i == count - 1) {
-      flush(at.tile, from == 0 && at.unit == p.units);
-      next_tile(at);
-      from = at.unit;
+    if (++at.unit == at.end) {
+      flush(at.tile, at.part);
+      ++at.done;
+      go(at);
     }
   }
   wait_all_memory();
@@ -364,7 +368,7 @@ hipError_t launch_int8_tile(const Int8ActRef &a, int m, int k, int n, int nmat, 
     auto codes = [&](int j) { return w[j].codes + (size_t)col0 * k; };
     const TileArgs p{a.codes, a.row_scale, m, k, q.columns, codes(0), nmat > 1 ? codes(1) : nullptr, w[0].scales + col0,
                      nmat > 1 ? w[1].scales + col0 : nullptr, (__bf16 *)y + col0, n, partial, counters, q.row_blocks,
-                     q.groups, q.units, q.whole};
+                     q.groups, q.units, q.whole, q.parts};
     hipError_t e;
     switch (q.shape) {
       case 0: e = launch_shape<2, 4>(p, 0, nmat, q.nwg, s); break;

@@ -305,7 +305,7 @@ bool int8_gemv_eligible(int m, int k);
 bool int8_gemv_quantizes(int m, int k);
 hipError_t launch_int8_gemv(const void *x, const float *row_scale, int m, int k, int n, int nmat, const Int8MatRef *w,
                             void *y, hipStream_t s);
-// Up to 256 rows, int8.  `counters`: kInt8Counters words, zero on entry, left
+// Up to kInt8RingRows rows, int8.  `counters`: kInt8Counters words, zero on entry, left
 // zero; `partial`: pl.partial_bytes.
 constexpr int kInt8Counters = 256;
 hipError_t launch_int8_gemm(const Int8ActRef &a, int m, int k, int n, int nmat, const Int8MatRef *w, void *y,

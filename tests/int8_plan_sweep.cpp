@@ -5,7 +5,6 @@
 // of plans at the end.
 #include <cstdio>
 #include <cstdlib>
-#include <map>
 #include <vector>
 
 #include "int8_plan.h"
@@ -25,44 +24,31 @@ static int bad = 0;
     }                              \
   } while (0)
 
-// Runs over `all` units, `units` a tile: [begin, end) of each workgroup.
-static void runs(int all, int units, int nwg, size_t piece, size_t bytes) {
-  CHECK(nwg >= 1 && nwg <= kInt8MaxWG && nwg <= all, "all %d nwg %d", all, nwg);
-  int at = 0;
-  std::map<int, int> arrivals, waits;  // by the counter a tile uses
-  for (int w = 0; w < nwg; ++w) {
-    const int b = int8_run_begin(all, nwg, w), e = int8_run_begin(all, nwg, w + 1);
-    CHECK(b == at && e > b, "all %d nwg %d w %d", all, nwg, w);
-    at = e;
-    CHECK(int8_run_owner(all, nwg, b) == w && int8_run_owner(all, nwg, e - 1) == w, "owner of %d", w);
-    std::vector<int> used;
-    for (int tile = b / units; tile * units < e; ++tile) {
-      const int u0 = tile * units, u1 = u0 + units;
-      if (u0 >= b && u1 <= e) continue;  // whole
-      const int which = u0 <= b ? 0 : 1;
-      for (int x : used) CHECK(x != which, "slot %d twice in %d", which, w);
-      used.push_back(which);
-      CHECK(((size_t)w * 2 + which + 1) * piece <= bytes, "piece of %d", w);
-      const int v0 = int8_run_owner(all, nwg, u0), v1 = int8_run_owner(all, nwg, u1 - 1);
-      CHECK(v0 >= 0 && v1 < nwg && v1 > v0 && v0 <= w && w <= v1, "owners %d %d of tile %d", v0, v1, tile);
-      CHECK(!waits.count(v0) || waits[v0] == tile + 1, "counter %d of tiles %d and %d", v0, waits[v0] - 1, tile);
-      waits[v0] = tile + 1;
-      ++arrivals[v0];
-    }
-  }
-  CHECK(at == all, "ends at %d of %d", at, all);
-  for (auto &a : arrivals) {
-    const int u0 = (waits[a.first] - 1) * units;
-    CHECK(a.second == int8_run_owner(all, nwg, u0 + units - 1) - a.first + 1, "arrivals at %d", a.first);
-  }
-}
-
-static void ring(int m, int n, int k, int nmat) {
-  const Int8Plan p = int8_plan(m, n, k, nmat);
-  CHECK(16 * p.mt >= m, "m %d mt %d", m, p.mt);
-  CHECK((int64_t)p.groups * (kInt8GroupCols / nmat) >= n && (int64_t)(p.groups - 1) * (kInt8GroupCols / nmat) < n, "n %d", n);
+static void ring(const Int8Plan &p, int m, int n, int k, int nmat) {
+  const int cols = 32 / nmat * p.slots;
+  CHECK(16 * p.mt >= m && p.slots >= 1 && p.slots <= kInt8MaxSlots, "m %d mt %d slots %d", m, p.mt, p.slots);
+  CHECK((int64_t)p.groups * cols >= n && (int64_t)(p.groups - 1) * cols < n, "n %d", n);
   CHECK((int64_t)p.units * kInt8UnitK >= k && (int64_t)(p.units - 1) * kInt8UnitK < k, "k %d", k);
-  runs(p.groups * p.units, p.units, p.nwg, int8_piece_bytes(p.mt), p.partial_bytes);
+  const int split = p.groups - p.whole, pairs = split * p.parts;
+  CHECK(p.whole >= 0 && split >= 0 && p.nwg >= 1 && p.nwg <= kInt8MaxWG, "whole %d nwg %d", p.whole, p.nwg);
+  CHECK(p.parts >= 1 && p.parts <= p.units && pairs <= p.nwg, "parts %d of %d units, %d pairs", p.parts, p.units, pairs);
+  CHECK((size_t)pairs * int8_piece_bytes(p.mt, p.slots) == p.partial_bytes, "partial sums of %d pairs", pairs);
+  std::vector<int> seen(split, 0);
+  int64_t units = 0;
+  for (int w = 0; w < p.nwg; ++w) {
+    int own = 0;
+    if (w < pairs) {
+      const int part = w / split;
+      own = p.units * (part + 1) / p.parts - p.units * part / p.parts;
+      CHECK(part < p.parts && own > 0, "part %d of %d", part, p.parts);
+      ++seen[w % split];
+    }
+    for (int i = w; i < p.whole; i += p.nwg) own += p.units;
+    CHECK(own > 0, "nothing for workgroup %d", w);
+    units += own;
+  }
+  CHECK(units == (int64_t)p.groups * p.units, "%lld units of %d groups", (long long)units, p.groups);
+  for (int x : seen) CHECK(x == p.parts, "%d parts end, %d are waited for", x, p.parts);
 }
 
 static void tiles(const Int8TilePlan &p, int m, int n, int k, int nmat) {
@@ -70,21 +56,34 @@ static void tiles(const Int8TilePlan &p, int m, int n, int k, int nmat) {
   CHECK((int64_t)p.row_blocks * t.rows >= m && (int64_t)(p.row_blocks - 1) * t.rows < m, "m %d", m);
   CHECK((int64_t)p.groups * (t.cols / nmat) >= n && (int64_t)(p.groups - 1) * (t.cols / nmat) < n, "n %d", n);
   CHECK((int64_t)p.units * kInt8TileK >= k && (int64_t)(p.units - 1) * kInt8TileK < k, "k %d", k);
-  const int all = p.row_blocks * p.groups;
-  CHECK(p.whole >= 0 && p.whole <= all && p.nwg >= 1 && p.nwg <= kInt8MaxWG, "whole %d nwg %d", p.whole, p.nwg);
-  CHECK(p.whole == all || p.whole == 0 || p.whole % p.nwg == 0, "whole %d of %d, nwg %d", p.whole, all, p.nwg);
-  CHECK(p.whole < all || p.nwg <= all, "an idle workgroup: %d tiles, nwg %d", all, p.nwg);
-  if (p.whole < all)
-    runs((all - p.whole) * p.units, p.units, p.nwg, (size_t)t.rows * t.cols * 4, p.partial_bytes);
-  else
-    CHECK(p.partial_bytes == 0, "partial sums without a split");
+  const int all = p.row_blocks * p.groups, split = all - p.whole, pairs = split * p.parts;
+  CHECK(p.whole >= 0 && split >= 0 && split < kInt8MaxWG && p.nwg >= 1 && p.nwg <= kInt8MaxWG, "whole %d nwg %d", p.whole, p.nwg);
+  CHECK(p.nwg <= (p.whole > pairs ? p.whole : pairs), "an idle workgroup: %d tiles, %d pairs, nwg %d", p.whole, pairs, p.nwg);
+  CHECK(p.parts >= 1 && p.parts <= p.units, "%d parts of %d units", p.parts, p.units);
+  CHECK((size_t)pairs * t.rows * t.cols * 4 == p.partial_bytes, "partial sums of %d pairs", pairs);
+  // the workgroups' units: each of them once, and at least one to a part
+  std::vector<int> seen(split, 0);
+  int64_t units = 0;
+  for (int w = 0; w < p.nwg; ++w) {
+    int own = 0;
+    for (int i = w; i < p.whole; i += p.nwg) own += p.units;
+    for (int i = w; i < pairs; i += p.nwg) {
+      const int part = i / split, len = p.units * (part + 1) / p.parts - p.units * part / p.parts;
+      CHECK(part < p.parts && len > 0, "part %d of %d", part, p.parts);
+      ++seen[i % split], own += len;
+    }
+    CHECK(own > 0, "nothing for workgroup %d", w);
+    units += own;
+  }
+  CHECK(units == (int64_t)all * p.units, "%lld units of %d tiles", (long long)units, all);
+  for (int x : seen) CHECK(x == p.parts, "%d parts end, %d are waited for", x, p.parts);
 }
 
 // what is planned for few rows fits what is bound for more
 static void bound(int few, int many, int n, int k, int nmat) {
   if (few > many) return;
   const size_t most = int8_partial_bound(many, n, k, nmat);
-  const size_t need = few <= 256 ? int8_plan(few, n, k, nmat).partial_bytes : int8_tile_partial_bytes(int8_tile_plan(few, n, k, nmat));
+  const size_t need = few <= kInt8RingRows ? int8_plan(few, n, k, nmat).partial_bytes : int8_tile_partial_bytes(int8_tile_plan(few, n, k, nmat));
   CHECK(need <= most, "m %d of %d, n %d k %d: %zu of %zu", few, many, n, k, need, most);
   CHECK(int8_partial_bound(few, n, k, nmat) <= most, "bound of m %d and %d", few, many);
 }
@@ -100,8 +99,10 @@ int main(int argc, char **argv) {
   };
   for (int i = 0; i < 30000; ++i) {
     const int n = pick(1 << 17), k = 32 * pick(4096), nmat = 1 + rand() % 2;
-    ring(1 + rand() % 256, n, k, nmat);
-    const int m = 257 + pick(1 << 15);
+    const int few = 1 + rand() % kInt8RingRows;
+    ring(int8_plan(few, n, k, nmat), few, n, k, nmat);
+    ring(int8_plan_of(1 + rand() % kInt8MaxSlots, 1 + rand() % kInt8RingParts, few, n, k, nmat), few, n, k, nmat);
+    const int m = kInt8RingRows + 1 + pick(1 << 15);
     const Int8TilePlans two = int8_tile_plan(m, n, k, nmat);
     int columns = 0;
     for (int j = 0; j < two.count; ++j) {
@@ -112,8 +113,8 @@ int main(int argc, char **argv) {
     }
     if (columns != n || two.count < 1 || two.count > 2) ++bad, printf("columns %d of %d\n", columns, n);
     const int shape = rand() % kInt8Shapes;
-    tiles(int8_tile_plan_of(shape, true, m, n, k, nmat), m, n, k, nmat);
-    tiles(int8_tile_plan_of(shape, false, m, n, k, nmat), m, n, k, nmat);
+    tiles(int8_tile_plan_of(shape, 1 + rand() % kInt8MaxParts, m, n, k, nmat), m, n, k, nmat);
+    tiles(int8_tile_plan_of(shape, 1, m, n, k, nmat), m, n, k, nmat);
     bound(1 + rand() % 600, m, n, k, nmat);
     bound(m - rand() % (m - 1), m, n, k, nmat);
     plans += 4;
