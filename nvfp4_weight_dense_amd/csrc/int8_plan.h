@@ -11,16 +11,16 @@ constexpr int kInt8MaxWG = 256;  // workgroups: one per CU
 constexpr int kInt8UnitK = 128;
 
 // Up to 64 rows: groups of `slots` slots of columns (32 of one matrix, 16 of
-// gate and up each).  Whole rounds of groups go to the workgroups in turn; the
-// groups left over may be split along K into `parts` parts each, at most one
-// to a workgroup.
+// gate and up each), which go to the workgroups in turn; or, where there are
+// few, each in `parts` parts along K, a workgroup each.  (Parts beside whole
+// groups do not pay: the sums that a part leaves in memory hold up the
+// transfers behind them, 10 us.)
 struct Int8Plan {
   int mt;      // 16-row tiles: 1, 2 or 4
   int slots;
   int groups;
   int units;   // units of K
-  int whole;   // groups that go whole, the first ones
-  int parts;   // of each of the others
+  int parts;   // of a group
   int nwg;
   size_t partial_bytes;
 };
@@ -37,26 +37,20 @@ inline Int8Plan int8_plan_of(int slots, int parts, int m, int n, int k, int nmat
   const int cols = 32 / nmat * slots;
   p.groups = (n + cols - 1) / cols;
   p.units = (k + kInt8UnitK - 1) / kInt8UnitK;
-  int rest = parts > 1 ? p.groups % kInt8MaxWG : 0;
-  if (rest * parts > kInt8MaxWG || parts > p.units) rest = 0;
-  p.whole = p.groups - rest;
-  p.parts = rest ? parts : 1;
-  const int pairs = rest * p.parts, most = p.whole > pairs ? p.whole : pairs;
-  p.nwg = most < kInt8MaxWG ? most : kInt8MaxWG;
-  p.partial_bytes = (size_t)pairs * int8_piece_bytes(p.mt, slots);
+  p.parts = (int64_t)p.groups * parts > kInt8MaxWG || parts > p.units ? 1 : parts;
+  const int64_t pairs = (int64_t)p.groups * p.parts;
+  p.nwg = (int)(pairs < kInt8MaxWG ? pairs : kInt8MaxWG);
+  p.partial_bytes = p.parts > 1 ? (size_t)pairs * int8_piece_bytes(p.mt, slots) : 0;
   return p;
 }
-// In microseconds, as measured: a CU takes in what its ring holds under way
-// every 2.2 us or 43 KB in one, whichever is slower; all weights come at 5.8
-// TB/s; then what it costs to join parts.
+// In microseconds, as measured: a unit of a workgroup takes 0.1 and 0.0185 for
+// each KB of it, all weights come at 5.8 TB/s; then what it costs to join parts.
 inline double int8_cost(const Int8Plan &p, int n, int k, int nmat) {
-  const double stage = 4.0 * p.slots + 2.0 * p.mt;  // KB
-  const double under_way = 160.0 - 4.0 - stage;
-  const double unit = stage / (under_way / 2.2 < 43.0 ? under_way / 2.2 : 43.0);
-  double units = (double)((p.whole + p.nwg - 1) / p.nwg) * p.units;
-  if (p.parts > 1) units += (p.units + p.parts - 1) / p.parts;
-  const double memory = (double)nmat * n * k / 5.8e6, busiest = units * unit;
-  return (busiest > memory ? busiest : memory) + (p.parts > 1 ? 3.0 + 0.1 * p.parts : 0.0);
+  const double unit = 0.1 + 0.0185 * (4.0 * p.slots + 2.0 * p.mt);
+  const int pairs = p.groups * p.parts;
+  const double busiest = (double)((pairs + p.nwg - 1) / p.nwg) * ((p.units + p.parts - 1) / p.parts) * unit;
+  const double memory = (double)nmat * n * k / 5.8e6;
+  return (busiest > memory ? busiest : memory) + (p.parts > 1 ? 1.5 + 0.3 * p.parts : 0.0);
 }
 inline Int8Plan int8_plan(int m, int n, int k, int nmat) {
   Int8Plan best{};

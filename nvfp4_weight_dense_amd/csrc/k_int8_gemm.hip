@@ -8,11 +8,11 @@
 // row's result does not depend on the rows beside it or on how K is split.
 //
 // A workgroup of eight waves computes groups of P slots of columns (32 of one
-// matrix, or 16 of gate and the same 16 of up): a part of K of one that is
-// split, then whole ones; P and the parts are chosen so that the CUs have
-// equal work (int8_plan.h).  A part's sums are left in memory before the whole
-// groups, and are joined behind them by the last of the parts' workgroups, so
-// nothing waits for them on the way.  K goes by units of 128: the weight
+// matrix, or 16 of gate and the same 16 of up), or a part of K of one group; P
+// and the parts are chosen so that the CUs have equal work (int8_plan.h).  K
+// goes by units of 128, each workgroup from a unit of its own around to it, so
+// that the rows' lines that are read at one time, a row's length apart, do not
+// all lie in the same few channels of memory.  The weight
 // rows and all activation rows of a unit, whole lines, are moved from memory
 // straight into a ring in LDS that holds as many units as fit, all but the
 // one in work under way.  One barrier a unit: it says that the next unit has
@@ -41,9 +41,9 @@ struct Int8Args {
   const int8_t *w0, *w1;  // gate and up, or the matrix and null
   const float *s0, *s1;
   void *y;
-  int *partial;        // [split group][part][P waves][2 MT][64 lanes][4]
-  unsigned *counters;  // [split group], zero between calls
-  int groups, units, whole, parts;
+  int *partial;        // [group][part][P waves][2 MT][64 lanes][4]
+  unsigned *counters;  // [group], zero between calls
+  int groups, units, parts;
 };
 
 // MT: 16-row tiles; P: slots
@@ -56,12 +56,11 @@ struct Cfg {
   // nowhere: all waves count alike)
   static constexpr int kW = (P + 1) / 2, kX = kW + 1;
   // The scales of a group come with its first unit, 64 to a wave: rows,
-  // columns.  A unit is requested kStages ahead, which may be as many
-  // groups; a part's stay until its end, in a set of their own.
+  // columns.  A unit is requested kStages ahead, which may be as many groups.
   static constexpr uint32_t kScaleBytes = 5 * 64 * 4;
-  static constexpr int kFit = (160 * 1024 - 1024 - 256 - 2 * kScaleBytes) / (kStage + kScaleBytes);
+  static constexpr int kFit = (160 * 1024 - 1024 - 256 - kScaleBytes) / (kStage + kScaleBytes);
   static constexpr int kStages = kFit > 16 ? 16 : kFit;
-  static constexpr int kScales = kStages + 2;
+  static constexpr int kScales = kStages + 1;
   static constexpr uint32_t kWavePiece = 2u * MT * 1024u;
   static_assert(kStages >= 3, "a ring of three units at least");
 };
@@ -80,27 +79,14 @@ __global__ __launch_bounds__(kWaves * 64, 2) void k_int8_gemm(Int8Args p) {
   const int c = lane & 15, g = lane >> 4;
   const uint32_t ring_at = lds_address(ring), nowhere_at = lds_address(nowhere);
 
-  // ---- this workgroup's work: pair `me` of the split groups and their parts,
-  // numbered part by part, then whole groups me, me + nwg, ..
-  const int me = (int)blockIdx.x, nwg = (int)gridDim.x, split = p.groups - p.whole, pairs = split * p.parts;
-  const bool has_part = me < pairs;
-  const int part = has_part ? me / split : 0, part_group = p.whole + me - part * split;
-  const int part_begin = p.units * part / p.parts, part_end = p.units * (part + 1) / p.parts;
-  const int mine = me < p.whole ? (p.whole - me + nwg - 1) / nwg : 0;
-  const int count = (has_part ? part_end - part_begin : 0) + mine * p.units;
-  struct At {
-    int group, unit, end, scales;
-  };
-  auto start = [&](At &a) __attribute__((always_inline)) {
-    if (has_part) a = At{part_group, part_begin, part_end, 0};
-    else a = At{me, 0, p.units, 1};
-  };
-  auto next = [&](At &a) __attribute__((always_inline)) {
-    a.group = a.scales == 0 ? me : a.group + nwg;
-    a.unit = 0, a.end = p.units;
-    a.scales = a.scales == C::kScales - 1 ? 1 : a.scales + 1;
-    if (a.group >= p.whole) a.group = 0;  // (past the work: not used)
-  };
+  // ---- this workgroup's work: groups me, me + nwg, .. , or with parts the
+  // pair `me` of the groups and their parts, numbered part by part
+  const int me = (int)blockIdx.x, nwg = (int)gridDim.x;
+  const int part = p.parts > 1 ? me / p.groups : 0, first = me - part * p.groups;
+  const int begin = p.units * part / p.parts, len = p.units * (part + 1) / p.parts - begin;
+  const int items = p.parts > 1 ? 1 : (p.groups - me + nwg - 1) / nwg;
+  const int count = items * len;
+  const int turn = ((me >> 3) + 32 * (me & 7)) % len;  // (workgroups go to the eight XCDs in turn)
 
   // ---- requests: row 8 t + lane / 8 of transfer t, of the group's weights
   // (with two matrices the gate's rows first) and of the activations
@@ -108,15 +94,13 @@ __global__ __launch_bounds__(kWaves * 64, 2) void k_int8_gemm(Int8Args p) {
   // (t is wave + 8 j: its row's swizzle goes by wave alone)
   const uint32_t lk = 16u * ((lane & 7u) ^ (4u * (wave & 1u) + (line >> 1)));
   const uint32_t voff = line * (uint32_t)p.k + lk;
-  At la;
-  start(la);
-  int requested = 0;
+  int lgroup = first, lunit = 0, lset = 0, requested = 0;
   bool fresh = true;  // the next request is a group's first
   u32x4_t wr[C::kW], sr;
   const u32x4_t xr = range_of(p.x + (size_t)min(8 * wave, p.m) * p.k, (size_t)max(min(8, p.m - 8 * wave), 0) * p.k);
   const uint32_t scales_at = wave < 5 ? lds_address(scales) + (uint32_t)wave * 256u : nowhere_at;
   auto ranges = [&]() __attribute__((always_inline)) {
-    const int col0 = la.group * kCols;
+    const int col0 = min(lgroup, p.groups - 1) * kCols;
 #pragma unroll
     for (int j = 0; j < C::kW; ++j) {
       const int row = 8 * (wave + 8 * j);
@@ -136,10 +120,12 @@ __global__ __launch_bounds__(kWaves * 64, 2) void k_int8_gemm(Int8Args p) {
   ranges();
   auto request = [&](uint32_t stage) __attribute__((always_inline)) {
     const bool live = requested < count;
-    const uint32_t k0 = live ? (uint32_t)la.unit * kInt8UnitK : 0u;
+    const int unit = lunit + turn < len ? lunit + turn : lunit + turn - len;
+    const uint32_t k0 = live ? (uint32_t)(begin + unit) * kInt8UnitK : 0u;
     const uint32_t to = ring_at + stage * C::kStage;
     if (live && fresh) {
-      words_to_lds(sr, scales_at + (wave < 5 ? (uint32_t)la.scales * C::kScaleBytes : 0u), 4u * (uint32_t)lane);
+      words_to_lds(sr, scales_at + (wave < 5 ? (uint32_t)lset * C::kScaleBytes : 0u), 4u * (uint32_t)lane);
+      lset = lset == C::kScales - 1 ? 0 : lset + 1;
     }
     fresh = false;
 #pragma unroll
@@ -151,8 +137,8 @@ __global__ __launch_bounds__(kWaves * 64, 2) void k_int8_gemm(Int8Args p) {
     to_lds(xr, wave < 2 * MT ? to + C::kWeights + (uint32_t)wave * 1024u : nowhere_at,
            live && wave < 2 * MT && k0 + lk < (uint32_t)p.k ? voff : kOOB, xr[2] ? k0 : 0u);
     ++requested;
-    if (++la.unit == la.end) {
-      next(la);
+    if (++lunit == len) {
+      lunit = 0, lgroup += nwg;
       ranges();
       fresh = true;
     }
@@ -224,21 +210,13 @@ __global__ __launch_bounds__(kWaves * 64, 2) void k_int8_gemm(Int8Args p) {
     }
   };
   auto piece = [&](int v) __attribute__((always_inline)) {
-    const size_t at = ((size_t)(part_group - p.whole) * p.parts + v) * P + wave;
+    const size_t at = ((size_t)first * p.parts + v) * P + wave;
     return rsrc_uniform((const uint8_t *)p.partial + at * C::kWavePiece, C::kWavePiece);
-  };
-  unsigned *const counter = p.counters + (part_group - p.whole);
-  unsigned before = 0;   // parts that had arrived before this one (thread 0)
-  int arrive_at = -1;    // unit at which this part's sums are known to be in memory
-  auto arrive = [&]() __attribute__((always_inline)) {
-    if (tid == 0) before = __hip_atomic_fetch_add(counter, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    arrive_at = -1;
   };
 
 #pragma unroll
   for (int i = 0; i < S; ++i) request((uint32_t)i);
-  At at;
-  start(at);
+  int group = first, unit = 0, set = 0;
   uint32_t stage = 0;
   Half f0, f1;
   wait_transfers<(S - 1) * C::kX>();
@@ -252,55 +230,56 @@ __global__ __launch_bounds__(kWaves * 64, 2) void k_int8_gemm(Int8Args p) {
     // the S - 2 units behind the next may be under way
     wait_transfers<(S - 2) * C::kX>();
     ring_barrier();
-    if (i == arrive_at) arrive();
     request(stage);
     stage = stage == S - 1 ? 0 : stage + 1;
     if (wave < P) {
       read(stage, 0, f0);
       multiply(f1);
     }
-    // (Memory operations end in order, so with stores among the youngest the
-    // waits above cover more transfers than they ask for, never fewer; and
-    // S - 1 units later this wave's stores here are among those waited for.)
-    if (++at.unit == at.end) {
-      if (at.scales == 0) {
-        if (wave < P) {
-          const __amdgpu_buffer_rsrc_t out = piece(part);
-#pragma unroll
-          for (int j = 0; j < 2; ++j)
-#pragma unroll
-            for (int t = 0; t < MT; ++t) st16_coherent(out, (uint32_t)(j * MT + t) * 1024u + 16u * lane, acc[j][t]);
-        }
-        arrive_at = i + S;
-      } else if (wave < P) {
-        epilogue(at.group, at.scales);
-      }
+    if (p.parts == 1 && ++unit == len) {
+      // (Memory operations end in order, so with stores among the youngest the
+      // waits above cover more transfers than they ask for, never fewer.)
+      if (wave < P) epilogue(group, set);
       clear();
-      next(at);
+      unit = 0, group += nwg;
+      set = set == C::kScales - 1 ? 0 : set + 1;
     }
   }
-  wait_all_memory();
-  if (!has_part) return;
+  if (p.parts == 1) {
+    wait_all_memory();
+    return;
+  }
 
-  // ---- the part's group, if no other part is still to come
+  // ---- a part: its sums to memory; the last of the group's to arrive joins them
+  if (wave < P) {
+    const __amdgpu_buffer_rsrc_t out = piece(part);
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int t = 0; t < MT; ++t) st16_coherent(out, (uint32_t)(j * MT + t) * 1024u + 16u * lane, acc[j][t]);
+  }
+  wait_all_memory();
   __syncthreads();
-  if (arrive_at >= 0) arrive();
-  if (tid == 0) last_flag = before == (unsigned)(p.parts - 1);
+  if (tid == 0)
+    last_flag = __hip_atomic_fetch_add(&p.counters[first], 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) ==
+                (unsigned)(p.parts - 1);
   __syncthreads();
   if (!last_flag) return;
-  if (tid == 0) __hip_atomic_store(counter, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  if (tid == 0) __hip_atomic_store(&p.counters[first], 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   if (wave >= P) return;
   constexpr int kAtOnce = 8 / MT;  // pieces in flight
   for (int v = 0; v < p.parts; v += kAtOnce) {
     i32x4 w[kAtOnce][2][MT];
 #pragma unroll
     for (int d = 0; d < kAtOnce; ++d) {
+      // (this part's sums are still in registers)
+      const bool other = v + d < p.parts && v + d != part;
       const __amdgpu_buffer_rsrc_t r = piece(min(v + d, p.parts - 1));
 #pragma unroll
       for (int j = 0; j < 2; ++j)
 #pragma unroll
         for (int t = 0; t < MT; ++t)
-          w[d][j][t] = ld16_coherent(r, v + d < p.parts ? (uint32_t)(j * MT + t) * 1024u + 16u * lane : kOOB);
+          w[d][j][t] = ld16_coherent(r, other ? (uint32_t)(j * MT + t) * 1024u + 16u * lane : kOOB);
     }
 #pragma unroll
     for (int d = 0; d < kAtOnce; ++d)
@@ -309,7 +288,7 @@ __global__ __launch_bounds__(kWaves * 64, 2) void k_int8_gemm(Int8Args p) {
 #pragma unroll
         for (int t = 0; t < MT; ++t) acc[j][t] += w[d][j][t];
   }
-  epilogue(part_group, 0);
+  epilogue(first, 0);
 }
 
 template <int MT, int P>
@@ -339,7 +318,7 @@ hipError_t launch_mt(const Int8Args &p, int slots, int nmat, int nwg, hipStream_
 hipError_t launch_int8_gemm(const Int8ActRef &a, int m, int k, int n, int nmat, const Int8MatRef *w, void *y,
                             const Int8Plan &pl, unsigned *counters, int *partial, hipStream_t s) {
   const Int8Args p{a.codes, a.row_scale, m, k, n, w[0].codes, nmat > 1 ? w[1].codes : nullptr, w[0].scales,
-                   nmat > 1 ? w[1].scales : nullptr, y, partial, counters, pl.groups, pl.units, pl.whole, pl.parts};
+                   nmat > 1 ? w[1].scales : nullptr, y, partial, counters, pl.groups, pl.units, pl.parts};
   if (m > 16 * pl.mt) return hipErrorInvalidValue;
   switch (pl.mt) {
     case 1: return launch_mt<1>(p, pl.slots, nmat, pl.nwg, s);

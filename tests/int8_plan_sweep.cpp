@@ -29,24 +29,18 @@ static void ring(const Int8Plan &p, int m, int n, int k, int nmat) {
   CHECK(16 * p.mt >= m && p.slots >= 1 && p.slots <= kInt8MaxSlots, "m %d mt %d slots %d", m, p.mt, p.slots);
   CHECK((int64_t)p.groups * cols >= n && (int64_t)(p.groups - 1) * cols < n, "n %d", n);
   CHECK((int64_t)p.units * kInt8UnitK >= k && (int64_t)(p.units - 1) * kInt8UnitK < k, "k %d", k);
-  const int split = p.groups - p.whole, pairs = split * p.parts;
-  CHECK(p.whole >= 0 && split >= 0 && p.nwg >= 1 && p.nwg <= kInt8MaxWG, "whole %d nwg %d", p.whole, p.nwg);
-  CHECK(p.parts >= 1 && p.parts <= p.units && pairs <= p.nwg, "parts %d of %d units, %d pairs", p.parts, p.units, pairs);
-  CHECK((size_t)pairs * int8_piece_bytes(p.mt, p.slots) == p.partial_bytes, "partial sums of %d pairs", pairs);
-  std::vector<int> seen(split, 0);
+  const int pairs = p.groups * p.parts;
+  CHECK(p.parts >= 1 && p.parts <= p.units && p.nwg >= 1 && p.nwg <= kInt8MaxWG && p.nwg <= pairs, "parts %d nwg %d", p.parts, p.nwg);
+  CHECK(p.parts == 1 || pairs == p.nwg, "%d pairs, nwg %d", pairs, p.nwg);
+  CHECK(p.partial_bytes == (p.parts > 1 ? (size_t)pairs * int8_piece_bytes(p.mt, p.slots) : 0), "partial sums of %d pairs", pairs);
+  std::vector<int> seen(p.groups, 0);
   int64_t units = 0;
-  for (int w = 0; w < p.nwg; ++w) {
-    int own = 0;
-    if (w < pairs) {
-      const int part = w / split;
-      own = p.units * (part + 1) / p.parts - p.units * part / p.parts;
-      CHECK(part < p.parts && own > 0, "part %d of %d", part, p.parts);
-      ++seen[w % split];
+  for (int w = 0; w < p.nwg; ++w)
+    for (int i = w; i < pairs; i += p.nwg) {
+      const int part = i / p.groups, len = p.units * (part + 1) / p.parts - p.units * part / p.parts;
+      CHECK(part < p.parts && len > 0, "part %d of %d", part, p.parts);
+      ++seen[i % p.groups], units += len;
     }
-    for (int i = w; i < p.whole; i += p.nwg) own += p.units;
-    CHECK(own > 0, "nothing for workgroup %d", w);
-    units += own;
-  }
   CHECK(units == (int64_t)p.groups * p.units, "%lld units of %d groups", (long long)units, p.groups);
   for (int x : seen) CHECK(x == p.parts, "%d parts end, %d are waited for", x, p.parts);
 }
