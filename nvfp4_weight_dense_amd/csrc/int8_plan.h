@@ -44,13 +44,14 @@ inline Int8Plan int8_plan_of(int slots, int parts, int m, int n, int k, int nmat
   return p;
 }
 // In microseconds, as measured: a unit of a workgroup takes 0.1 and 0.0185 for
-// each KB of it, all weights come at 5.8 TB/s; then what it costs to join parts.
+// each KB of it, all weights come at 5.8 TB/s (the shorter of the two counts a
+// little: nothing overlaps quite); then what it costs to join parts.
 inline double int8_cost(const Int8Plan &p, int n, int k, int nmat) {
   const double unit = 0.1 + 0.0185 * (4.0 * p.slots + 2.0 * p.mt);
   const int pairs = p.groups * p.parts;
   const double busiest = (double)((pairs + p.nwg - 1) / p.nwg) * ((p.units + p.parts - 1) / p.parts) * unit;
   const double memory = (double)nmat * n * k / 5.8e6;
-  return (busiest > memory ? busiest : memory) + (p.parts > 1 ? 1.5 + 0.3 * p.parts : 0.0);
+  return (busiest > memory ? busiest + 0.2 * memory : memory + 0.2 * busiest) + (p.parts > 1 ? 1.5 + 0.3 * p.parts : 0.0);
 }
 inline Int8Plan int8_plan(int m, int n, int k, int nmat) {
   Int8Plan best{};

@@ -6,13 +6,15 @@
 //   residual: h = bf16(residual + scale * gate * norm(y)), then norm(h)
 //   int8:    s = amax / 127, code = x / s (int8_common.h)
 //
-// All are bound by memory: one workgroup takes a row, each thread keeps its
-// pieces of eight values in registers from the one read of the row to the
-// one write, and what the row needs as a whole (a sum of squares, a largest
+// All are bound by memory: a workgroup takes a row -- for the quantizer, where
+// there are many rows that are not too long, a wave --, each thread keeps its
+// pieces of eight values in registers from the one read of the row to the one
+// write, and what the row needs as a whole (a sum of squares, a largest
 // magnitude) is exchanged once each.  Statistics are fp32.  The norm's
 // result is rounded to bf16 before it is quantized, and h before it is
 // normed, so that the fused calls give the bits of the calls one by one.
 #include <algorithm>
+#include <type_traits>
 
 #include "int8_common.h"
 
@@ -38,14 +40,32 @@ __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
   return uint4{w[0], w[1], w[2], w[3]};
 }
 
-// One value of every thread combined over the workgroup.  `slots`: 16 words
-// of LDS that no other exchange of the kernel uses.
-template <class T, class Op>
+// The pieces stay packed: without this the compiler keeps the values that a
+// pass over them unpacked for the next one, twice the registers.
+template <int P>
+__device__ __forceinline__ void stay_packed(uint4 (&v)[P]) {
+#pragma unroll
+  for (int i = 0; i < P; ++i) asm volatile("" : "+v"(v[i].x), "+v"(v[i].y), "+v"(v[i].z), "+v"(v[i].w));
+}
+
+// A row's threads: a wave's (WAVE), or the workgroup's.
+template <bool WAVE>
+__device__ __forceinline__ int row_thread() {
+  return WAVE ? (int)threadIdx.x & 63 : (int)threadIdx.x;
+}
+template <bool WAVE>
+__device__ __forceinline__ int row_threads() {
+  return WAVE ? 64 : (int)blockDim.x;
+}
+
+// One value of every thread combined over the row's.  `slots`: 16 words of
+// LDS that no other exchange of the kernel uses.
+template <bool WAVE, class T, class Op>
 __device__ __forceinline__ T over_row(T v, T *slots, Op op) {
 #pragma unroll
   for (int off = 32; off > 0; off >>= 1) v = op(v, __shfl_xor(v, off));
   const int waves = (int)blockDim.x >> 6;
-  if (waves == 1) return v;
+  if (WAVE || waves == 1) return v;
   if ((threadIdx.x & 63) == 0) slots[threadIdx.x >> 6] = v;
   __syncthreads();
   T r = slots[0];
@@ -57,7 +77,7 @@ __device__ __forceinline__ T over_row(T v, T *slots, Op op) {
 // fp32's range (values past 2^50) is summed again with its values times
 // 2^-80.
 template <int P>
-__device__ __forceinline__ float row_rstd(const uint4 (&v)[P], int k, float eps, float (*slots)[16]) {
+__device__ __forceinline__ float row_rstd(uint4 (&v)[P], int k, float eps, float (*slots)[16]) {
   auto squares = [&](float by, float *at) {
     float ss = 0.0f;
 #pragma unroll
@@ -67,9 +87,10 @@ __device__ __forceinline__ float row_rstd(const uint4 (&v)[P], int k, float eps,
 #pragma unroll
       for (int j = 0; j < 8; ++j) ss = fmaf(f[j] * by, f[j] * by, ss);
     }
-    return over_row(ss, at, [](float a, float b) { return a + b; });
+    return over_row<false>(ss, at, [](float a, float b) { return a + b; });
   };
   const float ss = squares(1.0f, slots[0]);
+  stay_packed(v);
   if (ss < 0x1p100f) return __builtin_amdgcn_rsqf(ss / (float)k + eps);
   return __builtin_amdgcn_rsqf(squares(0x1p-80f, slots[1]) / (float)k) * 0x1p-80f;  // (eps is far below)
 }
@@ -96,13 +117,13 @@ __device__ __forceinline__ void scale_row(uint4 (&v)[P], const uint4 *weight, fl
 }
 
 // The row in v, to out or as codes and a scale.
-template <int P>
+template <bool WAVE, int P>
 __device__ __forceinline__ void write_row(const uint4 (&v)[P], const RowsOut &o, int row, int pieces, uint32_t *slots) {
   if (o.out) {
     uint4 *to = (uint4 *)o.out + (size_t)row * pieces;
 #pragma unroll
     for (int i = 0; i < P; ++i) {
-      const int p = (int)threadIdx.x + i * (int)blockDim.x;
+      const int p = row_thread<WAVE>() + i * row_threads<WAVE>();
       if (p < pieces) to[p] = v[i];
     }
     return;
@@ -111,32 +132,61 @@ __device__ __forceinline__ void write_row(const uint4 (&v)[P], const RowsOut &o,
 #pragma unroll
   for (int i = 0; i < P; ++i) top = amax_bits(top, v[i]);
   const Int8Row r =
-      int8_row(over_row(amax_fold(top), slots, [](uint32_t a, uint32_t b) { return max(a, b); }));
-  if (threadIdx.x == 0) o.row_scale[row] = r.s;
+      int8_row(over_row<WAVE>(amax_fold(top), slots, [](uint32_t a, uint32_t b) { return max(a, b); }));
+  if (row_thread<WAVE>() == 0) o.row_scale[row] = r.s;
   uint2 *to = (uint2 *)o.codes + (size_t)row * pieces;
 #pragma unroll
   for (int i = 0; i < P; ++i) {
-    const int p = (int)threadIdx.x + i * (int)blockDim.x;
+    const int p = row_thread<WAVE>() + i * row_threads<WAVE>();
     if (p < pieces) to[p] = int8_codes(v[i], r);
   }
 }
 
-template <int P>
+template <bool WAVE, int P>
 __device__ __forceinline__ void read_row(const void *x, int row, int pieces, uint4 (&v)[P]) {
   const uint4 *at = (const uint4 *)x + (size_t)row * pieces;
 #pragma unroll
   for (int i = 0; i < P; ++i) {
-    const int p = (int)threadIdx.x + i * (int)blockDim.x;
+    const int p = row_thread<WAVE>() + i * row_threads<WAVE>();
     v[i] = p < pieces ? at[p] : uint4{0u, 0u, 0u, 0u};
   }
 }
 
-template <int P>
-__global__ __launch_bounds__(kMaxThreads) void k_int8_rows(const void *x, int k, RowsOut o) {
+// The row of this wave or workgroup; past the last: -1.
+constexpr int kWaveRows = 4;  // rows of a workgroup whose waves take one each
+template <bool WAVE>
+__device__ __forceinline__ int own_row(int m) {
+  if (!WAVE) return (int)blockIdx.x;
+  const int row = (int)blockIdx.x * kWaveRows + __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  return row < m ? row : -1;
+}
+template <bool WAVE>
+constexpr int most_threads() { return WAVE ? 64 * kWaveRows : kMaxThreads; }
+
+// With gridDim.y > 1 (few rows) each slice of a row is a workgroup: it looks
+// for the largest magnitude in all of the row and encodes its own pieces, so
+// that the divisions of a row spread over several CUs.
+template <bool WAVE, int P>
+__global__ __launch_bounds__(most_threads<WAVE>()) void k_int8_rows(const void *x, int m, int k, RowsOut o) {
   __shared__ uint32_t top[16];
+  const int row = own_row<WAVE>(m), pieces = k >> 3;
+  if (row < 0) return;
   uint4 v[P];
-  read_row(x, (int)blockIdx.x, k >> 3, v);
-  write_row(v, o, (int)blockIdx.x, k >> 3, top);
+  read_row<WAVE>(x, row, pieces, v);
+  if (WAVE || gridDim.y == 1) {
+    write_row<WAVE>(v, o, row, pieces, top);
+    return;
+  }
+  uint32_t bits = 0;
+#pragma unroll
+  for (int i = 0; i < P; ++i) bits = amax_bits(bits, v[i]);
+  const Int8Row r =
+      int8_row(over_row<WAVE>(amax_fold(bits), top, [](uint32_t a, uint32_t b) { return max(a, b); }));
+  if (threadIdx.x == 0 && blockIdx.y == 0) o.row_scale[row] = r.s;
+  const int per = (pieces + (int)gridDim.y - 1) / (int)gridDim.y;
+  const int last = min(pieces, per * ((int)blockIdx.y + 1));
+  for (int p = per * (int)blockIdx.y + (int)threadIdx.x; p < last; p += (int)blockDim.x)
+    ((uint2 *)o.codes)[(size_t)row * pieces + p] = int8_codes(((const uint4 *)x)[(size_t)row * pieces + p], r);
 }
 
 template <int P>
@@ -145,10 +195,10 @@ __global__ __launch_bounds__(kMaxThreads) void k_rms_norm(const void *x, int k, 
   __shared__ uint32_t top[16];
   const int row = (int)blockIdx.x, pieces = k >> 3;
   uint4 v[P];
-  read_row(x, row, pieces, v);
+  read_row<false>(x, row, pieces, v);
   const float rstd = row_rstd(v, k, eps, sums);
   scale_row(v, (const uint4 *)n.weight, n.offset, rstd, pieces);
-  write_row(v, o, row, pieces, top);
+  write_row<false>(v, o, row, pieces, top);
 }
 
 template <int P>
@@ -157,8 +207,8 @@ __global__ __launch_bounds__(kMaxThreads) void k_rms_norm_residual(ResidualArgs 
   __shared__ uint32_t top[16];
   const int row = (int)blockIdx.x, pieces = k >> 3;
   uint4 v[P], r[P];
-  read_row(a.y, row, pieces, v);
-  read_row(a.residual, row, pieces, r);
+  read_row<false>(a.y, row, pieces, v);
+  read_row<false>(a.residual, row, pieces, r);
   const float rstd = a.post.on ? row_rstd(v, k, eps, sums) : 1.0f;
   const uint4 *post = a.post.on ? (const uint4 *)a.post.weight : nullptr;
   const uint4 *gate = a.gate ? (const uint4 *)a.gate + (size_t)(row / a.rows_per_gate) * pieces : nullptr;
@@ -190,19 +240,20 @@ __global__ __launch_bounds__(kMaxThreads) void k_rms_norm_residual(ResidualArgs 
   if (!a.next.on) return;
   const float next = row_rstd(v, k, eps, sums + 2);
   scale_row(v, (const uint4 *)a.next.weight, a.next.offset, next, pieces);
-  write_row(v, o, row, pieces, top);
+  write_row<false>(v, o, row, pieces, top);
 }
 
-// Threads that hold a row of k values in P pieces each.
-struct RowShape {
-  int p, threads;
-};
-RowShape row_shape(int k) {
+// Pieces of a thread, for a workgroup to a row: two or four, so that a row of
+// 4096 or 5120 values is four or three waves' (8192 rows of 5120: norm 32, end
+// of a block 60 us; 40 and 88 with one piece a thread, 35 and 62 with eight),
+// and more where 1024 threads do not hold a row so.
+int row_pieces(int k) {
   const int pieces = k >> 3;
-  int p = 1;
+  int p = pieces > 512 ? 4 : pieces > 256 ? 2 : 1;
   while (cdiv(pieces, p) > kMaxThreads) p *= 2;
-  return RowShape{p, cdiv(cdiv(pieces, p), 64) * 64};
+  return p;
 }
+int row_block(int k, int p) { return cdiv(cdiv(k >> 3, p), 64) * 64; }
 
 template <class F>
 hipError_t with_pieces(int p, F &&f) {
@@ -217,27 +268,45 @@ hipError_t with_pieces(int p, F &&f) {
   return hipGetLastError();
 }
 
+// The quantizer's rows go to a wave each from this many on and up to this
+// many pieces a lane (17408 rows of 5120: 45 us, with a workgroup to a row 75;
+// 1024 rows of 4096: 8.4 and 9.8).
+constexpr int kWaveMinRows = 1024, kWaveMaxPieces = 16;
+
 }  // namespace
 
 hipError_t launch_int8_rows(const void *x, int m, int k, int8_t *codes, float *row_scale, hipStream_t s) {
-  const RowShape r = row_shape(k);
-  return with_pieces(r.p, [&](auto p) {
-    hipLaunchKernelGGL((k_int8_rows<decltype(p)::value>), dim3(m), dim3(r.threads), 0, s, x, k,
-                       (RowsOut{nullptr, codes, row_scale}));
+  const RowsOut o{nullptr, codes, row_scale};
+  const int pieces = k >> 3, lane_pieces = cdiv(pieces, 64);
+  if (m >= kWaveMinRows && lane_pieces <= kWaveMaxPieces) {
+    auto run = [&](auto p) {
+      hipLaunchKernelGGL((k_int8_rows<true, decltype(p)::value>), dim3(cdiv(m, kWaveRows)), dim3(64 * kWaveRows), 0, s, x,
+                         m, k, o);
+    };
+    if (lane_pieces <= 2) run(std::integral_constant<int, 2>());
+    else if (lane_pieces <= 4) run(std::integral_constant<int, 4>());
+    else if (lane_pieces <= 8) run(std::integral_constant<int, 8>());
+    else if (lane_pieces <= 10) run(std::integral_constant<int, 10>());
+    else run(std::integral_constant<int, kWaveMaxPieces>());
+    return hipGetLastError();
+  }
+  // few rows: slices of 256 pieces or more, for about as many workgroups as CUs
+  const int slices = std::max(1, std::min({8, 256 / m, pieces / 256}));
+  const int p = row_pieces(k);
+  return with_pieces(p, [&](auto p) {
+    hipLaunchKernelGGL((k_int8_rows<false, decltype(p)::value>), dim3(m, slices), dim3(row_block(k, p)), 0, s, x, m, k, o);
   });
 }
 
 hipError_t launch_rms_norm(const void *x, int m, int k, const NormRef &n, float eps, const RowsOut &o, hipStream_t s) {
-  const RowShape r = row_shape(k);
-  return with_pieces(r.p, [&](auto p) {
-    hipLaunchKernelGGL((k_rms_norm<decltype(p)::value>), dim3(m), dim3(r.threads), 0, s, x, k, n, eps, o);
+  return with_pieces(row_pieces(k), [&](auto p) {
+    hipLaunchKernelGGL((k_rms_norm<decltype(p)::value>), dim3(m), dim3(row_block(k, p)), 0, s, x, k, n, eps, o);
   });
 }
 
 hipError_t launch_rms_norm_residual(const ResidualArgs &a, int m, int k, float eps, const RowsOut &o, hipStream_t s) {
-  const RowShape r = row_shape(k);
-  return with_pieces(r.p, [&](auto p) {
-    hipLaunchKernelGGL((k_rms_norm_residual<decltype(p)::value>), dim3(m), dim3(r.threads), 0, s, a, k, eps, o);
+  return with_pieces(row_pieces(k), [&](auto p) {
+    hipLaunchKernelGGL((k_rms_norm_residual<decltype(p)::value>), dim3(m), dim3(row_block(k, p)), 0, s, a, k, eps, o);
   });
 }
 
