@@ -1,6 +1,6 @@
 """One decoder layer with NVFP4 weights, generating over the 8-bit KV cache.
 
-    python examples/decode_layer.py [--steps N] [--budget TOKENS]
+    python examples/decode_layer.py [--steps N] [--budget TOKENS] [--int8]
 
 A batch of prompts of different lengths is run through the layer, then one
 token per sequence and step.  Each call of the layer is
@@ -9,7 +9,10 @@ token per sequence and step.  Each call of the layer is
     x += FFN(norm(x))
 
 with nvfp4_gemm_w4a16 for the projections, kv8_append and kv8_attention for
-the cache, and dense_ffn_forward for the FFN.  kv8_attention also keeps the
+the cache, dense_ffn_forward for the FFN, and rms_norm and rms_norm_residual
+around them.  With --int8 the projections and the FFN are int8_gemm_w8a8 and
+dense_ffn_forward_int8 on int8 weights, and the norms hand them int8 rows.
+kv8_attention also keeps the
 attention weight that each token has received; a sequence that reaches the
 budget is cut by kv8_evict to its first, its last and its most attended
 tokens, and its old pages are free again.  Weights are random, position
@@ -36,29 +39,32 @@ def _weight(n: int, k: int, g: torch.Generator) -> nv.NVFP4Weight:
     return nv.NVFP4Weight(codes.cuda(), scales.cuda(), 0.35 * k ** -0.5)
 
 
-def _norm(x: torch.Tensor) -> torch.Tensor:
-    f = x.float()
-    return (f * torch.rsqrt(f.square().mean(-1, keepdim=True) + 1e-6)).bfloat16()
+def _weight_int8(n: int, k: int, g: torch.Generator) -> nv.Int8Weight:
+    """A random weight, quantized by its output channels."""
+    return nv.Int8Weight(*nv.int8_quantize_rows((torch.randn(n, k, generator=g) * k ** -0.5).bfloat16().cuda()))
 
 
 class Layer:
-    def __init__(self, hidden=1024, inter=2816, q_heads=8, kv_heads=2, dim=128, seed=0):
+    def __init__(self, hidden=1024, inter=2816, q_heads=8, kv_heads=2, dim=128, seed=0, int8=False):
         g = torch.Generator().manual_seed(seed)
-        self.q_heads, self.kv_heads, self.dim = q_heads, kv_heads, dim
-        self.wqkv = _weight((q_heads + 2 * kv_heads) * dim, hidden, g)
-        self.wo = _weight(hidden, q_heads * dim, g)
-        self.wg, self.wu = _weight(inter, hidden, g), _weight(inter, hidden, g)
-        self.wd = _weight(hidden, inter, g)
+        self.q_heads, self.kv_heads, self.dim, self.int8 = q_heads, kv_heads, dim, int8
+        weight = _weight_int8 if int8 else _weight
+        self.wqkv = weight((q_heads + 2 * kv_heads) * dim, hidden, g)
+        self.wo = weight(hidden, q_heads * dim, g)
+        self.wg, self.wu = weight(inter, hidden, g), weight(inter, hidden, g)
+        self.wd = weight(hidden, inter, g)
+        self.project, self.ffn = (nv.int8_gemm_w8a8, nv.dense_ffn_forward_int8) if int8 else \
+            (nv.nvfp4_gemm_w4a16, nv.dense_ffn_forward)
 
     def __call__(self, x, cache, table, lens, starts=None, max_rows=None, max_len=None, workspace=None):
-        qkv = nv.nvfp4_gemm_w4a16(_norm(x), self.wqkv).view(x.shape[0], -1, self.dim)
+        qkv = self.project(nv.rms_norm(x, int8=self.int8), self.wqkv).view(x.shape[0], -1, self.dim)
         q, k, v = qkv.split((self.q_heads, self.kv_heads, self.kv_heads), 1)
         nv.kv8_append(k, v, cache, table, lens, starts, max_rows=max_rows)
         a = nv.kv8_attention(q, cache, table, lens, starts, max_rows=max_rows, max_len=max_len,
                              accumulate=cache.weights is not None, workspace=workspace)
         self.last = q, a
-        x = x + nv.nvfp4_gemm_w4a16(a.view(x.shape[0], -1), self.wo)
-        return x + nv.dense_ffn_forward(_norm(x), self.wg, self.wu, self.wd)
+        x, n = nv.rms_norm_residual(x, self.project(a.view(x.shape[0], -1), self.wo), norm=True, int8=self.int8)
+        return nv.rms_norm_residual(x, self.ffn(n, self.wg, self.wu, self.wd))[0]
 
 
 class Pages:
@@ -123,7 +129,7 @@ def generate(layer: Layer, prompts, steps: int, budget: int, page: int = 64, sin
         lens = [m + 1 for m in lens]
         n += 1
         table = pages.grow(lens)
-        x = layer(_norm(x), cache, table, n, max_len=top, workspace=workspace)
+        x = layer(nv.rms_norm(x), cache, table, n, max_len=top, workspace=workspace)
     return x, cache, pages, table, lens, n
 
 
@@ -131,8 +137,9 @@ def main() -> None:
     ap = argparse.ArgumentParser(description=__doc__.splitlines()[0])
     ap.add_argument("--steps", type=int, default=200)
     ap.add_argument("--budget", type=int, default=512)
+    ap.add_argument("--int8", action="store_true")
     args = ap.parse_args()
-    layer = Layer()
+    layer = Layer(int8=args.int8)
     g = torch.Generator().manual_seed(1)
     prompts = [torch.randn(n, 1024, generator=g).bfloat16().cuda() for n in (500, 37, 256, 1)]
     x, cache, pages, _, lens, _ = generate(layer, prompts, args.steps, args.budget)

@@ -720,11 +720,11 @@ def _int8_x(x, k: int):
     return c, s
 
 
-def _on_current(first: torch.Tensor, *rest):
-    """_gpu, and that GPU is the current one (the library's launches and scratch are the current device's)."""
-    _gpu(first, *rest)
-    if first.get_device() != torch._C._cuda_getDevice():
-        raise ValueError(f"tensors on {first.device}, the current device is cuda:{torch._C._cuda_getDevice()}")
+def _on_current(first: torch.Tensor, *rest) -> int:
+    """Every tensor on one GPU, which is the current one (checked after the shapes); its index."""
+    dev = first.get_device()
+    _kv8_on(dev, *rest)
+    return dev
 
 
 def _rows_workspace(t):
@@ -746,9 +746,8 @@ def int8_quantize_rows(x: torch.Tensor, stream=None) -> Int8Rows:
     [m]) of bf16 rows (activations, or a weight by its output channels)."""
     L = load_library()
     x = _act(x, "x")
-    _on_current(x)
+    dev = _on_current(x)
     m, k = x.shape
-    dev = x.get_device()
     codes = _kv8_empty((m, k), _I8, x.device, stream)
     rs = _kv8_empty((m,), _F32, x.device, stream)
     _check(L.int8_quantize_rows(x.data_ptr(), m, k, codes.data_ptr(), rs.data_ptr(), _kv8_stream(stream, dev)))
@@ -783,11 +782,11 @@ def int8_gemm_w8a8(x, w, y: torch.Tensor | None = None, *, workspace: torch.Tens
     m = xt.shape[0]
     y = _bf16_out(y, (m, n), "y")
     ws, nbytes = _rows_workspace(workspace)
-    _on_current(xt, xs, y, workspace, w.codes, w.scales)
+    dev = _on_current(xt, xs, y, workspace, w.codes, w.scales)
     if y is None:
         y = _kv8_empty((m, n), _BF16, xt.device, stream)
     _check(L.int8_gemm_w8a8(xt.data_ptr(), None if xs is None else xs.data_ptr(), m, cw, y.data_ptr(), ws, nbytes,
-                            _kv8_stream(stream, xt.get_device())))
+                            _kv8_stream(stream, dev)))
     return y
 
 
@@ -804,11 +803,11 @@ def dense_ffn_forward_int8(x, wg, wu, wd, out: torch.Tensor | None = None, *,
     m = xt.shape[0]
     out = _bf16_out(out, (m, hidden), "out")
     ws, nbytes = _rows_workspace(workspace)
-    _on_current(xt, xs, out, workspace, wg.codes, wg.scales, wu.codes, wu.scales, wd.codes, wd.scales)
+    dev = _on_current(xt, xs, out, workspace, wg.codes, wg.scales, wu.codes, wu.scales, wd.codes, wd.scales)
     if out is None:
         out = _kv8_empty((m, hidden), _BF16, xt.device, stream)
     _check(L.dense_ffn_forward_int8(xt.data_ptr(), None if xs is None else xs.data_ptr(), m, hidden, inter, cg, cu, cd,
-                                    out.data_ptr(), ws, nbytes, _kv8_stream(stream, xt.get_device())))
+                                    out.data_ptr(), ws, nbytes, _kv8_stream(stream, dev)))
     return out
 
 
@@ -841,8 +840,7 @@ def rms_norm(x: torch.Tensor, weight: torch.Tensor | None = None, *, eps: float 
     out = _bf16_out(out, (m, k), "out")
     if int8 and out is not None:
         raise ValueError("out: int8 rows are returned anew")
-    _on_current(x, w, out)
-    dev = x.get_device()
+    dev = _on_current(x, w, out)
     q = None
     if int8:
         q = Int8Rows(_kv8_empty((m, k), _I8, x.device, stream), _kv8_empty((m,), _F32, x.device, stream))
@@ -885,7 +883,7 @@ def rms_norm_residual(residual: torch.Tensor, y: torch.Tensor, *, post=None, gat
         raise ValueError("out: only the bf16 result of a norm is written to it")
     if int8 and not nxt:
         raise ValueError("int8: there is no norm to quantize")
-    _on_current(residual, y, pw, nw, gate, h, out)
+    dev = _on_current(residual, y, pw, nw, gate, h, out)
     if h is None:
         h = _kv8_empty((m, k), _BF16, y.device, stream)
     q = None
@@ -896,7 +894,7 @@ def rms_norm_residual(residual: torch.Tensor, y: torch.Tensor, *, post=None, gat
     _check(L.rms_norm_residual(residual.data_ptr(), y.data_ptr(), m, k, post, _at(pw), _at(gate), gates, float(scale),
                                nxt, _at(nw), float(weight_offset), float(eps), h.data_ptr(), _at(out),
                                q and q.codes.data_ptr(), q and q.row_scale.data_ptr(),
-                               _kv8_stream(stream, y.get_device())))
+                               _kv8_stream(stream, dev)))
     return h, q if int8 else out
 
 

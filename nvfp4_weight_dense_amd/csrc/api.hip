@@ -1306,6 +1306,7 @@ int int8_gemm_w8a8(const void *x, const float *row_scale, int32_t m, const int8_
   if ((rc = check_int8_x(x, row_scale, m)) || (rc = check_act(y, m, "y")) || (rc = check_int8_weight(w, "w")))
     return rc;
   if (m == 0) return NVFP4_OK;
+  if (x == y) return fail(NVFP4_EINVAL, "int8_gemm_w8a8: y is x");
   hipStream_t s = (hipStream_t)stream;
   const Int8Product pr(row_scale != nullptr, m, w->n, w->k, 1);
   unsigned *counters = nullptr;
@@ -1391,6 +1392,7 @@ int rms_norm_residual(const void *residual, const void *y, int32_t m, int32_t k,
   if (m == 0) return NVFP4_OK;
   if (gate && m % gates != 0) return fail(NVFP4_ESHAPE, "%s: gates=%d does not divide m=%d", name, gates, m);
   if (next && (rc = check_rows_out(out, codes, row_scale, name))) return rc;
+  if (out && out == h) return fail(NVFP4_EINVAL, "%s: h and out are one array", name);
   if (!next && (out || codes || row_scale)) return fail(NVFP4_EINVAL, "%s: an output without a next norm", name);
   const ResidualArgs a{residual, y, gate, gate ? m / gates : 1, scale, {post_weight, offset, post != 0},
                        {next_weight, offset, next != 0}, h};

@@ -1,6 +1,7 @@
 """Products and the FFN in 8-bit integers against their 64-bit definitions (tests/int8_ref.py), on the GPU."""
 
 import math
+import random
 
 import pytest
 import torch
@@ -67,6 +68,42 @@ def test_product(m, n, k):
     assert bool((y[m:] == 7.0).all())
     rows = nv.Int8Rows(codes.cuda(), s.cuda())
     assert torch.equal(nv.int8_gemm_w8a8(rows, gw), got)
+
+
+def _large(m, n, k, seed):
+    """A product against the sum in 64 bits, taken on the GPU (exact: whole numbers below 2^53)."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    x = nv.Int8Rows(torch.randint(-127, 128, (m, k), generator=g, device="cuda").to(torch.int8),
+                    torch.rand(m, generator=g, device="cuda") + 0.5)
+    w = nv.Int8Weight(torch.randint(-128, 128, (n, k), generator=g, device="cuda").to(torch.int8),
+                      torch.rand(n, generator=g, device="cuda") + 0.5)
+    y = torch.full((m * n + 64,), 7.0, dtype=BF, device="cuda")
+    got = nv.int8_gemm_w8a8(x, w, y[:m * n].view(m, n))
+    for r in range(0, m, 1024):
+        want = x.codes[r:r + 1024].double() @ w.codes.double().t()
+        want *= x.row_scale[r:r + 1024].double()[:, None] * w.scales.double()
+        over = ((got[r:r + 1024].double() - want).abs() / ref.product_bound(want)).nan_to_num(nan=math.inf)
+        assert float(over.max()) <= 1.0, (m, n, k, r)
+    assert bool((y[m * n:] == 7.0).all())
+
+
+# whole rounds of tiles with columns left over, tiles cut along K, more groups than workgroups
+@pytest.mark.parametrize("m,n,k", [(2048, 17408, 512), (2048, 5120, 17408), (513, 17408, 1024), (512, 5120, 17408),
+                                   (1025, 8200, 4096), (4099, 4104, 1056), (300, 40000, 160), (128, 5120, 17408), (66, 70001, 96),
+                                   (96, 33000, 2048), (64, 17408, 5120), (33, 17416, 4096), (17, 50000, 512), (9, 5120, 17408),
+                                   (4, 130000, 256), (2, 300000, 64), (1, 17408, 5120), (1024, 64, 131072), (40, 64, 131072)])
+def test_product_large(m, n, k):
+    _say("product", m, n, k)
+    _large(m, n, k, m + n + k)
+
+
+@pytest.mark.parametrize("seed", range(40))
+def test_product_of_any_size(seed):
+    r = random.Random(seed)
+    log = lambda lo, hi: int(round(math.exp(r.uniform(math.log(lo), math.log(hi)))))  # noqa: E731
+    m, n, k = log(1, 3000), log(1, 20000), 32 * log(1, 600)
+    _say("product", m, n, k)
+    _large(m, n, k, seed)
 
 
 @pytest.mark.parametrize("n,k", [(129, 4128), (5120, 96), (48, 17408)])

@@ -24,7 +24,7 @@ def _w(n=64, k=64, codes=P, scales=P):
     return nv._CInt8Weight(codes, scales, n, k)
 
 
-def _gemm(m=2, w=None, x=P, xs=None, y=P, workspace=None, size=0):
+def _gemm(m=2, w=None, x=P, xs=None, y=2 * P, workspace=None, size=0):
     return _lib().int8_gemm_w8a8(x, xs, m, None if w is None else ctypes.byref(w), y, workspace, size, None)
 
 
@@ -46,6 +46,7 @@ def _ffn(m=2, hidden=64, inter=96, wg=None, wu=None, wd=None, x=P, xs=None, out=
     (dict(w=_w(), workspace=P + 16, size=1 << 30), nv.NVFP4_EINVAL, "256-byte"),
     (dict(w=_w(), workspace=P, size=1), nv.NVFP4_EINVAL, "bytes"),
     (dict(w=_w(), workspace=P, size=-1), nv.NVFP4_EINVAL, "bytes"),
+    (dict(w=_w(), y=P), nv.NVFP4_EINVAL, "y is x"),
     (dict(w=_w(), m=0), nv.NVFP4_OK, ""), (dict(w=_w(), m=0, x=None, y=None), nv.NVFP4_OK, ""),
 ])
 def test_product_refusals(kw, code, text):
@@ -118,7 +119,7 @@ def test_norm_refusals(kw, code, text):
 
 
 def _residual(m=6, k=64, residual=P, y=P, post=1, pw=P, gate=None, gates=0, scale=1.0, next=1, nw=P, offset=0.0, eps=1e-6,
-              h=P, out=P, codes=None, rs=None):
+              h=P, out=2 * P, codes=None, rs=None):
     return _lib().rms_norm_residual(residual, y, m, k, post, pw, gate, gates, scale, next, nw, offset, eps, h, out, codes,
                                     rs, None)
 
@@ -131,6 +132,7 @@ def _residual(m=6, k=64, residual=P, y=P, post=1, pw=P, gate=None, gates=0, scal
     (dict(gate=P, gates=-2), nv.NVFP4_EINVAL, "gates=-2"), (dict(gate=P, gates=4), nv.NVFP4_ESHAPE, "divide"),
     (dict(gate=P + 8, gates=2), nv.NVFP4_EINVAL, "gate must"), (dict(out=None), nv.NVFP4_EINVAL, "expected out"),
     (dict(next=0), nv.NVFP4_EINVAL, "without a next norm"), (dict(next=0, out=None, codes=P), nv.NVFP4_EINVAL, "without"),
+    (dict(out=P), nv.NVFP4_EINVAL, "one array"),
     (dict(eps=0.0), nv.NVFP4_EINVAL, "eps"), (dict(m=0), nv.NVFP4_OK, ""), (dict(m=0, gate=P, gates=4), nv.NVFP4_OK, ""),
 ])
 def test_residual_refusals(kw, code, text):
