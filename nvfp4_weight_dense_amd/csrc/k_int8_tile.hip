@@ -335,12 +335,14 @@ __global__ __launch_bounds__(kWaves * 64, 2) void k_int8_tile(TileArgs p) {
     ring_barrier();
     request(stage);
     stage = stage == S - 1 ? 0 : stage + 1;
-    read(stage, 0, f0);
+    const bool ends = ++at.unit == at.end;
+    if (!ends) read(stage, 0, f0);
     multiply(f1);
-    if (++at.unit == at.end) {
+    if (ends) {  // (the next operands only behind it: it has no registers to spare)
       flush(at.tile, at.part);
       ++at.done;
       go(at);
+      read(stage, 0, f0);
     }
   }
   wait_all_memory();
