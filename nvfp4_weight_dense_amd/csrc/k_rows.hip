@@ -164,8 +164,8 @@ template <bool WAVE>
 constexpr int most_threads() { return WAVE ? 64 * kWaveRows : kMaxThreads; }
 
 // With gridDim.y > 1 (few rows) each slice of a row is a workgroup: it looks
-// for the largest magnitude in all of the row and encodes its own pieces, so
-// that the divisions of a row spread over several CUs.
+// for the largest magnitude in all of the row and encodes every gridDim.y-th of
+// its threads' pieces, so that the divisions of a row spread over several CUs.
 template <bool WAVE, int P>
 __global__ __launch_bounds__(most_threads<WAVE>()) void k_int8_rows(const void *x, int m, int k, RowsOut o) {
   __shared__ uint32_t top[16];
@@ -183,10 +183,12 @@ __global__ __launch_bounds__(most_threads<WAVE>()) void k_int8_rows(const void *
   const Int8Row r =
       int8_row(over_row<WAVE>(amax_fold(bits), top, [](uint32_t a, uint32_t b) { return max(a, b); }));
   if (threadIdx.x == 0 && blockIdx.y == 0) o.row_scale[row] = r.s;
-  const int per = (pieces + (int)gridDim.y - 1) / (int)gridDim.y;
-  const int last = min(pieces, per * ((int)blockIdx.y + 1));
-  for (int p = per * (int)blockIdx.y + (int)threadIdx.x; p < last; p += (int)blockDim.x)
-    ((uint2 *)o.codes)[(size_t)row * pieces + p] = int8_codes(((const uint4 *)x)[(size_t)row * pieces + p], r);
+#pragma unroll
+  for (int i = 0; i < P; ++i) {
+    const int p = (int)threadIdx.x + i * (int)blockDim.x;
+    if (i % (int)gridDim.y == (int)blockIdx.y && p < pieces)
+      ((uint2 *)o.codes)[(size_t)row * pieces + p] = int8_codes(v[i], r);
+  }
 }
 
 template <int P>
@@ -290,10 +292,11 @@ hipError_t launch_int8_rows(const void *x, int m, int k, int8_t *codes, float *r
     else run(std::integral_constant<int, kWaveMaxPieces>());
     return hipGetLastError();
   }
-  // few rows: slices of 256 pieces or more, for about as many workgroups as CUs
-  const int slices = std::max(1, std::min({8, 256 / m, pieces / 256}));
-  const int p = row_pieces(k);
-  return with_pieces(p, [&](auto p) {
+  // few rows: up to eight slices, for about as many workgroups as CUs (64 rows
+  // of 17408: 8.4 us a call, 9.6 without), and a piece of a thread for each
+  int slices = 1;
+  while (slices < 8 && slices * 2 * m <= 256 && slices * 2 * 64 <= pieces) slices *= 2;
+  return with_pieces(std::max(row_pieces(k), slices), [&](auto p) {
     hipLaunchKernelGGL((k_int8_rows<false, decltype(p)::value>), dim3(m, slices), dim3(row_block(k, p)), 0, s, x, m, k, o);
   });
 }
