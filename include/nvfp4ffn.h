@@ -364,7 +364,8 @@ int dense_ffn_forward_int8(const void *x, const float *row_scale, int32_t m, int
  * norm(x) = x / sqrt(mean(x^2) + eps) * (offset + weight), over rows of k
  * values, k a positive multiple of 8 up to 131072; without a weight (null) the
  * last factor is 1.  offset is 0, or 1 for weights kept as their distance from
- * one.  1e-18 <= eps <= 1.  Statistics are fp32 and hold for every finite row. */
+ * one.  1e-18 <= eps <= 1.  Statistics are fp32 and hold for every finite row.  Row r's
+ * bits are the same for every m. */
 
 /* The norm before a block.  x: bf16 [m][k]; weight: bf16 [k] or null.  The
  * result is rounded to bf16 and written to out (bf16 [m][k]; may be x), or,

@@ -6,7 +6,11 @@
 //   residual: h = bf16(residual + scale * gate * norm(y)), then norm(h)
 //   int8:    s = amax / 127, code = x / s (int8_common.h)
 //
-// All are bound by memory: a workgroup takes a row -- for the quantizer, where
+// All are bound by memory: norm of 8192 rows of 5120 28.8 us (5.8 TB/s), end
+// of a block with post norm, int8 and no gate 64 us (4.6), quantizer of 17408
+// rows of 5120 44 us (6.0); a large copy makes 4.8.  With few rows what counts
+// is the way of one row through memory and the exchanges: 64 rows of 5120
+// 4.6, 6.3 and 4 us.  A workgroup takes a row -- for the quantizer, where
 // there are many rows that are not too long, a wave --, each thread keeps its
 // pieces of eight values in registers from the one read of the row to the one
 // write, and what the row needs as a whole (a sum of squares, a largest
@@ -58,6 +62,16 @@ __device__ __forceinline__ int row_threads() {
   return WAVE ? 64 : (int)blockDim.x;
 }
 
+template <bool WAVE, int P>
+__device__ __forceinline__ void read_row(const void *x, int row, int pieces, uint4 (&v)[P]) {
+  const uint4 *at = (const uint4 *)x + (size_t)row * pieces;
+#pragma unroll
+  for (int i = 0; i < P; ++i) {
+    const int p = row_thread<WAVE>() + i * row_threads<WAVE>();
+    v[i] = p < pieces ? at[p] : uint4{0u, 0u, 0u, 0u};
+  }
+}
+
 // One value of every thread combined over the row's.  `slots`: 16 words of
 // LDS that no other exchange of the kernel uses.
 template <bool WAVE, class T, class Op>
@@ -95,20 +109,39 @@ __device__ __forceinline__ float row_rstd(uint4 (&v)[P], int k, float eps, float
   return __builtin_amdgcn_rsqf(squares(0x1p-80f, slots[1]) / (float)k) * 0x1p-80f;  // (eps is far below)
 }
 
+// A row beside the one that is normed (weights, gate, residual).  It is
+// requested with it, so that nothing waits for memory behind a sum (64 rows of
+// 5120, end of a block with all of them: 8.1 -> 6.2 us; 4099 rows of 4096 with
+// a gate to a row: 31.4 -> 27.9); rows too long for the registers are read
+// where they are used.
+template <int P>
+struct Beside {
+  static constexpr bool kHeld = P <= 4;
+  const uint4 *at;  // null: there is none
+  uint4 v[kHeld ? P : 1];
+  __device__ __forceinline__ Beside(const void *base, int row, int pieces)
+      : at(base ? (const uint4 *)base + (size_t)row * pieces : nullptr) {
+    if constexpr (kHeld) {
+      if (at) read_row<false>(base, row, pieces, v);
+    }
+  }
+  __device__ __forceinline__ void get(int i, int p, int pieces, float (&f)[8]) const {
+    if constexpr (kHeld) unpack8(v[i], f);
+    else unpack8(p < pieces ? at[p] : uint4{0u, 0u, 0u, 0u}, f);
+  }
+};
+
 // v = bf16(v * rstd * (offset + weight)), or without a weight bf16(v * rstd)
 template <int P>
-__device__ __forceinline__ void scale_row(uint4 (&v)[P], const uint4 *weight, float offset, float rstd, int pieces) {
+__device__ __forceinline__ void scale_row(uint4 (&v)[P], const Beside<P> &weight, float offset, float rstd, int pieces) {
 #pragma unroll
   for (int i = 0; i < P; ++i) {
-    const int p = (int)threadIdx.x + i * (int)blockDim.x;
-    if (p >= pieces) break;
-    float f[8];
+    float f[8], w[8];
     unpack8(v[i], f);
 #pragma unroll
     for (int j = 0; j < 8; ++j) f[j] *= rstd;
-    if (weight) {
-      float w[8];
-      unpack8(weight[p], w);
+    if (weight.at) {
+      weight.get(i, (int)threadIdx.x + i * (int)blockDim.x, pieces, w);
 #pragma unroll
       for (int j = 0; j < 8; ++j) f[j] *= offset + w[j];
     }
@@ -139,16 +172,6 @@ __device__ __forceinline__ void write_row(const uint4 (&v)[P], const RowsOut &o,
   for (int i = 0; i < P; ++i) {
     const int p = row_thread<WAVE>() + i * row_threads<WAVE>();
     if (p < pieces) to[p] = int8_codes(v[i], r);
-  }
-}
-
-template <bool WAVE, int P>
-__device__ __forceinline__ void read_row(const void *x, int row, int pieces, uint4 (&v)[P]) {
-  const uint4 *at = (const uint4 *)x + (size_t)row * pieces;
-#pragma unroll
-  for (int i = 0; i < P; ++i) {
-    const int p = row_thread<WAVE>() + i * row_threads<WAVE>();
-    v[i] = p < pieces ? at[p] : uint4{0u, 0u, 0u, 0u};
   }
 }
 
@@ -198,8 +221,9 @@ __global__ __launch_bounds__(kMaxThreads) void k_rms_norm(const void *x, int k, 
   const int row = (int)blockIdx.x, pieces = k >> 3;
   uint4 v[P];
   read_row<false>(x, row, pieces, v);
+  const Beside<P> weight(n.weight, 0, pieces);
   const float rstd = row_rstd(v, k, eps, sums);
-  scale_row(v, (const uint4 *)n.weight, n.offset, rstd, pieces);
+  scale_row(v, weight, n.offset, rstd, pieces);
   write_row<false>(v, o, row, pieces, top);
 }
 
@@ -208,50 +232,49 @@ __global__ __launch_bounds__(kMaxThreads) void k_rms_norm_residual(ResidualArgs 
   __shared__ float sums[4][16];
   __shared__ uint32_t top[16];
   const int row = (int)blockIdx.x, pieces = k >> 3;
-  uint4 v[P], r[P];
+  uint4 v[P];
   read_row<false>(a.y, row, pieces, v);
-  read_row<false>(a.residual, row, pieces, r);
+  const Beside<P> residual(a.residual, row, pieces), gate(a.gate, row / a.rows_per_gate, pieces),
+      post(a.post.on ? a.post.weight : nullptr, 0, pieces), next(a.next.on ? a.next.weight : nullptr, 0, pieces);
   const float rstd = a.post.on ? row_rstd(v, k, eps, sums) : 1.0f;
-  const uint4 *post = a.post.on ? (const uint4 *)a.post.weight : nullptr;
-  const uint4 *gate = a.gate ? (const uint4 *)a.gate + (size_t)(row / a.rows_per_gate) * pieces : nullptr;
   uint4 *h = (uint4 *)a.h + (size_t)row * pieces;
 #pragma unroll
   for (int i = 0; i < P; ++i) {
     const int p = (int)threadIdx.x + i * (int)blockDim.x;
-    if (p >= pieces) break;
     float f[8], g[8];
     unpack8(v[i], f);
 #pragma unroll
     for (int j = 0; j < 8; ++j) f[j] *= rstd;
-    if (post) {
-      unpack8(post[p], g);
+    if (post.at) {
+      post.get(i, p, pieces, g);
 #pragma unroll
       for (int j = 0; j < 8; ++j) f[j] *= a.post.offset + g[j];
     }
-    if (gate) {
-      unpack8(gate[p], g);
+    if (gate.at) {
+      gate.get(i, p, pieces, g);
 #pragma unroll
       for (int j = 0; j < 8; ++j) f[j] *= g[j];
     }
-    unpack8(r[i], g);
+    residual.get(i, p, pieces, g);
 #pragma unroll
     for (int j = 0; j < 8; ++j) f[j] = fmaf(a.scale, f[j], g[j]);
-    v[i] = pack8(f);
-    h[p] = v[i];
+    v[i] = p < pieces ? pack8(f) : uint4{0u, 0u, 0u, 0u};
+    if (p < pieces) h[p] = v[i];
   }
   if (!a.next.on) return;
-  const float next = row_rstd(v, k, eps, sums + 2);
-  scale_row(v, (const uint4 *)a.next.weight, a.next.offset, next, pieces);
+  const float again = row_rstd(v, k, eps, sums + 2);
+  scale_row(v, next, a.next.offset, again, pieces);
   write_row<false>(v, o, row, pieces, top);
 }
 
-// Pieces of a thread, for a workgroup to a row: two or four, so that a row of
-// 4096 or 5120 values is four or three waves' (8192 rows of 5120: norm 32, end
-// of a block 60 us; 40 and 88 with one piece a thread, 35 and 62 with eight),
-// and more where 1024 threads do not hold a row so.
+// Pieces of a thread, for a workgroup to a row: two (8192 rows of 5120, norm
+// 28 and end of a block 64 us; with one 36 and 87, with four 32 and 68), and
+// more where 1024 threads do not hold a row so.  Not by the number of rows: a
+// row's sums then have one order and its results the same bits in any batch
+// (with one piece 64 rows would take 4.4 and 5.9 us in place of 4.6 and 6.2).
 int row_pieces(int k) {
   const int pieces = k >> 3;
-  int p = pieces > 512 ? 4 : pieces > 256 ? 2 : 1;
+  int p = pieces > 256 ? 2 : 1;
   while (cdiv(pieces, p) > kMaxThreads) p *= 2;
   return p;
 }

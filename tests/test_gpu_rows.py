@@ -191,3 +191,17 @@ def test_no_rows():
     assert nv.rms_norm(x).shape == (0, 64) and nv.rms_norm(x, int8=True).codes.shape == (0, 64)
     h, n = nv.rms_norm_residual(x, x, norm=True, gate=torch.ones(64, dtype=BF, device="cuda"))
     assert h.shape == n.shape == (0, 64)
+
+
+@pytest.mark.parametrize("k", [8, 4096, 5128, 17408, 40000])
+def test_a_row_does_not_depend_on_its_batch(k):
+    _say("rows alone", k)
+    m, few = 1100 if k < 17408 else 300, (1, 7, 257)
+    r, y, w = _rows(m, k, 11).cuda(), _rows(m, k, 12).cuda(), _vec(k, 13).cuda()
+    norm, quant = nv.rms_norm(y, w), nv.int8_quantize_rows(y)
+    h, n = nv.rms_norm_residual(r, y, post=w, scale=0.5, norm=True)
+    for i in few:
+        assert torch.equal(nv.rms_norm(y[:i], w), norm[:i])
+        assert _same_rows(nv.int8_quantize_rows(y[:i]), (quant.codes[:i], quant.row_scale[:i]))
+        h2, n2 = nv.rms_norm_residual(r[:i], y[:i], post=w, scale=0.5, norm=True)
+        assert torch.equal(h2, h[:i]) and torch.equal(n2, n[:i])
