@@ -326,7 +326,7 @@ typedef struct int8_weight {
 } int8_weight;
 
 /* Per-row int8 quantizer.  x: bf16 [m][k], k a multiple of 8, at most 131072.
- * Outputs: codes int8 [m][k], row_scale fp32 [m]. */
+ * Outputs, apart from x: codes int8 [m][k], row_scale fp32 [m]. */
 int int8_quantize_rows(const void *x, int32_t m, int32_t k, int8_t *codes, float *row_scale, void *stream);
 
 /* Bytes of workspace that int8_gemm_w8a8 takes for these sizes or fewer rows;
@@ -364,13 +364,14 @@ int dense_ffn_forward_int8(const void *x, const float *row_scale, int32_t m, int
  * norm(x) = x / sqrt(mean(x^2) + eps) * (offset + weight), over rows of k
  * values, k a positive multiple of 8 up to 131072; without a weight (null) the
  * last factor is 1.  offset is 0, or 1 for weights kept as their distance from
- * one.  1e-18 <= eps <= 1.  Statistics are fp32 and hold for every finite row.  Row r's
- * bits are the same for every m. */
+ * one.  1e-18 <= eps <= 1.  Statistics are fp32 and hold for every finite row.
+ * Row r's bits are the same for every m. */
 
 /* The norm before a block.  x: bf16 [m][k]; weight: bf16 [k] or null.  The
  * result is rounded to bf16 and written to out (bf16 [m][k]; may be x), or,
  * where out is null, quantized by rows (see above) to codes (int8 [m][k]) and
- * row_scale (fp32 [m]) -- the bits of int8_quantize_rows on out. */
+ * row_scale (fp32 [m]), neither of them an input -- the bits of
+ * int8_quantize_rows on out. */
 int rms_norm(const void *x, int32_t m, int32_t k, const void *weight, float offset, float eps, void *out,
              int8_t *codes, float *row_scale, void *stream);
 

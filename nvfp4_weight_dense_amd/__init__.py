@@ -757,8 +757,8 @@ def int8_quantize_rows(x: torch.Tensor, stream=None) -> Int8Rows:
 def int8_workspace(m: int, *weights) -> torch.Tensor:
     """A workspace for calls of int8_gemm_w8a8 (one weight) or
     dense_ffn_forward_int8 (wg, wu, wd) with these weights and m rows or fewer,
-    for one stream.  Without one, calls share the library's scratch arena; a
-    captured call has to bring one."""
+    for one stream (it is cleared on the current one).  Without one, calls
+    share the library's scratch arena; a captured call has to bring one."""
     L = load_library()
     c = [_cint8(w) for w in weights]
     m = _i32(m, "m")

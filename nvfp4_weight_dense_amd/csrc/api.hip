@@ -19,6 +19,10 @@
 //          kernel, more rows the many-row kernel when k % 64 == 0 (gate+up+
 //          silu fused, then down; the weights dequantized in registers, never
 //          copied to bf16), else the streaming kernel with 64-row blocks.
+//   INT8:  quantize x -> gate+up+silu -> act -> quantize act -> down; up to 4
+//          rows the projections quantize their rows themselves.  Sums are of
+//          whole numbers, so the kernels for 1..4, 5..64 and more rows give a
+//          row the same bits.
 // Every check runs before the first launch; a forced path that cannot serve a
 // shape is an error, never a silent fallback (the pages refuse to start with
 // a requested but missing variant: page layers/mod.rs, `w4a16_v2_kernel`).
@@ -1288,6 +1292,7 @@ int int8_quantize_rows(const void *x, int32_t m, int32_t k, int8_t *codes, float
   if (m == 0) return NVFP4_OK;
   if (!codes || !row_scale) return fail(NVFP4_EINVAL, "int8_quantize_rows: null output pointer");
   if ((rc = check_rows_out(nullptr, codes, row_scale, "int8_quantize_rows"))) return rc;
+  if (codes == x) return fail(NVFP4_EINVAL, "int8_quantize_rows: codes is x");
   return hip_status(launch_int8_rows(x, m, k, codes, row_scale, (hipStream_t)stream), "int8_quantize_rows launch");
 }
 
@@ -1369,6 +1374,7 @@ int rms_norm(const void *x, int32_t m, int32_t k, const void *weight, float offs
     return rc;
   if (m == 0) return NVFP4_OK;
   if ((rc = check_rows_out(out, codes, row_scale, "rms_norm"))) return rc;
+  if (codes == x) return fail(NVFP4_EINVAL, "rms_norm: codes is x");
   return hip_status(launch_rms_norm(x, m, k, NormRef{weight, offset, true}, eps, RowsOut{out, codes, row_scale},
                                     (hipStream_t)stream),
                     "rms_norm launch");
@@ -1394,6 +1400,8 @@ int rms_norm_residual(const void *residual, const void *y, int32_t m, int32_t k,
   if (next && (rc = check_rows_out(out, codes, row_scale, name))) return rc;
   if (out && out == h) return fail(NVFP4_EINVAL, "%s: h and out are one array", name);
   if (!next && (out || codes || row_scale)) return fail(NVFP4_EINVAL, "%s: an output without a next norm", name);
+  if (codes && (codes == residual || codes == y || codes == h))
+    return fail(NVFP4_EINVAL, "%s: codes is residual, y or h", name);
   const ResidualArgs a{residual, y, gate, gate ? m / gates : 1, scale, {post_weight, offset, post != 0},
                        {next_weight, offset, next != 0}, h};
   return hip_status(launch_rms_norm_residual(a, m, k, eps, RowsOut{out, codes, row_scale}, (hipStream_t)stream),

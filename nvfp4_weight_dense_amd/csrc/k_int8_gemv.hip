@@ -8,7 +8,10 @@
 // in equal runs whatever the number of columns: sums of whole numbers may be
 // joined in any order, so a row that several waves share is summed with LDS
 // atomics.  Eight pieces are requested while eight are summed (128 to 256 KB
-// in flight for a CU).
+// in flight for a CU).  One row of 4096, 12288: gate and up with the row
+// quantized 21.8 us (4.6 TB/s), down 12.6 us (4.0); a product of 6144 x 4096
+// of quantized rows 8.5 us, of which start, the first way through memory and
+// the end are some 5.
 //
 // The activation rows lie in LDS as codes; lane l multiplies codes 16 l .. of
 // a piece with dot products of four.  bf16 rows are quantized here, in every

@@ -18,6 +18,13 @@
 // neighbouring columns of one row, and after a trade between lanes stores
 // eight of them at once.  The scales come into LDS with a tile's first unit,
 // so that a tile's end waits for no memory.
+//
+// 8192 x 8192 x 8192 465 to 480 us (2290 to 2360 TOP/s; a library's product of
+// that size 534); 2048 rows of 17408 x 5120 in two launches 205, gate and up
+// of the same FFN 340 to 350, down 185 to 195.  The matrix cores are 55% busy
+// in tiles of 256 x 256 (48% in 256 x 128), 80% of the lines come from L2, no
+// bank conflicts.  Of the products and the transfers either alone takes 80% of
+// the time: they share the LDS.
 #include "int8_common.h"
 
 namespace nvfp4 {

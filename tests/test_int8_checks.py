@@ -139,6 +139,16 @@ def test_residual_refusals(kw, code, text):
     assert _residual(**kw) == code and text in nv.nvfp4_last_error()
 
 
+@pytest.mark.parametrize("call,kw", [
+    (_quant, dict()), (_norm, dict(out=None, codes=P, rs=2 * P)), (_residual, dict(out=None, codes=P, rs=2 * P, y=3 * P, h=4 * P)),
+    (_residual, dict(out=None, codes=P, rs=2 * P, residual=3 * P, h=4 * P)),
+    (_residual, dict(out=None, codes=P, rs=2 * P, residual=3 * P, y=4 * P)),
+])
+def test_codes_are_no_input(call, kw):
+    """A row's codes lie where other rows' values would still be read."""
+    assert call(**kw) == nv.NVFP4_EINVAL and "codes is" in nv.nvfp4_last_error()
+
+
 BF = torch.bfloat16
 
 
