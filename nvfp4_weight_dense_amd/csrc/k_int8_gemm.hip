@@ -203,10 +203,9 @@ __global__ __launch_bounds__(kWaves * 64, 2) void k_int8_gemm(Int8Args p) {
         }
         __bf16 *to = (__bf16 *)p.y + (size_t)r * p.n + col;
         if (r >= p.m) continue;
-        if ((p.n & 3) == 0) {
-          if (col < p.n)
-            *(uint2 *)to = uint2{__builtin_bit_cast(uint32_t, bf16x2{v[0], v[1]}),
-                                 __builtin_bit_cast(uint32_t, bf16x2{v[2], v[3]})};
+        if (col + 4 <= p.n) {
+          *(u32x2_at2 *)to = u32x2_at2{__builtin_bit_cast(uint32_t, bf16x2{v[0], v[1]}),
+                                       __builtin_bit_cast(uint32_t, bf16x2{v[2], v[3]})};
         } else {
 #pragma unroll
           for (int e = 0; e < 4; ++e)

@@ -226,7 +226,6 @@ __global__ __launch_bounds__(kWaves * 64, 2) void k_int8_tile(TileArgs p) {
     place(tile, rb, cg);
     const float *set = scales[epilogue_set];
     const int row0 = rb * C::kRows + wm * MT * 32 + c;
-    const bool pieces = (p.ldy & 7) == 0;
 #pragma unroll
     for (int j = 0; j < (NMAT > 1 ? 1 : 2); ++j)
 #pragma unroll
@@ -255,19 +254,18 @@ __global__ __launch_bounds__(kWaves * 64, 2) void k_int8_tile(TileArgs p) {
             v[e >> 1] = __builtin_bit_cast(uint32_t, two);
           }
           __bf16 *to = (__bf16 *)p.y + (size_t)r * p.ldy + col0;
-          if (pieces) {
-            // Lane (c, 0) holds columns 0..3 of either eight and lane (c, 1)
-            // columns 4..7: they trade halves, and each has a whole eight.
-            const auto lo = __builtin_amdgcn_permlane32_swap(v[0], v[2], false, false);
-            const auto hi = __builtin_amdgcn_permlane32_swap(v[1], v[3], false, false);
-            if (r < p.m && col0 + 8 * h < p.n) *(uint4 *)(to + 8 * h) = uint4{lo[0], hi[0], lo[1], hi[1]};
-          } else {
+          // Lane (c, 0) holds columns 0..3 of either eight and lane (c, 1)
+          // columns 4..7: they trade halves, and each has a whole eight.
+          const auto lo = __builtin_amdgcn_permlane32_swap(v[0], v[2], false, false);
+          const auto hi = __builtin_amdgcn_permlane32_swap(v[1], v[3], false, false);
+          const u32x4_at2 eight{lo[0], hi[0], lo[1], hi[1]};
+          const int left = p.n - (col0 + 8 * h);
+          if (r < p.m && left >= 8) {
+            *(u32x4_at2 *)(to + 8 * h) = eight;
+          } else if (r < p.m) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const int at = 8 * (e >> 2) + 4 * h + (e & 3);
-              if (r < p.m && col0 + at < p.n)
-                to[at] = __builtin_bit_cast(__bf16, (uint16_t)(e & 1 ? v[e >> 1] >> 16 : v[e >> 1]));
-            }
+            for (int e = 0; e < 8; ++e)
+              if (e < left) to[8 * h + e] = __builtin_bit_cast(__bf16, (uint16_t)(e & 1 ? eight[e >> 1] >> 16 : eight[e >> 1]));
           }
         }
       }
