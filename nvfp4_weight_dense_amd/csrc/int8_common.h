@@ -97,14 +97,14 @@ __device__ __forceinline__ void to_lds(u32x4_t r, uint32_t lds, uint32_t voff, u
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
                :
                : "s"(lds), "v"(voff), "s"(r), "s"(soff)
-               : "memory", "m0");
+               : "memory");
 }
 // Likewise 4 bytes a lane.
 __device__ __forceinline__ void words_to_lds(u32x4_t r, uint32_t lds, uint32_t voff) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds"
                :
                : "s"(lds), "v"(voff), "s"(r)
-               : "memory", "m0");
+               : "memory");
 }
 __device__ __forceinline__ u32x4_t range_of(const void *base, size_t bytes) {
   const uint64_t a = (uint64_t)base;
