@@ -326,7 +326,7 @@ typedef struct int8_weight {
 } int8_weight;
 
 /* Per-row int8 quantizer.  x: bf16 [m][k], k a multiple of 8, at most 131072.
- * Outputs, apart from x: codes int8 [m][k], row_scale fp32 [m]. */
+ * Outputs, apart from x and one another: codes int8 [m][k], row_scale fp32 [m]. */
 int int8_quantize_rows(const void *x, int32_t m, int32_t k, int8_t *codes, float *row_scale, void *stream);
 
 /* Bytes of workspace that int8_gemm_w8a8 takes for these sizes or fewer rows;
@@ -355,7 +355,7 @@ int64_t dense_ffn_int8_workspace(int32_t m, int32_t hidden, int32_t inter);
  * each projection; gate, up and act are rounded to bf16.  Row r's output bits
  * do not depend on m, and are those of int8_gemm_w8a8 and silu_mul one by one.
  * x and row_scale, workspace: as in int8_gemm_w8a8.  wg, wu: [inter][hidden];
- * wd: [hidden][inter]; out: bf16 [m][hidden], none of the inputs. */
+ * wd: [hidden][inter]; out: bf16 [m][hidden], apart from the weights. */
 int dense_ffn_forward_int8(const void *x, const float *row_scale, int32_t m, int32_t hidden, int32_t inter,
                            const int8_weight *wg, const int8_weight *wu, const int8_weight *wd, void *out,
                            void *workspace, int64_t workspace_bytes, void *stream);
@@ -370,8 +370,8 @@ int dense_ffn_forward_int8(const void *x, const float *row_scale, int32_t m, int
 /* The norm before a block.  x: bf16 [m][k]; weight: bf16 [k] or null.  The
  * result is rounded to bf16 and written to out (bf16 [m][k]; may be x), or,
  * where out is null, quantized by rows (see above) to codes (int8 [m][k]) and
- * row_scale (fp32 [m]), neither of them an input -- the bits of
- * int8_quantize_rows on out. */
+ * row_scale (fp32 [m]) -- the bits of int8_quantize_rows on out.  Outputs
+ * share no memory with weight, nor (out that is x apart) with x. */
 int rms_norm(const void *x, int32_t m, int32_t k, const void *weight, float offset, float eps, void *out,
              int8_t *codes, float *row_scale, void *stream);
 
@@ -382,7 +382,9 @@ int rms_norm(const void *x, int32_t m, int32_t k, const void *weight, float offs
  * next_weight: bf16 [k] or null (no weight).  gate: bf16 [gates][k], gates a
  * divisor of m: row r takes gate row r / (m / gates) (1: one value for each
  * channel; m: one for each value; between: one for each sequence of equal
- * length); null with gates 0: no gate.  fp32 up to the two roundings. */
+ * length); null with gates 0: no gate.  fp32 up to the two roundings.
+ * Outputs share no memory with the weights, the gate or one another; h and
+ * out share none with residual or y but as those whole arrays. */
 int rms_norm_residual(const void *residual, const void *y, int32_t m, int32_t k, int32_t post,
                       const void *post_weight, const void *gate, int32_t gates, float scale, int32_t next,
                       const void *next_weight, float offset, float eps, void *h, void *out, int8_t *codes,

@@ -33,6 +33,7 @@
 #include <cstdio>
 #include <cstdlib>
 #include <cstring>
+#include <initializer_list>
 #include <mutex>
 #include <set>
 #include <string>
@@ -700,6 +701,26 @@ int check_rows_out(const void *out, const int8_t *codes, const float *row_scale,
   return NVFP4_OK;
 }
 
+// An array of a call: its name, and where it lies.
+struct Span {
+  const char *name;
+  const void *at;
+  size_t bytes;
+};
+bool meet(const Span &a, const Span &b) {
+  return a.at && b.at && (uintptr_t)a.at < (uintptr_t)b.at + b.bytes && (uintptr_t)b.at < (uintptr_t)a.at + a.bytes;
+}
+// An output shares no memory with what rows other than the one being written
+// still read or write: with none of `others`, and with the rows of `same` only
+// where it is that whole array.
+int check_apart(const char *name, const Span &out, std::initializer_list<Span> others, std::initializer_list<Span> same = {}) {
+  for (const Span &o : others)
+    if (meet(out, o)) return fail(NVFP4_EINVAL, "%s: %s %s %s", name, out.name, out.at == o.at ? "is" : "shares memory with", o.name);
+  for (const Span &o : same)
+    if (out.at != o.at && meet(out, o)) return fail(NVFP4_EINVAL, "%s: %s shares memory with other rows of %s", name, out.name, o.name);
+  return NVFP4_OK;
+}
+
 int check_norm(const void *weight, float offset, float eps, const char *name) {
   if (misaligned(weight)) return fail(NVFP4_EINVAL, "%s: weights must be 16-byte aligned", name);
   if (!(fabsf(offset) < INFINITY)) return fail(NVFP4_EINVAL, "%s: offset is not finite", name);
@@ -1292,7 +1313,8 @@ int int8_quantize_rows(const void *x, int32_t m, int32_t k, int8_t *codes, float
   if (m == 0) return NVFP4_OK;
   if (!codes || !row_scale) return fail(NVFP4_EINVAL, "int8_quantize_rows: null output pointer");
   if ((rc = check_rows_out(nullptr, codes, row_scale, "int8_quantize_rows"))) return rc;
-  if (codes == x) return fail(NVFP4_EINVAL, "int8_quantize_rows: codes is x");
+  const Span in{"x", x, (size_t)2 * m * k}, co{"codes", codes, (size_t)m * k}, rs{"row_scale", row_scale, (size_t)4 * m};
+  if ((rc = check_apart("int8_quantize_rows", co, {in})) || (rc = check_apart("int8_quantize_rows", rs, {in, co}))) return rc;
   return hip_status(launch_int8_rows(x, m, k, codes, row_scale, (hipStream_t)stream), "int8_quantize_rows launch");
 }
 
@@ -1311,7 +1333,11 @@ int int8_gemm_w8a8(const void *x, const float *row_scale, int32_t m, const int8_
   if ((rc = check_int8_x(x, row_scale, m)) || (rc = check_act(y, m, "y")) || (rc = check_int8_weight(w, "w")))
     return rc;
   if (m == 0) return NVFP4_OK;
-  if (x == y) return fail(NVFP4_EINVAL, "int8_gemm_w8a8: y is x");
+  if ((rc = check_apart("int8_gemm_w8a8", Span{"y", y, (size_t)2 * m * w->n},
+                        {Span{"x", x, (size_t)(row_scale ? 1 : 2) * m * w->k}, Span{"row_scale", row_scale, (size_t)4 * m},
+                         Span{"the weight's codes", w->codes, (size_t)w->n * w->k},
+                         Span{"the weight's scales", w->scales, (size_t)4 * w->n}})))
+    return rc;
   hipStream_t s = (hipStream_t)stream;
   const Int8Product pr(row_scale != nullptr, m, w->n, w->k, 1);
   unsigned *counters = nullptr;
@@ -1356,6 +1382,10 @@ int dense_ffn_forward_int8(const void *x, const float *row_scale, int32_t m, int
   if ((rc = int8_scratch("dense_ffn_forward_int8", workspace, workspace_bytes, act_b + std::max(up.bytes, down.bytes), s,
                          &counters, &base)))
     return rc;
+  // (x may be out: the last launch, which writes out, does not read it)
+  if ((rc = check_apart("dense_ffn_forward_int8", Span{"out", out, (size_t)2 * m * hidden},
+                        {Span{"wd's codes", wd->codes, (size_t)hidden * inter}, Span{"wd's scales", wd->scales, (size_t)4 * hidden}})))
+    return rc;
   ProfileScope ps("dense_total int8", m, s);
   const Int8MatRef w2[2] = {int8_mat(wg), int8_mat(wu)}, wdm = int8_mat(wd);
   char *act = base, *rest = base + act_b;
@@ -1374,7 +1404,10 @@ int rms_norm(const void *x, int32_t m, int32_t k, const void *weight, float offs
     return rc;
   if (m == 0) return NVFP4_OK;
   if ((rc = check_rows_out(out, codes, row_scale, "rms_norm"))) return rc;
-  if (codes == x) return fail(NVFP4_EINVAL, "rms_norm: codes is x");
+  const Span in{"x", x, (size_t)2 * m * k}, we{"weight", weight, (size_t)2 * k}, co{"codes", codes, (size_t)m * k};
+  if ((rc = check_apart("rms_norm", Span{"out", out, in.bytes}, {we}, {in})) || (rc = check_apart("rms_norm", co, {in, we})) ||
+      (rc = check_apart("rms_norm", Span{"row_scale", row_scale, (size_t)4 * m}, {in, we, co})))
+    return rc;
   return hip_status(launch_rms_norm(x, m, k, NormRef{weight, offset, true}, eps, RowsOut{out, codes, row_scale},
                                     (hipStream_t)stream),
                     "rms_norm launch");
@@ -1400,8 +1433,14 @@ int rms_norm_residual(const void *residual, const void *y, int32_t m, int32_t k,
   if (next && (rc = check_rows_out(out, codes, row_scale, name))) return rc;
   if (out && out == h) return fail(NVFP4_EINVAL, "%s: h and out are one array", name);
   if (!next && (out || codes || row_scale)) return fail(NVFP4_EINVAL, "%s: an output without a next norm", name);
-  if (codes && (codes == residual || codes == y || codes == h))
-    return fail(NVFP4_EINVAL, "%s: codes is residual, y or h", name);
+  const size_t rows = (size_t)2 * m * k, vec = (size_t)2 * k;
+  const Span re{"residual", residual, rows}, yy{"y", y, rows}, hh{"h", h, rows}, ga{"gate", gate, gates * vec},
+      pw{"post_weight", post ? post_weight : nullptr, vec}, nw{"next_weight", next ? next_weight : nullptr, vec},
+      co{"codes", codes, rows / 2};
+  if ((rc = check_apart(name, co, {re, yy, hh, ga, pw, nw})) || (rc = check_apart(name, hh, {ga, pw, nw}, {re, yy})) ||
+      (rc = check_apart(name, Span{"out", out, rows}, {hh, ga, pw, nw}, {re, yy})) ||
+      (rc = check_apart(name, Span{"row_scale", row_scale, (size_t)4 * m}, {re, yy, hh, ga, pw, nw, co})))
+    return rc;
   const ResidualArgs a{residual, y, gate, gate ? m / gates : 1, scale, {post_weight, offset, post != 0},
                        {next_weight, offset, next != 0}, h};
   return hip_status(launch_rms_norm_residual(a, m, k, eps, RowsOut{out, codes, row_scale}, (hipStream_t)stream),
