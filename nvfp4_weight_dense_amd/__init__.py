@@ -876,8 +876,10 @@ def rms_norm_residual(residual: torch.Tensor, y: torch.Tensor, *, post=None, gat
                 or gate.dim() not in (1, 2) or gate.shape[-1] != k:
             raise ValueError(f"gate: expected a contiguous bfloat16 [{k}] or [gates, {k}] tensor")
         gates = 1 if gate.dim() == 1 else gate.shape[0]
-        if gates == 0 or m % gates:
+        if m % gates if gates else m:
             raise ValueError(f"gate: {gates} rows do not divide {m}")
+        if not gates:  # (no rows, no gates)
+            gate = None
     h, out = _bf16_out(h, (m, k), "h"), _bf16_out(out, (m, k), "out")
     if out is not None and (int8 or not nxt):
         raise ValueError("out: only the bf16 result of a norm is written to it")
