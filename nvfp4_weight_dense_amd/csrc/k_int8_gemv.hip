@@ -27,7 +27,13 @@ namespace {
 constexpr int kThreads = 1024, kWaves = 16;
 constexpr int kBatch = 8;     // pieces requested together by a wave
 constexpr int kMaxCols = 512; // columns of a workgroup
-constexpr int kXPieces = 9;   // pieces of eight bf16 values that a thread quantizes
+// Pieces of eight bf16 values that a thread quantizes: one or two rows of any
+// length that LDS takes, three or four up to 16384.  Each workgroup encodes
+// all rows, so longer ones of three or four go faster through the quantizer
+// and the kernel for up to 64 rows: 4 rows of 5120 x 12288 19.8 us here and
+// 20.2 there, 5120 x 17408 26.3 and 24.7, 8192 x 16384 35.6 and 31.4 (5120 x
+// 16384 24.6 and 27.1); 2 rows of 5120 x 17408 21.6 and 24.7.
+constexpr int kXPieces = 8;
 
 struct GemvArgs {
   const void *x;        // bf16 [m][k], or int8 [m][k] with

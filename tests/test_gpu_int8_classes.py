@@ -54,3 +54,17 @@ def test_two_matrices(m, inter, hidden):
     act = nv.silu_mul(nv.int8_gemm_w8a8(x, wg), nv.int8_gemm_w8a8(x, wu))
     assert torch.equal(got, nv.int8_gemm_w8a8(act, wd))
     assert bool((out[m:] == 7.0).all()) and bool(got.any())
+
+
+# where the kernel for few rows takes bf16 rows no more (longest rows of 3 and 4, of 1 and 2), and where its LDS ends
+@pytest.mark.parametrize("k", [16352, 16384, 16416, 18464, 32768, 32800])
+@pytest.mark.parametrize("m", [1, 2, 3, 4])
+def test_few_long_rows(m, k):
+    """The bits of the same rows among more, as bf16 and as int8."""
+    print("few rows", m, k, flush=True)
+    g = torch.Generator(device="cuda").manual_seed(m + k)
+    x = torch.randn(7, k, generator=g, device="cuda").to(BF)
+    w = nv.Int8Weight(_codes(g, 300, k), torch.rand(300, generator=g, device="cuda") + 0.5)
+    want = nv.int8_gemm_w8a8(x, w)[:m]
+    assert torch.equal(nv.int8_gemm_w8a8(x[:m], w), want)
+    assert torch.equal(nv.int8_gemm_w8a8(nv.int8_quantize_rows(x[:m]), w), want)
