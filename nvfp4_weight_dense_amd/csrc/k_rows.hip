@@ -293,27 +293,39 @@ hipError_t with_pieces(int p, F &&f) {
   return hipGetLastError();
 }
 
-// The quantizer's rows go to a wave each from this many on and up to this
-// many pieces a lane (17408 rows of 5120: 45 us, with a workgroup to a row 75;
-// 1024 rows of 4096: 8.4 and 9.8).
-constexpr int kWaveMinRows = 1024, kWaveMaxPieces = 16;
+// The quantizer's rows go to a wave each where there are many: short ones (of
+// up to four pieces a lane, 2048 values) from 2048 rows on, where a workgroup
+// has little to exchange (17408 rows of 2048: 17.9 us, with a workgroup to a
+// row 21.2; 4096 rows 6.8 and 7.2; 2048 rows 4.9 and 4.8), longer ones up to
+// 12 pieces from 16384 on (17408 rows of 2560 22.6 and 23.1, of 4096 35.0 and
+// 33.8, of 4608 40.0 and 42.7, of 5120 44.4 and 46.4, of 6144 59.5 and 57.7;
+// but 4096 rows of 4096 11.9 and 11.0, 17408 rows of 7168 73.2 and 65.8).
+constexpr int kWaveMaxPieces = 12;
+bool rows_to_waves(int m, int lane_pieces) {
+  return lane_pieces <= kWaveMaxPieces && m >= (lane_pieces <= 4 ? 2048 : 16384);
+}
+
+// The smallest even number of pieces that holds `pieces` of a lane.
+template <int P, class F>
+hipError_t with_wave_pieces(int pieces, F &&f) {
+  if (pieces <= P) {
+    f(std::integral_constant<int, P>());
+    return hipGetLastError();
+  }
+  if constexpr (P + 2 <= kWaveMaxPieces) return with_wave_pieces<P + 2>(pieces, f);
+  else return hipErrorInvalidValue;
+}
 
 }  // namespace
 
 hipError_t launch_int8_rows(const void *x, int m, int k, int8_t *codes, float *row_scale, hipStream_t s) {
   const RowsOut o{nullptr, codes, row_scale};
   const int pieces = k >> 3, lane_pieces = cdiv(pieces, 64);
-  if (m >= kWaveMinRows && lane_pieces <= kWaveMaxPieces) {
-    auto run = [&](auto p) {
+  if (rows_to_waves(m, lane_pieces)) {
+    return with_wave_pieces<2>(lane_pieces, [&](auto p) {
       hipLaunchKernelGGL((k_int8_rows<true, decltype(p)::value>), dim3(cdiv(m, kWaveRows)), dim3(64 * kWaveRows), 0, s, x,
                          m, k, o);
-    };
-    if (lane_pieces <= 2) run(std::integral_constant<int, 2>());
-    else if (lane_pieces <= 4) run(std::integral_constant<int, 4>());
-    else if (lane_pieces <= 8) run(std::integral_constant<int, 8>());
-    else if (lane_pieces <= 10) run(std::integral_constant<int, 10>());
-    else run(std::integral_constant<int, kWaveMaxPieces>());
-    return hipGetLastError();
+    });
   }
   // few rows: up to eight slices, for about as many workgroups as CUs (64 rows
   // of 17408: 8.4 us a call, 9.6 without), and a piece of a thread for each
