@@ -343,7 +343,8 @@ int64_t int8_gemm_workspace(int32_t m, const int8_weight *w);
  * zero before its first use and left as it needs to be for the next call, of
  * whatever sizes; one per stream that calls may overlap on.  Null: the
  * library's scratch arena (see above); a call on a stream that is being
- * captured has to bring a workspace (NVFP4_EINVAL without). */
+ * captured has to bring a workspace (NVFP4_EINVAL without), whatever its
+ * sizes: which rows need none is not part of this interface. */
 int int8_gemm_w8a8(const void *x, const float *row_scale, int32_t m, const int8_weight *w, void *y,
                    void *workspace, int64_t workspace_bytes, void *stream);
 

@@ -82,8 +82,12 @@ struct Int8TilePlan {
   size_t partial_bytes;
 };
 // What a round of tiles costs, and a split of one, in microseconds (measured
-// at K of 4096 to 17408): a unit of K, the rest of a tile (its first unit's
-// way from memory, its end), and to join its parts, each.
+// at K of 4096 to 17408, where several row blocks share the weights): a unit
+// of K, the rest of a tile (its first unit's way from memory, its end), and to
+// join its parts, each.  What a single row block waits for memory is not in
+// it, nor that a join finds the parts in a cache (66 rows of 5120 x 17408: 33.6
+// by these, 29.5 measured; 333 rows of 7001 x 4128: 23.9 and 25 to 32; 2048 of
+// 17408 x 5120: 177 and 186 to 205).
 struct Int8Tile {
   int rows, cols;  // (cols: half of them gate and half up, with two matrices)
   double unit, tile, join;

@@ -27,7 +27,7 @@
 // so that the sixteen rows of a read lie in different banks.  The weights are
 // the first operand: a lane then holds four neighbouring columns of one row.
 //
-// 64 rows of 5120, 17408: gate and up 39.6 us (4.5 TB/s of weights), down 23
+// 64 rows of 5120, 17408: gate and up 40.0 us (4.5 TB/s of weights), down 23
 // to 25 us (3.6 to 3.9; its columns alone do not fill the CUs: 40 groups of
 // four slots in six parts of K, whose sums go through memory; twice the pieces
 // of them in flight gain nothing).  The matrix cores are 10 and 7% busy; no

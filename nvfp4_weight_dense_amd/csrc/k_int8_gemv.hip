@@ -9,9 +9,10 @@
 // joined in any order, so a row that several waves share is summed with LDS
 // atomics.  Eight pieces are requested while eight are summed (128 to 256 KB
 // in flight for a CU).  One row of 4096, 12288: gate and up with the row
-// quantized 21.8 us (4.6 TB/s), down 12.6 us (4.0); a product of 6144 x 4096
-// of quantized rows 8.5 us, of which start, the first way through memory and
-// the end are some 5.
+// quantized 21.6 us (4.7 TB/s), down 12.5 us (4.0); a product of 6144 x 4096
+// of quantized rows 9.0 us (8.7 with one weight again and again), of which
+// start, the first way through memory and the end are some 5.  Four rows are
+// bound by the products: 29.0, 17.3 and 11.3 us.
 //
 // The activation rows lie in LDS as codes; lane l multiplies codes 16 l .. of
 // a piece with dot products of four.  bf16 rows are quantized here, in every

@@ -19,9 +19,11 @@
 // eight of them at once.  The scales come into LDS with a tile's first unit,
 // so that a tile's end waits for no memory.
 //
-// 8192 x 8192 x 8192 465 to 480 us (2290 to 2360 TOP/s; a library's product of
-// that size 534); 2048 rows of 17408 x 5120 in two launches 205, gate and up
-// of the same FFN 340 to 350, down 185 to 195.  The matrix cores are 55% busy
+// 8192 x 8192 x 8192 477 to 487 us (2260 to 2305 TOP/s; a library's product of
+// that size 534); 2048 rows of 17408 x 5120 in two launches 198 to 205 (186
+// with one set of operands again and again, which the last cache holds), gate
+// and up of the same FFN 359, down 196.  (Operands in turn; a kernel's time
+// under the profiler.)  The matrix cores are 55% busy
 // in tiles of 256 x 256 (48% in 256 x 128), 80% of the lines come from L2, no
 // bank conflicts.  Of the products and the transfers either alone takes 80% of
 // the time: they share the LDS.

@@ -6,15 +6,20 @@
 //   residual: h = bf16(residual + scale * gate * norm(y)), then norm(h)
 //   int8:    s = amax / 127, code = x / s (int8_common.h)
 //
-// All are bound by memory: norm of 8192 rows of 5120 28.8 us (5.8 TB/s), end
-// of a block with post norm, int8 and no gate 64 us (4.6), quantizer of 17408
-// rows of 5120 44 us (6.0); a large copy makes 4.8.  With few rows what counts
+// All are bound by memory: norm of 8192 rows of 5120 28.7 us (5.8 TB/s), to
+// int8 35 (3.6: its divisions count), end of a block with post norm, int8 and
+// no gate 56 to 65 us (4.5 to 5.3), quantizer of 17408 rows of 5120 45 us
+// (5.9); a large copy makes 4.8.  With few rows what counts
 // is the way of one row through memory and the exchanges: 64 rows of 5120
 // 4.6, 6.3 and 4 us.  A workgroup takes a row -- for the quantizer, where
 // there are many rows that are not too long, a wave --, each thread keeps its
 // pieces of eight values in registers from the one read of the row to the one
 // write, and what the row needs as a whole (a sum of squares, a largest
-// magnitude) is exchanged once each.  Statistics are fp32.  The norm's
+// magnitude) is exchanged once each.  Of rows past 65536, sixteen pieces a
+// thread, the norms hold some fifty registers in scratch memory (norm of 512
+// rows of 131072 89 us, 3.0 TB/s; of 65536 32 us, 4.1).  Rows of 512 and less
+// fill a wave or less of a workgroup (norm of 131072 rows of 256 36 us, 3.8
+// TB/s; of 65536 of 512 22 us, 6.1).  Statistics are fp32.  The norm's
 // result is rounded to bf16 before it is quantized, and h before it is
 // normed, so that the fused calls give the bits of the calls one by one.
 #include <algorithm>
